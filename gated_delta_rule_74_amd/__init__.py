@@ -10,6 +10,9 @@ Functions mirror the C entry points by name:
   kda_prefill_state_pass,
   kda_decode_step, kda_conv_prologue, kda_prefill_workspace_size,
   kda_status_string, kda_abi_version
+and, from ``layer.py``, the operators around the mixer:
+  kda_scan, kda_scan_backward, kda_scan_step, kda_gated_norm,
+  kda_gated_norm_backward, kda_block_norm, kda_block_norm_backward
 """
 from __future__ import annotations
 
@@ -457,3 +460,11 @@ def kda_conv_prologue(xq, xk, xv, wq, wk, wv, *, H, Dk, Dv, conv_state=None,
                H, Dk, Dv, int(bool(l2norm_qk)), eps, _stream(stream))
     _check(st, "kda_conv_prologue")
     return q, k, v
+
+
+from .layer import (  # noqa: E402  (needs the names above)
+    KDA_SCAN_CHUNK, kda_block_norm, kda_block_norm_backward,
+    kda_block_norm_backward_workspace_size, kda_gated_norm,
+    kda_gated_norm_backward, kda_gated_norm_backward_workspace_size, kda_scan,
+    kda_scan_backward, kda_scan_backward_workspace_size, kda_scan_step,
+    kda_scan_workspace_size)

@@ -1,0 +1,435 @@
+// kda_norm.hip -- RMS norm of a mixer's heads times a gate, and the norms
+// around a block with its gate and scaled residual, with their gradients
+// (see include/kda.h for the formulas).
+//
+// Both are bound by HBM: about ten operations per element.  A row is read
+// once into registers and everything is made from there.  All sums are fp32
+// in a fixed order; the gradients of the weights, sums over all rows, go
+// through one partial row per workgroup and a second kernel that adds those
+// in a fixed order, so a call's results do not change from run to run.
+//
+// With n = v r, r = 1 / sqrt(mean v^2 + eps), and t the gradient of n, the
+// gradient of v is r (t - n mean(t n)).
+#include "kda_layer.h"
+#include "kda_vec.h"
+
+namespace kda {
+
+// logistic function and the gates made of it; fp32 data takes the library's
+// exp and a correctly rounded division, bf16 data the hardware ones (about
+// 2 ulp of fp32, 2^14 times finer than the rounding of the result)
+template <bool FAST> __device__ __forceinline__ float logistic(float z) {
+  if constexpr (FAST) return __builtin_amdgcn_rcpf(1.f + __expf(-z));
+  else return 1.f / (1.f + expf(-z));
+}
+template <bool FAST>
+__device__ __forceinline__ float gate_of(float z, int act) {
+  const float s = logistic<FAST>(z);
+  return act == ACT_SILU ? z * s : s;
+}
+// the gate and its derivative
+template <bool FAST>
+__device__ __forceinline__ float2 gate_grad(float z, int act) {
+  const float s = logistic<FAST>(z), m = s * (1.f - s);
+  return act == ACT_SILU ? make_float2(z * s, s + z * m) : make_float2(s, m);
+}
+
+__device__ __forceinline__ float inv_rms(float sumsq, int n, float eps) {
+  return 1.f / sqrtf(sumsq / (float)n + eps);
+}
+
+// ---------------------------------------------------------------------------
+// gated head norm: D / 8 lanes hold one row of D values
+
+constexpr int GN_THREADS = 256;
+constexpr int GN_MAX_WG = 1024;  // partial rows of the weight gradient
+
+template <typename IO, int D>
+__global__ __launch_bounds__(GN_THREADS) void kda_gated_norm_fwd(
+    GatedNormParams p) {
+  constexpr bool FAST = sizeof(IO) == 2;
+  const long long v = (long long)blockIdx.x * GN_THREADS + threadIdx.x;
+  const long long row = v / (D / 8);
+  const int ch = (int)(v % (D / 8)) * 8;
+  const bool on = row < p.rows;
+  const size_t at = on ? (size_t)row * D + ch : (size_t)ch;
+  Raw8<IO> o, z;
+  o.load((const IO *)p.o + at);
+  if (p.z) z.load((const IO *)p.z + at);
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) ss += o.get(i) * o.get(i);
+  const float r = inv_rms(group_sum<D / 8>(ss), D, p.eps);
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    y[i] = o.get(i) * r * p.w[ch + i];
+    if (p.z) y[i] *= gate_of<FAST>(z.get(i), p.act);
+  }
+  if (on) store8((IO *)p.y + at, y);
+}
+
+template <typename IO, int D>
+__global__ __launch_bounds__(GN_THREADS) void kda_gated_norm_bwd(
+    GatedNormParams p) {
+  constexpr bool FAST = sizeof(IO) == 2;
+  constexpr int G = D / 8, RPW = GN_THREADS / G;  // rows per pass
+  __shared__ float part[RPW][D];
+  const int ch = (int)(threadIdx.x % G) * 8, rr = threadIdx.x / G;
+  float w[8], dw[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) { w[i] = p.w[ch + i]; dw[i] = 0.f; }
+  // every lane of a wave takes part in every sum: rows past the end are
+  // read as the last row and contribute nothing
+  for (long long base = (long long)blockIdx.x * RPW; base < p.rows;
+       base += (long long)gridDim.x * RPW) {
+    const long long row = base + rr;
+    const bool on = row < p.rows;
+    const size_t at = (size_t)(on ? row : p.rows - 1) * D + ch;
+    Raw8<IO> o, z, dy;
+    o.load((const IO *)p.o + at);
+    dy.load((const IO *)p.dy + at);
+    if (p.z) z.load((const IO *)p.z + at);
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss += o.get(i) * o.get(i);
+    const float r = inv_rms(group_sum<G>(ss), D, p.eps);
+    float t[8], dz[8], tn = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float n = o.get(i) * r, d = dy.get(i);
+      float2 g = make_float2(1.f, 0.f);
+      if (p.z) g = gate_grad<FAST>(z.get(i), p.act);
+      dz[i] = d * n * w[i] * g.y;
+      const float dg = d * g.x;
+      dw[i] += on ? dg * n : 0.f;
+      t[i] = dg * w[i];
+      tn += t[i] * n;
+    }
+    const float m = group_sum<G>(tn) / (float)D;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = r * (t[i] - o.get(i) * r * m);
+    if (on) {
+      store8((IO *)p.y + at, t);
+      if (p.z) store8((IO *)p.dz + at, dz);
+    }
+  }
+  store8(&part[rr][ch], dw);
+  __syncthreads();
+  if (threadIdx.x < D) {
+    float a = 0.f;
+    for (int k = 0; k < RPW; ++k) a += part[k][threadIdx.x];
+    p.ws[(size_t)blockIdx.x * D + threadIdx.x] = a;
+  }
+}
+
+// out[c] = sum over n rows of part[row][stride], columns c < width: a
+// workgroup takes 16 columns, 16 row lanes each, joined in a fixed order
+__global__ __launch_bounds__(256) void kda_sum_rows(const float *part,
+                                                    long long stride, int n,
+                                                    int width, float *out) {
+  __shared__ float s[16][17];
+  const int c = threadIdx.x % 16, k = threadIdx.x / 16;
+  const int col = blockIdx.x * 16 + c;
+  float a = 0.f;
+  if (col < width)
+    for (int i = k; i < n; i += 16) a += part[(size_t)i * stride + col];
+  s[k][c] = a;
+  __syncthreads();
+  if (k == 0 && col < width) {
+    a = 0.f;
+    for (int i = 0; i < 16; ++i) a += s[i][c];
+    out[col] = a;
+  }
+}
+
+static int gn_groups(long long rows, int D) {
+  const long long rpw = GN_THREADS / (D / 8);
+  const long long n = (rows + rpw - 1) / rpw;
+  return (int)(n < GN_MAX_WG ? n : GN_MAX_WG);
+}
+
+template <typename IO, int D>
+static hipError_t gn_t(const GatedNormParams &p, hipStream_t s, bool bwd) {
+  if (!bwd) {
+    const long long v = p.rows * (D / 8);
+    hipLaunchKernelGGL((kda_gated_norm_fwd<IO, D>),
+                       dim3((unsigned)((v + GN_THREADS - 1) / GN_THREADS)),
+                       dim3(GN_THREADS), 0, s, p);
+    return hipGetLastError();
+  }
+  const int n = gn_groups(p.rows, D);
+  hipLaunchKernelGGL((kda_gated_norm_bwd<IO, D>), dim3(n), dim3(GN_THREADS), 0,
+                     s, p);
+  hipLaunchKernelGGL(kda_sum_rows, dim3((D + 15) / 16), dim3(256), 0, s, p.ws,
+                     (long long)D, n, D, p.dw);
+  return hipGetLastError();
+}
+
+template <typename IO>
+static hipError_t gn_d(const GatedNormParams &p, hipStream_t s, bool bwd) {
+  switch (p.D) {
+    case 16: return gn_t<IO, 16>(p, s, bwd);
+    case 32: return gn_t<IO, 32>(p, s, bwd);
+    case 64: return gn_t<IO, 64>(p, s, bwd);
+    case 128: return gn_t<IO, 128>(p, s, bwd);
+  }
+  return hipErrorInvalidValue;
+}
+
+hipError_t launch_gated_norm(const GatedNormParams &p, hipStream_t s) {
+  return p.io_bf16 ? gn_d<bf16>(p, s, false) : gn_d<float>(p, s, false);
+}
+hipError_t launch_gated_norm_backward(const GatedNormParams &p,
+                                      hipStream_t s) {
+  return p.io_bf16 ? gn_d<bf16>(p, s, true) : gn_d<float>(p, s, true);
+}
+size_t gated_norm_bwd_ws_bytes(long long rows, int D) {
+  return (size_t)gn_groups(rows, D) * D * 4;
+}
+
+// ---------------------------------------------------------------------------
+// norms around a block: a workgroup holds one row of C values, V consecutive
+// ones per thread and step
+
+// sum over the wave, every lane getting it
+__device__ __forceinline__ float wave_sum(float x) {
+  x = group_sum<32>(x);
+  return x + __shfl_xor(x, 32, 64);
+}
+// sums over the workgroup of N values at once; `s`: N * 16 floats that no
+// wave still reads from an earlier call (callers alternate two)
+template <int N>
+__device__ __forceinline__ void block_sum(float (&x)[N], float *s) {
+  const int waves = blockDim.x / 64, w = threadIdx.x / 64;
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = wave_sum(x[i]);
+  if (waves == 1) return;
+  if (threadIdx.x % 64 == 0)
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i * 16 + w] = x[i];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    x[i] = 0.f;
+    for (int k = 0; k < waves; ++k) x[i] += s[i * 16 + k];
+  }
+}
+
+template <typename IO, typename RT, int V, int NV>
+__global__ __launch_bounds__(1024) void kda_block_norm_fwd(BlockNormParams p) {
+  constexpr bool FAST = sizeof(IO) == 2;
+  __shared__ float s1[16], s2[16];
+  const size_t row = (size_t)blockIdx.x * p.C;
+  RawV<IO, V> y[NV], z[NV];
+  RawV<RT, V> r[NV];
+  int at[NV];
+  bool on[NV];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    at[k] = (k * (int)blockDim.x + (int)threadIdx.x) * V;
+    on[k] = at[k] < p.C;
+    if (!on[k]) at[k] = 0;
+    y[k].load((const IO *)p.y + row + at[k]);
+    if (p.z) z[k].load((const IO *)p.z + row + at[k]);
+    r[k].load((const RT *)p.r + row + at[k]);
+  }
+  float r1 = 1.f;
+  if (p.w_post) {
+    float ss[1] = {0.f};
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        ss[0] += on[k] ? y[k].get(i) * y[k].get(i) : 0.f;
+    block_sum(ss, s1);
+    r1 = inv_rms(ss[0], p.C, p.eps);
+  }
+  float h[NV][V], ss[1] = {0.f};
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float u = y[k].get(i);
+      if (p.w_post) u = u * r1 * p.w_post[at[k] + i];
+      if (p.z) u *= gate_of<FAST>(z[k].get(i), p.act);
+      h[k][i] = p.res_scale * r[k].get(i) + p.branch_scale * u;
+      ss[0] += on[k] ? h[k][i] * h[k][i] : 0.f;
+    }
+    if (on[k]) store_v<V>((RT *)p.r_out + row + at[k], h[k]);
+  }
+  if (!p.w_pre) return;
+  block_sum(ss, s2);
+  const float r2 = inv_rms(ss[0], p.C, p.eps);
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) h[k][i] = h[k][i] * r2 * p.w_pre[at[k] + i];
+    if (on[k]) store_v<V>((IO *)p.x + row + at[k], h[k]);
+  }
+}
+
+constexpr int BN_MAX_WG = 512;  // partial rows of the weight gradients
+
+// partial rows: workgroup g's dw_post at ws[g][0][C], dw_pre at ws[g][1][C]
+template <typename IO, typename RT, int V, int NV>
+__global__ __launch_bounds__(1024) void kda_block_norm_bwd(BlockNormParams p) {
+  constexpr bool FAST = sizeof(IO) == 2;
+  __shared__ float s1[2][16 * 3], s2[2][16];
+  int at[NV];
+  bool on[NV];
+  float a_post[NV][V], a_pre[NV][V];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    at[k] = (k * (int)blockDim.x + (int)threadIdx.x) * V;
+    on[k] = at[k] < p.C;
+    if (!on[k]) at[k] = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) a_post[k][i] = a_pre[k][i] = 0.f;
+  }
+  int turn = 0;
+  for (int n = blockIdx.x; n < p.rows; n += gridDim.x, turn ^= 1) {
+    const size_t row = (size_t)n * p.C;
+    RawV<IO, V> y[NV], z[NV], dx[NV];
+    RawV<RT, V> r[NV], dr[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      y[k].load((const IO *)p.y + row + at[k]);
+      if (p.z) z[k].load((const IO *)p.z + row + at[k]);
+      if (p.dx) {
+        dx[k].load((const IO *)p.dx + row + at[k]);
+        r[k].load((const RT *)p.r + row + at[k]);
+      }
+      if (p.dr_out) dr[k].load((const RT *)p.dr_out + row + at[k]);
+    }
+    // sums of r^2, of (w_pre dx) r and of y^2
+    float q[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (on[k]) {
+          if (p.dx) {
+            q[0] += r[k].get(i) * r[k].get(i);
+            q[1] += r[k].get(i) * dx[k].get(i) * p.w_pre[at[k] + i];
+          }
+          if (p.w_post) q[2] += y[k].get(i) * y[k].get(i);
+        }
+    block_sum(q, s1[turn]);
+    const float r2 = inv_rms(q[0], p.C, p.eps);
+    const float m2 = r2 * r2 * q[1] / (float)p.C;
+    const float r1 = inv_rms(q[2], p.C, p.eps);
+    float d[NV][V], tn[1] = {0.f};
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      float o[V], oz[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float g = p.dr_out ? dr[k].get(i) : 0.f;
+        if (p.dx) {
+          const float x = dx[k].get(i);
+          a_pre[k][i] += on[k] ? x * r[k].get(i) * r2 : 0.f;
+          g += r2 * (x * p.w_pre[at[k] + i] - r[k].get(i) * m2);
+        }
+        o[i] = p.res_scale * g;
+        float du = p.branch_scale * g;
+        const float nv = p.w_post ? y[k].get(i) * r1 : y[k].get(i);
+        const float w = p.w_post ? p.w_post[at[k] + i] : 1.f;
+        if (p.z) {
+          const float2 gg = gate_grad<FAST>(z[k].get(i), p.act);
+          oz[i] = du * nv * w * gg.y;
+          du *= gg.x;
+        }
+        if (p.w_post) {
+          a_post[k][i] += on[k] ? du * nv : 0.f;
+          du *= w;
+          tn[0] += on[k] ? du * nv : 0.f;
+        }
+        d[k][i] = du;
+      }
+      if (on[k]) {
+        store_v<V>((RT *)p.dr + row + at[k], o);
+        if (p.z) store_v<V>((IO *)p.dz + row + at[k], oz);
+      }
+    }
+    if (p.w_post) {
+      block_sum(tn, s2[turn]);
+      const float m1 = tn[0] / (float)p.C;
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          d[k][i] = r1 * (d[k][i] - y[k].get(i) * r1 * m1);
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+      if (on[k]) store_v<V>((IO *)p.dy + row + at[k], d[k]);
+  }
+  float *out = p.ws + (size_t)blockIdx.x * 2 * p.C;
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (on[k]) {
+        if (p.w_post) out[at[k] + i] = a_post[k][i];
+        if (p.dx) out[p.C + at[k] + i] = a_pre[k][i];
+      }
+}
+
+static int bn_groups(int rows) { return rows < BN_MAX_WG ? rows : BN_MAX_WG; }
+
+template <typename IO, typename RT, int V, int NV>
+static hipError_t bn_launch(const BlockNormParams &p, hipStream_t s,
+                            bool bwd) {
+  const int steps = (p.C + V * NV - 1) / (V * NV);
+  const int threads = (steps + 63) / 64 * 64;  // at most 1024: see bn_t
+  if (!bwd) {
+    hipLaunchKernelGGL((kda_block_norm_fwd<IO, RT, V, NV>), dim3(p.rows),
+                       dim3(threads), 0, s, p);
+    return hipGetLastError();
+  }
+  const int n = bn_groups(p.rows);
+  hipLaunchKernelGGL((kda_block_norm_bwd<IO, RT, V, NV>), dim3(n),
+                     dim3(threads), 0, s, p);
+  const dim3 cols((p.C + 15) / 16);
+  if (p.w_post)
+    hipLaunchKernelGGL(kda_sum_rows, cols, dim3(256), 0, s, p.ws,
+                       (long long)2 * p.C, n, p.C, p.dw_post);
+  if (p.dx)
+    hipLaunchKernelGGL(kda_sum_rows, cols, dim3(256), 0, s, p.ws + p.C,
+                       (long long)2 * p.C, n, p.C, p.dw_pre);
+  return hipGetLastError();
+}
+
+// C <= 16384.  Rows of a multiple of 8 values start 16-byte aligned and move
+// as vectors; others value by value.
+template <typename IO, typename RT>
+static hipError_t bn_t(const BlockNormParams &p, hipStream_t s, bool bwd) {
+  if (p.C % 8 == 0)
+    return p.C <= 8192 ? bn_launch<IO, RT, 8, 1>(p, s, bwd)
+                       : bn_launch<IO, RT, 8, 2>(p, s, bwd);
+  return p.C <= 4096 ? bn_launch<IO, RT, 1, 4>(p, s, bwd)
+                     : bn_launch<IO, RT, 1, 16>(p, s, bwd);
+}
+
+static hipError_t bn_any(const BlockNormParams &p, hipStream_t s, bool bwd) {
+  switch (p.pair) {
+    case PAIR_F32: return bn_t<float, float>(p, s, bwd);
+    case PAIR_BF16_F32: return bn_t<bf16, float>(p, s, bwd);
+    case PAIR_BF16_BF16: return bn_t<bf16, bf16>(p, s, bwd);
+  }
+  return hipErrorInvalidValue;
+}
+
+hipError_t launch_block_norm(const BlockNormParams &p, hipStream_t s) {
+  return bn_any(p, s, false);
+}
+hipError_t launch_block_norm_backward(const BlockNormParams &p,
+                                      hipStream_t s) {
+  return bn_any(p, s, true);
+}
+size_t block_norm_bwd_ws_bytes(int rows, int C) {
+  return (size_t)bn_groups(rows) * 2 * C * 4;
+}
+
+}  // namespace kda

@@ -1,0 +1,56 @@
+// kda_vec.h -- V consecutive values of one dtype as a thread holds them, for
+// the streaming layer operators (scan, norms).
+#pragma once
+#include "kda_device.h"
+
+namespace kda {
+
+// 8 consecutive values, raw; converted where they are used
+template <typename IO> struct Raw8;
+template <> struct Raw8<bf16> {
+  uint4 r;
+  __device__ __forceinline__ void load(const bf16 *p) { r = *(const uint4 *)p; }
+  __device__ __forceinline__ float get(int i) const {
+    const unsigned w = i < 2 ? r.x : i < 4 ? r.y : i < 6 ? r.z : r.w;
+    return __uint_as_float((i & 1) ? (w & 0xffff0000u) : (w << 16));
+  }
+};
+template <> struct Raw8<float> {
+  f32x4 lo, hi;
+  __device__ __forceinline__ void load(const float *p) {
+    lo = *(const f32x4 *)p;
+    hi = *(const f32x4 *)(p + 4);
+  }
+  __device__ __forceinline__ float get(int i) const {
+    return i < 4 ? lo[i] : hi[i - 4];
+  }
+};
+__device__ __forceinline__ void store8(bf16 *p, const float *v) {
+  bf16x8 r;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = (bf16)v[i];
+  *(bf16x8 *)p = r;
+}
+__device__ __forceinline__ void store8(float *p, const float *v) {
+  *(f32x4 *)p = f32x4{v[0], v[1], v[2], v[3]};
+  *(f32x4 *)(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+}
+
+// one value, for rows whose width is no multiple of 8
+template <typename IO> struct Raw1 {
+  IO r;
+  __device__ __forceinline__ void load(const IO *p) { r = *p; }
+  __device__ __forceinline__ float get(int) const { return to_f32(r); }
+};
+template <typename IO, int V> struct RawSel;
+template <typename IO> struct RawSel<IO, 8> { typedef Raw8<IO> type; };
+template <typename IO> struct RawSel<IO, 1> { typedef Raw1<IO> type; };
+template <typename IO, int V> using RawV = typename RawSel<IO, V>::type;
+
+template <int V, typename IO>
+__device__ __forceinline__ void store_v(IO *p, const float *v) {
+  if constexpr (V == 8) store8(p, v);
+  else *p = from_f32<IO>(v[0]);
+}
+
+}  // namespace kda

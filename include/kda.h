@@ -318,6 +318,147 @@ kda_status kda_conv_prologue(const void *xq, const void *xk, const void *xv,
                              int B, int T, int H, int Dk, int Dv,
                              int l2norm_qk, float eps, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * The operators around the KDA mixer in a block of such a model: a gated
+ * linear recurrence with a vector state (the plain sibling of KDA's matrix
+ * state), the mixer's output norm and gate, and the norms and residual around
+ * a block.  The conventions above hold (device pointers, 16-byte alignment,
+ * dense row-major tensors, asynchronous on `stream`, nothing allocated,
+ * nothing written on an error), with these dtype pairs: (F32,F32),
+ * (BF16,F32), (BF16,BF16).  All sums, norms and states are fp32, and every
+ * result is the same from call to call on the same inputs. */
+
+/* Tokens per chunk of kda_scan's chunk_states. */
+#define KDA_SCAN_CHUNK 128
+
+/* Bytes of device workspace kda_scan and kda_scan_backward need (0 if the
+ * sizes are invalid or unsupported); contents need no initialisation.  Calls
+ * that may overlap in time need workspaces of their own. */
+size_t kda_scan_workspace_size(int B, int T, int H, int D);
+size_t kda_scan_backward_workspace_size(int B, int T, int H, int D);
+
+/* Gated linear recurrence with a state h of one value per channel.  Per
+ * sequence, head and channel, for each token t:
+ *     h_t = exp(g_t) h_{t-1} + beta_t x_t,     y_t = h_t
+ *   x        [B,T,H,D] in io_dtype, D in {16,32,64,128}
+ *   g        log-decay, [B,T,H,D] in gate_dtype, or one per token and head
+ *            [B,T,H] with KDA_GATE_HEAD; g <= 0, -inf forgets exactly
+ *   beta     write strength [B,T,H] in gate_dtype, or NULL (all ones)
+ *   h0       initial state [B,H,D] fp32, or NULL for zeros
+ *   lengths  [B] int32 on the device, or NULL (every sequence has T tokens):
+ *            sequence b ends after lengths[b] tokens (clamped to 0..T).
+ *            Tokens from there on leave the state alone whatever the inputs
+ *            hold there, and their outputs are written as zeros.
+ *   y        [B,T,H,D] in io_dtype; must not alias an input
+ *   h_out    state after the last token [B,H,D] fp32, or NULL; may equal h0
+ *   chunk_states  [B,ceil(T/KDA_SCAN_CHUNK),H,D] fp32, or NULL: the state
+ *            before each chunk of KDA_SCAN_CHUNK tokens, which
+ *            kda_scan_backward takes in place of a recomputation
+ * With a few tokens per sequence this is also the multi-token step.
+ * Errors: KDA_EINVAL as elsewhere; KDA_EUNSUPPORTED for other D, dtype pairs,
+ * T > 2^30, H*D > 2^30, or more than 2^23 - 1 tiles
+ * B * ceil(T/128) * ceil(H*D/128). */
+kda_status kda_scan(const void *x, kda_dtype io_dtype, const void *g,
+                    const void *beta, kda_dtype gate_dtype, const float *h0,
+                    const int *lengths, void *y, float *h_out,
+                    float *chunk_states, int B, int T, int H, int D,
+                    void *workspace, size_t workspace_bytes, void *stream);
+
+/* Gradient of kda_scan for the loss sum(y * dy) + sum(h_out * dhT):
+ *   dh_t = dy_t + exp(g_{t+1}) dh_{t+1}  (dh of the last token: dy + dhT)
+ *   dx = beta dh;  dbeta = sum over the head's channels of dh x;
+ *   dg = dh exp(g_t) h_{t-1} (summed over the head's channels with
+ *   KDA_GATE_HEAD);  dh0 = exp(g_1) dh_1 (dhT for an empty sequence)
+ *   dy            [B,T,H,D] in io_dtype
+ *   dhT           [B,H,D] fp32 gradient of the final state, or NULL (zero)
+ *   chunk_states  those that kda_scan wrote for the same inputs, or NULL: they
+ *                 are then recomputed
+ *   dx            [B,T,H,D] in io_dtype
+ *   dg            shaped like g, in gate_dtype
+ *   dbeta         [B,T,H] in gate_dtype; NULL exactly when beta is
+ *   dh0           [B,H,D] fp32, or NULL
+ * Gradients of tokens past a sequence's length are written as zeros.  No
+ * output may alias an input or another output. */
+kda_status kda_scan_backward(const void *x, kda_dtype io_dtype, const void *g,
+                             const void *beta, kda_dtype gate_dtype,
+                             const float *h0, const int *lengths,
+                             const void *dy, const float *dhT,
+                             const float *chunk_states, void *dx, void *dg,
+                             void *dbeta, float *dh0, int B, int T, int H,
+                             int D, void *workspace, size_t workspace_bytes,
+                             void *stream);
+
+/* One token of that recurrence for N sequences: x [N,H,D], g [N,H,D] (or
+ * [N,H]), beta [N,H] or NULL, state [N,H,D] fp32 updated IN PLACE, y [N,H,D]
+ * in io_dtype (must not alias an input or the state). */
+kda_status kda_scan_step(const void *x, kda_dtype io_dtype, const void *g,
+                         const void *beta, kda_dtype gate_dtype, float *state,
+                         void *y, int N, int H, int D, void *stream);
+
+/* Gates of the norms below: none, logistic(z), z logistic(z). */
+typedef enum kda_act {
+  KDA_ACT_NONE = 0,
+  KDA_ACT_SIGMOID = 1,
+  KDA_ACT_SILU = 2
+} kda_act;
+
+/* RMS norm of a mixer's heads times a gate, over `rows` rows of D values
+ * (rows = tokens * heads of kda_prefill's or kda_scan's output):
+ *     y = o / sqrt(mean(o^2) + eps) * w * act(z)
+ *   o, z, y  [rows,D] in io_dtype, D in {16,32,64,128}; z NULL exactly when
+ *            act is KDA_ACT_NONE; w [D] fp32; y must not alias an input
+ * KDA_EUNSUPPORTED: other D, rows * D > 2^34. */
+kda_status kda_gated_norm(const void *o, const void *z, kda_dtype io_dtype,
+                          const float *w, kda_act act, float eps, void *y,
+                          long long rows, int D, void *stream);
+
+/* Its gradient: d_o and dz [rows,D] in io_dtype (dz NULL exactly when z is),
+ * dw [D] fp32 (summed over the rows in a fixed order). */
+size_t kda_gated_norm_backward_workspace_size(long long rows, int D);
+kda_status kda_gated_norm_backward(const void *o, const void *z,
+                                   kda_dtype io_dtype, const float *w,
+                                   kda_act act, float eps, const void *dy,
+                                   void *d_o, void *dz, float *dw,
+                                   long long rows, int D, void *workspace,
+                                   size_t workspace_bytes, void *stream);
+
+/* Between two blocks, over `rows` rows of C values:
+ *     u     = act(z) * norm(y; w_post)     norm(v; w) = v / sqrt(mean(v^2) +
+ *     r_out = res_scale r + branch_scale u                          eps) * w
+ *     x     = norm(r_out; w_pre)
+ *   y        the block's output [rows,C] in io_dtype
+ *   r, r_out the residual stream [rows,C] in stream_dtype; r_out may equal r
+ *            (x is made from r_out before its rounding)
+ *   z        gate [rows,C] in io_dtype, NULL exactly when act is KDA_ACT_NONE
+ *   w_post   [C] fp32, or NULL: no norm behind the block (u = act(z) y)
+ *   w_pre    [C] fp32, or NULL: no norm in front of the next one (x NULL)
+ *   x        [rows,C] in io_dtype; NULL exactly when w_pre is
+ * 1 <= C <= 16384, rows < 2^22 (KDA_EUNSUPPORTED beyond).  Apart from
+ * r_out = r no output may alias an input or another output. */
+kda_status kda_block_norm(const void *y, kda_dtype io_dtype, const void *r,
+                          kda_dtype stream_dtype, const void *z, kda_act act,
+                          const float *w_post, const float *w_pre,
+                          float res_scale, float branch_scale, float eps,
+                          void *r_out, void *x, int rows, int C, void *stream);
+
+/* Its gradient, from the stream r_out that the forward call left (r itself is
+ * not needed):
+ *   dx       gradient of x [rows,C] in io_dtype; NULL exactly when w_pre is
+ *   dr_out   gradient that reaches r_out from behind, in stream_dtype, or
+ *            NULL (zero); dx and dr_out are not both NULL
+ *   dy, dz   in io_dtype (dz NULL exactly when z is), dr in stream_dtype
+ *   dw_post, dw_pre  [C] fp32, NULL exactly when the weights are (summed over
+ *            the rows in a fixed order)
+ * No output may alias an input or another output. */
+size_t kda_block_norm_backward_workspace_size(int rows, int C);
+kda_status kda_block_norm_backward(
+    const void *y, kda_dtype io_dtype, const void *r_out,
+    kda_dtype stream_dtype, const void *z, kda_act act, const float *w_post,
+    const float *w_pre, float res_scale, float branch_scale, float eps,
+    const void *dx, const void *dr_out, void *dy, void *dr, void *dz,
+    float *dw_post, float *dw_pre, int rows, int C, void *workspace,
+    size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
