@@ -36,6 +36,15 @@ __device__ __forceinline__ void store8(float *p, const float *v) {
   *(f32x4 *)(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
 }
 
+// Make the raw registers opaque: what was converted from them before is then
+// made again, not kept in registers across what lies between.
+__device__ __forceinline__ void forget(Raw8<bf16> &v) {
+  asm volatile("" : "+v"(v.r.x), "+v"(v.r.y), "+v"(v.r.z), "+v"(v.r.w));
+}
+__device__ __forceinline__ void forget(Raw8<float> &v) {
+  asm volatile("" : "+v"(v.lo), "+v"(v.hi));
+}
+
 // one value, for rows whose width is no multiple of 8
 template <typename IO> struct Raw1 {
   IO r;
