@@ -11,6 +11,15 @@ namespace kda {
 // dtype pairs, as everywhere in this library
 enum LayerPair { PAIR_F32, PAIR_BF16_F32, PAIR_BF16_BF16 };
 
+// compute units of the current device
+inline hipError_t layer_cus(int *cus) {
+  int dev = 0;
+  const hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  return hipDeviceGetAttribute(cus, hipDeviceAttributeMultiprocessorCount,
+                               dev);
+}
+
 // tokens per chunk of the scan (KDA_SCAN_CHUNK in include/kda.h)
 constexpr int SCAN_L = 128;
 

@@ -44,29 +44,50 @@ __device__ __forceinline__ float inv_rms(float sumsq, int n, float eps) {
 constexpr int GN_THREADS = 256;
 constexpr int GN_MAX_WG = 1024;  // partial rows of the weight gradient
 
+// 8 fp32 weights
+__device__ __forceinline__ void load_w(const float *p, float (&w)[8]) {
+  const f32x4 lo = *(const f32x4 *)p, hi = *(const f32x4 *)(p + 4);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) { w[i] = lo[i]; w[4 + i] = hi[i]; }
+}
+
+// a thread takes GN_VPT pieces of 8 values, all loads issued first
+constexpr int GN_VPT = 4;
+
 template <typename IO, int D>
 __global__ __launch_bounds__(GN_THREADS) void kda_gated_norm_fwd(
     GatedNormParams p) {
   constexpr bool FAST = sizeof(IO) == 2;
-  const long long v = (long long)blockIdx.x * GN_THREADS + threadIdx.x;
-  const long long row = v / (D / 8);
-  const int ch = (int)(v % (D / 8)) * 8;
-  const bool on = row < p.rows;
-  const size_t at = on ? (size_t)row * D + ch : (size_t)ch;
-  Raw8<IO> o, z;
-  o.load((const IO *)p.o + at);
-  if (p.z) z.load((const IO *)p.z + at);
-  float ss = 0.f;
+  const long long v0 =
+      (long long)blockIdx.x * (GN_THREADS * GN_VPT) + threadIdx.x;
+  const long long nv = p.rows * (D / 8);
+  const int ch = (int)(threadIdx.x % (D / 8)) * 8;
+  Raw8<IO> o[GN_VPT], z[GN_VPT];
+  float w[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) ss += o.get(i) * o.get(i);
-  const float r = inv_rms(group_sum<D / 8>(ss), D, p.eps);
-  float y[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    y[i] = o.get(i) * r * p.w[ch + i];
-    if (p.z) y[i] *= gate_of<FAST>(z.get(i), p.act);
+  for (int k = 0; k < GN_VPT; ++k) {
+    // pieces past the end are read as the first row's
+    const long long v = v0 + k * GN_THREADS;
+    const size_t at = v < nv ? (size_t)v * 8 : (size_t)ch;
+    o[k].load((const IO *)p.o + at);
+    if (p.z) z[k].load((const IO *)p.z + at);
   }
-  if (on) store8((IO *)p.y + at, y);
+  load_w(p.w + ch, w);
+#pragma unroll
+  for (int k = 0; k < GN_VPT; ++k) {
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss += o[k].get(i) * o[k].get(i);
+    const float r = inv_rms(group_sum<D / 8>(ss), D, p.eps);
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      y[i] = o[k].get(i) * r * w[i];
+      if (p.z) y[i] *= gate_of<FAST>(z[k].get(i), p.act);
+    }
+    const long long v = v0 + k * GN_THREADS;
+    if (v < nv) store8((IO *)p.y + v * 8, y);
+  }
 }
 
 template <typename IO, int D>
@@ -123,23 +144,28 @@ __global__ __launch_bounds__(GN_THREADS) void kda_gated_norm_bwd(
   }
 }
 
-// out[c] = sum over n rows of part[row][stride], columns c < width: a
-// workgroup takes 16 columns, 16 row lanes each, joined in a fixed order
+// sums over n rows of part[row][stride], columns lo <= c < hi: column c goes
+// to out0[c], or from C on to out1[c - C].  A workgroup takes 16 columns, 16
+// row lanes each, joined in a fixed order.
 __global__ __launch_bounds__(256) void kda_sum_rows(const float *part,
                                                     long long stride, int n,
-                                                    int width, float *out) {
+                                                    int lo, int hi, int C,
+                                                    float *out0, float *out1) {
   __shared__ float s[16][17];
   const int c = threadIdx.x % 16, k = threadIdx.x / 16;
-  const int col = blockIdx.x * 16 + c;
+  const int col = lo + blockIdx.x * 16 + c;
   float a = 0.f;
-  if (col < width)
+  if (col < hi) {
+#pragma unroll 8
     for (int i = k; i < n; i += 16) a += part[(size_t)i * stride + col];
+  }
   s[k][c] = a;
   __syncthreads();
-  if (k == 0 && col < width) {
+  if (k == 0 && col < hi) {
     a = 0.f;
     for (int i = 0; i < 16; ++i) a += s[i][c];
-    out[col] = a;
+    if (col < C) out0[col] = a;
+    else out1[col - C] = a;
   }
 }
 
@@ -152,9 +178,9 @@ static int gn_groups(long long rows, int D) {
 template <typename IO, int D>
 static hipError_t gn_t(const GatedNormParams &p, hipStream_t s, bool bwd) {
   if (!bwd) {
-    const long long v = p.rows * (D / 8);
+    const long long v = p.rows * (D / 8), per = GN_THREADS * GN_VPT;
     hipLaunchKernelGGL((kda_gated_norm_fwd<IO, D>),
-                       dim3((unsigned)((v + GN_THREADS - 1) / GN_THREADS)),
+                       dim3((unsigned)((v + per - 1) / per)),
                        dim3(GN_THREADS), 0, s, p);
     return hipGetLastError();
   }
@@ -162,7 +188,7 @@ static hipError_t gn_t(const GatedNormParams &p, hipStream_t s, bool bwd) {
   hipLaunchKernelGGL((kda_gated_norm_bwd<IO, D>), dim3(n), dim3(GN_THREADS), 0,
                      s, p);
   hipLaunchKernelGGL(kda_sum_rows, dim3((D + 15) / 16), dim3(256), 0, s, p.ws,
-                     (long long)D, n, D, p.dw);
+                     (long long)D, n, 0, D, D, p.dw, p.dw);
   return hipGetLastError();
 }
 
@@ -216,91 +242,142 @@ __device__ __forceinline__ void block_sum(float (&x)[N], float *s) {
   }
 }
 
-template <typename IO, typename RT, int V, int NV>
-__global__ __launch_bounds__(1024) void kda_block_norm_fwd(BlockNormParams p) {
-  constexpr bool FAST = sizeof(IO) == 2;
-  __shared__ float s1[16], s2[16];
-  const size_t row = (size_t)blockIdx.x * p.C;
-  RawV<IO, V> y[NV], z[NV];
-  RawV<RT, V> r[NV];
+// columns of a thread: NV pieces of V values
+template <int V, int NV> struct Cols {
   int at[NV];
   bool on[NV];
+  __device__ __forceinline__ Cols(int C) {
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    at[k] = (k * (int)blockDim.x + (int)threadIdx.x) * V;
-    on[k] = at[k] < p.C;
-    if (!on[k]) at[k] = 0;
-    y[k].load((const IO *)p.y + row + at[k]);
-    if (p.z) z[k].load((const IO *)p.z + row + at[k]);
-    r[k].load((const RT *)p.r + row + at[k]);
-  }
-  float r1 = 1.f;
-  if (p.w_post) {
-    float ss[1] = {0.f};
-#pragma unroll
-    for (int k = 0; k < NV; ++k)
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        ss[0] += on[k] ? y[k].get(i) * y[k].get(i) : 0.f;
-    block_sum(ss, s1);
-    r1 = inv_rms(ss[0], p.C, p.eps);
-  }
-  float h[NV][V], ss[1] = {0.f};
-#pragma unroll
-  for (int k = 0; k < NV; ++k) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      float u = y[k].get(i);
-      if (p.w_post) u = u * r1 * p.w_post[at[k] + i];
-      if (p.z) u *= gate_of<FAST>(z[k].get(i), p.act);
-      h[k][i] = p.res_scale * r[k].get(i) + p.branch_scale * u;
-      ss[0] += on[k] ? h[k][i] * h[k][i] : 0.f;
+    for (int k = 0; k < NV; ++k) {
+      at[k] = (k * (int)blockDim.x + (int)threadIdx.x) * V;
+      on[k] = at[k] < C;
+      if (!on[k]) at[k] = 0;
     }
-    if (on[k]) store_v<V>((RT *)p.r_out + row + at[k], h[k]);
   }
-  if (!p.w_pre) return;
-  block_sum(ss, s2);
-  const float r2 = inv_rms(ss[0], p.C, p.eps);
+};
+
+template <int V, int NV>
+__device__ __forceinline__ void load_weights(const float *w,
+                                             const Cols<V, NV> &c,
+                                             RawV<float, V> (&out)[NV]) {
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
+  for (int k = 0; k < NV; ++k)
+    if (w) out[k].load(w + c.at[k]);
+}
+
+template <typename IO, typename RT, int V, int NV> struct FwdRow {
+  RawV<IO, V> y[NV], z[NV];
+  RawV<RT, V> r[NV];
+  __device__ __forceinline__ void load(const BlockNormParams &p, int n,
+                                       const Cols<V, NV> &c) {
+    const size_t row = (size_t)n * p.C;
 #pragma unroll
-    for (int i = 0; i < V; ++i) h[k][i] = h[k][i] * r2 * p.w_pre[at[k] + i];
-    if (on[k]) store_v<V>((IO *)p.x + row + at[k], h[k]);
+    for (int k = 0; k < NV; ++k) {
+      y[k].load((const IO *)p.y + row + c.at[k]);
+      if (p.z) z[k].load((const IO *)p.z + row + c.at[k]);
+      r[k].load((const RT *)p.r + row + c.at[k]);
+    }
+  }
+};
+
+// A workgroup walks rows, weights in registers, the next row's loads issued
+// before this row's sums are waited for.
+template <typename IO, typename RT, int V, int NV, int MAXT>
+__global__ __launch_bounds__(MAXT) void kda_block_norm_fwd(BlockNormParams p) {
+  constexpr bool FAST = sizeof(IO) == 2;
+  __shared__ float s1[2][16], s2[2][16];
+  const Cols<V, NV> c(p.C);
+  RawV<float, V> wp[NV], wq[NV];
+  load_weights(p.w_post, c, wp);
+  load_weights(p.w_pre, c, wq);
+  FwdRow<IO, RT, V, NV> t, next;
+  next.load(p, blockIdx.x, c);
+  int turn = 0;
+  for (int n = blockIdx.x; n < p.rows; n += gridDim.x, turn ^= 1) {
+    const size_t row = (size_t)n * p.C;
+    t = next;
+    if (n + (int)gridDim.x < p.rows) next.load(p, n + gridDim.x, c);
+    float r1 = 1.f;
+    if (p.w_post) {
+      float ss[1] = {0.f};
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          ss[0] += c.on[k] ? t.y[k].get(i) * t.y[k].get(i) : 0.f;
+      block_sum(ss, s1[turn]);
+      r1 = inv_rms(ss[0], p.C, p.eps);
+    }
+    float h[NV][V], ss[1] = {0.f};
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float u = t.y[k].get(i);
+        if (p.w_post) u = u * r1 * wp[k].get(i);
+        if (p.z) u *= gate_of<FAST>(t.z[k].get(i), p.act);
+        h[k][i] = p.res_scale * t.r[k].get(i) + p.branch_scale * u;
+        ss[0] += c.on[k] ? h[k][i] * h[k][i] : 0.f;
+      }
+      if (c.on[k]) store_v<V>((RT *)p.r_out + row + c.at[k], h[k]);
+    }
+    if (!p.w_pre) continue;
+    block_sum(ss, s2[turn]);
+    const float r2 = inv_rms(ss[0], p.C, p.eps);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) h[k][i] = h[k][i] * r2 * wq[k].get(i);
+      if (c.on[k]) store_v<V>((IO *)p.x + row + c.at[k], h[k]);
+    }
   }
 }
+
+template <typename IO, typename RT, int V, int NV> struct BwdRow {
+  RawV<IO, V> y[NV], z[NV], dx[NV];
+  RawV<RT, V> r[NV], dr[NV];
+  __device__ __forceinline__ void load(const BlockNormParams &p, int n,
+                                       const Cols<V, NV> &c) {
+    const size_t row = (size_t)n * p.C;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      y[k].load((const IO *)p.y + row + c.at[k]);
+      if (p.z) z[k].load((const IO *)p.z + row + c.at[k]);
+      if (p.dx) {
+        dx[k].load((const IO *)p.dx + row + c.at[k]);
+        r[k].load((const RT *)p.r + row + c.at[k]);
+      }
+      if (p.dr_out) dr[k].load((const RT *)p.dr_out + row + c.at[k]);
+    }
+  }
+};
 
 constexpr int BN_MAX_WG = 512;  // partial rows of the weight gradients
 
 // partial rows: workgroup g's dw_post at ws[g][0][C], dw_pre at ws[g][1][C]
-template <typename IO, typename RT, int V, int NV>
-__global__ __launch_bounds__(1024) void kda_block_norm_bwd(BlockNormParams p) {
+template <typename IO, typename RT, int V, int NV, int MAXT, bool AHEAD>
+__global__ __launch_bounds__(MAXT) void kda_block_norm_bwd(BlockNormParams p) {
   constexpr bool FAST = sizeof(IO) == 2;
   __shared__ float s1[2][16 * 3], s2[2][16];
-  int at[NV];
-  bool on[NV];
+  const Cols<V, NV> c(p.C);
+  RawV<float, V> wp[NV], wq[NV];
+  load_weights(p.w_post, c, wp);
+  load_weights(p.w_pre, c, wq);
   float a_post[NV][V], a_pre[NV][V];
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    at[k] = (k * (int)blockDim.x + (int)threadIdx.x) * V;
-    on[k] = at[k] < p.C;
-    if (!on[k]) at[k] = 0;
+  for (int k = 0; k < NV; ++k)
 #pragma unroll
     for (int i = 0; i < V; ++i) a_post[k][i] = a_pre[k][i] = 0.f;
-  }
+  BwdRow<IO, RT, V, NV> t, next;
+  if constexpr (AHEAD) next.load(p, blockIdx.x, c);
   int turn = 0;
   for (int n = blockIdx.x; n < p.rows; n += gridDim.x, turn ^= 1) {
     const size_t row = (size_t)n * p.C;
-    RawV<IO, V> y[NV], z[NV], dx[NV];
-    RawV<RT, V> r[NV], dr[NV];
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      y[k].load((const IO *)p.y + row + at[k]);
-      if (p.z) z[k].load((const IO *)p.z + row + at[k]);
-      if (p.dx) {
-        dx[k].load((const IO *)p.dx + row + at[k]);
-        r[k].load((const RT *)p.r + row + at[k]);
-      }
-      if (p.dr_out) dr[k].load((const RT *)p.dr_out + row + at[k]);
+    if constexpr (AHEAD) {
+      t = next;
+      if (n + (int)gridDim.x < p.rows) next.load(p, n + gridDim.x, c);
+    } else {
+      t.load(p, n, c);
     }
     // sums of r^2, of (w_pre dx) r and of y^2
     float q[3] = {0.f, 0.f, 0.f};
@@ -308,12 +385,12 @@ __global__ __launch_bounds__(1024) void kda_block_norm_bwd(BlockNormParams p) {
     for (int k = 0; k < NV; ++k)
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (on[k]) {
+        if (c.on[k]) {
           if (p.dx) {
-            q[0] += r[k].get(i) * r[k].get(i);
-            q[1] += r[k].get(i) * dx[k].get(i) * p.w_pre[at[k] + i];
+            q[0] += t.r[k].get(i) * t.r[k].get(i);
+            q[1] += t.r[k].get(i) * t.dx[k].get(i) * wq[k].get(i);
           }
-          if (p.w_post) q[2] += y[k].get(i) * y[k].get(i);
+          if (p.w_post) q[2] += t.y[k].get(i) * t.y[k].get(i);
         }
     block_sum(q, s1[turn]);
     const float r2 = inv_rms(q[0], p.C, p.eps);
@@ -325,31 +402,31 @@ __global__ __launch_bounds__(1024) void kda_block_norm_bwd(BlockNormParams p) {
       float o[V], oz[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        float g = p.dr_out ? dr[k].get(i) : 0.f;
+        float g = p.dr_out ? t.dr[k].get(i) : 0.f;
         if (p.dx) {
-          const float x = dx[k].get(i);
-          a_pre[k][i] += on[k] ? x * r[k].get(i) * r2 : 0.f;
-          g += r2 * (x * p.w_pre[at[k] + i] - r[k].get(i) * m2);
+          const float x = t.dx[k].get(i);
+          a_pre[k][i] += c.on[k] ? x * t.r[k].get(i) * r2 : 0.f;
+          g += r2 * (x * wq[k].get(i) - t.r[k].get(i) * m2);
         }
         o[i] = p.res_scale * g;
         float du = p.branch_scale * g;
-        const float nv = p.w_post ? y[k].get(i) * r1 : y[k].get(i);
-        const float w = p.w_post ? p.w_post[at[k] + i] : 1.f;
+        const float nv = p.w_post ? t.y[k].get(i) * r1 : t.y[k].get(i);
+        const float w = p.w_post ? wp[k].get(i) : 1.f;
         if (p.z) {
-          const float2 gg = gate_grad<FAST>(z[k].get(i), p.act);
+          const float2 gg = gate_grad<FAST>(t.z[k].get(i), p.act);
           oz[i] = du * nv * w * gg.y;
           du *= gg.x;
         }
         if (p.w_post) {
-          a_post[k][i] += on[k] ? du * nv : 0.f;
+          a_post[k][i] += c.on[k] ? du * nv : 0.f;
           du *= w;
-          tn[0] += on[k] ? du * nv : 0.f;
+          tn[0] += c.on[k] ? du * nv : 0.f;
         }
         d[k][i] = du;
       }
-      if (on[k]) {
-        store_v<V>((RT *)p.dr + row + at[k], o);
-        if (p.z) store_v<V>((IO *)p.dz + row + at[k], oz);
+      if (c.on[k]) {
+        store_v<V>((RT *)p.dr + row + c.at[k], o);
+        if (p.z) store_v<V>((IO *)p.dz + row + c.at[k], oz);
       }
     }
     if (p.w_post) {
@@ -359,45 +436,51 @@ __global__ __launch_bounds__(1024) void kda_block_norm_bwd(BlockNormParams p) {
       for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int i = 0; i < V; ++i)
-          d[k][i] = r1 * (d[k][i] - y[k].get(i) * r1 * m1);
+          d[k][i] = r1 * (d[k][i] - t.y[k].get(i) * r1 * m1);
     }
 #pragma unroll
     for (int k = 0; k < NV; ++k)
-      if (on[k]) store_v<V>((IO *)p.dy + row + at[k], d[k]);
+      if (c.on[k]) store_v<V>((IO *)p.dy + row + c.at[k], d[k]);
   }
   float *out = p.ws + (size_t)blockIdx.x * 2 * p.C;
 #pragma unroll
   for (int k = 0; k < NV; ++k)
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (on[k]) {
-        if (p.w_post) out[at[k] + i] = a_post[k][i];
-        if (p.dx) out[p.C + at[k] + i] = a_pre[k][i];
+      if (c.on[k]) {
+        if (p.w_post) out[c.at[k] + i] = a_post[k][i];
+        if (p.dx) out[p.C + c.at[k] + i] = a_pre[k][i];
       }
 }
 
 static int bn_groups(int rows) { return rows < BN_MAX_WG ? rows : BN_MAX_WG; }
 
-template <typename IO, typename RT, int V, int NV>
+template <typename IO, typename RT, int V, int NV, int MAXT, bool AHEAD>
 static hipError_t bn_launch(const BlockNormParams &p, hipStream_t s,
                             bool bwd) {
   const int steps = (p.C + V * NV - 1) / (V * NV);
-  const int threads = (steps + 63) / 64 * 64;  // at most 1024: see bn_t
+  const int threads = (steps + 63) / 64 * 64;  // at most MAXT: see bn_t
   if (!bwd) {
-    hipLaunchKernelGGL((kda_block_norm_fwd<IO, RT, V, NV>), dim3(p.rows),
-                       dim3(threads), 0, s, p);
+    int cus = 0;
+    const hipError_t e = layer_cus(&cus);
+    if (e != hipSuccess) return e;
+    // what the CUs hold at 8 waves per SIMD
+    const int most = cus * (2048 / threads < 16 ? 2048 / threads : 16);
+    hipLaunchKernelGGL((kda_block_norm_fwd<IO, RT, V, NV, MAXT>),
+                       dim3(p.rows < most ? p.rows : most), dim3(threads), 0,
+                       s, p);
     return hipGetLastError();
   }
   const int n = bn_groups(p.rows);
-  hipLaunchKernelGGL((kda_block_norm_bwd<IO, RT, V, NV>), dim3(n),
+  hipLaunchKernelGGL((kda_block_norm_bwd<IO, RT, V, NV, MAXT, AHEAD>), dim3(n),
                      dim3(threads), 0, s, p);
-  const dim3 cols((p.C + 15) / 16);
-  if (p.w_post)
-    hipLaunchKernelGGL(kda_sum_rows, cols, dim3(256), 0, s, p.ws,
-                       (long long)2 * p.C, n, p.C, p.dw_post);
-  if (p.dx)
-    hipLaunchKernelGGL(kda_sum_rows, cols, dim3(256), 0, s, p.ws + p.C,
-                       (long long)2 * p.C, n, p.C, p.dw_pre);
+  if (p.w_post || p.dx) {
+    // columns of dw_post, then of dw_pre; the ones not asked for are skipped
+    const int lo = p.w_post ? 0 : p.C, hi = p.dx ? 2 * p.C : p.C;
+    hipLaunchKernelGGL(kda_sum_rows, dim3((hi - lo + 15) / 16), dim3(256), 0,
+                       s, p.ws, (long long)2 * p.C, n, lo, hi, p.C, p.dw_post,
+                       p.dw_pre);
+  }
   return hipGetLastError();
 }
 
@@ -405,11 +488,13 @@ static hipError_t bn_launch(const BlockNormParams &p, hipStream_t s,
 // as vectors; others value by value.
 template <typename IO, typename RT>
 static hipError_t bn_t(const BlockNormParams &p, hipStream_t s, bool bwd) {
-  if (p.C % 8 == 0)
-    return p.C <= 8192 ? bn_launch<IO, RT, 8, 1>(p, s, bwd)
-                       : bn_launch<IO, RT, 8, 2>(p, s, bwd);
-  return p.C <= 4096 ? bn_launch<IO, RT, 1, 4>(p, s, bwd)
-                     : bn_launch<IO, RT, 1, 16>(p, s, bwd);
+  if (p.C % 8 == 0) {
+    if (p.C <= 4096) return bn_launch<IO, RT, 8, 1, 512, true>(p, s, bwd);
+    if (p.C <= 8192) return bn_launch<IO, RT, 8, 1, 1024, false>(p, s, bwd);
+    return bn_launch<IO, RT, 8, 2, 1024, false>(p, s, bwd);
+  }
+  return p.C <= 4096 ? bn_launch<IO, RT, 1, 4, 1024, false>(p, s, bwd)
+                     : bn_launch<IO, RT, 1, 16, 1024, false>(p, s, bwd);
 }
 
 static hipError_t bn_any(const BlockNormParams &p, hipStream_t s, bool bwd) {

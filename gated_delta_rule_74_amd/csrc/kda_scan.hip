@@ -579,11 +579,8 @@ static ScanLink link_at(const ScanParams &p, int which) {
 template <typename IO, typename GT, bool HEAD>
 static hipError_t scan_t(const ScanParams &p, hipStream_t s, bool bwd) {
   const int ncb = div_up(p.C, SCAN_W), tiles = p.B * p.NC * ncb;
-  int dev = 0, cus = 0;
-  hipError_t e = hipGetDevice(&dev);
-  if (e == hipSuccess)
-    e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount,
-                              dev);
+  int cus = 0;
+  const hipError_t e = layer_cus(&cus);
   if (e != hipSuccess) return e;
   // as many workgroups as the card holds at once (two per CU); they take
   // tiles until none is left
