@@ -31,7 +31,8 @@ struct ScanParams {
   void *y;                    // [B,T,H,D]
   float *h_out;               // [B,H,D] or null
   float *states;              // [B,NC,H,D]: state before every chunk, or null
-  int B, T, H, D, NC, C;      // NC = ceil(T / SCAN_L), C = H * D
+  int B, T, H, D, NC, C;      // NC = ceil(T / SCAN_L), C = H * D <= 2^22
+  int log2D;
   // backward
   const void *dy;
   const float *dhT;           // [B,H,D] or null
@@ -45,7 +46,7 @@ struct ScanParams {
 size_t scan_ws_bytes(int B, int C, int NC);
 size_t scan_bwd_ws_bytes(int B, int C, int NC);
 hipError_t launch_scan(const ScanParams &p, hipStream_t s);
-// p.states: the forward's chunk states if have_states, else null
+// p.states: the forward's chunk states, or null
 hipError_t launch_scan_backward(const ScanParams &p, hipStream_t s);
 
 struct ScanStepParams {

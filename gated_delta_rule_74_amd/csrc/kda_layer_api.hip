@@ -60,7 +60,7 @@ kda_status scan_sizes(int B, int T, int H, int D, int *NC) {
   if (B <= 0 || T <= 0 || H <= 0 || D <= 0) return KDA_EINVAL;
   if (!dim_ok(D)) return KDA_EUNSUPPORTED;
   const long long C = (long long)H * D;
-  if (T > (1 << 30) || C > (1 << 30)) return KDA_EUNSUPPORTED;
+  if (T > (1 << 30) || C > (1 << 22)) return KDA_EUNSUPPORTED;
   const long long nc = (T + kda::SCAN_L - 1) / kda::SCAN_L;
   const long long per = nc * ((C + 127) / 128);
   const long long most = (1 << 23) - 1;  // 512 threads each: a grid's limit
@@ -87,6 +87,7 @@ kda_status scan_check(const void *x, kda_dtype io, const void *g,
   p.gate_head = (gt & KDA_GATE_HEAD) ? 1 : 0;
   p.x = x; p.g = g; p.beta = beta; p.h0 = h0; p.lengths = lengths;
   p.B = B; p.T = T; p.H = H; p.D = D; p.C = H * D;
+  p.log2D = __builtin_ctz(D);
   p.ws = (char *)ws;
   return KDA_OK;
 }

@@ -41,7 +41,15 @@
 #include "kda_layer.h"
 #include "kda_vec.h"
 
+// Every multiply-add is written as such: the forward kernel and its
+// states-only variant then round alike, bit for bit.
+#pragma clang fp contract(off)
+
 namespace kda {
+
+__device__ __forceinline__ float fma_(float a, float b, float c) {
+  return __builtin_fmaf(a, b, c);
+}
 
 constexpr int SCAN_W = 128;       // channels per workgroup
 constexpr int SCAN_NT = 4;        // tokens per thread
@@ -51,15 +59,20 @@ constexpr int SCAN_SUB = SCAN_L / SCAN_NT;    // token groups
 constexpr int SCAN_THREADS = SCAN_CL * SCAN_SUB;
 static_assert(SCAN_THREADS == 512, "eight waves");
 
-// where a thread of a scan workgroup stands
+// where a thread of a scan workgroup stands.  What is the same for the whole
+// workgroup stays in scalar registers; a thread adds 32-bit byte offsets
+// (C <= 2^22: a tile spans less than 2^31 bytes).
 struct ScanAt {
-  int b, c, cb;               // batch, chunk, channel block
-  int k;                      // chunk in the order of processing
-  int cl, sub;                // lane across the channels, token group
-  int ch;                     // first channel, clamped into the row
+  int b, c, cb, k;            // batch, chunk, channel block; chunk in the
+                              // order of processing
+  int len;                    // sequence length
+  int r0, lim;                // first row to load from, last one (from r0)
+  int tid, cl, sub;           // thread, lane across the channels, token group
+  int lc;                     // first channel in the block, clamped
   bool on;                    // the channels exist
-  int len, t0;                // sequence length, first token of the thread
-  size_t row0;                // first token row of the batch
+  __device__ __forceinline__ int t0() const {
+    return c * SCAN_L + sub * SCAN_NT;
+  }
 };
 
 // tile `id` in the order of processing: chunk-major
@@ -72,137 +85,218 @@ __device__ __forceinline__ ScanAt scan_at(const ScanParams &p, int id) {
   a.b = id / ncb;
   a.cb = id - a.b * ncb;
   a.c = BWD ? p.NC - 1 - a.k : a.k;
-  a.cl = threadIdx.x % SCAN_CL;
-  a.sub = threadIdx.x / SCAN_CL;
-  const int ch = a.cb * SCAN_W + a.cl * SCAN_V;
-  a.on = ch < p.C;
-  a.ch = a.on ? ch : p.C - SCAN_V;
   a.len = p.T;
   if (p.lengths) a.len = min(max(p.lengths[a.b], 0), p.T);
-  a.t0 = a.c * SCAN_L + a.sub * SCAN_NT;
-  a.row0 = (size_t)a.b * p.T;
+  a.r0 = max(min(a.c * SCAN_L, a.len - 1), 0);
+  a.lim = max(a.len - 1 - a.r0, 0);
+  // an opaque copy of the thread's number for every tile: otherwise the
+  // compiler keeps dozens of addresses alive across the loop over the tiles,
+  // past the registers
+  a.tid = threadIdx.x;
+  asm volatile("" : "+v"(a.tid));
+  a.cl = a.tid % SCAN_CL;
+  a.sub = a.tid / SCAN_CL;
+  a.lc = a.cl * SCAN_V;
+  const int left = p.C - a.cb * SCAN_W;
+  a.on = a.lc < left;
+  if (!a.on) a.lc = left - SCAN_V;
   return a;
 }
 
+template <typename T>
+__device__ __forceinline__ T *at_byte(T *base, unsigned off) {
+  return (T *)((char *)base + off);
+}
+template <typename T>
+__device__ __forceinline__ const T *at_byte(const T *base, unsigned off) {
+  return (const T *)((const char *)base + off);
+}
+
+// exp(g) within 1.5 ulp: t = g log2(e) in fp32, the hardware's 2^t, and the
+// part of the product that t lost (about half of the library's instructions;
+// results under 2^-126 may be flushed to 0).  exp(-inf) = 0, exp(0) = 1,
+// exp(NaN) = NaN.
+__device__ __forceinline__ float decay_of(float g) {
+  constexpr float L = 1.44269504f, Llo = 1.92596299e-8f, ln2 = 0.693147181f;
+  const float t = g * L;
+  const float r = __builtin_amdgcn_exp2f(t);
+  float lo = __builtin_fmaf(g, Llo, __builtin_fmaf(g, L, -t));
+  lo = g < -150.f ? 0.f : lo;  // not inf - inf; exp(g) is 0 there
+  return __builtin_fmaf(r, lo * ln2, r);
+}
+
 // the thread's tokens: raw inputs first (every load issued before the first
-// use), then decays and write strengths
+// use), then the decays
 template <typename IO, typename GT, bool HEAD> struct ScanTile {
   Raw8<IO> x[SCAN_NT];
   Raw8<GT> g[HEAD ? 1 : SCAN_NT];
-  GT gh[SCAN_NT], bt[SCAN_NT];
+  float gh[SCAN_NT], bt[SCAN_NT];
 
-  __device__ __forceinline__ size_t row(const ScanParams &p, const ScanAt &at,
-                                        int j) const {
-    return at.row0 + (size_t)max(min(at.t0 + j, at.len - 1), 0);
-  }
-  __device__ __forceinline__ void load(const ScanParams &p, const ScanAt &at,
-                                       bool want_x) {
-    const int h = at.ch / p.D;
+  __device__ __forceinline__ void load(const ScanParams &p,
+                                       const ScanAt &at) {
+    const size_t row = (size_t)at.b * p.T + at.r0;
+    const IO *const px = (const IO *)p.x + row * p.C + at.cb * SCAN_W;
+    const GT *const pg = (const GT *)p.g + row * p.C + at.cb * SCAN_W;
+    const GT *const ph = (const GT *)p.g + row * p.H;
+    const GT *const pb = (const GT *)p.beta + row * p.H;
+    const unsigned h = (unsigned)(at.cb * SCAN_W + at.lc) >> p.log2D;
 #pragma unroll
     for (int j = 0; j < SCAN_NT; ++j) {
-      const size_t r = row(p, at, j);
-      if (want_x) x[j].load((const IO *)p.x + r * p.C + at.ch);
-      if constexpr (HEAD) {
-        gh[j] = ((const GT *)p.g)[r * p.H + h];
-      } else {
-        g[j].load((const GT *)p.g + r * p.C + at.ch);
-      }
-      if (p.beta) bt[j] = ((const GT *)p.beta)[r * p.H + h];
+      const unsigned r = min(at.sub * SCAN_NT + j, at.lim);
+      const unsigned o = r * p.C + at.lc, oh = (r * p.H + h) * sizeof(GT);
+      x[j].load(at_byte(px, o * sizeof(IO)));
+      if constexpr (HEAD) gh[j] = to_f32(*at_byte(ph, oh));
+      else g[j].load(at_byte(pg, o * sizeof(GT)));
+      bt[j] = 1.f;
     }
+    if (p.beta)
+#pragma unroll
+      for (int j = 0; j < SCAN_NT; ++j) {
+        const unsigned r = min(at.sub * SCAN_NT + j, at.lim);
+        bt[j] = to_f32(*at_byte(pb, (r * p.H + h) * sizeof(GT)));
+      }
+  }
+  // tokens past the end: x = 0, beta = 0, g = 0
+  __device__ __forceinline__ void cut(const ScanAt &at) {
+#pragma unroll
+    for (int j = 0; j < SCAN_NT; ++j)
+      if (at.t0() + j >= at.len) {
+        x[j].zero();
+        if constexpr (HEAD) gh[j] = 0.f;
+        else g[j].zero();
+        bt[j] = 0.f;
+      }
   }
   __device__ __forceinline__ void forget_x() {
 #pragma unroll
     for (int j = 0; j < SCAN_NT; ++j) forget(x[j]);
   }
-  __device__ __forceinline__ float decay(const ScanAt &at, int j,
-                                         int i) const {
-    const float v = HEAD ? to_f32(gh[j]) : g[HEAD ? 0 : j].get(i);
-    return at.t0 + j < at.len ? expf(v) : 1.f;
-  }
-  __device__ __forceinline__ float strength(const ScanParams &p, int j) const {
-    return p.beta ? to_f32(bt[j]) : 1.f;
-  }
-  __device__ __forceinline__ float value(const ScanAt &at, int j, int i,
-                                         float b) const {
-    return at.t0 + j < at.len ? b * x[j].get(i) : 0.f;
-  }
-};
-
-template <typename IO, typename GT, bool HEAD>
-__device__ __forceinline__ void scan_decays(
-    const ScanTile<IO, GT, HEAD> &t, const ScanAt &at,
-    float (&a)[SCAN_NT][SCAN_V]) {
+  __device__ __forceinline__ void decays(float (&a)[SCAN_NT][SCAN_V]) const {
 #pragma unroll
-  for (int j = 0; j < SCAN_NT; ++j) {
-    if constexpr (HEAD) {
-      const float d = t.decay(at, j, 0);
+    for (int j = 0; j < SCAN_NT; ++j) {
+      if constexpr (HEAD) {
+        const float d = decay_of(gh[j]);
 #pragma unroll
-      for (int i = 0; i < SCAN_V; ++i) a[j][i] = d;
-    } else {
+        for (int i = 0; i < SCAN_V; ++i) a[j][i] = d;
+      } else {
 #pragma unroll
-      for (int i = 0; i < SCAN_V; ++i) a[j][i] = t.decay(at, j, i);
+        for (int i = 0; i < SCAN_V; ++i) a[j][i] = decay_of(g[j].get(i));
+      }
+      // a token at a time: the raw registers are free as early as possible
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
-}
-
-// LDS: one composed map (A, U) per token group and channel
-struct ScanLds {
-  float A[SCAN_SUB][SCAN_W];
-  float U[SCAN_SUB][SCAN_W];
 };
 
-__device__ __forceinline__ void lds_put(float (*dst)[SCAN_W], const ScanAt &at,
-                                        const float *v) {
-  store8(&dst[at.sub][at.cl * SCAN_V], v);
-}
-__device__ __forceinline__ void lds_get(const float (*src)[SCAN_W],
-                                        const ScanAt &at, float *v) {
-  const f32x4 lo = *(const f32x4 *)&src[at.sub][at.cl * SCAN_V];
-  const f32x4 hi = *(const f32x4 *)&src[at.sub][at.cl * SCAN_V + 4];
+// LDS: one composed map (A, U) per wave and channel
+constexpr int SCAN_WAVES = SCAN_THREADS / 64;
+struct ScanLds {
+  float A[SCAN_WAVES][SCAN_W];
+  float U[SCAN_WAVES][SCAN_W];
+};
+
+__device__ __forceinline__ void lds_get(const float *src, float *v) {
+  const f32x4 lo = *(const f32x4 *)src, hi = *(const f32x4 *)(src + 4);
 #pragma unroll
   for (int i = 0; i < 4; ++i) { v[i] = lo[i]; v[4 + i] = hi[i]; }
 }
 
-// the thread's composed map, forward: (prod a, u folded)
-template <typename IO, typename GT, bool HEAD>
-__device__ __forceinline__ void fold_fwd(const ScanParams &p, const ScanAt &at,
-                                         const ScanTile<IO, GT, HEAD> &t,
-                                         const float (&a)[SCAN_NT][SCAN_V],
-                                         float *A, float *U) {
+// v of the lower (x) and upper (y) of each pair of 16-lane rows (ROWS) or of
+// the two 32-lane halves, in every lane of the pair
+template <bool ROWS> __device__ __forceinline__ float2 pair_of(float v) {
+  typedef unsigned u2 __attribute__((ext_vector_type(2)));
+  const unsigned w = __float_as_uint(v);
+  const u2 r = ROWS ? __builtin_amdgcn_permlane16_swap(w, w, false, false)
+                    : __builtin_amdgcn_permlane32_swap(w, w, false, false);
+  return make_float2(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// The maps (A, U) of a wave's four token groups, 16 lanes each: (A, U)
+// becomes the map of the wave's groups before this one, and the wave's own
+// map goes to LDS.  BWD: later tokens come first.
+template <bool BWD>
+__device__ __forceinline__ void fold_wave(ScanLds &s, const ScanAt &at,
+                                          float *A, float *U) {
+  const int wave = at.tid / 64, row = at.tid / 16 % 4;
+  const bool second = BWD ? row % 2 == 0 : row % 2 == 1;
+  const bool upper = BWD ? row < 2 : row >= 2;
+  float wa[SCAN_V], wu[SCAN_V];
 #pragma unroll
-  for (int i = 0; i < SCAN_V; ++i) { A[i] = 1.f; U[i] = 0.f; }
-#pragma unroll
-  for (int j = 0; j < SCAN_NT; ++j) {
-    const float b = t.strength(p, j);
-#pragma unroll
-    for (int i = 0; i < SCAN_V; ++i) {
-      U[i] = a[j][i] * U[i] + t.value(at, j, i, b);
-      A[i] *= a[j][i];
-    }
+  for (int i = 0; i < SCAN_V; ++i) {
+    float2 a = pair_of<true>(A[i]), u = pair_of<true>(U[i]);
+    if (BWD) { a = make_float2(a.y, a.x); u = make_float2(u.y, u.x); }
+    // .x comes first
+    const float ea = second ? a.x : 1.f, eu = second ? u.x : 0.f;
+    float2 pa = pair_of<false>(a.y * a.x);
+    float2 pu = pair_of<false>(fma_(a.y, u.x, u.y));
+    if (BWD) { pa = make_float2(pa.y, pa.x); pu = make_float2(pu.y, pu.x); }
+    wa[i] = pa.y * pa.x;
+    wu[i] = fma_(pa.y, pu.x, pu.y);
+    A[i] = upper ? ea * pa.x : ea;
+    U[i] = upper ? fma_(ea, pu.x, eu) : eu;
+    if (i % 2) __builtin_amdgcn_sched_barrier(0);  // registers: two at a time
+  }
+  if (row == 0) {
+    store8(&s.A[wave][at.cl * SCAN_V], wa);
+    store8(&s.U[wave][at.cl * SCAN_V], wu);
   }
 }
 
-// backward: e -> A e + E over the thread's tokens, last to first
-template <typename IO>
-__device__ __forceinline__ float dy_of(const ScanAt &at, const Raw8<IO> &d,
-                                       int j, int i) {
-  return at.t0 + j < at.len ? d.get(i) : 0.f;
+// The waves' maps, one lane per channel: each becomes the map of the waves
+// before it, and the chunk's own is returned.
+template <bool BWD>
+__device__ __forceinline__ void fold_chunk(ScanLds &s, int w, float &A,
+                                           float &U) {
+  float a[SCAN_WAVES], u[SCAN_WAVES];
+#pragma unroll
+  for (int q = 0; q < SCAN_WAVES; ++q) {
+    a[q] = s.A[q][w];
+    u[q] = s.U[q][w];
+  }
+  A = 1.f;
+  U = 0.f;
+#pragma unroll
+  for (int i = 0; i < SCAN_WAVES; ++i) {
+    const int q = BWD ? SCAN_WAVES - 1 - i : i;
+    s.A[q][w] = A;
+    s.U[q][w] = U;
+    U = fma_(a[q], U, u[q]);
+    A *= a[q];
+  }
 }
-template <typename IO>
-__device__ __forceinline__ void fold_bwd(const ScanAt &at,
-                                         const Raw8<IO> (&dy)[SCAN_NT],
+
+// the thread's composed map, forward: (prod a, u folded)
+template <typename IO, typename GT, bool HEAD>
+__device__ __forceinline__ void fold_fwd(const ScanTile<IO, GT, HEAD> &t,
                                          const float (&a)[SCAN_NT][SCAN_V],
-                                         float *A, float *E) {
+                                         float *A, float *U) {
 #pragma unroll
-  for (int i = 0; i < SCAN_V; ++i) { A[i] = 1.f; E[i] = 0.f; }
+  for (int i = 0; i < SCAN_V; ++i) {
+    A[i] = a[0][i];
+    U[i] = t.bt[0] * t.x[0].get(i);
+  }
 #pragma unroll
-  for (int j = SCAN_NT - 1; j >= 0; --j) {
+  for (int j = 1; j < SCAN_NT; ++j)
 #pragma unroll
     for (int i = 0; i < SCAN_V; ++i) {
-      E[i] = a[j][i] * (E[i] + dy_of(at, dy[j], j, i));
+      U[i] = fma_(a[j][i], U[i], t.bt[j] * t.x[j].get(i));
       A[i] *= a[j][i];
     }
-  }
+}
+
+// backward: e -> A e + E over the thread's tokens, last to first (A as
+// forward)
+template <typename IO>
+__device__ __forceinline__ void fold_bwd(const Raw8<IO> (&dy)[SCAN_NT],
+                                         const float (&a)[SCAN_NT][SCAN_V],
+                                         float *E) {
+#pragma unroll
+  for (int i = 0; i < SCAN_V; ++i) E[i] = 0.f;
+#pragma unroll
+  for (int j = SCAN_NT - 1; j >= 0; --j)
+#pragma unroll
+    for (int i = 0; i < SCAN_V; ++i)
+      E[i] = a[j][i] * (E[i] + dy[j].get(i));
 }
 
 // ---------------------------------------------------------------------------
@@ -212,13 +306,16 @@ constexpr int LINK_R = 8;  // chunks per group, groups per supergroup
 constexpr int LINK_SPINS = 1 << 20;  // about a second
 typedef unsigned long long u64;
 
-// word arrays of one pass, indexed [batch][chunk | group | supergroup][C]
+// word arrays of one pass: chunk words [batch][group][channel block][LINK_R]
+// [SCAN_W], group words [batch][supergroup][channel block][LINK_R][SCAN_W],
+// values entering a supergroup [batch][supergroup][channel block][SCAN_W]
+// (written from the second on).  What a workgroup reads is contiguous.
 struct ScanLink {
   int *next;       // the next tile to take
   int *fail;       // a wait was given up: wait for nothing any more
   u64 *chunk, *group;
-  unsigned *super; // the value entering the supergroup (from the second on)
-  int NG, NS;
+  unsigned *super;
+  int NG, NS, ncb;
 };
 
 __device__ __forceinline__ unsigned link_bits(float v) {
@@ -232,7 +329,8 @@ template <typename W> __device__ __forceinline__ W link_get(const W *p) {
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 __device__ __forceinline__ void link_apply(u64 w, float &h) {
-  h = __uint_as_float((unsigned)w) * h + __uint_as_float((unsigned)(w >> 32));
+  h = fma_(__uint_as_float((unsigned)w), h,
+           __uint_as_float((unsigned)(w >> 32)));
 }
 
 // one more turn of a wait: false once it has taken too long here or elsewhere
@@ -244,74 +342,105 @@ __device__ __forceinline__ bool link_turn(const ScanLink &l, int &spin) {
   return false;
 }
 
-// Publish channel `ch`'s map (A, U) of chunk at.k and return the value
-// entering the chunk; `first`: the value entering the sequence's first chunk.
-__device__ __forceinline__ float link_chunk(const ScanParams &p,
-                                            const ScanLink &l,
-                                            const ScanAt &at, int ch, float A,
-                                            float U, float first) {
-  if (p.NC == 1) return first;
-  const size_t C = p.C;
-  const int k = at.k, g = k / LINK_R, s = g / LINK_R;
-  const bool more = k + 1 < p.NC, last_i = k % LINK_R == LINK_R - 1;
-  const int ni = k % LINK_R, ng = g % LINK_R;
-  u64 *const ck = l.chunk + ((size_t)at.b * p.NC + g * LINK_R) * C + ch;
-  u64 *const gk = l.group + ((size_t)at.b * l.NG + s * LINK_R) * C + ch;
-  unsigned *const sk = l.super + ((size_t)at.b * l.NS + s) * C + ch;
-  if (more && !last_i) link_put(ck + (size_t)ni * C, A, U);
-  u64 wc[LINK_R - 1], wg[LINK_R - 1];
-  unsigned ws = s ? link_get(sk) : 0u;
-#pragma unroll
-  for (int i = 0; i < LINK_R - 1; ++i) {
-    wc[i] = i < ni ? link_get(ck + i * C) : 0;
-    wg[i] = i < ng ? link_get(gk + i * C) : 0;
+// where a chunk stands: the words of its group and of its supergroup
+struct LinkAt {
+  int ni, ng, sup;   // chunk in its group, group in its supergroup
+  bool more;         // not the last chunk
+  u64 *chunk, *group;
+  unsigned *super;
+  __device__ __forceinline__ LinkAt(const ScanParams &p, const ScanLink &l,
+                                    const ScanAt &at) {
+    const int g = at.k / LINK_R;
+    sup = g / LINK_R;
+    ni = at.k % LINK_R;
+    ng = g % LINK_R;
+    more = at.k + 1 < p.NC;
+    const size_t s = (size_t)(at.b * l.NS + sup) * l.ncb + at.cb;
+    chunk = l.chunk + ((size_t)(at.b * l.NG + g) * l.ncb + at.cb) *
+                          (LINK_R * SCAN_W);
+    group = l.group + s * (LINK_R * SCAN_W);
+    super = l.super + s * SCAN_W;
   }
-  // the chunks of this group, for the group's map first
+};
+
+// the first n < LINK_R words of channel w, all read at once and again until
+// they are there
+__device__ __forceinline__ void link_wait(const ScanLink &l, const u64 *base,
+                                          unsigned w, int n,
+                                          u64 (&v)[LINK_R - 1]) {
+#pragma unroll
+  for (int i = 0; i < LINK_R - 1; ++i)
+    v[i] = i < n ? link_get(at_byte(base, w * 8 + i * (SCAN_W * 8))) : 0;
   int spin = 0;
   bool wait;
   do {
     wait = false;
 #pragma unroll
     for (int i = 0; i < LINK_R - 1; ++i)
-      if (wc[i] == ~0ull) {
+      if (v[i] == ~0ull) {
         wait = true;
-        wc[i] = link_get(ck + i * C);
+        v[i] = link_get(at_byte(base, w * 8 + i * (SCAN_W * 8)));
       }
   } while (wait && link_turn(l, spin));
-  if (more && last_i && ng != LINK_R - 1) {
-    float ga = 1.f, gu = 0.f;
+}
+
+// Publish the chunk's map (A, U) of channel w and return the composed map of
+// the chunks before it in its group; the last of a group publishes the
+// group's map.
+__device__ __forceinline__ float2 link_group(const ScanLink &l,
+                                             const LinkAt &k, unsigned w,
+                                             float A, float U) {
+  const bool last = k.ni == LINK_R - 1;
+  if (k.more && !last) link_put(at_byte(k.chunk + k.ni * SCAN_W, w * 8), A, U);
+  u64 v[LINK_R - 1];
+  link_wait(l, k.chunk, w, k.ni, v);
+  float ga = 1.f, gu = 0.f;
 #pragma unroll
-    for (int i = 0; i < LINK_R - 1; ++i) {
-      ga *= __uint_as_float((unsigned)wc[i]);
-      link_apply(wc[i], gu);
+  for (int i = 0; i < LINK_R - 1; ++i)
+    if (i < k.ni) {
+      ga *= __uint_as_float((unsigned)v[i]);
+      link_apply(v[i], gu);
     }
-    link_put(gk + (size_t)ng * C, A * ga, A * gu + U);
+  if (k.more && last && k.ng != LINK_R - 1)
+    link_put(at_byte(k.group + k.ng * SCAN_W, w * 8), A * ga, fma_(A, gu, U));
+  return make_float2(ga, gu);
+}
+
+// the value entering the chunk's group; `first`: the value entering the
+// sequence
+__device__ __forceinline__ float link_base(const ScanLink &l, const LinkAt &k,
+                                           unsigned w, float first) {
+  u64 v[LINK_R - 1];
+  link_wait(l, k.group, w, k.ng, v);
+  float h = first;
+  if (k.sup) {
+    const unsigned *const q = at_byte(k.super, w * 4);
+    unsigned s = link_get(q);
+    for (int spin = 0; s == ~0u && link_turn(l, spin);) s = link_get(q);
+    h = __uint_as_float(s);
   }
-  do {
-    wait = false;
-#pragma unroll
-    for (int i = 0; i < LINK_R - 1; ++i)
-      if (wg[i] == ~0ull) {
-        wait = true;
-        wg[i] = link_get(gk + i * C);
-      }
-    if (ws == ~0u) {
-      wait = true;
-      ws = link_get(sk);
-    }
-  } while (wait && link_turn(l, spin));
-  float h = s ? __uint_as_float(ws) : first;
 #pragma unroll
   for (int i = 0; i < LINK_R - 1; ++i)
-    if (i < ng) link_apply(wg[i], h);
-#pragma unroll
-  for (int i = 0; i < LINK_R - 1; ++i)
-    if (i < ni) link_apply(wc[i], h);
-  if (more && last_i && ng == LINK_R - 1)
-    __hip_atomic_store(sk + C, link_bits(A * h + U), __ATOMIC_RELAXED,
-                       __HIP_MEMORY_SCOPE_AGENT);
+    if (i < k.ng) link_apply(v[i], h);
   return h;
 }
+
+// the value leaving the chunk: the last of a supergroup publishes it
+__device__ __forceinline__ void link_leave(const ScanLink &l, const LinkAt &k,
+                                           unsigned w, float h) {
+  if (k.more && k.ni == LINK_R - 1 && k.ng == LINK_R - 1)
+    __hip_atomic_store(at_byte(k.super + l.ncb * SCAN_W, w * 4), link_bits(h),
+                       __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// the value entering the chunk, made by all threads from what two pairs of
+// waves fetched
+struct ScanCarry {
+  float ga[SCAN_W], gu[SCAN_W], base[SCAN_W];
+  __device__ __forceinline__ float at(int w) const {
+    return fma_(ga[w], base[w], gu[w]);
+  }
+};
 
 __global__ __launch_bounds__(256) void kda_scan_clear(uint4 *w, size_t n,
                                                       int *counters) {
@@ -320,22 +449,24 @@ __global__ __launch_bounds__(256) void kda_scan_clear(uint4 *w, size_t n,
   if (i < 4) counters[i] = 0;
 }
 
-// The maps of a chunk's token groups, one lane per channel: each becomes the
-// map of everything before it in the chunk, and the chunk's own is returned.
-template <bool BWD>
-__device__ __forceinline__ void fold_subs(float (*sA)[SCAN_W],
-                                          float (*sU)[SCAN_W], int w,
-                                          float &A, float &U) {
-  A = 1.f;
-  U = 0.f;
-#pragma unroll 8
-  for (int i = 0; i < SCAN_SUB; ++i) {
-    const int q = BWD ? SCAN_SUB - 1 - i : i;
-    const float a = sA[q][w], u = sU[q][w];
-    sA[q][w] = A;
-    sU[q][w] = U;
-    U = a * U + u;
-    A *= a;
+// The value entering a thread's tokens, from the carry of its chunk, the
+// waves before its own and (A, U), the groups before its own in the wave
+__device__ __forceinline__ void enter(const ScanLds &s, const ScanCarry &c,
+                                      const ScanAt &at, const float *A,
+                                      const float *U, float *h) {
+  const int wave = at.tid / 64, w = at.cl * SCAN_V;
+#pragma unroll
+  for (int q = 0; q < SCAN_V; q += 4) {
+    const f32x4 base = *(const f32x4 *)(c.base + w + q);
+    const f32x4 ga = *(const f32x4 *)(c.ga + w + q);
+    const f32x4 gu = *(const f32x4 *)(c.gu + w + q);
+    const f32x4 wa = *(const f32x4 *)&s.A[wave][w + q];
+    const f32x4 wu = *(const f32x4 *)&s.U[wave][w + q];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      h[q + i] = fma_(A[q + i],
+                      fma_(wa[i], fma_(ga[i], base[i], gu[i]), wu[i]),
+                      U[q + i]);
   }
 }
 
@@ -345,61 +476,76 @@ template <typename IO, typename GT, bool HEAD, bool STATES>
 __global__ __launch_bounds__(SCAN_THREADS, 4) void kda_scan_fwd(
     ScanParams p, ScanLink l, int tiles) {
   __shared__ ScanLds s;
-  __shared__ float sc[SCAN_W];
+  __shared__ ScanCarry sc;
   __shared__ int s_next;
   int id = blockIdx.x;
   if (p.NC > 1) {
     if (threadIdx.x == 0) s_next = atomicAdd(l.next, 1);
     __syncthreads();
-    id = s_next;
+    id = __builtin_amdgcn_readfirstlane(s_next);
   }
   while (id < tiles) {
     const ScanAt at = scan_at<false>(p, id);
     ScanTile<IO, GT, HEAD> t;
-    t.load(p, at, true);
+    t.load(p, at);
     __syncthreads();  // s_next, s and sc of the tile before are read
     // the next tile is taken now: the counter's latency passes meanwhile
     if (threadIdx.x == 0)
       s_next = p.NC > 1 ? atomicAdd(l.next, 1) : id + (int)gridDim.x;
     float a[SCAN_NT][SCAN_V], A[SCAN_V], U[SCAN_V];
-    scan_decays(t, at, a);
-    fold_fwd(p, at, t, a, A, U);
+    const bool cut = at.c * SCAN_L + SCAN_L > at.len;  // in the workgroup
+    if (cut) t.cut(at);
+    t.decays(a);
+    fold_fwd(t, a, A, U);
     t.forget_x();
-    lds_put(s.A, at, A);
-    lds_put(s.U, at, U);
+    fold_wave<false>(s, at, A, U);
     __syncthreads();
-    const int w = threadIdx.x, ch = at.cb * SCAN_W + w;
-    if (w < SCAN_W && ch < p.C) {
-      float ca, cu;
-      fold_subs<false>(s.A, s.U, w, ca, cu);
-      const size_t o = (size_t)at.b * p.C + ch;
-      const float h = link_chunk(p, l, at, ch, ca, cu, p.h0 ? p.h0[o] : 0.f);
-      sc[w] = h;
-      if (p.states)
-        p.states[((size_t)at.b * p.NC + at.c) * p.C + ch] = h;
-      if (!STATES && p.h_out && at.c == p.NC - 1) p.h_out[o] = ca * h + cu;
+    // waves 0, 1: the chunk and its group; waves 2, 3: what enters the group
+    const unsigned w = at.tid % SCAN_W;
+    const bool ok = at.cb * SCAN_W + (int)w < p.C;
+    const size_t o = (size_t)at.b * p.C + at.cb * SCAN_W;  // per sequence
+    float ca, cu;
+    if (ok && at.tid < 2 * SCAN_W && p.NC > 1) {
+      const LinkAt k(p, l, at);
+      if (at.tid < SCAN_W) {
+        fold_chunk<false>(s, w, ca, cu);
+        const float2 g = link_group(l, k, w, ca, cu);
+        sc.ga[w] = g.x;
+        sc.gu[w] = g.y;
+      } else {
+        sc.base[w] = link_base(l, k, w, p.h0 ? (p.h0 + o)[w] : 0.f);
+      }
+    } else if (ok && at.tid < SCAN_W) {
+      fold_chunk<false>(s, w, ca, cu);
+      sc.ga[w] = 1.f;
+      sc.gu[w] = 0.f;
+      sc.base[w] = p.h0 ? (p.h0 + o)[w] : 0.f;
     }
     __syncthreads();
-    id = s_next;
+    id = __builtin_amdgcn_readfirstlane(s_next);
+    if (ok && at.tid < SCAN_W) {
+      const float h = sc.at(w), end = fma_(ca, h, cu);
+      link_leave(l, LinkAt(p, l, at), w, end);
+      if (p.states)
+        (p.states + ((size_t)at.b * p.NC + at.c) * p.C + at.cb * SCAN_W)[w] =
+            h;
+      if (!STATES && p.h_out && at.c == p.NC - 1) (p.h_out + o)[w] = end;
+    }
     if constexpr (!STATES) {
       float h[SCAN_V];
-      lds_get(s.A, at, A);
-      lds_get(s.U, at, U);
-#pragma unroll
-      for (int i = 0; i < SCAN_V; ++i)
-        h[i] = A[i] * sc[at.cl * SCAN_V + i] + U[i];
+      enter(s, sc, at, A, U, h);
+      IO *const py = (IO *)p.y +
+                     ((size_t)at.b * p.T + at.c * SCAN_L) * p.C +
+                     at.cb * SCAN_W;
 #pragma unroll
       for (int j = 0; j < SCAN_NT; ++j) {
-        const float b = t.strength(p, j);
-        const bool live = at.t0 + j < at.len;
-        float o[SCAN_V];
 #pragma unroll
-        for (int i = 0; i < SCAN_V; ++i) {
-          h[i] = a[j][i] * h[i] + t.value(at, j, i, b);
-          o[i] = live ? h[i] : 0.f;
-        }
-        if (at.on && at.t0 + j < p.T)
-          store8((IO *)p.y + (at.row0 + at.t0 + j) * p.C + at.ch, o);
+        for (int i = 0; i < SCAN_V; ++i)
+          h[i] = fma_(a[j][i], h[i], t.bt[j] * t.x[j].get(i));
+        const unsigned r = at.sub * SCAN_NT + j;
+        IO *const y = at_byte(py, (r * p.C + at.lc) * (unsigned)sizeof(IO));
+        if (at.on && at.t0() + j < at.len) store8(y, h);
+        else if (at.on && at.t0() + j < p.T) store8_zero(y);
       }
     }
   }
@@ -414,100 +560,127 @@ __device__ __forceinline__ float head_sum(float v, int D) {
 }
 
 template <typename IO, typename GT, bool HEAD>
-__global__ __launch_bounds__(SCAN_THREADS) void kda_scan_grad(
+__global__ __launch_bounds__(SCAN_THREADS, 2)
+void kda_scan_grad(
     ScanParams p, ScanLink l, const float *states, int tiles) {
-  __shared__ ScanLds s;                             // forward maps
-  __shared__ float sB[SCAN_SUB][SCAN_W], sE[SCAN_SUB][SCAN_W];  // reverse
-  __shared__ float sc[2][SCAN_W];
+  __shared__ ScanLds s, sr;       // forward and reverse maps
+  __shared__ ScanCarry sf, sc;
   __shared__ int s_next;
   int id = blockIdx.x;
   if (p.NC > 1) {
     if (threadIdx.x == 0) s_next = atomicAdd(l.next, 1);
     __syncthreads();
-    id = s_next;
+    id = __builtin_amdgcn_readfirstlane(s_next);
   }
   while (id < tiles) {
     const ScanAt at = scan_at<true>(p, id);
     ScanTile<IO, GT, HEAD> t;
     Raw8<IO> dy[SCAN_NT];
-    t.load(p, at, true);
+    t.load(p, at);
+    const IO *const pd = (const IO *)p.dy +
+                         ((size_t)at.b * p.T + at.r0) * p.C + at.cb * SCAN_W;
 #pragma unroll
-    for (int j = 0; j < SCAN_NT; ++j)
-      dy[j].load((const IO *)p.dy + t.row(p, at, j) * p.C + at.ch);
+    for (int j = 0; j < SCAN_NT; ++j) {
+      const unsigned r = min(at.sub * SCAN_NT + j, at.lim);
+      dy[j].load(at_byte(pd, (r * p.C + at.lc) * (unsigned)sizeof(IO)));
+    }
     __syncthreads();  // the LDS contents of the tile before are read
     if (threadIdx.x == 0)
       s_next = p.NC > 1 ? atomicAdd(l.next, 1) : id + (int)gridDim.x;
-    float a[SCAN_NT][SCAN_V], A[SCAN_V], U[SCAN_V];
-    scan_decays(t, at, a);
-    fold_fwd(p, at, t, a, A, U);
-    lds_put(s.A, at, A);
-    lds_put(s.U, at, U);
-    fold_bwd(at, dy, a, A, U);
+    float a[SCAN_NT][SCAN_V], A[SCAN_V], U[SCAN_V], B[SCAN_V], E[SCAN_V];
+    const bool cut = at.c * SCAN_L + SCAN_L > at.len;  // in the workgroup
+    if (cut) {
+      t.cut(at);
+#pragma unroll
+      for (int j = 0; j < SCAN_NT; ++j)
+        if (at.t0() + j >= at.len) dy[j].zero();
+    }
+    t.decays(a);
+    fold_fwd(t, a, A, U);
+    fold_bwd(dy, a, E);
+#pragma unroll
+    for (int i = 0; i < SCAN_V; ++i) B[i] = A[i];
     t.forget_x();
 #pragma unroll
     for (int j = 0; j < SCAN_NT; ++j) forget(dy[j]);
-    lds_put(sB, at, A);
-    lds_put(sE, at, U);
+    fold_wave<false>(s, at, A, U);
+    fold_wave<true>(sr, at, B, E);
     __syncthreads();
-    const int w = threadIdx.x % SCAN_W, ch = at.cb * SCAN_W + w;
-    if (threadIdx.x < 2 * SCAN_W && ch < p.C) {
-      const size_t o = (size_t)at.b * p.C + ch;
-      float ca, cu;
-      if (threadIdx.x < SCAN_W) {
-        fold_subs<true>(sB, sE, w, ca, cu);
-        const float e =
-            link_chunk(p, l, at, ch, ca, cu, p.dhT ? p.dhT[o] : 0.f);
-        sc[1][w] = e;
-        if (p.dh0 && at.c == 0) p.dh0[o] = ca * e + cu;
+    // waves 0, 1: the chunk and its group; 2, 3: what enters the group; 4, 5:
+    // the forward maps and the state before the chunk
+    const unsigned w = at.tid % SCAN_W;
+    const bool ok = at.cb * SCAN_W + (int)w < p.C;
+    const size_t o = (size_t)at.b * p.C + at.cb * SCAN_W;  // per sequence
+    float ca, cu;
+    if (ok && at.tid < 3 * SCAN_W) {
+      const LinkAt k(p, l, at);
+      if (at.tid < SCAN_W) {
+        fold_chunk<true>(sr, w, ca, cu);
+        const float2 g = p.NC > 1 ? link_group(l, k, w, ca, cu)
+                                  : make_float2(1.f, 0.f);
+        sc.ga[w] = g.x;
+        sc.gu[w] = g.y;
+      } else if (at.tid < 2 * SCAN_W) {
+        const float f = p.dhT ? (p.dhT + o)[w] : 0.f;
+        sc.base[w] = p.NC > 1 ? link_base(l, k, w, f) : f;
       } else {
-        sc[0][w] = states[((size_t)at.b * p.NC + at.c) * p.C + ch];
-        fold_subs<false>(s.A, s.U, w, ca, cu);
+        sf.base[w] = (states + ((size_t)at.b * p.NC + at.c) * p.C +
+                      at.cb * SCAN_W)[w];
+        sf.ga[w] = 1.f;
+        sf.gu[w] = 0.f;
+        fold_chunk<false>(s, w, ca, cu);
       }
     }
     __syncthreads();
-    id = s_next;
-    float h[SCAN_NT][SCAN_V], e[SCAN_V];  // h: the state before each token
-    lds_get(s.A, at, A);
-    lds_get(s.U, at, U);
-  #pragma unroll
-    for (int i = 0; i < SCAN_V; ++i)
-      h[0][i] = A[i] * sc[0][at.cl * SCAN_V + i] + U[i];
-    lds_get(sB, at, A);
-    lds_get(sE, at, U);
-  #pragma unroll
-    for (int i = 0; i < SCAN_V; ++i)
-      e[i] = A[i] * sc[1][at.cl * SCAN_V + i] + U[i];
-  #pragma unroll
-    for (int j = 0; j + 1 < SCAN_NT; ++j) {
-      const float b = t.strength(p, j);
-  #pragma unroll
-      for (int i = 0; i < SCAN_V; ++i)
-        h[j + 1][i] = a[j][i] * h[j][i] + t.value(at, j, i, b);
+    id = __builtin_amdgcn_readfirstlane(s_next);
+    if (ok && at.tid < SCAN_W) {
+      const float end = fma_(ca, sc.at(w), cu);
+      link_leave(l, LinkAt(p, l, at), w, end);
+      if (p.dh0 && at.c == 0) (p.dh0 + o)[w] = end;
     }
-  #pragma unroll
+    float h[SCAN_NT][SCAN_V], e[SCAN_V];  // h: the state before each token
+    enter(s, sf, at, A, U, h[0]);
+    enter(sr, sc, at, B, E, e);
+    const size_t row = (size_t)at.b * p.T + at.c * SCAN_L;
+    IO *const px = (IO *)p.dx + row * p.C + at.cb * SCAN_W;
+    GT *const pg = (GT *)p.dg + row * p.C + at.cb * SCAN_W;
+    GT *const ph = (GT *)p.dg + row * p.H;
+    GT *const pb = (GT *)p.dbeta + row * p.H;
+    const unsigned hd = (unsigned)(at.cb * SCAN_W + at.lc) >> p.log2D;
+#pragma unroll
+    for (int j = 0; j + 1 < SCAN_NT; ++j)
+#pragma unroll
+      for (int i = 0; i < SCAN_V; ++i)
+        h[j + 1][i] = fma_(a[j][i], h[j][i], t.bt[j] * t.x[j].get(i));
+#pragma unroll
     for (int j = SCAN_NT - 1; j >= 0; --j) {
-      const bool live = at.t0 + j < at.len;
-      const float b = t.strength(p, j);
       float dx[SCAN_V], dg[SCAN_V], sb = 0.f, sg = 0.f;
-  #pragma unroll
+#pragma unroll
       for (int i = 0; i < SCAN_V; ++i) {
-        const float dh = e[i] + dy_of(at, dy[j], j, i);
+        const float dh = e[i] + dy[j].get(i);
         e[i] = a[j][i] * dh;
-        dx[i] = live ? b * dh : 0.f;
-        dg[i] = live ? e[i] * h[j][i] : 0.f;
-        sb += live ? dh * t.x[j].get(i) : 0.f;
+        dx[i] = t.bt[j] * dh;
+        dg[i] = e[i] * h[j][i];
+        sb = fma_(dh, t.x[j].get(i), sb);
         sg += dg[i];
       }
-      const bool store = at.on && at.t0 + j < p.T;
-      const size_t r = at.row0 + at.t0 + j;
-      if (store) store8((IO *)p.dx + r * p.C + at.ch, dx);
       if (p.beta) sb = head_sum(sb, p.D);
       if constexpr (HEAD) sg = head_sum(sg, p.D);
-      else if (store) store8((GT *)p.dg + r * p.C + at.ch, dg);
-      if (store && at.ch % p.D == 0) {
-        const size_t o = r * p.H + at.ch / p.D;
-        if (p.beta) ((GT *)p.dbeta)[o] = from_f32<GT>(sb);
-        if constexpr (HEAD) ((GT *)p.dg)[o] = from_f32<GT>(sg);
+      if (!at.on || at.t0() + j >= p.T) continue;
+      const unsigned r = at.sub * SCAN_NT + j, v = r * p.C + at.lc;
+      const bool live = at.t0() + j < at.len;
+      IO *const qx = at_byte(px, v * (unsigned)sizeof(IO));
+      if (live) store8(qx, dx);
+      else store8_zero(qx);
+      if constexpr (!HEAD) {
+        GT *const qg = at_byte(pg, v * (unsigned)sizeof(GT));
+        if (live) store8(qg, dg);
+        else store8_zero(qg);
+      }
+      if ((at.lc & (p.D - 1)) == 0) {
+        const unsigned q = (r * p.H + hd) * (unsigned)sizeof(GT);
+        if (p.beta) *at_byte(pb, q) = from_f32<GT>(live ? sb : 0.f);
+        if constexpr (HEAD) *at_byte(ph, q) = from_f32<GT>(live ? sg : 0.f);
       }
     }
   }
@@ -525,13 +698,13 @@ __global__ __launch_bounds__(256) void kda_scan_step_k(ScanStepParams p) {
   h.load(p.state + i);
   x.load((const IO *)p.x + i);
   float gh = 0.f;
-  if constexpr (HEAD) gh = expf(to_f32(((const GT *)p.g)[hd]));
+  if constexpr (HEAD) gh = decay_of(to_f32(((const GT *)p.g)[hd]));
   else g.load((const GT *)p.g + i);
   const float b = p.beta ? to_f32(((const GT *)p.beta)[hd]) : 1.f;
   float o[SCAN_V];
 #pragma unroll
   for (int k = 0; k < SCAN_V; ++k)
-    o[k] = (HEAD ? gh : expf(g.get(k))) * h.get(k) + b * x.get(k);
+    o[k] = fma_(HEAD ? gh : decay_of(g.get(k)), h.get(k), b * x.get(k));
   store8(p.state + i, o);
   store8((IO *)p.y + i, o);
 }
@@ -544,12 +717,12 @@ static int div_up(int a, int b) { return (a + b - 1) / b; }
 // one pass's words, all to be filled with ones, behind its counter
 struct LinkBytes { size_t chunk, group, super, total; };
 static LinkBytes link_bytes(int B, int C, int NC) {
-  const size_t bc = (size_t)B * C;
+  const size_t w = (size_t)B * div_up(C, SCAN_W) * SCAN_W;
   const int NG = div_up(NC, LINK_R), NS = div_up(NG, LINK_R);
   LinkBytes n;
-  n.chunk = al256(bc * NC * 8);
-  n.group = al256(bc * NG * 8);
-  n.super = al256(bc * NS * 4);
+  n.chunk = al256(w * NG * LINK_R * 8);
+  n.group = al256(w * NS * LINK_R * 8);
+  n.super = al256(w * NS * 4);
   n.total = NC > 1 ? n.chunk + n.group + n.super : 0;
   return n;
 }
@@ -573,6 +746,7 @@ static ScanLink link_at(const ScanParams &p, int which) {
   l.super = (unsigned *)(w + n.chunk + n.group);
   l.NG = div_up(p.NC, LINK_R);
   l.NS = div_up(l.NG, LINK_R);
+  l.ncb = div_up(p.C, SCAN_W);
   return l;
 }
 

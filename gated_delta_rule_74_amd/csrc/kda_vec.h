@@ -10,6 +10,7 @@ template <typename IO> struct Raw8;
 template <> struct Raw8<bf16> {
   uint4 r;
   __device__ __forceinline__ void load(const bf16 *p) { r = *(const uint4 *)p; }
+  __device__ __forceinline__ void zero() { r = uint4{0, 0, 0, 0}; }
   __device__ __forceinline__ float get(int i) const {
     const unsigned w = i < 2 ? r.x : i < 4 ? r.y : i < 6 ? r.z : r.w;
     return __uint_as_float((i & 1) ? (w & 0xffff0000u) : (w << 16));
@@ -21,6 +22,7 @@ template <> struct Raw8<float> {
     lo = *(const f32x4 *)p;
     hi = *(const f32x4 *)(p + 4);
   }
+  __device__ __forceinline__ void zero() { lo = hi = f32x4{0, 0, 0, 0}; }
   __device__ __forceinline__ float get(int i) const {
     return i < 4 ? lo[i] : hi[i - 4];
   }
@@ -34,6 +36,14 @@ __device__ __forceinline__ void store8(bf16 *p, const float *v) {
 __device__ __forceinline__ void store8(float *p, const float *v) {
   *(f32x4 *)p = f32x4{v[0], v[1], v[2], v[3]};
   *(f32x4 *)(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+}
+
+__device__ __forceinline__ void store8_zero(bf16 *p) {
+  *(uint4 *)p = uint4{0, 0, 0, 0};
+}
+__device__ __forceinline__ void store8_zero(float *p) {
+  *(f32x4 *)p = f32x4{0, 0, 0, 0};
+  *(f32x4 *)(p + 4) = f32x4{0, 0, 0, 0};
 }
 
 // Make the raw registers opaque: what was converted from them before is then

@@ -356,7 +356,7 @@ size_t kda_scan_backward_workspace_size(int B, int T, int H, int D);
  *            kda_scan_backward takes in place of a recomputation
  * With a few tokens per sequence this is also the multi-token step.
  * Errors: KDA_EINVAL as elsewhere; KDA_EUNSUPPORTED for other D, dtype pairs,
- * T > 2^30, H*D > 2^30, or more than 2^23 - 1 tiles
+ * T > 2^30, H*D > 2^22, or more than 2^23 - 1 tiles
  * B * ceil(T/128) * ceil(H*D/128). */
 kda_status kda_scan(const void *x, kda_dtype io_dtype, const void *g,
                     const void *beta, kda_dtype gate_dtype, const float *h0,
