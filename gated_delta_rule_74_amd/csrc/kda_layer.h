@@ -6,18 +6,25 @@
 #include <hip/hip_runtime.h>
 #include <stddef.h>
 
+#include <atomic>
+
 namespace kda {
 
 // dtype pairs, as everywhere in this library
 enum LayerPair { PAIR_F32, PAIR_BF16_F32, PAIR_BF16_BF16 };
 
-// compute units of the current device
+// compute units of the current device (asked for once per device)
 inline hipError_t layer_cus(int *cus) {
+  constexpr int MAX = 64;
+  static std::atomic<int> known[MAX];
   int dev = 0;
-  const hipError_t e = hipGetDevice(&dev);
+  hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return e;
-  return hipDeviceGetAttribute(cus, hipDeviceAttributeMultiprocessorCount,
-                               dev);
+  if (dev >= 0 && dev < MAX && (*cus = known[dev].load()) > 0)
+    return hipSuccess;
+  e = hipDeviceGetAttribute(cus, hipDeviceAttributeMultiprocessorCount, dev);
+  if (e == hipSuccess && dev >= 0 && dev < MAX) known[dev].store(*cus);
+  return e;
 }
 
 // tokens per chunk of the scan (KDA_SCAN_CHUNK in include/kda.h)

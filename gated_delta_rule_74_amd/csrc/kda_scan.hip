@@ -302,12 +302,13 @@ __device__ __forceinline__ void fold_bwd(const Raw8<IO> (&dy)[SCAN_NT],
 // ---------------------------------------------------------------------------
 // hand-over between chunks
 
-constexpr int LINK_R = 8;  // chunks per group, groups per supergroup
+constexpr int LINK_R = 8;  // chunks per group
+constexpr int LINK_G = 4;  // groups per supergroup
 constexpr int LINK_SPINS = 1 << 20;  // about a second
 typedef unsigned long long u64;
 
 // word arrays of one pass: chunk words [batch][group][channel block][LINK_R]
-// [SCAN_W], group words [batch][supergroup][channel block][LINK_R][SCAN_W],
+// [SCAN_W], group words [batch][supergroup][channel block][LINK_G][SCAN_W],
 // values entering a supergroup [batch][supergroup][channel block][SCAN_W]
 // (written from the second on).  What a workgroup reads is contiguous.
 struct ScanLink {
@@ -351,32 +352,33 @@ struct LinkAt {
   __device__ __forceinline__ LinkAt(const ScanParams &p, const ScanLink &l,
                                     const ScanAt &at) {
     const int g = at.k / LINK_R;
-    sup = g / LINK_R;
+    sup = g / LINK_G;
     ni = at.k % LINK_R;
-    ng = g % LINK_R;
+    ng = g % LINK_G;
     more = at.k + 1 < p.NC;
     const size_t s = (size_t)(at.b * l.NS + sup) * l.ncb + at.cb;
     chunk = l.chunk + ((size_t)(at.b * l.NG + g) * l.ncb + at.cb) *
                           (LINK_R * SCAN_W);
-    group = l.group + s * (LINK_R * SCAN_W);
+    group = l.group + s * (LINK_G * SCAN_W);
     super = l.super + s * SCAN_W;
   }
 };
 
-// the first n < LINK_R words of channel w, all read at once and again until
-// they are there
+// the first n <= N words of channel w, all read at once and again until they
+// are there
+template <int N>
 __device__ __forceinline__ void link_wait(const ScanLink &l, const u64 *base,
                                           unsigned w, int n,
-                                          u64 (&v)[LINK_R - 1]) {
+                                          u64 (&v)[N]) {
 #pragma unroll
-  for (int i = 0; i < LINK_R - 1; ++i)
+  for (int i = 0; i < N; ++i)
     v[i] = i < n ? link_get(at_byte(base, w * 8 + i * (SCAN_W * 8))) : 0;
   int spin = 0;
   bool wait;
   do {
     wait = false;
 #pragma unroll
-    for (int i = 0; i < LINK_R - 1; ++i)
+    for (int i = 0; i < N; ++i)
       if (v[i] == ~0ull) {
         wait = true;
         v[i] = link_get(at_byte(base, w * 8 + i * (SCAN_W * 8)));
@@ -401,7 +403,7 @@ __device__ __forceinline__ float2 link_group(const ScanLink &l,
       ga *= __uint_as_float((unsigned)v[i]);
       link_apply(v[i], gu);
     }
-  if (k.more && last && k.ng != LINK_R - 1)
+  if (k.more && last && k.ng != LINK_G - 1)
     link_put(at_byte(k.group + k.ng * SCAN_W, w * 8), A * ga, fma_(A, gu, U));
   return make_float2(ga, gu);
 }
@@ -410,7 +412,7 @@ __device__ __forceinline__ float2 link_group(const ScanLink &l,
 // sequence
 __device__ __forceinline__ float link_base(const ScanLink &l, const LinkAt &k,
                                            unsigned w, float first) {
-  u64 v[LINK_R - 1];
+  u64 v[LINK_G - 1];
   link_wait(l, k.group, w, k.ng, v);
   float h = first;
   if (k.sup) {
@@ -420,7 +422,7 @@ __device__ __forceinline__ float link_base(const ScanLink &l, const LinkAt &k,
     h = __uint_as_float(s);
   }
 #pragma unroll
-  for (int i = 0; i < LINK_R - 1; ++i)
+  for (int i = 0; i < LINK_G - 1; ++i)
     if (i < k.ng) link_apply(v[i], h);
   return h;
 }
@@ -428,7 +430,7 @@ __device__ __forceinline__ float link_base(const ScanLink &l, const LinkAt &k,
 // the value leaving the chunk: the last of a supergroup publishes it
 __device__ __forceinline__ void link_leave(const ScanLink &l, const LinkAt &k,
                                            unsigned w, float h) {
-  if (k.more && k.ni == LINK_R - 1 && k.ng == LINK_R - 1)
+  if (k.more && k.ni == LINK_R - 1 && k.ng == LINK_G - 1)
     __hip_atomic_store(at_byte(k.super + l.ncb * SCAN_W, w * 4), link_bits(h),
                        __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
@@ -718,10 +720,10 @@ static int div_up(int a, int b) { return (a + b - 1) / b; }
 struct LinkBytes { size_t chunk, group, super, total; };
 static LinkBytes link_bytes(int B, int C, int NC) {
   const size_t w = (size_t)B * div_up(C, SCAN_W) * SCAN_W;
-  const int NG = div_up(NC, LINK_R), NS = div_up(NG, LINK_R);
+  const int NG = div_up(NC, LINK_R), NS = div_up(NG, LINK_G);
   LinkBytes n;
   n.chunk = al256(w * NG * LINK_R * 8);
-  n.group = al256(w * NS * LINK_R * 8);
+  n.group = al256(w * NS * LINK_G * 8);
   n.super = al256(w * NS * 4);
   n.total = NC > 1 ? n.chunk + n.group + n.super : 0;
   return n;
@@ -745,7 +747,7 @@ static ScanLink link_at(const ScanParams &p, int which) {
   l.group = (u64 *)(w + n.chunk);
   l.super = (unsigned *)(w + n.chunk + n.group);
   l.NG = div_up(p.NC, LINK_R);
-  l.NS = div_up(l.NG, LINK_R);
+  l.NS = div_up(l.NG, LINK_G);
   l.ncb = div_up(p.C, SCAN_W);
   return l;
 }
