@@ -451,6 +451,17 @@ __global__ __launch_bounds__(256) void kda_scan_clear(uint4 *w, size_t n,
   if (i < 4) counters[i] = 0;
 }
 
+// One lane takes the workgroup's next tile.  This is done once a tile's wait
+// is over, not before: a workgroup that held the next tile through the wait
+// would start it late, and every later tile would wait for it (B1 T262144 H4
+// D128: 310 us so, against SCAN_LATE us).
+__device__ __forceinline__ void take_next(const ScanParams &p,
+                                          const ScanLink &l, int id,
+                                          int &s_next) {
+  if (threadIdx.x == SCAN_THREADS - 64)
+    s_next = p.NC > 1 ? atomicAdd(l.next, 1) : id + (int)gridDim.x;
+}
+
 // The value entering a thread's tokens, from the carry of its chunk, the
 // waves before its own and (A, U), the groups before its own in the wave
 __device__ __forceinline__ void enter(const ScanLds &s, const ScanCarry &c,
@@ -490,10 +501,6 @@ __global__ __launch_bounds__(SCAN_THREADS, 4) void kda_scan_fwd(
     const ScanAt at = scan_at<false>(p, id);
     ScanTile<IO, GT, HEAD> t;
     t.load(p, at);
-    __syncthreads();  // s_next, s and sc of the tile before are read
-    // the next tile is taken now: the counter's latency passes meanwhile
-    if (threadIdx.x == 0)
-      s_next = p.NC > 1 ? atomicAdd(l.next, 1) : id + (int)gridDim.x;
     float a[SCAN_NT][SCAN_V], A[SCAN_V], U[SCAN_V];
     const bool cut = at.c * SCAN_L + SCAN_L > at.len;  // in the workgroup
     if (cut) t.cut(at);
@@ -501,7 +508,7 @@ __global__ __launch_bounds__(SCAN_THREADS, 4) void kda_scan_fwd(
     fold_fwd(t, a, A, U);
     t.forget_x();
     fold_wave<false>(s, at, A, U);
-    __syncthreads();
+    barrier_keep_vmem();
     // waves 0, 1: the chunk and its group; waves 2, 3: what enters the group
     const unsigned w = at.tid % SCAN_W;
     const bool ok = at.cb * SCAN_W + (int)w < p.C;
@@ -523,8 +530,8 @@ __global__ __launch_bounds__(SCAN_THREADS, 4) void kda_scan_fwd(
       sc.gu[w] = 0.f;
       sc.base[w] = p.h0 ? (p.h0 + o)[w] : 0.f;
     }
-    __syncthreads();
-    id = __builtin_amdgcn_readfirstlane(s_next);
+    barrier_keep_vmem();
+    take_next(p, l, id, s_next);
     if (ok && at.tid < SCAN_W) {
       const float h = sc.at(w), end = fma_(ca, h, cu);
       link_leave(l, LinkAt(p, l, at), w, end);
@@ -550,6 +557,8 @@ __global__ __launch_bounds__(SCAN_THREADS, 4) void kda_scan_fwd(
         else if (at.on && at.t0() + j < p.T) store8_zero(y);
       }
     }
+    barrier_keep_vmem();  // s_next is there; s and sc are read
+    id = __builtin_amdgcn_readfirstlane(s_next);
   }
 }
 
@@ -586,9 +595,6 @@ void kda_scan_grad(
       const unsigned r = min(at.sub * SCAN_NT + j, at.lim);
       dy[j].load(at_byte(pd, (r * p.C + at.lc) * (unsigned)sizeof(IO)));
     }
-    __syncthreads();  // the LDS contents of the tile before are read
-    if (threadIdx.x == 0)
-      s_next = p.NC > 1 ? atomicAdd(l.next, 1) : id + (int)gridDim.x;
     float a[SCAN_NT][SCAN_V], A[SCAN_V], U[SCAN_V], B[SCAN_V], E[SCAN_V];
     const bool cut = at.c * SCAN_L + SCAN_L > at.len;  // in the workgroup
     if (cut) {
@@ -607,7 +613,7 @@ void kda_scan_grad(
     for (int j = 0; j < SCAN_NT; ++j) forget(dy[j]);
     fold_wave<false>(s, at, A, U);
     fold_wave<true>(sr, at, B, E);
-    __syncthreads();
+    barrier_keep_vmem();
     // waves 0, 1: the chunk and its group; 2, 3: what enters the group; 4, 5:
     // the forward maps and the state before the chunk
     const unsigned w = at.tid % SCAN_W;
@@ -633,8 +639,8 @@ void kda_scan_grad(
         fold_chunk<false>(s, w, ca, cu);
       }
     }
-    __syncthreads();
-    id = __builtin_amdgcn_readfirstlane(s_next);
+    barrier_keep_vmem();
+    take_next(p, l, id, s_next);
     if (ok && at.tid < SCAN_W) {
       const float end = fma_(ca, sc.at(w), cu);
       link_leave(l, LinkAt(p, l, at), w, end);
@@ -685,6 +691,8 @@ void kda_scan_grad(
         if constexpr (HEAD) *at_byte(ph, q) = from_f32<GT>(live ? sg : 0.f);
       }
     }
+    barrier_keep_vmem();  // s_next is there; the LDS contents are read
+    id = __builtin_amdgcn_readfirstlane(s_next);
   }
 }
 
