@@ -52,7 +52,7 @@ __device__ __forceinline__ void load_w(const float *p, float (&w)[8]) {
 }
 
 // a thread takes GN_VPT pieces of 8 values, all loads issued first
-constexpr int GN_VPT = 4;
+constexpr int GN_VPT = 2;
 
 template <typename IO, int D>
 __global__ __launch_bounds__(GN_THREADS) void kda_gated_norm_fwd(
@@ -145,25 +145,33 @@ __global__ __launch_bounds__(GN_THREADS) void kda_gated_norm_bwd(
 }
 
 // sums over n rows of part[row][stride], columns lo <= c < hi: column c goes
-// to out0[c], or from C on to out1[c - C].  A workgroup takes 16 columns, 16
-// row lanes each, joined in a fixed order.
-__global__ __launch_bounds__(256) void kda_sum_rows(const float *part,
-                                                    long long stride, int n,
-                                                    int lo, int hi, int C,
-                                                    float *out0, float *out1) {
-  __shared__ float s[16][17];
-  const int c = threadIdx.x % 16, k = threadIdx.x / 16;
-  const int col = lo + blockIdx.x * 16 + c;
+// to out0[c], or from C on to out1[c - C].  A workgroup takes 16 columns, 64
+// row lanes each (at most 16 rows a lane here: two rounds of loads), joined in
+// a fixed order.
+constexpr int SUM_COLS = 16, SUM_LANES = 64;
+__global__ __launch_bounds__(SUM_COLS * SUM_LANES) void kda_sum_rows(
+    const float *part, long long stride, int n, int lo, int hi, int C,
+    float *out0, float *out1) {
+  __shared__ float s[SUM_LANES][SUM_COLS + 1];
+  const int c = threadIdx.x % SUM_COLS, k = threadIdx.x / SUM_COLS;
+  const int col = lo + blockIdx.x * SUM_COLS + c;
   float a = 0.f;
   if (col < hi) {
 #pragma unroll 8
-    for (int i = k; i < n; i += 16) a += part[(size_t)i * stride + col];
+    for (int i = k; i < n; i += SUM_LANES) a += part[(size_t)i * stride + col];
   }
   s[k][c] = a;
   __syncthreads();
-  if (k == 0 && col < hi) {
+  if (k < 4) {
     a = 0.f;
-    for (int i = 0; i < 16; ++i) a += s[i][c];
+#pragma unroll
+    for (int i = 0; i < SUM_LANES / 4; ++i) a += s[k * (SUM_LANES / 4) + i][c];
+    s[k * (SUM_LANES / 4)][c] = a;  // read by nobody else before the barrier
+  }
+  __syncthreads();
+  if (k == 0 && col < hi) {
+    a = (s[0][c] + s[SUM_LANES / 4][c]) +
+        (s[SUM_LANES / 2][c] + s[3 * SUM_LANES / 4][c]);
     if (col < C) out0[col] = a;
     else out1[col - C] = a;
   }
@@ -187,7 +195,8 @@ static hipError_t gn_t(const GatedNormParams &p, hipStream_t s, bool bwd) {
   const int n = gn_groups(p.rows, D);
   hipLaunchKernelGGL((kda_gated_norm_bwd<IO, D>), dim3(n), dim3(GN_THREADS), 0,
                      s, p);
-  hipLaunchKernelGGL(kda_sum_rows, dim3((D + 15) / 16), dim3(256), 0, s, p.ws,
+  hipLaunchKernelGGL(kda_sum_rows, dim3((D + SUM_COLS - 1) / SUM_COLS),
+                     dim3(SUM_COLS * SUM_LANES), 0, s, p.ws,
                      (long long)D, n, 0, D, D, p.dw, p.dw);
   return hipGetLastError();
 }
@@ -352,8 +361,6 @@ template <typename IO, typename RT, int V, int NV> struct BwdRow {
   }
 };
 
-constexpr int BN_MAX_WG = 512;  // partial rows of the weight gradients
-
 // partial rows: workgroup g's dw_post at ws[g][0][C], dw_pre at ws[g][1][C]
 template <typename IO, typename RT, int V, int NV, int MAXT, bool AHEAD>
 __global__ __launch_bounds__(MAXT) void kda_block_norm_bwd(BlockNormParams p) {
@@ -453,13 +460,28 @@ __global__ __launch_bounds__(MAXT) void kda_block_norm_bwd(BlockNormParams p) {
       }
 }
 
-static int bn_groups(int rows) { return rows < BN_MAX_WG ? rows : BN_MAX_WG; }
+// the layout of a row of C values: values per step, steps per thread, threads
+struct BnShape { int V, NV, threads; };
+static BnShape bn_shape(int C) {
+  BnShape b;
+  b.V = C % 8 == 0 ? 8 : 1;
+  b.NV = b.V == 8 ? (C <= 8192 ? 1 : 2) : C <= 4096 ? 4 : 16;
+  const int per = b.V * b.NV;
+  b.threads = ((C + per - 1) / per + 63) / 64 * 64;  // at most 1024
+  return b;
+}
+// workgroups of the gradient, each with partial rows of the weight gradients:
+// eight waves for each of 256 CUs, in one round
+static int bn_groups(int rows, int C) {
+  const int threads = bn_shape(C).threads;
+  const int most = 256 * (threads < 512 ? 512 / threads : 1);
+  return rows < most ? rows : most;
+}
 
 template <typename IO, typename RT, int V, int NV, int MAXT, bool AHEAD>
 static hipError_t bn_launch(const BlockNormParams &p, hipStream_t s,
                             bool bwd) {
-  const int steps = (p.C + V * NV - 1) / (V * NV);
-  const int threads = (steps + 63) / 64 * 64;  // at most MAXT: see bn_t
+  const int threads = bn_shape(p.C).threads;  // at most MAXT: see bn_t
   if (!bwd) {
     int cus = 0;
     const hipError_t e = layer_cus(&cus);
@@ -471,14 +493,15 @@ static hipError_t bn_launch(const BlockNormParams &p, hipStream_t s,
                        s, p);
     return hipGetLastError();
   }
-  const int n = bn_groups(p.rows);
+  const int n = bn_groups(p.rows, p.C);
   hipLaunchKernelGGL((kda_block_norm_bwd<IO, RT, V, NV, MAXT, AHEAD>), dim3(n),
                      dim3(threads), 0, s, p);
   if (p.w_post || p.dx) {
     // columns of dw_post, then of dw_pre; the ones not asked for are skipped
     const int lo = p.w_post ? 0 : p.C, hi = p.dx ? 2 * p.C : p.C;
-    hipLaunchKernelGGL(kda_sum_rows, dim3((hi - lo + 15) / 16), dim3(256), 0,
-                       s, p.ws, (long long)2 * p.C, n, lo, hi, p.C, p.dw_post,
+    hipLaunchKernelGGL(kda_sum_rows,
+                       dim3((hi - lo + SUM_COLS - 1) / SUM_COLS),
+                       dim3(SUM_COLS * SUM_LANES), 0, s, p.ws, (long long)2 * p.C, n, lo, hi, p.C, p.dw_post,
                        p.dw_pre);
   }
   return hipGetLastError();
@@ -514,7 +537,7 @@ hipError_t launch_block_norm_backward(const BlockNormParams &p,
   return bn_any(p, s, true);
 }
 size_t block_norm_bwd_ws_bytes(int rows, int C) {
-  return (size_t)bn_groups(rows) * 2 * C * 4;
+  return (size_t)bn_groups(rows, C) * 2 * C * 4;
 }
 
 }  // namespace kda
