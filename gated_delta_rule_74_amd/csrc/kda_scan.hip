@@ -234,6 +234,9 @@ __device__ __forceinline__ void fold_wave(ScanLds &s, const ScanAt &at,
     wu[i] = fma_(pa.y, pu.x, pu.y);
     A[i] = upper ? ea * pa.x : ea;
     U[i] = upper ? fma_(ea, pu.x, eu) : eu;
+    // made here and now: the compiler would else keep its four operands until
+    // the use behind the wait, 16 registers more per direction
+    asm volatile("" : "+v"(A[i]), "+v"(U[i]));
     if (i % 2) __builtin_amdgcn_sched_barrier(0);  // registers: two at a time
   }
   if (row == 0) {
@@ -307,16 +310,17 @@ constexpr int LINK_G = 4;  // groups per supergroup
 constexpr int LINK_SPINS = 1 << 20;  // about a second
 typedef unsigned long long u64;
 
-// word arrays of one pass: chunk words [batch][group][channel block][LINK_R]
-// [SCAN_W], group words [batch][supergroup][channel block][LINK_G][SCAN_W],
-// values entering a supergroup [batch][supergroup][channel block][SCAN_W]
-// (written from the second on).  What a workgroup reads is contiguous.
+// word arrays of one pass: chunk words [batch][group][channel block][R]
+// [SCAN_W], group words [batch][supergroup][channel block][G][SCAN_W], values
+// entering a supergroup [batch][supergroup][channel block][SCAN_W] (written
+// from the second on); R and G are LINK_R and LINK_G, or the counts of chunks
+// and groups where there are fewer.  What a workgroup reads is contiguous.
 struct ScanLink {
   int *next;       // the next tile to take
   int *fail;       // a wait was given up: wait for nothing any more
   u64 *chunk, *group;
   unsigned *super;
-  int NG, NS, ncb;
+  int NG, NS, ncb, R, G;
 };
 
 __device__ __forceinline__ unsigned link_bits(float v) {
@@ -358,8 +362,8 @@ struct LinkAt {
     more = at.k + 1 < p.NC;
     const size_t s = (size_t)(at.b * l.NS + sup) * l.ncb + at.cb;
     chunk = l.chunk + ((size_t)(at.b * l.NG + g) * l.ncb + at.cb) *
-                          (LINK_R * SCAN_W);
-    group = l.group + s * (LINK_G * SCAN_W);
+                          (l.R * SCAN_W);
+    group = l.group + s * (l.G * SCAN_W);
     super = l.super + s * SCAN_W;
   }
 };
@@ -370,9 +374,12 @@ template <int N>
 __device__ __forceinline__ void link_wait(const ScanLink &l, const u64 *base,
                                           unsigned w, int n,
                                           u64 (&v)[N]) {
+  // from the middle: every word is within an instruction's offset of +-4 KiB
+  constexpr int MID = 4;
+  const u64 *const q = at_byte(base + MID * SCAN_W, w * 8);
 #pragma unroll
   for (int i = 0; i < N; ++i)
-    v[i] = i < n ? link_get(at_byte(base, w * 8 + i * (SCAN_W * 8))) : 0;
+    v[i] = i < n ? link_get(q + (i - MID) * SCAN_W) : 0;
   int spin = 0;
   bool wait;
   do {
@@ -381,7 +388,7 @@ __device__ __forceinline__ void link_wait(const ScanLink &l, const u64 *base,
     for (int i = 0; i < N; ++i)
       if (v[i] == ~0ull) {
         wait = true;
-        v[i] = link_get(at_byte(base, w * 8 + i * (SCAN_W * 8)));
+        v[i] = link_get(q + (i - MID) * SCAN_W);
       }
   } while (wait && link_turn(l, spin));
 }
@@ -454,7 +461,7 @@ __global__ __launch_bounds__(256) void kda_scan_clear(uint4 *w, size_t n,
 // One lane takes the workgroup's next tile.  This is done once a tile's wait
 // is over, not before: a workgroup that held the next tile through the wait
 // would start it late, and every later tile would wait for it (B1 T262144 H4
-// D128: 310 us so, against SCAN_LATE us).
+// D128: 310 us so, against 240).
 __device__ __forceinline__ void take_next(const ScanParams &p,
                                           const ScanLink &l, int id,
                                           int &s_next) {
@@ -730,8 +737,8 @@ static LinkBytes link_bytes(int B, int C, int NC) {
   const size_t w = (size_t)B * div_up(C, SCAN_W) * SCAN_W;
   const int NG = div_up(NC, LINK_R), NS = div_up(NG, LINK_G);
   LinkBytes n;
-  n.chunk = al256(w * NG * LINK_R * 8);
-  n.group = al256(w * NS * LINK_G * 8);
+  n.chunk = al256(w * NG * (NC < LINK_R ? NC : LINK_R) * 8);
+  n.group = al256(w * NS * (NG < LINK_G ? NG : LINK_G) * 8);
   n.super = al256(w * NS * 4);
   n.total = NC > 1 ? n.chunk + n.group + n.super : 0;
   return n;
@@ -757,6 +764,8 @@ static ScanLink link_at(const ScanParams &p, int which) {
   l.NG = div_up(p.NC, LINK_R);
   l.NS = div_up(l.NG, LINK_G);
   l.ncb = div_up(p.C, SCAN_W);
+  l.R = p.NC < LINK_R ? p.NC : LINK_R;
+  l.G = l.NG < LINK_G ? l.NG : LINK_G;
   return l;
 }
 
@@ -766,9 +775,10 @@ static hipError_t scan_t(const ScanParams &p, hipStream_t s, bool bwd) {
   int cus = 0;
   const hipError_t e = layer_cus(&cus);
   if (e != hipSuccess) return e;
-  // as many workgroups as the card holds at once (two per CU); they take
-  // tiles until none is left
+  // as many workgroups as the card holds at once (two per CU; one of the
+  // gradient's, by its registers); they take tiles until none is left
   const dim3 grid(tiles < 2 * cus ? tiles : 2 * cus), thr(SCAN_THREADS);
+  const dim3 ggrid(tiles < cus ? tiles : cus);
   const bool redo = bwd && !p.states;
   const LinkBytes n = link_bytes(p.B, p.C, p.NC);
   const ScanLink l0 = link_at(p, 0), l1 = link_at(p, 1);
@@ -788,7 +798,7 @@ static hipError_t scan_t(const ScanParams &p, hipStream_t s, bool bwd) {
     hipLaunchKernelGGL((kda_scan_fwd<IO, GT, HEAD, true>), grid, thr, 0, s, q,
                        l1, tiles);
   }
-  hipLaunchKernelGGL((kda_scan_grad<IO, GT, HEAD>), grid, thr, 0, s, q, l0,
+  hipLaunchKernelGGL((kda_scan_grad<IO, GT, HEAD>), ggrid, thr, 0, s, q, l0,
                      q.states, tiles);
   return hipGetLastError();
 }

@@ -337,3 +337,72 @@ def test_offsets_past_32_bits(kda):
     within("dx", dx[:, T - 200:], want["dx"])
     within("dg", dg[:, T - 200:], want["dg"])
     within("dbeta", db[:, T - 200:], want["dbeta"])
+
+
+@pytest.mark.parametrize("T", [896, 1024, 1025, 1152, 4096, 4097, 4224, 8193])
+def test_chunk_groups(kda, T):
+    """chunk counts on and beside the hand-over's groups (8 chunks) and
+    supergroups (4 groups), forward and from the other end"""
+    check(kda, inputs(1, T, 2, 16, kind="slow", reset=0, seed=50))
+
+
+@pytest.mark.parametrize("B,T,H,D", [(300, 3, 1, 16), (3, 1100, 5, 128),
+                                     (65, 130, 3, 32), (1, 129, 40, 64)])
+def test_many_columns(kda, B, T, H, D):
+    check(kda, inputs(B, T, H, D, seed=51))
+
+
+def test_small_call_after_a_large_one(kda):
+    """a workspace that held a longer call's words serves a shorter one"""
+    big, small = inputs(2, 5000, 2, 64, seed=52), inputs(2, 200, 2, 64, seed=53)
+    want = (forward(kda, small), backward(kda, small))
+    n = kda.kda_scan_backward_workspace_size(2, 5000, 2, 64)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    for _ in range(3):
+        forward(kda, big, workspace=ws)
+        backward(kda, big, workspace=ws)
+        f, b = (forward(kda, small, workspace=ws),
+                backward(kda, small, workspace=ws))
+        assert all(torch.equal(u, v) for u, v in zip(want[0][:2], f[:2]))
+        assert all(torch.equal(u, v) for u, v in zip(want[1], b))
+
+
+def test_graphs_side_by_side(kda):
+    """two captured scans with workspaces of their own, replayed on two
+    streams at once"""
+    qs = [inputs(1, 5000, 4, 128, seed=60 + i) for i in range(2)]
+    want = [forward(kda, q) for q in qs]
+    n = kda.kda_scan_workspace_size(1, 5000, 4, 128)
+    work = []
+    for q in qs:
+        ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            out = forward(kda, q, workspace=ws)
+        work.append((gr, out, ws, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for gr, _, _, s in work:
+            with torch.cuda.stream(s):
+                gr.replay()
+        torch.cuda.synchronize()
+        for w, (_, out, _, _) in zip(want, work):
+            assert all(torch.equal(u, v) for u, v in zip(w[:2], out[:2]))
+
+
+def test_refuses_strided_tensors(kda):
+    q = inputs(2, 10, 2, 32, seed=70)
+    with pytest.raises(ValueError, match="contiguous"):
+        kda.kda_scan(q["x"].transpose(0, 1).contiguous().transpose(0, 1),
+                     q["g"])
+    h = torch.zeros(2, 2, 64, device="cuda")[..., ::2]
+    x, g = q["x"][:, 0].contiguous(), q["g"][:, 0].contiguous()
+    with pytest.raises(ValueError, match="contiguous"):
+        kda.kda_scan_step(x, g, None, h)
+    with pytest.raises(ValueError, match="GPU"):
+        kda.kda_scan_step(x, g.cpu(), None, q["h0"])
+    with pytest.raises(kda.KdaError):  # a workspace that is too small
+        kda.kda_scan(q["x"], q["g"], workspace=torch.empty(
+            16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(kda.KdaError):  # y is x
+        kda.kda_scan(q["x"], q["g"], y=q["x"])
