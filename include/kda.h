@@ -355,6 +355,9 @@ size_t kda_scan_backward_workspace_size(int B, int T, int H, int D);
  *            before each chunk of KDA_SCAN_CHUNK tokens, which
  *            kda_scan_backward takes in place of a recomputation
  * With a few tokens per sequence this is also the multi-token step.
+ * Decays are composed in fp32: a product of gates under about 1e-38 counts as
+ * 0, and a state that is infinite reads as infinite or NaN from then on
+ * (0 * inf).
  * Errors: KDA_EINVAL as elsewhere; KDA_EUNSUPPORTED for other D, dtype pairs,
  * T > 2^30, H*D > 2^22, or more than 2^23 - 1 tiles
  * B * ceil(T/128) * ceil(H*D/128). */
@@ -404,7 +407,8 @@ typedef enum kda_act {
 
 /* RMS norm of a mixer's heads times a gate, over `rows` rows of D values
  * (rows = tokens * heads of kda_prefill's or kda_scan's output):
- *     y = o / sqrt(mean(o^2) + eps) * w * act(z)
+ *     y = o / sqrt(mean(o^2) + eps) * w * act(z)      (eps >= 0; with 0 a
+ *                                                       row of zeros is NaN)
  *   o, z, y  [rows,D] in io_dtype, D in {16,32,64,128}; z NULL exactly when
  *            act is KDA_ACT_NONE; w [D] fp32; y must not alias an input
  * KDA_EUNSUPPORTED: other D, rows * D > 2^34. */

@@ -406,3 +406,16 @@ def test_refuses_strided_tensors(kda):
             16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(kda.KdaError):  # y is x
         kda.kda_scan(q["x"], q["g"], y=q["x"])
+
+
+@pytest.mark.parametrize("T", [129, 300, 1500, 5000])
+def test_state_in_place_over_many_chunks(kda, T):
+    """the final state written over the initial one while other chunks of the
+    sequence are still to read it: every chunk starts from the initial one"""
+    q = inputs(3, T, 3, 128, kind="slow", reset=0, seed=80)
+    q["h0"] *= 100  # a chunk that started elsewhere would show
+    y, h, _ = forward(kda, q)
+    for _ in range(20):
+        st = q["h0"].clone()
+        y2, h2, _ = kda.kda_scan(q["x"], q["g"], q["beta"], h0=st, h_out=st)
+        assert h2 is st and torch.equal(h, st) and torch.equal(y, y2)
