@@ -482,17 +482,15 @@ __global__ __launch_bounds__(256) void kda_scan_clear(
   }
 }
 
-// One lane takes the workgroup's next tile, once what enters its group is
-// there (its wave waits for nothing else) and without waiting for the answer;
-// it leaves the number in s_next behind the barrier.  Not before the wait: a
-// workgroup that held the next tile through it would start that tile late,
-// and every later tile would wait for it (B1 T262144 H4 D128: 310 us so,
-// against 240); and not behind the barrier: its wave would start the tokens
-// a microsecond after the others.
-constexpr int SCAN_TAKER = SCAN_W;
-__device__ __forceinline__ int take_next(const ScanParams &p,
-                                         const ScanLink &l, int id) {
-  return p.NC > 1 ? atomicAdd(l.next, 1) : id + (int)gridDim.x;
+// One lane takes the workgroup's next tile.  This is done once a tile's wait
+// is over, not before: a workgroup that held the next tile through the wait
+// would start it late, and every later tile would wait for it (B1 T262144 H4
+// D128: 310 us so, against 240).
+__device__ __forceinline__ void take_next(const ScanParams &p,
+                                          const ScanLink &l, int id,
+                                          int &s_next) {
+  if (threadIdx.x == SCAN_THREADS - 64)
+    s_next = p.NC > 1 ? atomicAdd(l.next, 1) : id + (int)gridDim.x;
 }
 
 // The value entering a thread's tokens, from the carry of its chunk, the
@@ -565,10 +563,8 @@ __global__ __launch_bounds__(SCAN_THREADS, 4) void kda_scan_fwd(
       sc.gu[w] = 0.f;
       sc.base[w] = p.h0 ? (p.h0 + o)[w] : 0.f;
     }
-    int taken = 0;
-    if (at.tid == SCAN_TAKER) taken = take_next(p, l, id);
     barrier_keep_vmem();
-    if (at.tid == SCAN_TAKER) s_next = taken;
+    take_next(p, l, id, s_next);
     if (ok && at.tid < SCAN_W) {
       const float h = sc.at(w), end = fma_(ca, h, cu);
       link_leave(l, LinkAt(p, l, at), w, end);
@@ -680,10 +676,8 @@ void kda_scan_grad(
         fold_chunk<false>(s, w, ca, cu);
       }
     }
-    int taken = 0;
-    if (at.tid == SCAN_TAKER) taken = take_next(p, l, id);
     barrier_keep_vmem();
-    if (at.tid == SCAN_TAKER) s_next = taken;
+    take_next(p, l, id, s_next);
     if (ok && at.tid < SCAN_W) {
       const float end = fma_(ca, sc.at(w), cu);
       link_leave(l, LinkAt(p, l, at), w, end);
