@@ -246,7 +246,6 @@ __device__ __forceinline__ void fold_wave(ScanLds &s, const ScanAt &at,
     // made here and now: the compiler would else keep its four operands until
     // the use behind the wait, 16 registers more per direction
     asm volatile("" : "+v"(A[i]), "+v"(U[i]));
-    if (i % 2) __builtin_amdgcn_sched_barrier(0);  // registers: two at a time
   }
   if (row == 0) {
     store8(&s.A[wave][at.cl * SCAN_V], wa);
@@ -485,7 +484,8 @@ __global__ __launch_bounds__(256) void kda_scan_clear(
 // One lane takes the workgroup's next tile.  This is done once a tile's wait
 // is over, not before: a workgroup that held the next tile through the wait
 // would start it late, and every later tile would wait for it (B1 T262144 H4
-// D128: 310 us so, against 240).
+// D128: 310 us so, against 240).  Fetched before that barrier by a wave that
+// waits less, it is no faster (231 against 225 us).
 __device__ __forceinline__ void take_next(const ScanParams &p,
                                           const ScanLink &l, int id,
                                           int &s_next) {
