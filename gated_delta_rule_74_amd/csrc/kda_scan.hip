@@ -41,7 +41,7 @@
 //
 // Measured (bf16 data, fp32 gate, kernel alone): forward B1 T8192 H32 D128
 // 59 us, 219 MB read and 69 MB written (4.9 TB/s; a 1 GiB copy reaches 5.0);
-// B1 T262144 H4 D128 235 us (4.8 TB/s); gradient of the first 115 us (4.3 TB/s
+// B1 T262144 H4 D128 230 us (4.9 TB/s); gradient of the first 112 us (4.4 TB/s
 // of 285 + 207 MB) behind the recomputation's 52 us.  A tile's latency is
 // about 10 us (loads 2-3, decays and composition 3, hand-over 2-3, tokens 2),
 // and what is in flight meanwhile (two tiles of 96 KiB per CU) is what keeps
@@ -595,17 +595,32 @@ __global__ __launch_bounds__(SCAN_THREADS, 4) void kda_scan_fwd(
   }
 }
 
-// sum over the D / 8 lanes that hold one head's channels
-__device__ __forceinline__ float head_sum(float v, int D) {
-  if (D == 16) return group_sum<2>(v);
-  if (D == 32) return group_sum<4>(v);
-  if (D == 64) return group_sum<8>(v);
-  return group_sum<16>(v);
+// sums over the D / 8 lanes that hold one head's channels, of N values side by
+// side
+template <int N>
+__device__ __forceinline__ void head_sums(float (&v)[N], int D) {
+  if (D == 16) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = group_sum<2>(v[i]);
+  } else if (D == 32) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = group_sum<4>(v[i]);
+  } else if (D == 64) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = group_sum<8>(v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = group_sum<16>(v[i]);
+  }
 }
 
-// The gradient: one workgroup per CU (195 registers; two would need 128, and
-// a version with half of the channels at a time that came near it ran no
-// faster: 128 KiB of loads per tile are in flight as it is).
+// The gradient: one workgroup per CU (175 to 212 registers; two would need 128,
+// where a version that worked on half of the channels at a time still spilled
+// and took 161 us against 115, and without a spill, with one gate per head, was
+// no faster: 128 KiB of loads per tile are in flight as it is).  At B1 T8192
+// H32 D128 a tile takes 12.8 us: loads 3.6, decays and composition 3.3,
+// hand-over 1.5, tokens and stores 4.4; at the copy rate its bytes alone take
+// 11.8.
 template <typename IO, typename GT, bool HEAD>
 __global__ __launch_bounds__(SCAN_THREADS, 2)
 void kda_scan_grad(
@@ -697,22 +712,22 @@ void kda_scan_grad(
 #pragma unroll
       for (int i = 0; i < SCAN_V; ++i)
         h[j + 1][i] = fma_(a[j][i], h[j][i], t.bt[j] * t.x[j].get(i));
+    float sb[SCAN_NT], sg[SCAN_NT];
 #pragma unroll
     for (int j = SCAN_NT - 1; j >= 0; --j) {
-      float dx[SCAN_V], dg[SCAN_V], sb = 0.f, sg = 0.f;
+      float dx[SCAN_V], dg[SCAN_V];
+      sb[j] = sg[j] = 0.f;
 #pragma unroll
       for (int i = 0; i < SCAN_V; ++i) {
         const float dh = e[i] + dy[j].get(i);
         e[i] = a[j][i] * dh;
         dx[i] = t.bt[j] * dh;
         dg[i] = e[i] * h[j][i];
-        sb = fma_(dh, t.x[j].get(i), sb);
-        sg += dg[i];
+        sb[j] = fma_(dh, t.x[j].get(i), sb[j]);
+        sg[j] += dg[i];
       }
-      if (p.beta) sb = head_sum(sb, p.D);
-      if constexpr (HEAD) sg = head_sum(sg, p.D);
       if (!at.on || at.t0() + j >= p.T) continue;
-      const unsigned r = at.sub * SCAN_NT + j, v = r * p.C + at.lc;
+      const unsigned v = (at.sub * SCAN_NT + j) * p.C + at.lc;
       const bool live = at.t0() + j < at.len;
       IO *const qx = at_byte(px, v * (unsigned)sizeof(IO));
       if (live) store8(qx, dx);
@@ -722,10 +737,18 @@ void kda_scan_grad(
         if (live) store8(qg, dg);
         else store8_zero(qg);
       }
-      if ((at.lc & (p.D - 1)) == 0) {
-        const unsigned q = (r * p.H + hd) * (unsigned)sizeof(GT);
-        if (p.beta) *at_byte(pb, q) = from_f32<GT>(live ? sb : 0.f);
-        if constexpr (HEAD) *at_byte(ph, q) = from_f32<GT>(live ? sg : 0.f);
+    }
+    if (p.beta) head_sums(sb, p.D);
+    if constexpr (HEAD) head_sums(sg, p.D);
+    if (at.on && (at.lc & (p.D - 1)) == 0) {
+#pragma unroll
+      for (int j = 0; j < SCAN_NT; ++j) {
+        if (at.t0() + j >= p.T) continue;
+        const bool live = at.t0() + j < at.len;
+        const unsigned q = ((at.sub * SCAN_NT + j) * p.H + hd) *
+                           (unsigned)sizeof(GT);
+        if (p.beta) *at_byte(pb, q) = from_f32<GT>(live ? sb[j] : 0.f);
+        if constexpr (HEAD) *at_byte(ph, q) = from_f32<GT>(live ? sg[j] : 0.f);
       }
     }
     barrier_keep_vmem();  // s_next is there; the LDS contents are read
