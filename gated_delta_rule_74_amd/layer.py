@@ -44,6 +44,7 @@ _block_ws = _sig("kda_block_norm_backward_workspace_size", _sz, [_i, _i])
 _ACTS = {"sigmoid": 1, "silu": 2}
 _CODE = {torch.float32: KDA_F32, torch.bfloat16: KDA_BF16}
 _F32 = torch.float32
+_INT_MAX = 2 ** 31 - 1
 # the handle of a device's current stream without building a Stream object
 # (2 us of a decode step's host time)
 _raw_stream = torch._C._cuda_getCurrentRawStream
@@ -59,6 +60,13 @@ def _must(t, shape, dtype, name):
     """_need, quick where all is well"""
     if t is not None and (t.shape != shape or t.dtype is not dtype):
         _need(t, shape, dtype, name)
+
+
+def _int(n, name):
+    """a size that the C interface takes as an int: anything above would be
+    cut to its lower bits on the way"""
+    if n > _INT_MAX:
+        raise KdaError(KDA_EUNSUPPORTED, f"{name} = {n}")
 
 
 def _bad(t, dev):
@@ -108,6 +116,7 @@ def _scan_codes(x, g, beta, nd):
     xs = x.shape
     if len(xs) != nd + 1:
         raise ValueError(f"x has {len(xs)} dimensions, expected {nd + 1}")
+    _int(max(xs), "size of x")
     io, gt = _CODE.get(x.dtype), _CODE.get(g.dtype)
     if io is None or gt is None:
         _io_dtype(x, "x")
@@ -241,6 +250,7 @@ def _gated_codes(o, z, w):
     io, D = _CODE.get(o.dtype), o.shape[-1]
     if io is None:
         _io_dtype(o, "o")
+    _int(D, "width of o")
     _must(z, o.shape, o.dtype, "z (must have o's shape and dtype)")
     _must(w, (D,), _F32, "w")
     return io, D, o.numel() // max(D, 1)
@@ -307,7 +317,9 @@ def _block_codes(y, r, z, w_post, w_pre, r_name):
     _must(z, shape, y.dtype, "z (must have y's shape and dtype)")
     _must(w_post, (C,), _F32, "w_post")
     _must(w_pre, (C,), _F32, "w_pre")
-    return io, rt, C, y.numel() // max(C, 1)
+    rows = y.numel() // max(C, 1)
+    _int(max(rows, C), "rows or width of y")
+    return io, rt, C, rows
 
 
 def kda_block_norm(y, r, *, w_post=None, z=None, w_pre=None, act="sigmoid",

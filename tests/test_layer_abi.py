@@ -253,6 +253,29 @@ def test_binding_rejects_norms():
             kda.kda_block_norm_backward(y, r, **kw)
 
 
+def test_binding_refuses_sizes_past_an_int():
+    """A size above 2^31 - 1 is refused, not cut to its lower 32 bits (these
+    would be calls of 5 rows, 3 tokens, one sequence, 16 values)."""
+    def m(*s, dt=torch.bfloat16):
+        return torch.empty(*s, dtype=dt, device="meta")
+
+    P = 1 << 32
+    y = m(P + 5, 1)
+    calls = [
+        lambda: kda.kda_block_norm(y, y),
+        lambda: kda.kda_block_norm_backward(y, y, dr_out=y),
+        lambda: kda.kda_scan(m(1, P + 3, 1, 16), m(1, P + 3, 1)),
+        lambda: kda.kda_scan_backward(m(1, P + 3, 1, 16), m(1, P + 3, 1), None,
+                                      m(1, P + 3, 1, 16)),
+        lambda: kda.kda_scan_step(m(P + 1, 1, 16), m(P + 1, 1), None,
+                                  m(P + 1, 1, 16, dt=F32)),
+        lambda: kda.kda_gated_norm(m(2, P + 16), None, m(P + 16, dt=F32)),
+    ]
+    for call in calls:
+        with pytest.raises(kda.KdaError, match="unsupported"):
+            call()
+
+
 @pytest.mark.skipif(shutil.which("hipcc") is None and
                     not os.path.exists("/opt/rocm/bin/hipcc"),
                     reason="hipcc not available")
