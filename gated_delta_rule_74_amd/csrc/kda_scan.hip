@@ -16,13 +16,13 @@
 // the chunk.
 //
 // Hand-over between chunks (in the order of processing: k = 0 is the first
-// chunk, in the gradient the last).  8 chunks make a group, 8 groups a
+// chunk, in the gradient the last).  8 chunks make a group, 4 groups a
 // supergroup.  A workgroup publishes its chunk's composed map; the last chunk
 // of a group publishes the group's map, the last of a supergroup the value
 // that leaves it.  The value entering chunk k is then the supergroup's
 // entering value, taken through the maps of the groups before k's in it, and
-// of the chunks before k in its group: at most 15 words per channel, read all
-// at once, and one hop of latency per 64 chunks.  The order of these
+// of the chunks before k in its group: at most 11 words per channel, read all
+// at once, and one hop of latency per 32 chunks.  The order of these
 // operations is fixed, so results do not depend on which workgroup was
 // faster.
 //  - A word carries its own readiness: the workspace is filled with ones

@@ -8,7 +8,7 @@ be off by a further half step, finfo(t).eps / 2 of its value (see `within`).
 
 u = 2^-24 is the rounding of one fp32 operation.
 
-Scan.  A token costs at most: the exp (1 ulp = 2u of a), the product into the
+Scan.  A token costs at most: the exp (1.5 ulp = 3u of a), the product into the
 composed decay (u), the multiply-add (u), the product beta x (u), and below
 one more for the composition of maps over groups of tokens: 8u of the
 magnitudes covers it.  With |h|_t = a |h|_{t-1} + |u_t| (all terms positive),

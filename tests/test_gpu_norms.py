@@ -70,6 +70,24 @@ def test_gated_norm_far_values(kda, dtype):
                                                  dtype=dtype))
 
 
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_gate_gradient_far_out(kda, dtype):
+    """dz of the sigmoid gate keeps its relative accuracy where the gate is
+    nearly 1 or 0: with a row norm off by rr, the derivative's exponential by
+    (|z| + 8) 2u (its argument |z| u, a few u for the rest) and the products,
+    the value is off by that share of itself and its own rounding."""
+    o = rn(24, 1, 32, seed=60, dtype=dtype)
+    z = rn(24, 1, 32, seed=61, dtype=dtype)
+    z += (torch.arange(24, device="cuda") * 6.0 - 69.0).view(24, 1, 1).to(dtype)
+    w, dy = rn(32, seed=62), rn(24, 1, 32, seed=63, dtype=dtype)
+    _, dz, _ = kda.kda_gated_norm_backward(o, z, w, dy, eps=EPS)
+    o8, z8, w8, dy8 = map(ref.c8, (o, z, w, dy))
+    r, rr = ref._rms(o8, EPS)
+    want = dy8 * o8 * r * w8 * torch.sigmoid(z8) * torch.sigmoid(-z8)
+    rel = rr + (z8.abs() + 8) * 2 * ref.U + 8 * ref.U
+    within("dz", dz, (want, rel * want.abs()))
+
+
 def test_gated_norm_nan_stays_in_its_row(kda):
     o, z = rn(50, 3, 32, seed=13, dtype=BF), rn(50, 3, 32, seed=14, dtype=BF)
     w, dy = rn(32, seed=15), rn(50, 3, 32, seed=16, dtype=BF)
