@@ -10,6 +10,8 @@
 //
 // With n = v r, r = 1 / sqrt(mean v^2 + eps), and t the gradient of n, the
 // gradient of v is r (t - n mean(t n)).
+#include <type_traits>
+
 #include "kda_layer.h"
 #include "kda_vec.h"
 
@@ -106,7 +108,7 @@ __global__ __launch_bounds__(GN_THREADS) void kda_gated_norm_bwd(
     GatedNormParams p) {
   constexpr bool FAST = sizeof(IO) == 2;
   constexpr int G = D / 8, RPW = GN_THREADS / G;  // rows per pass
-  __shared__ float part[RPW][D];
+  __shared__ alignas(16) float part[RPW][D];
   const int ch = (int)(threadIdx.x % G) * 8, rr = threadIdx.x / G;
   float w[8], dw[8];
 #pragma unroll
@@ -235,283 +237,456 @@ size_t gated_norm_bwd_ws_bytes(long long rows, int D) {
 }
 
 // ---------------------------------------------------------------------------
-// norms around a block: a workgroup holds one row of C values, V consecutive
-// ones per thread and step.  Bound by HBM: 8192 rows x 4096 with a gate and an
-// fp32 stream take 90 us for 470 MB (5.2 TB/s), the gradient 144 us for
-// 738 MB and 8 MB of partial rows (5.2 TB/s) and 5 us for their sum.  With
-// one row per workgroup, its weights read from the L2 for every row, they
-// took 129 and 278 us.
+// norms around a block: a row of C values is held by G lanes of a wave (C <
+// 520) or by a workgroup, 8 consecutive values per thread and piece, and one
+// value more for the last C % 8.  Rows of such widths start at any address;
+// their pieces move as vectors all the same (value by value, C = 4097 took
+// 406 and 1431 us where 4096 takes 90 and 141).  Bound by HBM: 8192 rows x 4096
+// with a gate and an fp32 stream take 90 us for 470 MB (5.2 TB/s), the
+// gradient 144 us for 738 MB and 8 MB of partial rows (5.2 TB/s) and 5 us for
+// their sum.  With one row per workgroup, its weights read from the L2 for
+// every row, they took 129 and 278 us.
+
+// where a thread's values lie in a row: NV pieces of 8 and, with TAIL, one of
+// the last C % 8 values
+template <int NV, bool TAIL> struct Cols {
+  unsigned at[NV], tail;
+  bool in[NV], in_tail, any;  // any: a row has whole pieces at all
+  __device__ __forceinline__ Cols(int C, int lane, int lanes) {
+    const int C8 = C & ~7;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      at[k] = (k * lanes + lane) * 8;
+      in[k] = (int)at[k] < C8;
+      if (!in[k]) at[k] = 0;
+    }
+    any = C8 > 0;
+    in_tail = TAIL && C8 + lane < C;
+    tail = min(C8 + lane, C - 1);
+  }
+  __device__ __forceinline__ bool on(int e) const {
+    return e < NV * 8 ? in[e / 8] : in_tail;
+  }
+  // an opaque copy for every row: otherwise the compiler keeps the 64-bit
+  // address of every array and piece alive across the rows, past the registers
+  __device__ __forceinline__ void fresh() {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) asm volatile("" : "+v"(at[k]));
+    if constexpr (TAIL) asm volatile("" : "+v"(tail));
+  }
+};
+
+// a thread's values of one row of one array; value e is vector element e or,
+// behind those, the tail
+template <typename T, int NV, bool TAIL> struct Vals {
+  Raw8<T> v[NV];
+  T t;
+  typedef Cols<NV, TAIL> At;
+  // value i of a row: a 32-bit offset from what is the same for the workgroup
+  // where a row is (64-bit addresses of every array and piece would spill)
+  template <typename P>
+  __device__ static __forceinline__ P *value(P *row, unsigned i) {
+    typedef std::conditional_t<std::is_const_v<P>, const char, char> byte;
+    return (P *)((byte *)row + i * (unsigned)sizeof(T));
+  }
+  // piece k; the tail is piece NV
+  __device__ __forceinline__ void load(const T *row, const At &c, int k) {
+    if (k == NV) t = *value(row, c.tail);
+    else if constexpr (!TAIL) v[k].load(value(row, c.at[k]));
+    else if (c.any) v[k].load_any(value(row, c.at[k]));
+  }
+  __device__ __forceinline__ void load(const T *row, const At &c) {
+#pragma unroll
+    for (int k = 0; k < NV + TAIL; ++k) load(row, c, k);
+  }
+  __device__ __forceinline__ float get(int e) const {
+    return e < NV * 8 ? v[e / 8].get(e % 8) : to_f32(t);
+  }
+  // with several pieces: convert again, rather than keep the converted values
+  __device__ __forceinline__ void fresh() {
+    if constexpr (NV > 1)
+#pragma unroll
+      for (int k = 0; k < NV; ++k) forget(v[k]);
+  }
+  __device__ static __forceinline__ void store(T *row, const At &c, int k,
+                                               const float *f) {
+    if (k == NV) {
+      if (c.in_tail) *value(row, c.tail) = from_f32<T>(f[0]);
+    } else if (c.in[k]) {
+      if constexpr (TAIL) store8_any(value(row, c.at[k]), f);
+      else store8(value(row, c.at[k]), f);
+    }
+  }
+  __device__ static __forceinline__ void store(T *row, const At &c,
+                                               const float *f) {
+#pragma unroll
+    for (int k = 0; k < NV + TAIL; ++k) store(row, c, k, f + 8 * k);
+  }
+};
+
+// between two pieces where a thread has several: one after the other, or the
+// registers do not suffice
+template <int NV> __device__ __forceinline__ void piece_done() {
+  if constexpr (NV > 1) __builtin_amdgcn_sched_barrier(0);
+}
 
 // sum over the wave, every lane getting it
 __device__ __forceinline__ float wave_sum(float x) {
   x = group_sum<32>(x);
   return x + __shfl_xor(x, 32, 64);
 }
-// sums over the workgroup of N values at once; `s`: N * 16 floats that no
-// wave still reads from an earlier call (callers alternate two)
-template <int N>
-__device__ __forceinline__ void block_sum(float (&x)[N], float *s) {
-  const int waves = blockDim.x / 64, w = threadIdx.x / 64;
+// sums of N values at once over the threads of a row: a group of G lanes, or
+// (G = 0) the workgroup.  `s`: N * 16 floats that no wave still reads from an
+// earlier call (callers alternate two)
+template <bool WG, int N>
+__device__ __forceinline__ void row_sum(float (&x)[N], int G, float *s) {
+  if constexpr (!WG) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) x[i] = wave_sum(x[i]);
-  if (waves == 1) return;
-  if (threadIdx.x % 64 == 0)
+    for (int i = 0; i < N; ++i)
+      x[i] = G == 8    ? group_sum<8>(x[i])
+             : G == 16 ? group_sum<16>(x[i])
+             : G == 32 ? group_sum<32>(x[i])
+                       : wave_sum(x[i]);
+  } else {
+    const int waves = blockDim.x / 64, w = threadIdx.x / 64;
 #pragma unroll
-    for (int i = 0; i < N; ++i) s[i * 16 + w] = x[i];
-  __syncthreads();
+    for (int i = 0; i < N; ++i) x[i] = wave_sum(x[i]);
+    if (threadIdx.x % 64 == 0)
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    x[i] = 0.f;
-    for (int k = 0; k < waves; ++k) x[i] += s[i * 16 + k];
+      for (int i = 0; i < N; ++i) s[i * 16 + w] = x[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      x[i] = 0.f;
+      for (int k = 0; k < waves; ++k) x[i] += s[i * 16 + k];
+    }
   }
 }
 
-// columns of a thread: NV pieces of V values
-template <int V, int NV> struct Cols {
-  int at[NV];
-  bool on[NV];
-  __device__ __forceinline__ Cols(int C) {
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      at[k] = (k * (int)blockDim.x + (int)threadIdx.x) * V;
-      on[k] = at[k] < C;
-      if (!on[k]) at[k] = 0;
-    }
+// which rows a thread takes: its own number `mine` in a turn of `step` rows;
+// all threads make the same turns, past the end with the last row again
+template <bool WG> struct Rows {
+  int G, mine, per, step;
+  __device__ __forceinline__ Rows(int lanes) {
+    G = lanes;
+    per = WG ? 1 : (int)blockDim.x / G;
+    mine = WG ? 0 : (int)threadIdx.x / G;
+    step = (int)gridDim.x * per;
+  }
+  __device__ __forceinline__ int first() const { return blockIdx.x * per; }
+  __device__ __forceinline__ int lane() const {
+    return WG ? threadIdx.x : threadIdx.x % G;
+  }
+  __device__ __forceinline__ int lanes() const { return WG ? blockDim.x : G; }
+  __device__ __forceinline__ int row(int base, int rows) const {
+    return WG ? base : min(base + mine, rows - 1);
+  }
+  __device__ __forceinline__ bool on(int base, int rows) const {
+    return WG || base + mine < rows;
   }
 };
 
-template <int V, int NV>
-__device__ __forceinline__ void load_weights(const float *w,
-                                             const Cols<V, NV> &c,
-                                             RawV<float, V> (&out)[NV]) {
-#pragma unroll
-  for (int k = 0; k < NV; ++k)
-    if (w) out[k].load(w + c.at[k]);
-}
-
-template <typename IO, typename RT, int V, int NV> struct FwdRow {
-  RawV<IO, V> y[NV], z[NV];
-  RawV<RT, V> r[NV];
+template <typename IO, typename RT, int NV, bool TAIL> struct FwdRow {
+  Vals<IO, NV, TAIL> y, z;
+  Vals<RT, NV, TAIL> r;
   __device__ __forceinline__ void load(const BlockNormParams &p, int n,
-                                       const Cols<V, NV> &c) {
+                                       const Cols<NV, TAIL> &c) {
     const size_t row = (size_t)n * p.C;
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      y[k].load((const IO *)p.y + row + c.at[k]);
-      if (p.z) z[k].load((const IO *)p.z + row + c.at[k]);
-      r[k].load((const RT *)p.r + row + c.at[k]);
-    }
+    y.load((const IO *)p.y + row, c);
+    if (p.z) z.load((const IO *)p.z + row, c);
+    r.load((const RT *)p.r + row, c);
   }
 };
 
-// A workgroup walks rows, weights in registers, the next row's loads issued
-// before this row's sums are waited for.
-template <typename IO, typename RT, int V, int NV, int MAXT>
-__global__ __launch_bounds__(MAXT) void kda_block_norm_fwd(BlockNormParams p) {
-  constexpr bool FAST = sizeof(IO) == 2;
+// Weights stay in registers (but not with two pieces a thread, where they are
+// read again for every row, from the L2), and the next rows' loads are issued
+// before these rows' sums are waited for.
+template <typename IO, typename RT, bool WG, int NV, bool TAIL, int MAXT>
+__global__ __launch_bounds__(MAXT) void kda_block_norm_fwd(BlockNormParams p,
+                                                           int lanes) {
+  constexpr bool FAST = sizeof(IO) == 2, KEEP = NV == 1;
+  constexpr int N = NV * 8 + TAIL;
   __shared__ float s1[2][16], s2[2][16];
-  const Cols<V, NV> c(p.C);
-  RawV<float, V> wp[NV], wq[NV];
-  load_weights(p.w_post, c, wp);
-  load_weights(p.w_pre, c, wq);
-  FwdRow<IO, RT, V, NV> t, next;
-  next.load(p, blockIdx.x, c);
+  const Rows<WG> at(lanes);
+  Cols<NV, TAIL> c(p.C, at.lane(), at.lanes());
+  Vals<float, NV, TAIL> kp, kq;
+  if (KEEP && p.w_post) kp.load(p.w_post, c);
+  if (KEEP && p.w_pre) kq.load(p.w_pre, c);
+  FwdRow<IO, RT, NV, TAIL> next;
+  next.load(p, at.row(at.first(), p.rows), c);
   int turn = 0;
-  for (int n = blockIdx.x; n < p.rows; n += gridDim.x, turn ^= 1) {
-    const size_t row = (size_t)n * p.C;
-    t = next;
-    if (n + (int)gridDim.x < p.rows) next.load(p, n + gridDim.x, c);
+  for (int base = at.first(); base < p.rows; base += at.step, turn ^= 1) {
+    if constexpr (WG) c.fresh();
+    const size_t row = (size_t)at.row(base, p.rows) * p.C;
+    const bool live = at.on(base, p.rows);
+    const FwdRow<IO, RT, NV, TAIL> t = next;
+    Vals<float, NV, TAIL> wp, wq;
+    if constexpr (KEEP) {
+      wp = kp;
+      wq = kq;
+    }
+    if (base + at.step < p.rows)
+      next.load(p, at.row(base + at.step, p.rows), c);
     float r1 = 1.f;
     if (p.w_post) {
       float ss[1] = {0.f};
 #pragma unroll
-      for (int k = 0; k < NV; ++k)
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          ss[0] += c.on[k] ? t.y[k].get(i) * t.y[k].get(i) : 0.f;
-      block_sum(ss, s1[turn]);
+      for (int e = 0; e < N; ++e)
+        ss[0] += c.on(e) ? t.y.get(e) * t.y.get(e) : 0.f;
+      row_sum<WG>(ss, at.G, s1[turn]);
       r1 = inv_rms(ss[0], p.C, p.eps);
     }
-    float h[NV][V], ss[1] = {0.f};
+    float h[N], ss[1] = {0.f};
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
+    for (int k = 0; k < NV + TAIL; ++k) {
+      if (!KEEP && p.w_post) wp.load(p.w_post, c, k);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float u = t.y[k].get(i);
-        if (p.w_post) u = u * r1 * wp[k].get(i);
-        if (p.z) u *= gate_of<FAST>(t.z[k].get(i), p.act);
-        h[k][i] = p.res_scale * t.r[k].get(i) + p.branch_scale * u;
-        ss[0] += c.on[k] ? h[k][i] * h[k][i] : 0.f;
+      for (int e = 8 * k; e < 8 * k + 8 && e < N; ++e) {
+        float u = t.y.get(e);
+        if (p.w_post) u = u * r1 * wp.get(e);
+        if (p.z) u *= gate_of<FAST>(t.z.get(e), p.act);
+        h[e] = p.res_scale * t.r.get(e) + p.branch_scale * u;
+        ss[0] += c.on(e) ? h[e] * h[e] : 0.f;
       }
-      if (c.on[k]) store_v<V>((RT *)p.r_out + row + c.at[k], h[k]);
+      if (live) Vals<RT, NV, TAIL>::store((RT *)p.r_out + row, c, k, h + 8 * k);
+      piece_done<NV>();
     }
     if (!p.w_pre) continue;
-    block_sum(ss, s2[turn]);
+    row_sum<WG>(ss, at.G, s2[turn]);
     const float r2 = inv_rms(ss[0], p.C, p.eps);
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
+    for (int k = 0; k < NV + TAIL; ++k) {
+      if (!KEEP) wq.load(p.w_pre, c, k);
 #pragma unroll
-      for (int i = 0; i < V; ++i) h[k][i] = h[k][i] * r2 * wq[k].get(i);
-      if (c.on[k]) store_v<V>((IO *)p.x + row + c.at[k], h[k]);
+      for (int e = 8 * k; e < 8 * k + 8 && e < N; ++e)
+        h[e] = h[e] * r2 * wq.get(e);
+      if (live) Vals<IO, NV, TAIL>::store((IO *)p.x + row, c, k, h + 8 * k);
+      piece_done<NV>();
     }
   }
 }
 
-template <typename IO, typename RT, int V, int NV> struct BwdRow {
-  RawV<IO, V> y[NV], z[NV], dx[NV];
-  RawV<RT, V> r[NV], dr[NV];
+template <typename IO, typename RT, int NV, bool TAIL> struct BwdRow {
+  Vals<IO, NV, TAIL> y, z, dx;
+  Vals<RT, NV, TAIL> r, dr;
   __device__ __forceinline__ void load(const BlockNormParams &p, int n,
-                                       const Cols<V, NV> &c) {
+                                       const Cols<NV, TAIL> &c) {
     const size_t row = (size_t)n * p.C;
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      y[k].load((const IO *)p.y + row + c.at[k]);
-      if (p.z) z[k].load((const IO *)p.z + row + c.at[k]);
-      if (p.dx) {
-        dx[k].load((const IO *)p.dx + row + c.at[k]);
-        r[k].load((const RT *)p.r + row + c.at[k]);
-      }
-      if (p.dr_out) dr[k].load((const RT *)p.dr_out + row + c.at[k]);
+    y.load((const IO *)p.y + row, c);
+    if (p.dx) {
+      dx.load((const IO *)p.dx + row, c);
+      r.load((const RT *)p.r + row, c);
     }
+    if constexpr (NV == 1) late(p, row, c, 0);
+    if constexpr (NV == 1 && TAIL) late(p, row, c, 1);
+  }
+  // piece k of what the sums do not need; with several pieces it is loaded
+  // behind them
+  __device__ __forceinline__ void late(const BlockNormParams &p, size_t row,
+                                       const Cols<NV, TAIL> &c, int k) {
+    if (p.z) z.load((const IO *)p.z + row, c, k);
+    if (p.dr_out) dr.load((const RT *)p.dr_out + row, c, k);
   }
 };
 
+// the most values of all rows that a workgroup of 256 threads holds at once, G
+// lanes a row: 32 of 71, 16 of 135, 8 of 263 or 4 of 519
+constexpr int BN_SMALL = 2304;
+
+// a thread's sums for the gradients of its weights: in registers, or with
+// several pieces in LDS (their 32 registers would spill: 16384 bf16 values a
+// row took 445 us)
+template <int N, bool LDS> struct Sums {
+  float v[N];
+  __device__ __forceinline__ Sums(float *) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[e] = 0.f;
+  }
+  __device__ __forceinline__ void add(int e, float f) { v[e] += f; }
+  __device__ __forceinline__ float get(int e) const { return v[e]; }
+};
+template <int N> struct Sums<N, true> {
+  float *s;
+  __device__ __forceinline__ Sums(float *lds) : s(lds + threadIdx.x) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) s[e * 1024] = 0.f;
+  }
+  __device__ __forceinline__ void add(int e, float f) { s[e * 1024] += f; }
+  __device__ __forceinline__ float get(int e) const { return s[e * 1024]; }
+};
+
 // partial rows: workgroup g's dw_post at ws[g][0][C], dw_pre at ws[g][1][C]
-template <typename IO, typename RT, int V, int NV, int MAXT, bool AHEAD>
-__global__ __launch_bounds__(MAXT) void kda_block_norm_bwd(BlockNormParams p) {
-  constexpr bool FAST = sizeof(IO) == 2;
+template <typename IO, typename RT, bool WG, int NV, bool TAIL, int MAXT,
+          bool AHEAD>
+__global__ __launch_bounds__(MAXT) void kda_block_norm_bwd(BlockNormParams p,
+                                                           int lanes) {
+  constexpr bool FAST = sizeof(IO) == 2, KEEP = NV == 1;
+  constexpr int N = NV * 8 + TAIL;
   __shared__ float s1[2][16 * 3], s2[2][16];
-  const Cols<V, NV> c(p.C);
-  RawV<float, V> wp[NV], wq[NV];
-  load_weights(p.w_post, c, wp);
-  load_weights(p.w_pre, c, wq);
-  float a_post[NV][V], a_pre[NV][V];
-#pragma unroll
-  for (int k = 0; k < NV; ++k)
-#pragma unroll
-    for (int i = 0; i < V; ++i) a_post[k][i] = a_pre[k][i] = 0.f;
-  BwdRow<IO, RT, V, NV> t, next;
-  if constexpr (AHEAD) next.load(p, blockIdx.x, c);
+  __shared__ alignas(16) float part[WG ? 1 : BN_SMALL];
+  __shared__ float sums[KEEP ? 1 : 2 * N * 1024];  // at most 136 KiB
+  const Rows<WG> at(lanes);
+  Cols<NV, TAIL> c(p.C, at.lane(), at.lanes());
+  Vals<float, NV, TAIL> kp, kq;
+  if (KEEP && p.w_post) kp.load(p.w_post, c);
+  if (KEEP && p.w_pre) kq.load(p.w_pre, c);
+  Sums<N, !KEEP> a_post(sums), a_pre(sums + (KEEP ? 0 : N * 1024));
+  BwdRow<IO, RT, NV, TAIL> next;
+  if constexpr (AHEAD) next.load(p, at.row(at.first(), p.rows), c);
   int turn = 0;
-  for (int n = blockIdx.x; n < p.rows; n += gridDim.x, turn ^= 1) {
+  for (int base = at.first(); base < p.rows; base += at.step, turn ^= 1) {
+    if constexpr (WG) c.fresh();
+    const int n = at.row(base, p.rows);
     const size_t row = (size_t)n * p.C;
+    const bool live = at.on(base, p.rows);
+    BwdRow<IO, RT, NV, TAIL> t;
+    Vals<float, NV, TAIL> wp, wq;
+    if constexpr (KEEP) {
+      wp = kp;
+      wq = kq;
+    }
     if constexpr (AHEAD) {
       t = next;
-      if (n + (int)gridDim.x < p.rows) next.load(p, n + gridDim.x, c);
+      if (base + at.step < p.rows)
+        next.load(p, at.row(base + at.step, p.rows), c);
     } else {
       t.load(p, n, c);
     }
+    if (!KEEP && p.w_pre) wq.load(p.w_pre, c);
     // sums of r^2, of (w_pre dx) r and of y^2
     float q[3] = {0.f, 0.f, 0.f};
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (c.on[k]) {
-          if (p.dx) {
-            q[0] += t.r[k].get(i) * t.r[k].get(i);
-            q[1] += t.r[k].get(i) * t.dx[k].get(i) * wq[k].get(i);
-          }
-          if (p.w_post) q[2] += t.y[k].get(i) * t.y[k].get(i);
+    for (int e = 0; e < N; ++e)
+      if (c.on(e)) {
+        if (p.dx) {
+          q[0] += t.r.get(e) * t.r.get(e);
+          q[1] += t.r.get(e) * t.dx.get(e) * wq.get(e);
         }
-    block_sum(q, s1[turn]);
+        if (p.w_post) q[2] += t.y.get(e) * t.y.get(e);
+      }
+    row_sum<WG>(q, at.G, s1[turn]);
+    t.y.fresh(); t.dx.fresh(); t.r.fresh();
     const float r2 = inv_rms(q[0], p.C, p.eps);
     const float m2 = r2 * r2 * q[1] / (float)p.C;
     const float r1 = inv_rms(q[2], p.C, p.eps);
-    float d[NV][V], tn[1] = {0.f};
+    float d[N], tn[1] = {0.f};
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      float o[V], oz[V];
+    for (int k = 0; k < NV + TAIL; ++k) {
+      if (!KEEP && p.w_post) wp.load(p.w_post, c, k);
+      if (!KEEP && p.w_pre) wq.load(p.w_pre, c, k);
+      if constexpr (!KEEP) t.late(p, row, c, k);
+      float o[8], oz[8];
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float g = p.dr_out ? t.dr[k].get(i) : 0.f;
+      for (int e = 8 * k; e < 8 * k + 8 && e < N; ++e) {
+        const bool on = live && c.on(e);
+        float g = p.dr_out ? t.dr.get(e) : 0.f;
         if (p.dx) {
-          const float x = t.dx[k].get(i);
-          a_pre[k][i] += c.on[k] ? x * t.r[k].get(i) * r2 : 0.f;
-          g += r2 * (x * wq[k].get(i) - t.r[k].get(i) * m2);
+          const float x = t.dx.get(e);
+          a_pre.add(e, on ? x * t.r.get(e) * r2 : 0.f);
+          g += r2 * (x * wq.get(e) - t.r.get(e) * m2);
         }
-        o[i] = p.res_scale * g;
+        o[e - 8 * k] = p.res_scale * g;
         float du = p.branch_scale * g;
-        const float nv = p.w_post ? t.y[k].get(i) * r1 : t.y[k].get(i);
-        const float w = p.w_post ? wp[k].get(i) : 1.f;
+        const float nv = p.w_post ? t.y.get(e) * r1 : t.y.get(e);
+        const float w = p.w_post ? wp.get(e) : 1.f;
         if (p.z) {
-          const float2 gg = gate_grad<FAST>(t.z[k].get(i), p.act);
-          oz[i] = du * nv * w * gg.y;
+          const float2 gg = gate_grad<FAST>(t.z.get(e), p.act);
+          oz[e - 8 * k] = du * nv * w * gg.y;
           du *= gg.x;
         }
         if (p.w_post) {
-          a_post[k][i] += c.on[k] ? du * nv : 0.f;
+          a_post.add(e, on ? du * nv : 0.f);
           du *= w;
-          tn[0] += c.on[k] ? du * nv : 0.f;
+          tn[0] += c.on(e) ? du * nv : 0.f;
         }
-        d[k][i] = du;
+        d[e] = du;
       }
-      if (c.on[k]) {
-        store_v<V>((RT *)p.dr + row + c.at[k], o);
-        if (p.z) store_v<V>((IO *)p.dz + row + c.at[k], oz);
+      if (live) {
+        Vals<RT, NV, TAIL>::store((RT *)p.dr + row, c, k, o);
+        if (p.z) Vals<IO, NV, TAIL>::store((IO *)p.dz + row, c, k, oz);
       }
+      piece_done<NV>();
     }
     if (p.w_post) {
-      block_sum(tn, s2[turn]);
+      t.y.fresh();
+      row_sum<WG>(tn, at.G, s2[turn]);
       const float m1 = tn[0] / (float)p.C;
 #pragma unroll
-      for (int k = 0; k < NV; ++k)
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          d[k][i] = r1 * (d[k][i] - t.y[k].get(i) * r1 * m1);
+      for (int e = 0; e < N; ++e)
+        d[e] = r1 * (d[e] - t.y.get(e) * r1 * m1);
     }
+    if (live) Vals<IO, NV, TAIL>::store((IO *)p.dy + row, c, d);
+  }
+  float f_post[N], f_pre[N];
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
-      if (c.on[k]) store_v<V>((IO *)p.dy + row + c.at[k], d[k]);
+  for (int e = 0; e < N; ++e) {
+    f_post[e] = a_post.get(e);
+    f_pre[e] = a_pre.get(e);
   }
   float *out = p.ws + (size_t)blockIdx.x * 2 * p.C;
-#pragma unroll
-  for (int k = 0; k < NV; ++k)
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (c.on[k]) {
-        if (p.w_post) out[c.at[k] + i] = a_post[k][i];
-        if (p.dx) out[p.C + c.at[k] + i] = a_pre[k][i];
+  if constexpr (WG) {
+    if (p.w_post) Vals<float, NV, TAIL>::store(out, c, f_post);
+    if (p.dx) Vals<float, NV, TAIL>::store(out + p.C, c, f_pre);
+  } else {
+    // the workgroup's rows side by side in LDS, summed in order
+    for (int which = 0; which < 2; ++which) {
+      if (which ? !p.dx : !p.w_post) continue;
+      __syncthreads();  // the one before is read
+      Vals<float, NV, TAIL>::store(part + at.mine * p.C, c,
+                                   which ? f_pre : f_post);
+      __syncthreads();
+      for (int col = threadIdx.x; col < p.C; col += (int)blockDim.x) {
+        float a = 0.f;
+        for (int k = 0; k < at.per; ++k) a += part[k * p.C + col];
+        out[which * p.C + col] = a;
       }
+    }
+  }
 }
 
-// the layout of a row of C values: values per step, steps per thread, threads
-struct BnShape { int V, NV, threads; };
+// the layout of a row of C values: G lanes of a wave, or 0 and a workgroup's
+// threads with NV pieces each
+struct BnShape { int G, NV, threads; };
 static BnShape bn_shape(int C) {
-  BnShape b;
-  b.V = C % 8 == 0 ? 8 : 1;
-  b.NV = b.V == 8 ? (C <= 8192 ? 1 : 2) : C <= 4096 ? 4 : 16;
-  const int per = b.V * b.NV;
-  b.threads = ((C + per - 1) / per + 63) / 64 * 64;  // at most 1024
-  return b;
+  const int n = C / 8;  // whole pieces; the tail needs 7 lanes
+  if (n <= 64) return {n <= 8 ? 8 : n <= 16 ? 16 : n <= 32 ? 32 : 64, 1, 256};
+  const int NV = n <= 1024 ? 1 : 2;
+  return {0, NV, ((n + NV - 1) / NV + 63) / 64 * 64};  // at most 1024
+}
+static int bn_turns(int rows, const BnShape &b) {
+  const int per = b.G ? b.threads / b.G : 1;
+  return (rows + per - 1) / per;
 }
 // workgroups of the gradient, each with partial rows of the weight gradients:
 // eight waves for each of 256 CUs, in one round (twice as many: 158 against
 // 148 us at 8192 x 4096, and twice the partial rows)
 static int bn_groups(int rows, int C) {
-  const int threads = bn_shape(C).threads;
-  const int most = 256 * (threads < 512 ? 512 / threads : 1);
-  return rows < most ? rows : most;
+  const BnShape b = bn_shape(C);
+  const int most = 256 * (b.threads < 512 ? 512 / b.threads : 1);
+  const int turns = bn_turns(rows, b);
+  return turns < most ? turns : most;
 }
 
-template <typename IO, typename RT, int V, int NV, int MAXT, bool AHEAD>
+template <typename IO, typename RT, bool WG, int NV, bool TAIL, int MAXT,
+          bool AHEAD>
 static hipError_t bn_launch(const BlockNormParams &p, hipStream_t s,
                             bool bwd) {
-  const int threads = bn_shape(p.C).threads;  // at most MAXT: see bn_t
+  const BnShape b = bn_shape(p.C);  // at most MAXT threads: see bn_t
   if (!bwd) {
     int cus = 0;
     const hipError_t e = layer_cus(&cus);
     if (e != hipSuccess) return e;
     // what the CUs hold at 8 waves per SIMD
-    const int most = cus * (2048 / threads < 16 ? 2048 / threads : 16);
-    hipLaunchKernelGGL((kda_block_norm_fwd<IO, RT, V, NV, MAXT>),
-                       dim3(p.rows < most ? p.rows : most), dim3(threads), 0,
-                       s, p);
+    const int most = cus * (2048 / b.threads < 16 ? 2048 / b.threads : 16);
+    const int turns = bn_turns(p.rows, b);
+    hipLaunchKernelGGL((kda_block_norm_fwd<IO, RT, WG, NV, TAIL, MAXT>),
+                       dim3(turns < most ? turns : most), dim3(b.threads), 0,
+                       s, p, b.G);
     return hipGetLastError();
   }
   const int n = bn_groups(p.rows, p.C);
-  hipLaunchKernelGGL((kda_block_norm_bwd<IO, RT, V, NV, MAXT, AHEAD>), dim3(n),
-                     dim3(threads), 0, s, p);
+  hipLaunchKernelGGL((kda_block_norm_bwd<IO, RT, WG, NV, TAIL, MAXT, AHEAD>),
+                     dim3(n), dim3(b.threads), 0, s, p, b.G);
   if (p.w_post || p.dx) {
     // columns of dw_post, then of dw_pre; the ones not asked for are skipped
     const int lo = p.w_post ? 0 : p.C, hi = p.dx ? 2 * p.C : p.C;
@@ -524,18 +699,22 @@ static hipError_t bn_launch(const BlockNormParams &p, hipStream_t s,
   return hipGetLastError();
 }
 
-// C <= 16384.  Rows of a multiple of 8 values start 16-byte aligned and move
-// as vectors; others value by value.  The gradient holds the next row's loads
-// ahead where the registers allow it (C <= 4096, 512 threads).
+// C <= 16384.  The gradient holds the next rows' loads ahead where the
+// registers allow it (at most 512 threads).
+template <typename IO, typename RT, bool TAIL>
+static hipError_t bn_c(const BlockNormParams &p, hipStream_t s, bool bwd) {
+  const BnShape b = bn_shape(p.C);
+  if (b.G) return bn_launch<IO, RT, false, 1, TAIL, 256, true>(p, s, bwd);
+  if (b.threads <= 512 && b.NV == 1)
+    return bn_launch<IO, RT, true, 1, TAIL, 512, true>(p, s, bwd);
+  if (b.NV == 1)
+    return bn_launch<IO, RT, true, 1, TAIL, 1024, false>(p, s, bwd);
+  return bn_launch<IO, RT, true, 2, TAIL, 1024, false>(p, s, bwd);
+}
 template <typename IO, typename RT>
 static hipError_t bn_t(const BlockNormParams &p, hipStream_t s, bool bwd) {
-  if (p.C % 8 == 0) {
-    if (p.C <= 4096) return bn_launch<IO, RT, 8, 1, 512, true>(p, s, bwd);
-    if (p.C <= 8192) return bn_launch<IO, RT, 8, 1, 1024, false>(p, s, bwd);
-    return bn_launch<IO, RT, 8, 2, 1024, false>(p, s, bwd);
-  }
-  return p.C <= 4096 ? bn_launch<IO, RT, 1, 4, 1024, false>(p, s, bwd)
-                     : bn_launch<IO, RT, 1, 16, 1024, false>(p, s, bwd);
+  return p.C % 8 ? bn_c<IO, RT, true>(p, s, bwd)
+                 : bn_c<IO, RT, false>(p, s, bwd);
 }
 
 static hipError_t bn_any(const BlockNormParams &p, hipStream_t s, bool bwd) {

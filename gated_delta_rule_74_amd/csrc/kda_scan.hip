@@ -199,16 +199,10 @@ template <typename IO, typename GT, bool HEAD> struct ScanTile {
 
 // LDS: one composed map (A, U) per wave and channel
 constexpr int SCAN_WAVES = SCAN_THREADS / 64;
-struct ScanLds {
+struct alignas(16) ScanLds {
   float A[SCAN_WAVES][SCAN_W];
   float U[SCAN_WAVES][SCAN_W];
 };
-
-__device__ __forceinline__ void lds_get(const float *src, float *v) {
-  const f32x4 lo = *(const f32x4 *)src, hi = *(const f32x4 *)(src + 4);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) { v[i] = lo[i]; v[4 + i] = hi[i]; }
-}
 
 // v of the lower (x) and upper (y) of each pair of 16-lane rows (ROWS) or of
 // the two 32-lane halves, in every lane of the pair
@@ -459,7 +453,7 @@ __device__ __forceinline__ void link_leave(const ScanLink &l, const LinkAt &k,
 
 // the value entering the chunk, made by all threads from what two pairs of
 // waves fetched
-struct ScanCarry {
+struct alignas(16) ScanCarry {
   float ga[SCAN_W], gu[SCAN_W], base[SCAN_W];
   __device__ __forceinline__ float at(int w) const {
     return fma_(ga[w], base[w], gu[w]);
