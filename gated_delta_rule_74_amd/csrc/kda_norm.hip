@@ -477,14 +477,21 @@ template <typename IO, typename RT, int NV, bool TAIL> struct BwdRow {
       dx.load((const IO *)p.dx + row, c);
       r.load((const RT *)p.r + row, c);
     }
-    if constexpr (NV == 1) late(p, row, c, 0);
-    if constexpr (NV == 1 && TAIL) late(p, row, c, 1);
+    if constexpr (NV == 1)
+#pragma unroll
+      for (int k = 0; k < 1 + TAIL; ++k) {
+        late_z(p, row, c, k);
+        late_dr(p, row, c, k);
+      }
   }
   // piece k of what the sums do not need; with several pieces it is loaded
   // behind them
-  __device__ __forceinline__ void late(const BlockNormParams &p, size_t row,
-                                       const Cols<NV, TAIL> &c, int k) {
+  __device__ __forceinline__ void late_z(const BlockNormParams &p, size_t row,
+                                         const Cols<NV, TAIL> &c, int k) {
     if (p.z) z.load((const IO *)p.z + row, c, k);
+  }
+  __device__ __forceinline__ void late_dr(const BlockNormParams &p, size_t row,
+                                          const Cols<NV, TAIL> &c, int k) {
     if (p.dr_out) dr.load((const RT *)p.dr_out + row, c, k);
   }
 };
@@ -494,8 +501,8 @@ template <typename IO, typename RT, int NV, bool TAIL> struct BwdRow {
 constexpr int BN_SMALL = 2304;
 
 // a thread's sums for the gradients of its weights: in registers, or with
-// several pieces in LDS (their 32 registers would spill: 16384 bf16 values a
-// row took 445 us)
+// several pieces in LDS (their 32 registers would spill: 2048 rows of 16384
+// bf16 values took 445 us, against 225)
 template <int N, bool LDS> struct Sums {
   float v[N];
   __device__ __forceinline__ Sums(float *) {
@@ -555,38 +562,52 @@ __global__ __launch_bounds__(MAXT) void kda_block_norm_bwd(BlockNormParams p,
     if (!KEEP && p.w_pre) wq.load(p.w_pre, c);
     // sums of r^2, of (w_pre dx) r and of y^2
     float q[3] = {0.f, 0.f, 0.f};
+    if (p.dx)
 #pragma unroll
-    for (int e = 0; e < N; ++e)
-      if (c.on(e)) {
-        if (p.dx) {
-          q[0] += t.r.get(e) * t.r.get(e);
-          q[1] += t.r.get(e) * t.dx.get(e) * wq.get(e);
-        }
-        if (p.w_post) q[2] += t.y.get(e) * t.y.get(e);
+      for (int e = 0; e < N; ++e) {
+        const float r = t.r.get(e), x = t.dx.get(e) * wq.get(e);
+        q[0] += c.on(e) ? r * r : 0.f;
+        q[1] += c.on(e) ? r * x : 0.f;
       }
+    if (p.w_post)
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        q[2] += c.on(e) ? t.y.get(e) * t.y.get(e) : 0.f;
     row_sum<WG>(q, at.G, s1[turn]);
     t.y.fresh(); t.dx.fresh(); t.r.fresh();
     const float r2 = inv_rms(q[0], p.C, p.eps);
     const float m2 = r2 * r2 * q[1] / (float)p.C;
     const float r1 = inv_rms(q[2], p.C, p.eps);
     float d[N], tn[1] = {0.f};
+    // the stream's side first, then the block's: with several pieces dx and r
+    // are done with by then
 #pragma unroll
     for (int k = 0; k < NV + TAIL; ++k) {
-      if (!KEEP && p.w_post) wp.load(p.w_post, c, k);
       if (!KEEP && p.w_pre) wq.load(p.w_pre, c, k);
-      if constexpr (!KEEP) t.late(p, row, c, k);
-      float o[8], oz[8];
+      if constexpr (!KEEP) t.late_dr(p, row, c, k);
+      float o[8];
 #pragma unroll
       for (int e = 8 * k; e < 8 * k + 8 && e < N; ++e) {
-        const bool on = live && c.on(e);
         float g = p.dr_out ? t.dr.get(e) : 0.f;
         if (p.dx) {
           const float x = t.dx.get(e);
-          a_pre.add(e, on ? x * t.r.get(e) * r2 : 0.f);
+          a_pre.add(e, live && c.on(e) ? x * t.r.get(e) * r2 : 0.f);
           g += r2 * (x * wq.get(e) - t.r.get(e) * m2);
         }
         o[e - 8 * k] = p.res_scale * g;
-        float du = p.branch_scale * g;
+        d[e] = p.branch_scale * g;
+      }
+      if (live) Vals<RT, NV, TAIL>::store((RT *)p.dr + row, c, k, o);
+      piece_done<NV>();
+    }
+#pragma unroll
+    for (int k = 0; k < NV + TAIL; ++k) {
+      if (!KEEP && p.w_post) wp.load(p.w_post, c, k);
+      if constexpr (!KEEP) t.late_z(p, row, c, k);
+      float oz[8];
+#pragma unroll
+      for (int e = 8 * k; e < 8 * k + 8 && e < N; ++e) {
+        float du = d[e];
         const float nv = p.w_post ? t.y.get(e) * r1 : t.y.get(e);
         const float w = p.w_post ? wp.get(e) : 1.f;
         if (p.z) {
@@ -595,16 +616,13 @@ __global__ __launch_bounds__(MAXT) void kda_block_norm_bwd(BlockNormParams p,
           du *= gg.x;
         }
         if (p.w_post) {
-          a_post.add(e, on ? du * nv : 0.f);
+          a_post.add(e, live && c.on(e) ? du * nv : 0.f);
           du *= w;
           tn[0] += c.on(e) ? du * nv : 0.f;
         }
         d[e] = du;
       }
-      if (live) {
-        Vals<RT, NV, TAIL>::store((RT *)p.dr + row, c, k, o);
-        if (p.z) Vals<IO, NV, TAIL>::store((IO *)p.dz + row, c, k, oz);
-      }
+      if (live && p.z) Vals<IO, NV, TAIL>::store((IO *)p.dz + row, c, k, oz);
       piece_done<NV>();
     }
     if (p.w_post) {
@@ -659,7 +677,8 @@ static int bn_turns(int rows, const BnShape &b) {
 }
 // workgroups of the gradient, each with partial rows of the weight gradients:
 // eight waves for each of 256 CUs, in one round (twice as many: 158 against
-// 148 us at 8192 x 4096, and twice the partial rows)
+// 148 us at 8192 x 4096, 25.6 against 24.0 at 65536 x 64, and twice the partial
+// rows)
 static int bn_groups(int rows, int C) {
   const BnShape b = bn_shape(C);
   const int most = 256 * (b.threads < 512 ? 512 / b.threads : 1);
