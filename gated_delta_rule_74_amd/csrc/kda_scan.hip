@@ -678,8 +678,9 @@ void kda_scan_grad(
                      : p.dhT  ? (p.dhT + o)[w]
                               : 0.f;
       } else {
-        sf.base[w] = (states + ((size_t)at.b * p.NC + at.c) * p.C +
-                      at.cb * SCAN_W)[w];
+        sf.base[w] = states ? (states + ((size_t)at.b * p.NC + at.c) * p.C +
+                               at.cb * SCAN_W)[w]
+                            : 0.f;
         sf.ga[w] = 1.f;
         sf.gu[w] = 0.f;
         fold_chunk<false>(s, w, ca, cu);
@@ -834,7 +835,7 @@ static hipError_t scan_t(const ScanParams &p, hipStream_t s, bool bwd) {
   // gradient's, by its registers); they take tiles until none is left
   const dim3 grid(tiles < 2 * cus ? tiles : 2 * cus), thr(SCAN_THREADS);
   const dim3 ggrid(tiles < cus ? tiles : cus);
-  const bool redo = bwd && !p.states;
+  const bool redo = bwd && !p.states && p.NC > 1;
   const LinkBytes n = link_bytes(p.B, p.C, p.NC);
   const int passes = redo ? 2 : 1;
   const ScanLink l0 = link_at(p, 0, passes);
@@ -854,6 +855,7 @@ static hipError_t scan_t(const ScanParams &p, hipStream_t s, bool bwd) {
     return hipGetLastError();
   }
   ScanParams q = p;
+  if (p.NC == 1) q.states = (float *)p.h0;  // the state before the one chunk
   if (redo) {
     q.states = (float *)(p.ws + 256 + 2 * (n.total + n.entry));
     hipLaunchKernelGGL((kda_scan_fwd<IO, GT, HEAD, true>), grid, thr, 0, s, q,

@@ -166,6 +166,34 @@ def test_block_norm_largest_rows(kda):
         block(kda, 3, C, io, res, act="silu", seed=60)
 
 
+@pytest.mark.parametrize("C", [2, 4, 6, 9, 15, 71, 72, 135, 136, 137, 263,
+                               264, 519, 527, 4095, 4104, 4107, 8191, 8199,
+                               8200, 8201, 12296])
+@pytest.mark.parametrize("io,res", [(F, F), (BF, F), (BF, BF)])
+def test_block_norm_layout_borders(kda, C, io, res):
+    """widths where the lanes of a row, the pieces of a thread or the tail
+    change, with rows that do not fill the last workgroup's lanes"""
+    block(kda, 37 if C < 4000 else 5, C, io, res, act="silu", seed=130)
+
+
+@pytest.mark.parametrize("C", [1, 3, 65, 129, 777, 8197])
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_block_norm_writes_rows_only(kda, C, dtype):
+    """what lies behind the last row stays as it was, the tail's stores and
+    the vectors at odd addresses included"""
+    R, n = 13, 13 * C
+    y, r = rn(R, C, seed=140, dtype=dtype), rn(R, C, seed=141, dtype=dtype)
+    w = rn(C, seed=142)
+    h, x = kda.kda_block_norm(y, r, w_post=w, w_pre=w)
+    bufs = [torch.full((n + 64,), 7.0, dtype=dtype, device="cuda")
+            for _ in range(2)]
+    ho, xo = (b[:n].view(R, C) for b in bufs)
+    kda.kda_block_norm(y, r, w_post=w, w_pre=w, r_out=ho, x=xo)
+    assert torch.equal(h, ho) and torch.equal(x, xo)
+    for b in bufs:
+        assert bool((b[n:] == 7).all())
+
+
 def test_norms_repeatable_and_captured(kda):
     o, z, dy = (rn(700, 4, 64, seed=70 + i, dtype=BF) for i in range(3))
     w = rn(64, seed=74)
