@@ -243,7 +243,7 @@ size_t gated_norm_bwd_ws_bytes(long long rows, int D) {
 // their pieces move as vectors all the same (value by value, C = 4097 took
 // 406 and 1431 us where 4096 takes 90 and 141).  Bound by HBM: 8192 rows x 4096
 // with a gate and an fp32 stream take 90 us for 470 MB (5.2 TB/s), the
-// gradient 144 us for 738 MB and 8 MB of partial rows (5.2 TB/s) and 5 us for
+// gradient 139 us for 738 MB and 8 MB of partial rows (5.4 TB/s) and 5 us for
 // their sum.  With one row per workgroup, its weights read from the L2 for
 // every row, they took 129 and 278 us.
 

@@ -40,9 +40,9 @@
 // loads are clamped to the last valid token).
 //
 // Measured (bf16 data, fp32 gate, kernel alone): forward B1 T8192 H32 D128
-// 59 us, 219 MB read and 69 MB written (4.9 TB/s; a 1 GiB copy reaches 5.0);
-// B1 T262144 H4 D128 230 us (4.9 TB/s); gradient of the first 112 us (4.4 TB/s
-// of 285 + 207 MB) behind the recomputation's 52 us.  A tile's latency is
+// 57 us, 219 MB read and 69 MB written (5.0 TB/s; a 1 GiB copy reaches 5.0);
+// B1 T262144 H4 D128 224 us (5.0 TB/s); gradient of the first 106 us (4.6 TB/s
+// of 285 + 207 MB) behind the recomputation's 53 us.  A tile's latency is
 // about 10 us (loads 2-3, decays and composition 3, hand-over 2-3, tokens 2),
 // and what is in flight meanwhile (two tiles of 96 KiB per CU) is what keeps
 // the memory busy: with three kernels that read everything twice the same
@@ -511,7 +511,10 @@ __device__ __forceinline__ void enter(const ScanLds &s, const ScanCarry &c,
 // forward: y and the final state; or with STATES only the states before the
 // chunks (the gradient's recomputation).  127 registers: two workgroups share
 // a CU, one loading while the other composes; a spill of 100 bytes per lane
-// costs more than half of the rate.
+// costs more than half of the rate.  Three per CU are no gain where the
+// registers would allow it: the states alone (72) 2 us slower at B1 T8192 H32
+// D128; one gate per head (84, with 64 bytes of spills) 63 against 47 us at B1
+// T65536 H4 D128.
 template <typename IO, typename GT, bool HEAD, bool STATES>
 __global__ __launch_bounds__(SCAN_THREADS, 4) void kda_scan_fwd(
     ScanParams p, ScanLink l, int tiles) {
