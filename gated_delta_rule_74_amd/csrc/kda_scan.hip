@@ -858,7 +858,9 @@ static hipError_t scan_t(const ScanParams &p, hipStream_t s, bool bwd) {
     return hipGetLastError();
   }
   ScanParams q = p;
-  if (p.NC == 1) q.states = (float *)p.h0;  // the state before the one chunk
+  // the state before the one chunk: the forward call's copy where there is
+  // one, as h0 may since hold the final state
+  if (p.NC == 1 && !p.states) q.states = (float *)p.h0;
   if (redo) {
     q.states = (float *)(p.ws + 256 + 2 * (n.total + n.entry));
     hipLaunchKernelGGL((kda_scan_fwd<IO, GT, HEAD, true>), grid, thr, 0, s, q,

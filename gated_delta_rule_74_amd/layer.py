@@ -198,9 +198,9 @@ def kda_scan_backward(x, g, beta, dy, *, h0=None, dhT=None, lengths=None,
                       chunk_states=None, want_dh0=True, workspace=None,
                       stream=None):
     """Gradient of kda_scan for the loss sum(y*dy) + sum(h_out*dhT).
-    chunk_states: those kda_scan returned for the same inputs, or None (they
-    are recomputed).  Returns (dx, dg shaped like g, dbeta or None, dh0 or
-    None)."""
+    chunk_states: those kda_scan returned for the same inputs (h0 is then not
+    read and may have been overwritten), or None (they are recomputed).
+    Returns (dx, dg shaped like g, dbeta or None, dh0 or None)."""
     io, gt = _scan_codes(x, g, beta, 3)
     B, T, H, D = x.shape
     _must(dy, x.shape, x.dtype, "dy (must have x's dtype)")

@@ -375,7 +375,8 @@ kda_status kda_scan(const void *x, kda_dtype io_dtype, const void *g,
  *   dy            [B,T,H,D] in io_dtype
  *   dhT           [B,H,D] fp32 gradient of the final state, or NULL (zero)
  *   chunk_states  those that kda_scan wrote for the same inputs, or NULL: they
- *                 are then recomputed
+ *                 are then recomputed.  Where they are given h0 is not read,
+ *                 so it may have been overwritten (h_out = h0)
  *   dx            [B,T,H,D] in io_dtype
  *   dg            shaped like g, in gate_dtype
  *   dbeta         [B,T,H] in gate_dtype; NULL exactly when beta is

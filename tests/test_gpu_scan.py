@@ -419,3 +419,18 @@ def test_state_in_place_over_many_chunks(kda, T):
         st = q["h0"].clone()
         y2, h2, _ = kda.kda_scan(q["x"], q["g"], q["beta"], h0=st, h_out=st)
         assert h2 is st and torch.equal(h, st) and torch.equal(y, y2)
+
+
+@pytest.mark.parametrize("T", [1, 100, 128, 129, 700])
+def test_gradient_from_chunk_states_alone(kda, T):
+    """the chunk states take the place of h0, which the forward call may have
+    overwritten (h_out = h0)"""
+    q = inputs(2, T, 3, 64, seed=92, reset=0)
+    want = backward(kda, q)
+    h = q["h0"].clone()
+    _, _, cs = kda.kda_scan(q["x"], q["g"], q["beta"], h0=h, h_out=h,
+                            chunk_states=True)
+    for h0 in (h, None):
+        got = backward(kda, dict(q, h0=h0), chunk_states=cs)
+        for u, v in zip(want, got):
+            assert torch.equal(u, v)
