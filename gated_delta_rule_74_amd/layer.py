@@ -69,6 +69,14 @@ def _int(n, name):
         raise KdaError(KDA_EUNSUPPORTED, f"{name} = {n}")
 
 
+def _size(f, *n):
+    """The workspace size f(*n); 0 (unsupported) for sizes that the C interface
+    would cut to their lower bits."""
+    if any(c(v).value != v for c, v in zip(f.argtypes, n)):
+        return 0
+    return int(f(*n))
+
+
 def _bad(t, dev):
     if not t.is_cuda:
         raise ValueError("tensors must live on the GPU")
@@ -141,12 +149,12 @@ def _scan_codes(x, g, beta, nd):
 
 @functools.lru_cache(maxsize=256)
 def kda_scan_workspace_size(B, T, H, D) -> int:
-    return int(_scan_ws(B, T, H, D))
+    return _size(_scan_ws, B, T, H, D)
 
 
 @functools.lru_cache(maxsize=256)
 def kda_scan_backward_workspace_size(B, T, H, D) -> int:
-    return int(_scan_bwd_ws(B, T, H, D))
+    return _size(_scan_bwd_ws, B, T, H, D)
 
 
 def kda_scan(x, g, beta=None, *, h0=None, lengths=None, y=None, h_out=None,
@@ -285,7 +293,7 @@ def kda_gated_norm(o, z, w, *, act="sigmoid", eps=1e-6, y=None, stream=None):
 
 @functools.lru_cache(maxsize=256)
 def kda_gated_norm_backward_workspace_size(rows, D) -> int:
-    return int(_gated_ws(rows, D))
+    return _size(_gated_ws, rows, D)
 
 
 def kda_gated_norm_backward(o, z, w, dy, *, act="sigmoid", eps=1e-6,
@@ -364,7 +372,7 @@ def kda_block_norm(y, r, *, w_post=None, z=None, w_pre=None, act="sigmoid",
 
 @functools.lru_cache(maxsize=256)
 def kda_block_norm_backward_workspace_size(rows, C) -> int:
-    return int(_block_ws(rows, C))
+    return _size(_block_ws, rows, C)
 
 
 def kda_block_norm_backward(y, r_out, *, dx=None, dr_out=None, w_post=None,

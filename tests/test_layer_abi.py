@@ -276,6 +276,20 @@ def test_binding_refuses_sizes_past_an_int():
             call()
 
 
+def test_workspace_sizes_past_an_int():
+    """no workspace, rather than that of the sizes' lower 32 bits"""
+    P = 1 << 32
+    for f in (kda.kda_scan_workspace_size,
+              kda.kda_scan_backward_workspace_size):
+        for n in ((P + 1, 8, 1, 16), (1, P + 8, 1, 16), (1, 8, P + 1, 16),
+                  (1, 8, 1, P + 16), (1 - P, 8, 1, 16)):
+            assert f(*n) == 0, n
+    f = kda.kda_gated_norm_backward_workspace_size
+    assert f(5, P + 16) == 0 and f((1 << 64) + 5, 16) == 0
+    f = kda.kda_block_norm_backward_workspace_size
+    assert f(P + 3, 8) == 0 and f(3, P + 8) == 0
+
+
 @pytest.mark.skipif(shutil.which("hipcc") is None and
                     not os.path.exists("/opt/rocm/bin/hipcc"),
                     reason="hipcc not available")
