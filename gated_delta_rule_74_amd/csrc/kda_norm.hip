@@ -17,11 +17,26 @@
 
 namespace kda {
 
-// logistic function and the gates made of it; fp32 data takes the library's
-// exp and a correctly rounded division, bf16 data the hardware ones (about
-// 2 ulp of fp32, 2^14 times finer than the rounding of the result)
+// exp(x) for an x of 8 significant bits (a bf16 gate), within 2.5 ulp for |x|
+// <= 87 and 1.6 for |x| <= 30: 16 bits of log2(e) make the product with x exact,
+// the hardware's 2^t is good to an ulp, and what the other bits would add to
+// the exponent comes in as 1 + c (c^2 / 2 is left out).  Results under 2^-126
+// are flushed to 0; exp(-inf) = 0, exp(inf) = inf, exp(NaN) = NaN.
+__device__ __forceinline__ float exp_bf16(float x) {
+  constexpr float L = 47274.f / 32768.f, Llo_ln2 = 4.8884952e-6f;
+  const float r = __builtin_amdgcn_exp2f(x * L);
+  return __builtin_fmaf(r, fmaxf(x * Llo_ln2, -1.f), r);  // not 0 * inf
+}
+
+// logistic function and the gates made of it.  fp32 data takes the library's
+// exp and a correctly rounded division, bf16 data the above and the hardware's
+// reciprocal (1 ulp), which holds every gate to 5 ulp of fp32: the stream and
+// the weights' gradients beside bf16 data are fp32.  (With the hardware's exp
+// of the rounded product, off by 30 ulp at z = -60, the gradient takes 3 % less
+// time at 8192 x 4096, 119.8 against 122.4 us with its data in the cache; other
+// widths and the forward kernels at most 2 %.)
 template <bool FAST> __device__ __forceinline__ float logistic(float z) {
-  if constexpr (FAST) return __builtin_amdgcn_rcpf(1.f + __expf(-z));
+  if constexpr (FAST) return __builtin_amdgcn_rcpf(1.f + exp_bf16(-z));
   else return 1.f / (1.f + expf(-z));
 }
 template <bool FAST>
@@ -34,7 +49,7 @@ __device__ __forceinline__ float gate_of(float z, int act) {
 // would lose all of it where s rounds to 1.
 template <bool FAST>
 __device__ __forceinline__ float2 gate_grad(float z, int act) {
-  const float e = FAST ? __expf(-fabsf(z)) : expf(-fabsf(z));
+  const float e = FAST ? exp_bf16(-fabsf(z)) : expf(-fabsf(z));
   const float q = FAST ? __builtin_amdgcn_rcpf(1.f + e) : 1.f / (1.f + e);
   const float eq = e * q, s = z < 0.f ? eq : q, m = eq * q;
   return act == ACT_SILU ? make_float2(z * s, s + z * m) : make_float2(s, m);

@@ -322,3 +322,48 @@ def test_block_of_a_model(kda):
                             ("S", s, want[2]), ("h", hs, want[3])):
         err = float((got - ref_).abs().max() / ref_.abs().max())
         assert err <= 2e-4, (name, err)
+
+
+@pytest.mark.parametrize("act", ["sigmoid", "silu"])
+def test_gate_of_an_fp32_stream(kda, act):
+    """bf16 gates that reach fp32 results are good to fp32: with y = 1, r = 0
+    and no norms r_out is the gate itself, and dw of a head of equal values the
+    gate times its norm.
+
+    u = 2^-24.  exp(-|z|) is within 1.5 ulp = 3u, 1 + e then within 1.5u + u,
+    its reciprocal 2u more, the product with e (z < 0) 4u more; silu's product
+    u: 10u.  dw: the norm of 16 values (16 / 2 + 8) u, products 2u."""
+    z = torch.arange(-80, 80, 1 / 16).to(BF)
+    z = z[:len(z) // 16 * 16].view(-1, 16)
+    z8 = z.double()
+    want = torch.sigmoid(z8) * (z8 if act == "silu" else 1.0)
+    one = torch.ones(z.shape, dtype=BF, device="cuda")
+    r, _ = kda.kda_block_norm(one, torch.zeros(z.shape, device="cuda"),
+                              z=z.cuda(), act=act)
+    within("r_out", r, (want, 10 * ref.U * want.abs()))
+    # one row a call: dw is then the row's own term
+    w = torch.ones(16, device="cuda")
+    for i in range(0, z.shape[0], 8):
+        _, _, dw = kda.kda_gated_norm_backward(one[i:i + 1], z[i:i + 1].cuda(),
+                                               w, one[i:i + 1], act=act,
+                                               eps=EPS)
+        n = want[i] / math.sqrt(1 + EPS)
+        within("dw", dw, (n, 28 * ref.U * n.abs()))
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_gates_at_the_ends_of_the_range(kda, dtype):
+    """gates that are infinite, huge or NaN: the formula's limits"""
+    z = torch.tensor([math.inf, 3e38, 100.0, 0.0, -100.0, -3e38, -math.inf,
+                      math.nan], device="cuda").to(dtype).view(1, -1)
+    one = torch.ones(1, 8, dtype=dtype, device="cuda")
+    r = torch.zeros(1, 8, device="cuda")
+    s = torch.tensor([1, 1, 1, 0.5, 0, 0, 0, math.nan])
+    got = kda.kda_block_norm(one, r, z=z)[0].cpu()[0]
+    assert torch.allclose(got, s, rtol=0, atol=1e-37, equal_nan=True)
+    silu = kda.kda_block_norm(one, r, z=z, act="silu")[0].cpu()[0]
+    want = s * z.cpu().float()[0]  # -inf * 0 is NaN
+    assert torch.allclose(silu, want, rtol=0, atol=1e-37, equal_nan=True)
+    dz = kda.kda_block_norm_backward(one, r, dr_out=r + 1, z=z)[2].cpu()[0]
+    want = torch.tensor([0, 0, 0, 0.25, 0, 0, 0, math.nan])
+    assert torch.allclose(dz.float(), want, rtol=0, atol=1e-37, equal_nan=True)
