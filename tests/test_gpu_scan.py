@@ -434,3 +434,21 @@ def test_gradient_from_chunk_states_alone(kda, T):
         got = backward(kda, dict(q, h0=h0), chunk_states=cs)
         for u, v in zip(want, got):
             assert torch.equal(u, v)
+
+
+def test_decay_within_one_and_a_half_ulp(kda):
+    """exp(g) as a step makes it from a state of ones and no input: the
+    hardware's 2^t is off by at most an ulp, the last multiply-add by half of
+    one, and what the correction of t leaves out is under 2^-10 of one"""
+    gen = torch.Generator().manual_seed(93)
+    N = 1 << 16
+    g = -87.3 * torch.rand(N, 1, 16, generator=gen) ** 3
+    g[0], g[1], g[2] = 0.0, -math.inf, -1e-8
+    state = torch.ones(N, 1, 16, device="cuda")
+    kda.kda_scan_step(torch.zeros(N, 1, 16, device="cuda"), g.cuda(), None,
+                      state)
+    want = torch.exp(g.double())
+    ulp = torch.exp2(torch.floor(torch.log2(want.clamp_min(2.0 ** -126))) - 23)
+    err = (state.cpu().double() - want).abs() / ulp
+    assert bool((state[0] == 1).all()) and bool((state[1] == 0).all())
+    assert float(err.max()) <= 1.5 + 2.0 ** -10, float(err.max())
