@@ -290,6 +290,17 @@ def test_workspace_sizes_past_an_int():
     assert f(P + 3, 8) == 0 and f(3, P + 8) == 0
 
 
+@pytest.mark.parametrize("nc", [2, 7, 8, 9, 10, 16, 17, 32, 33, 34, 65, 1000])
+def test_most_tiles_can_be_cleared(nc):
+    """the two passes' words of the most tiles there may be: 16 bytes a thread,
+    and a launch of at most 2^32 - 1 threads"""
+    B = ((1 << 23) - 1) // nc
+    size = kda.kda_scan_backward_workspace_size(B, nc * 128, 1, 16)
+    words = size - B * 16 * nc * 4
+    assert size > 0 and 0 < words // 16 < 2 ** 32 - 256
+    assert kda.kda_scan_backward_workspace_size(B + nc, nc * 128, 1, 16) == 0
+
+
 @pytest.mark.skipif(shutil.which("hipcc") is None and
                     not os.path.exists("/opt/rocm/bin/hipcc"),
                     reason="hipcc not available")
