@@ -63,7 +63,7 @@ kda_status scan_sizes(int B, int T, int H, int D, int *NC) {
   if (T > (1 << 30) || C > (1 << 22)) return KDA_EUNSUPPORTED;
   const long long nc = (T + kda::SCAN_L - 1) / kda::SCAN_L;
   const long long per = nc * ((C + 127) / 128);
-  // the gradient's words are cleared by 16 bytes a thread: at most 263 threads
+  // the gradient's words are cleared by 16 bytes a thread: at most 264 threads
   // a tile (9 chunks), which with 2^23 tiles stay below a grid's 2^32 threads.
   // Tile numbers are ints.
   const long long most = (1 << 23) - 1;

@@ -62,7 +62,7 @@ __device__ __forceinline__ float inv_rms(float sumsq, int n, float eps) {
 // ---------------------------------------------------------------------------
 // gated head norm: D / 8 lanes hold one row of D values.  Bound by HBM: 32768
 // tokens x 32 heads x 128 in bf16 take 139 us for 805 MB (5.8 TB/s); the
-// gradient of 8191 tokens 63 us for 336 MB (5.3 TB/s) and 5 us for the sum of
+// gradient of 8191 tokens 65 us for 336 MB (5.2 TB/s) and 5 us for the sum of
 // dw's partial rows.  With the weights loaded one by one, which is 8 of 11
 // memory instructions, the first took 275 us.
 
@@ -258,9 +258,10 @@ size_t gated_norm_bwd_ws_bytes(long long rows, int D) {
 // their pieces move as vectors all the same (value by value, C = 4097 took
 // 406 and 1431 us where 4096 takes 90 and 141).  Bound by HBM: 8192 rows x 4096
 // with a gate and an fp32 stream take 90 us for 470 MB (5.2 TB/s), the
-// gradient 139 us for 738 MB and 8 MB of partial rows (5.4 TB/s) and 5 us for
+// gradient 142 us for 738 MB and 8 MB of partial rows (5.3 TB/s) and 5 us for
 // their sum.  With one row per workgroup, its weights read from the L2 for
-// every row, they took 129 and 278 us.
+// every row, they took 129 and 278 us.  Plain streams of the same reads to writes
+// over 2 GB reach 5.5 and 5.6 TB/s.
 
 // where a thread's values lie in a row: NV pieces of 8 and, with TAIL, one of
 // the last C % 8 values
@@ -415,7 +416,8 @@ template <typename IO, typename RT, int NV, bool TAIL> struct FwdRow {
 
 // Weights stay in registers (but not with two pieces a thread, where they are
 // read again for every row, from the L2), and the next rows' loads are issued
-// before these rows' sums are waited for.
+// before these rows' sums are waited for.  Two pieces of fp32 spill 8 registers,
+// 45 with a tail (2048 x 16384: 164 us, 4.1 TB/s).
 template <typename IO, typename RT, bool WG, int NV, bool TAIL, int MAXT>
 __global__ __launch_bounds__(MAXT) void kda_block_norm_fwd(BlockNormParams p,
                                                            int lanes) {

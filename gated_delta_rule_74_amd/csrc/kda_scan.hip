@@ -33,16 +33,19 @@
 //    chunk before the next chunk: one that waits only waits for chunks that
 //    were taken earlier, so some workgroup can always go on.
 //  - The wait is bounded all the same (about a second); what is missing then
-//    reads as NaN.
+//    reads as NaN, and so do the outputs made from it.
 //
 // Tokens at and past a sequence's length are the identity map; their outputs
 // are written as zeros, and what the inputs hold there is never used (the
 // loads are clamped to the last valid token).
 //
 // Measured (bf16 data, fp32 gate, kernel alone): forward B1 T8192 H32 D128
-// 57 us, 219 MB read and 69 MB written (5.0 TB/s; a 1 GiB copy reaches 5.0);
-// B1 T262144 H4 D128 224 us (5.0 TB/s); gradient of the first 106 us (4.6 TB/s
-// of 285 + 207 MB) behind the recomputation's 53 us.  A tile's latency is
+// 57 us, 219 MB read and 69 MB written (5.0 TB/s; a plain stream of three reads
+// to one write over 2 GB reaches 5.8, a 1 GiB copy 5.0); B1 T262144 H4 D128 220
+// us (5.1 TB/s); gradient of the first 106 us (4.6 TB/s of 285 + 207 MB) behind
+// the recomputation's 54 us.  Fewer bytes per tile take the same latency: one
+// gate per head in bf16 47 us at B1 T65536 H4 D128 (2.9 TB/s), 16 channels 29 us
+// at T65536 (0.3 TB/s), one token each of 256 sequences x 32 heads 104 us.  A tile's latency is
 // about 10 us (loads 2-3, decays and composition 3, hand-over 2-3, tokens 2),
 // and what is in flight meanwhile (two tiles of 96 KiB per CU) is what keeps
 // the memory busy: with three kernels that read everything twice the same
@@ -509,9 +512,10 @@ __device__ __forceinline__ void enter(const ScanLds &s, const ScanCarry &c,
 }
 
 // forward: y and the final state; or with STATES only the states before the
-// chunks (the gradient's recomputation).  127 registers: two workgroups share
+// chunks (the gradient's recomputation).  128 registers: two workgroups share
 // a CU, one loading while the other composes; a spill of 100 bytes per lane
-// costs more than half of the rate.  Three per CU are no gain where the
+// costs more than half of the rate (what is left, with a gate per channel, is
+// 20 bytes: 4 registers with bf16 data, 11 with fp32).  Three per CU are no gain where the
 // registers would allow it: the states alone (72) 2 us slower at B1 T8192 H32
 // D128; one gate per head (84, with 64 bytes of spills) 63 against 47 us at B1
 // T65536 H4 D128.

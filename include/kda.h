@@ -31,10 +31,11 @@
  * Conventions shared by every entry point.
  *  - All pointers are DEVICE pointers owned by the caller; the library
  *    never allocates device memory (the prefill workspace is passed in) and
- *    keeps no global mutable state, with two exceptions: the fixed scratch
- *    array of kda_prefill_noalloc (below), and one extra stream and two
- *    events per GPU that kda_prefill creates on first use when it runs its
- *    two phases concurrently (below) and keeps until the process ends.
+ *    keeps no global mutable state, with three exceptions: the fixed scratch
+ *    array of kda_prefill_noalloc (below), one extra stream and two events
+ *    per GPU that kda_prefill creates on first use when it runs its two
+ *    phases concurrently (below) and keeps until the process ends, and each
+ *    GPU's count of compute units, asked for once.
  *    Calls are thread-safe.
  *  - Every call is asynchronous on `stream` (a hipStream_t; NULL = the null
  *    stream) and never synchronises.
@@ -354,10 +355,16 @@ size_t kda_scan_backward_workspace_size(int B, int T, int H, int D);
  *   chunk_states  [B,ceil(T/KDA_SCAN_CHUNK),H,D] fp32, or NULL: the state
  *            before each chunk of KDA_SCAN_CHUNK tokens, which
  *            kda_scan_backward takes in place of a recomputation
- * With a few tokens per sequence this is also the multi-token step.
+ * With a few tokens per sequence this is also the multi-token step; for many
+ * sequences (256 x 32 heads x 128) T calls of kda_scan_step take less time up
+ * to T = 14, as a chunk costs the same however few of its tokens there are.
  * Decays are composed in fp32: a product of gates under about 1e-38 counts as
  * 0, and a state that is infinite reads as infinite or NaN from then on
  * (0 * inf).
+ * Chunks of a sequence run side by side and wait for each other's result on
+ * the GPU.  Every such wait ends: after about a second, far more than a running
+ * GPU takes, it is given up and what depends on it is NaN (the call has returned
+ * KDA_OK by then, being asynchronous).  The same holds for the gradient.
  * Errors: KDA_EINVAL as elsewhere; KDA_EUNSUPPORTED for other D, dtype pairs,
  * T > 2^30, H*D > 2^22, or more than 2^23 - 1 tiles
  * B * ceil(T/128) * ceil(H*D/128). */
@@ -412,6 +419,10 @@ typedef enum kda_act {
  *                                                       row of zeros is NaN)
  *   o, z, y  [rows,D] in io_dtype, D in {16,32,64,128}; z NULL exactly when
  *            act is KDA_ACT_NONE; w [D] fp32; y must not alias an input
+ * The mean of squares is fp32 in this norm and those below: a row whose squares
+ * sum to more than 3.4e38 is scaled to zeros, and with eps = 0 one whose squares
+ * all vanish in fp32 to infinities.  z = -inf gives 0 with KDA_ACT_SIGMOID and
+ * NaN (-inf * 0) with KDA_ACT_SILU.
  * KDA_EUNSUPPORTED: other D, rows * D > 2^34. */
 kda_status kda_gated_norm(const void *o, const void *z, kda_dtype io_dtype,
                           const float *w, kda_act act, float eps, void *y,
