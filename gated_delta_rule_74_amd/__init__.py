@@ -13,6 +13,10 @@ Functions mirror the C entry points by name:
 and, from ``layer.py``, the operators around the mixer:
   kda_scan, kda_scan_backward, kda_scan_step, kda_gated_norm,
   kda_gated_norm_backward, kda_block_norm, kda_block_norm_backward
+and, from ``linattn.py``, linear attention with one decay per head and the norm
+and rotation of queries and keys:
+  kda_linattn, kda_linattn_backward, kda_linattn_step, kda_qk_norm_rope,
+  kda_qk_norm_rope_backward
 """
 from __future__ import annotations
 
@@ -468,3 +472,8 @@ from .layer import (  # noqa: E402  (needs the names above)
     kda_gated_norm_backward, kda_gated_norm_backward_workspace_size, kda_scan,
     kda_scan_backward, kda_scan_backward_workspace_size, kda_scan_step,
     kda_scan_workspace_size)
+from .linattn import (  # noqa: E402
+    KDA_GATE_FIXED, kda_linattn, kda_linattn_backward,
+    kda_linattn_backward_workspace_size, kda_linattn_step,
+    kda_linattn_workspace_size, kda_qk_norm_rope, kda_qk_norm_rope_backward,
+    kda_qk_norm_rope_backward_workspace_size)

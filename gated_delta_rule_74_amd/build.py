@@ -25,7 +25,11 @@ SOURCES = ["kda_api.hip", "kda_prep_f32.hip", "kda_prep_bf16_f32.hip",
            "kda_prep_bf16_bf16.hip", "kda_prep_gdn.hip", "kda_prep_d128.hip", "kda_state.hip", "kda_decode.hip",
            "kda_backward.hip",
            "kda_conv.hip", "kda_layer_api.hip", "kda_scan.hip",
-           "kda_norm.hip"]
+           "kda_norm.hip", "kda_qk_norm.hip", "kda_linattn_api.hip",
+           "kda_linattn.hip"]
+# linear attention: one file per dtype and rows' width, the longest first
+SOURCES = [f"kda_linattn_{t}_{d}.hip" for d in (128, 64, 32, 16)
+           for t in ("bf16", "f32")] + SOURCES
 ARCH = os.environ.get("KDA_OFFLOAD_ARCH", "gfx950")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -98,4 +98,32 @@ hipError_t launch_block_norm(const BlockNormParams &p, hipStream_t s);
 size_t block_norm_bwd_ws_bytes(int rows, int C);
 hipError_t launch_block_norm_backward(const BlockNormParams &p, hipStream_t s);
 
+// sums over n partial rows of part[row][stride], columns lo <= c < hi: column
+// c goes to out0[c], or from C on to out1[c - C]
+hipError_t launch_sum_rows(const float *part, long long stride, int n, int lo,
+                           int hi, int C, float *out0, float *out1,
+                           hipStream_t s);
+
+// norm and rotation of query and key heads (kda_qk_norm.hip)
+struct QkNormParams {
+  const void *q, *k;          // tokens q_stride, k_stride elements apart
+  long long q_stride, k_stride;
+  const float *wq, *wk;       // [D], or null: that side is not normed
+  const int *positions;       // [rows], or null with rot = 0
+  const float *inv_freq;      // [rot / 2]
+  int rot, interleaved, io_bf16;
+  float eps;
+  void *q_out, *k_out;        // forward outputs; backward: dq, dk
+  long long qo_stride, ko_stride;
+  const void *dq_out, *dk_out;  // backward inputs
+  long long dqo_stride, dko_stride;
+  float *dwq, *dwk;
+  long long rows;
+  int Hq, Hk, D;
+  float *ws;
+};
+hipError_t launch_qk_norm(const QkNormParams &p, hipStream_t s);
+size_t qk_norm_bwd_ws_bytes(long long rows, int Hq, int Hk, int D);
+hipError_t launch_qk_norm_backward(const QkNormParams &p, hipStream_t s);
+
 }  // namespace kda

@@ -5,8 +5,7 @@
 
 #include <math.h>
 
-#include <initializer_list>
-
+#include "kda_check.h"
 #include "kda_layer.h"
 
 static_assert(KDA_SCAN_CHUNK == kda::SCAN_L, "chunk of the scan");
@@ -15,45 +14,7 @@ static_assert((int)KDA_ACT_SIGMOID == kda::ACT_SIGMOID &&
 
 namespace {
 
-bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
-bool dim_ok(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
-bool dtype_valid(int d) { return d == KDA_F32 || d == KDA_BF16; }
-
-// the dtype pair (data, gate or stream), or -1
-int pair_of(int io, int other) {
-  if (io == KDA_F32) return other == KDA_F32 ? kda::PAIR_F32 : -1;
-  return other == KDA_F32 ? kda::PAIR_BF16_F32 : kda::PAIR_BF16_BF16;
-}
-
-kda_status hip_status(hipError_t e) {
-  if (e == hipSuccess) return KDA_OK;
-  (void)hipGetLastError();
-  return KDA_EHIP;
-}
-
-typedef std::initializer_list<const void *> Ptrs;
-
-bool all_set(Ptrs ps) {
-  for (const void *p : ps)
-    if (!p) return false;
-  return true;
-}
-bool all_aligned(Ptrs ps) {
-  for (const void *p : ps)
-    if (!aligned16(p)) return false;
-  return true;
-}
-// no output is an input or another output (NULLs aside)
-bool distinct(Ptrs outs, Ptrs ins) {
-  for (auto o = outs.begin(); o != outs.end(); ++o) {
-    if (!*o) continue;
-    for (const void *i : ins)
-      if (*o == i) return false;
-    for (auto q = o + 1; q != outs.end(); ++q)
-      if (*o == *q) return false;
-  }
-  return true;
-}
+using namespace kda::check;
 
 // sizes of the scan; KDA_OK, KDA_EINVAL or KDA_EUNSUPPORTED
 kda_status scan_sizes(int B, int T, int H, int D, int *NC) {

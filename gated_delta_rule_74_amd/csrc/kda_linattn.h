@@ -1,0 +1,106 @@
+// kda_linattn.h -- interface between the C boundary of linear attention with
+// one decay per head (kda_linattn_api.hip), its launch logic
+// (kda_linattn.hip) and the sweep kernels (kda_linattn_impl.h, one
+// instantiation file per dtype and size).  Not installed; not part of the ABI.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+
+namespace kda {
+
+struct LinParams {
+  const void *q, *k, *v, *g;
+  int io_bf16, gate_bf16, gate_fixed;
+  const float *s0;            // [B,H,Dk,Dv] or null
+  const int *lengths;         // [B] or null
+  void *o;                    // forward
+  float *s_out;               // or null
+  const void *dO;             // backward
+  const float *dsT;           // or null
+  void *dq, *dk, *dv, *dg;    // dg or null
+  float *ds0;                 // or null
+  int B, T, Hk, H, Dk, Dv;
+  float scale;
+  char *ws;
+};
+// segments of all heads, the larger of both passes' and dtypes'
+long long linattn_segments(int B, int T, int H);
+size_t linattn_ws_bytes(int B, int T, int H, int Dk, int Dv, int io_bf16);
+size_t linattn_bwd_ws_bytes(int B, int T, int Hk, int H, int Dk, int Dv,
+                            int io_bf16);
+hipError_t launch_linattn(const LinParams &p, hipStream_t s);
+hipError_t launch_linattn_backward(const LinParams &p, hipStream_t s);
+
+struct LinStepParams {
+  const void *q, *k, *v, *g;
+  int io_bf16, gate_bf16, gate_fixed;
+  float *state;
+  void *o;
+  int N, Hk, H, Dk, Dv;
+  float scale;
+};
+hipError_t launch_linattn_step(const LinStepParams &p, hipStream_t s);
+
+// What the sweep and the local pass share: where a sequence's tokens, gates
+// and segments are.
+struct LinSeq {
+  const void *g;
+  int gate_bf16, gate_fixed;
+  const int *lengths;
+  int B, T, H, G;             // G value heads share a query/key head
+  int NS, seg;                // segments per sequence, tokens per segment
+};
+
+// an operand [B,T,H,D], or [B,T,H/G,D] where its heads are shared
+struct LinOperand {
+  const void *p;
+  int shared;
+};
+
+// One sweep over every segment: out = causal map of (a, b, c) with the state
+// sum of b c^T (see kda_linattn_impl.h).
+struct LinSweep {
+  LinSeq q;
+  LinOperand a, b, c, d;      // [.., D1], [.., D1], [.., D2], [.., D2]
+  void *out;                  // [B,T,H,D2]
+  int out_f32;
+  float pair_scale, far_scale, add_scale;
+  const float *s_in;          // [B,H,NS,D1,D2] (transposed: D2,D1) or null
+  float *s_end;               // [B,H,D1,D2], of the last segment, or null
+  int s_transposed;           // s_in and e_with are [.., D2, D1]
+  float *far_dot;             // [B,H,T]: d . (out's part from the state)
+  float *pair_dot;            // [B,H,T]: the pairs across each token
+  const float *e_with;        // laid out as s_in, or null (zeros)
+  float *e_out;               // [B,H,NS]: <state behind the segment, e_with>
+};
+
+// the state that each segment adds to a zero one
+struct LinLocal {
+  LinSeq q;
+  LinOperand b, c;            // [.., D1], [.., D2]
+  float add_scale;
+  int rev;
+  float *s;                   // [B,H,NS,D1,D2]
+  float *decay;               // [B,H,NS]
+};
+
+// chunk of a sweep
+constexpr int lin_chunk(int io_bf16) { return io_bf16 ? 64 : 32; }
+
+// variants of a sweep
+enum LinDot { LIN_PLAIN = 0, LIN_FAR = 1, LIN_FAR_PAIRS = 2 };
+
+#define KDA_LIN_DECLARE(IO, D1)                                            \
+  hipError_t lin_sweep_##IO##_##D1(int D2, int rev, int dot,               \
+                                   const LinSweep &p, hipStream_t s);      \
+  hipError_t lin_local_##IO##_##D1(int D2, const LinLocal &p, hipStream_t s)
+KDA_LIN_DECLARE(bf16, 16);
+KDA_LIN_DECLARE(bf16, 32);
+KDA_LIN_DECLARE(bf16, 64);
+KDA_LIN_DECLARE(bf16, 128);
+KDA_LIN_DECLARE(f32, 16);
+KDA_LIN_DECLARE(f32, 32);
+KDA_LIN_DECLARE(f32, 64);
+KDA_LIN_DECLARE(f32, 128);
+
+}  // namespace kda

@@ -1,0 +1,496 @@
+// kda_linattn.hip -- linear attention with one decay per head (formulas in
+// include/kda.h): how the sweeps of kda_linattn_impl.h make up the forward
+// pass and the gradient, the small kernels between them, and the single-token
+// step.
+//
+// A sequence's chunks depend on each other through the state only, and the
+// state's map is S' = decay S + local.  Where there are fewer heads than the
+// GPU holds workgroups, sequences are cut into segments: a local pass makes
+// what each segment adds to a zero state, a scan over the segments makes the
+// state before each (after each, for gradients), and the sweeps run from
+// there.
+//
+// The gate's gradient is exp(g_t) <dS_t, S_{t-1}>: the sum over all pairs of a
+// token i >= t and a token j < t.  In chunks: both in t's chunk (made from
+// the products themselves, pair_dot), i alone (far_dot of dq's sweep, summed
+// from t on), j alone (far_dot of dk's, summed up to t), neither (Z).  With E
+// the sum over the pairs across a chunk's end, Z = E - sum of the chunk's
+// j-terms, and E across its start is Z + sum of its i-terms; E at a segment's
+// end is the product of both states there.  Where a chunk forgets all but
+// 2^-40, Z is 0.
+#include "kda_linattn.h"
+#include "kda_vec.h"
+
+namespace kda {
+namespace lin {
+
+constexpr size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+struct Split {
+  int NS, seg;
+};
+
+// Workgroups wanted, and the tokens that a segment has at least and (gradient)
+// at most: see the end of this file's launch logic.
+constexpr int WANTED = 512, MIN_CHUNKS = 4, MAX_CHUNKS = 64;
+
+Split split(int B, int T, int H, int io_bf16, bool grad) {
+  const int C = lin_chunk(io_bf16);
+  const int nc = (T + C - 1) / C;
+  const long long chains = (long long)B * H;
+  long long ns = (WANTED + chains - 1) / chains;
+  if (ns > nc / MIN_CHUNKS) ns = nc / MIN_CHUNKS;
+  if (ns < 1) ns = 1;
+  int per = (int)((nc + ns - 1) / ns);
+  if (grad && per > MAX_CHUNKS) per = MAX_CHUNKS;
+  return Split{(nc + per - 1) / per, per * C};
+}
+
+// ---------------------------------------------------------------------------
+// states before (after) every segment, from what each adds: the local sums are
+// replaced in place.  One thread has 4 elements of one head's states.
+
+struct ScanSegs {
+  float *s;                  // [BH,NS,n]
+  const float *decay;        // [BH,NS]
+  const float *first;        // [BH,n] or null
+  int rev;
+};
+__global__ __launch_bounds__(256) void kda_lin_scan(ScanSegs f, ScanSegs r,
+                                                    int NS, int n) {
+  const ScanSegs p = blockIdx.z ? r : f;
+  const int i = (blockIdx.y * 256 + threadIdx.x) * 4;
+  if (i >= n) return;
+  const size_t chain = blockIdx.x;
+  float *const s = p.s + chain * NS * n + i;
+  const float *const d = p.decay + chain * NS;
+  f32x4 S{0, 0, 0, 0};
+  if (p.first) S = *(const f32x4 *)(p.first + chain * n + i);
+  for (int k = 0; k < NS; ++k) {
+    const size_t at = p.rev ? NS - 1 - k : k;
+    if (k + 1 < NS) {
+      const f32x4 x = *(const f32x4 *)(s + at * n);
+      const float a = d[at];
+      *(f32x4 *)(s + at * n) = S;
+      S = S * a + x;
+    } else {
+      *(f32x4 *)(s + at * n) = S;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// the gate's gradient from its parts; one wave has one segment of one head
+
+struct GateGrad {
+  LinSeq q;
+  const float *late, *early, *pairs;  // [B,H,T]
+  const float *ends;                  // [B,H,NS]
+  void *dg;                           // [B,T,H] in the gate's type
+  double *sums;                       // [B,H,NS] instead, for a fixed decay
+};
+
+__global__ __launch_bounds__(64) void kda_lin_gate_grad(GateGrad p, int C) {
+  const LinSeq &q = p.q;
+  const int lane = threadIdx.x;
+  const int h = blockIdx.x % q.H, bs = blockIdx.x / q.H;
+  const int s = bs % q.NS, b = bs / q.NS;
+  const size_t chain = (size_t)b * q.H + h;
+  int len = q.T;
+  if (q.lengths) len = min(max(q.lengths[b], 0), q.T);
+  const int t_begin = s * q.seg, t_end = min(q.T, t_begin + q.seg);
+  const int live_end = min(len, t_end);
+  float E = p.ends[chain * q.NS + s];
+  double total = 0.0;
+  for (int t0 = t_begin + (t_end - t_begin - 1) / C * C; t0 >= t_begin;
+       t0 -= C) {
+    const int t = t0 + lane;
+    const bool in = lane < C && t < t_end, live = lane < C && t < live_end;
+    float late = 0.f, early = 0.f, pairs = 0.f, g = 0.f;
+    if (live) {
+      late = p.late[chain * q.T + t];
+      early = p.early[chain * q.T + t];
+      pairs = p.pairs[chain * q.T + t];
+      const size_t i = q.gate_fixed ? (size_t)h
+                                    : ((size_t)b * q.T + t) * q.H + h;
+      g = q.gate_bf16 ? (float)((const bf16 *)q.g)[i]
+                      : ((const float *)q.g)[i];
+    }
+    float x = late, y = early, G = g;  // from the token on; up to it; the chunk
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const float a = __shfl_down(x, d, 64), c = __shfl_up(y, d, 64);
+      if (lane + d < 64) x += a;
+      if (lane >= d) y += c;
+      G += __shfl_xor(G, d, 64);
+    }
+    const float sum_late = __shfl(x, 0, 64), sum_early = __shfl(y, 63, 64);
+    // exp(G) < 2^-40
+    const float Z = G < -27.7f ? 0.f : E - sum_early;
+    // a token that forgets everything has no gradient, whatever the sums say
+    const float up = __shfl_up(y, 1, 64);
+    float dg = pairs + x + (lane == 0 ? 0.f : up) + Z;
+    if (!live || g < -1e4f) dg = 0.f;
+    if (p.sums) {
+      total += dg;
+    } else if (in) {
+      const size_t i = ((size_t)b * q.T + t) * q.H + h;
+      if (q.gate_bf16) ((bf16 *)p.dg)[i] = (bf16)dg;
+      else ((float *)p.dg)[i] = dg;
+    }
+    E = Z + sum_late;
+  }
+  if (p.sums) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) total += __shfl_xor(total, d, 64);
+    if (lane == 0) p.sums[chain * q.NS + s] = total;
+  }
+}
+
+// the gradient of a decay that all tokens of a head share
+__global__ __launch_bounds__(256) void kda_lin_gate_sum(const double *sums,
+                                                        void *dg,
+                                                        int gate_bf16, int B,
+                                                        int H, int NS) {
+  const int h = blockIdx.x * 256 + threadIdx.x;
+  if (h >= H) return;
+  double x = 0.0;
+  for (int b = 0; b < B; ++b)
+    for (int s = 0; s < NS; ++s) x += sums[((size_t)b * H + h) * NS + s];
+  if (gate_bf16) ((bf16 *)dg)[h] = (bf16)(float)x;
+  else ((float *)dg)[h] = (float)x;
+}
+
+// ---------------------------------------------------------------------------
+// gradients of shared query and key heads: the sum over the value heads that
+// share one, in their order
+
+template <typename IO>
+__global__ __launch_bounds__(256) void kda_lin_heads(const float *x, IO *y,
+                                                     size_t n4, int D4,
+                                                     int G) {
+  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n4) return;
+  const f32x4 *v = (const f32x4 *)x + i / D4 * G * D4 + i % D4;
+  f32x4 s = v[0];
+  for (int k = 1; k < G; ++k) s += v[(size_t)k * D4];
+  if constexpr (sizeof(IO) == 2)
+    ((bf16x4 *)y)[i] = bf16x4{(bf16)s[0], (bf16)s[1], (bf16)s[2], (bf16)s[3]};
+  else
+    ((f32x4 *)y)[i] = s;
+}
+
+// ---------------------------------------------------------------------------
+// one token: S = exp(g) S + k v^T, o = scale S^T q.  The state is read and
+// written once and everything else is small.  A thread has 4 columns of every
+// R-th row of one head; the rows' sums meet in LDS.
+
+template <typename IO, int DK, int DV>
+__global__ __launch_bounds__(256) void kda_lin_step(LinStepParams p) {
+  constexpr int Q = DV / 4;                       // threads across a row
+  constexpr int PER = DK * DV / 4 < 256 ? DK * DV / 4 : 256;  // threads a head
+  constexpr int HPB = 256 / PER, R = PER / Q, N = DK / R;
+  __shared__ alignas(16) float sq[HPB][DK], sk[HPB][DK];
+  __shared__ f32x4 part[256];
+  const int tid = threadIdx.x, sub = tid / PER, th = tid % PER;
+  const size_t heads = (size_t)p.N * p.H;
+  const size_t head = (size_t)blockIdx.x * HPB + sub;
+  const bool on = head < heads;
+  const size_t n = head / p.H;
+  const int h = (int)(head % p.H);
+  const int c = th % Q, r = th / Q;
+  f32x4 S[N];
+  f32x4 v{0, 0, 0, 0};
+  float a = 0.f;
+  float *const st = p.state + head * DK * DV;
+  if (on) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      S[i] = ld_stream<f32x4>(st + (size_t)(r + i * R) * DV + c * 4);
+    const size_t hq = n * p.Hk + h / (p.H / p.Hk);
+    for (int i = th; i < DK; i += PER) {
+      sq[sub][i] = to_f32(((const IO *)p.q)[hq * DK + i]) * p.scale;
+      sk[sub][i] = to_f32(((const IO *)p.k)[hq * DK + i]);
+    }
+    const IO *pv = (const IO *)p.v + head * DV + c * 4;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = to_f32(pv[e]);
+    const size_t gi = p.gate_fixed ? (size_t)h : head;
+    a = expf(p.gate_bf16 ? (float)((const bf16 *)p.g)[gi]
+                         : ((const float *)p.g)[gi]);
+  }
+  __syncthreads();
+  f32x4 o{0, 0, 0, 0};
+  if (on) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int row = r + i * R;
+      const float k = sk[sub][row], q = sq[sub][row];
+      S[i] = S[i] * a + v * k;
+      o += S[i] * q;
+      st_stream(st + (size_t)row * DV + c * 4, S[i]);
+    }
+  }
+  part[tid] = o;
+  __syncthreads();
+  if (on && r == 0) {
+#pragma unroll
+    for (int i = 1; i < R; ++i) o += part[tid + i * Q];
+    IO *po = (IO *)p.o + head * DV + c * 4;
+    if constexpr (sizeof(IO) == 2)
+      *(bf16x4 *)po =
+          bf16x4{(bf16)o[0], (bf16)o[1], (bf16)o[2], (bf16)o[3]};
+    else
+      *(f32x4 *)po = o;
+  }
+}
+
+template <typename IO, int DK, int DV>
+hipError_t step(const LinStepParams &p, hipStream_t s) {
+  constexpr int PER = DK * DV / 4 < 256 ? DK * DV / 4 : 256;
+  constexpr int HPB = 256 / PER;
+  const size_t heads = (size_t)p.N * p.H;
+  kda_lin_step<IO, DK, DV><<<(unsigned)((heads + HPB - 1) / HPB), 256, 0, s>>>(
+      p);
+  return hipGetLastError();
+}
+template <typename IO, int DK>
+hipError_t step_dv(const LinStepParams &p, hipStream_t s) {
+  switch (p.Dv) {
+    case 16: return step<IO, DK, 16>(p, s);
+    case 32: return step<IO, DK, 32>(p, s);
+    case 64: return step<IO, DK, 64>(p, s);
+    case 128: return step<IO, DK, 128>(p, s);
+  }
+  return hipErrorInvalidValue;
+}
+template <typename IO>
+hipError_t step_dk(const LinStepParams &p, hipStream_t s) {
+  switch (p.Dk) {
+    case 16: return step_dv<IO, 16>(p, s);
+    case 32: return step_dv<IO, 32>(p, s);
+    case 64: return step_dv<IO, 64>(p, s);
+    case 128: return step_dv<IO, 128>(p, s);
+  }
+  return hipErrorInvalidValue;
+}
+
+// ---------------------------------------------------------------------------
+// launch logic
+
+hipError_t sweep(int io_bf16, int D1, int D2, int rev, int dot,
+                 const LinSweep &p, hipStream_t s) {
+  switch (D1) {
+    case 16: return io_bf16 ? lin_sweep_bf16_16(D2, rev, dot, p, s)
+                            : lin_sweep_f32_16(D2, rev, dot, p, s);
+    case 32: return io_bf16 ? lin_sweep_bf16_32(D2, rev, dot, p, s)
+                            : lin_sweep_f32_32(D2, rev, dot, p, s);
+    case 64: return io_bf16 ? lin_sweep_bf16_64(D2, rev, dot, p, s)
+                            : lin_sweep_f32_64(D2, rev, dot, p, s);
+    case 128: return io_bf16 ? lin_sweep_bf16_128(D2, rev, dot, p, s)
+                             : lin_sweep_f32_128(D2, rev, dot, p, s);
+  }
+  return hipErrorInvalidValue;
+}
+hipError_t local(int io_bf16, int D1, int D2, const LinLocal &p,
+                 hipStream_t s) {
+  switch (D1) {
+    case 16: return io_bf16 ? lin_local_bf16_16(D2, p, s)
+                            : lin_local_f32_16(D2, p, s);
+    case 32: return io_bf16 ? lin_local_bf16_32(D2, p, s)
+                            : lin_local_f32_32(D2, p, s);
+    case 64: return io_bf16 ? lin_local_bf16_64(D2, p, s)
+                            : lin_local_f32_64(D2, p, s);
+    case 128: return io_bf16 ? lin_local_bf16_128(D2, p, s)
+                             : lin_local_f32_128(D2, p, s);
+  }
+  return hipErrorInvalidValue;
+}
+
+LinSeq seq_of(const LinParams &p, Split sp) {
+  LinSeq q{};
+  q.g = p.g; q.gate_bf16 = p.gate_bf16; q.gate_fixed = p.gate_fixed;
+  q.lengths = p.lengths;
+  q.B = p.B; q.T = p.T; q.H = p.H; q.G = p.H / p.Hk;
+  q.NS = sp.NS; q.seg = sp.seg;
+  return q;
+}
+
+// the workspace, part by part
+struct Layout {
+  size_t s, ds, decay, ddecay, late, early, pairs, ends, sums, dq, dk, bytes;
+};
+Layout layout(int B, int T, int Hk, int H, int Dk, int Dv, Split sp,
+              bool grad) {
+  Layout l{};
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t r = at;
+    at += align256(n);
+    return r;
+  };
+  const size_t chains = (size_t)B * H, segs = chains * sp.NS;
+  const size_t states = sp.NS > 1 ? segs * Dk * Dv * 4 : 0;
+  const size_t rows = chains * T * 4;
+  l.s = take(states);
+  l.decay = take(segs * 4);
+  if (grad) {
+    l.ds = take(states);
+    l.ddecay = take(segs * 4);
+    l.late = take(rows);
+    l.early = take(rows);
+    l.pairs = take(rows);
+    l.ends = take(segs * 4);
+    l.sums = take(segs * 8);
+    const size_t part = H != Hk ? rows * Dk : 0;
+    l.dq = take(part);
+    l.dk = take(part);
+  }
+  l.bytes = at;
+  return l;
+}
+
+hipError_t scan_segments(const ScanSegs &f, const ScanSegs *r, int chains,
+                         int NS, int n, hipStream_t s) {
+  const dim3 grid(chains, (n + 1023) / 1024, r ? 2 : 1);
+  kda_lin_scan<<<grid, 256, 0, s>>>(f, r ? *r : f, NS, n);
+  return hipGetLastError();
+}
+
+}  // namespace lin
+
+long long linattn_segments(int B, int T, int H) {
+  long long most = 0;
+  for (int i = 0; i < 4; ++i) {
+    const lin::Split sp = lin::split(B, T, H, i & 1, i & 2);
+    const long long n = (long long)B * H * sp.NS;
+    most = n > most ? n : most;
+  }
+  return most;
+}
+size_t linattn_ws_bytes(int B, int T, int H, int Dk, int Dv, int io_bf16) {
+  return lin::layout(B, T, H, H, Dk, Dv, lin::split(B, T, H, io_bf16, false),
+                     false).bytes;
+}
+size_t linattn_bwd_ws_bytes(int B, int T, int Hk, int H, int Dk, int Dv,
+                            int io_bf16) {
+  return lin::layout(B, T, Hk, H, Dk, Dv, lin::split(B, T, H, io_bf16, true),
+                     true).bytes;
+}
+
+#define LIN_TRY(x)                      \
+  do {                                  \
+    const hipError_t e_ = (x);          \
+    if (e_ != hipSuccess) return e_;    \
+  } while (0)
+
+hipError_t launch_linattn(const LinParams &p, hipStream_t st) {
+  const lin::Split sp = lin::split(p.B, p.T, p.H, p.io_bf16, false);
+  const lin::Layout l =
+      lin::layout(p.B, p.T, p.Hk, p.H, p.Dk, p.Dv, sp, false);
+  const LinOperand q{p.q, 1}, k{p.k, 1}, v{p.v, 0};
+  LinSweep w{};
+  w.q = lin::seq_of(p, sp);
+  w.s_in = p.s0;
+  if (sp.NS > 1) {
+    float *const s = (float *)(p.ws + l.s);
+    LinLocal x{w.q, k, v, 1.f, 0, s, (float *)(p.ws + l.decay)};
+    LIN_TRY(lin::local(p.io_bf16, p.Dk, p.Dv, x, st));
+    const lin::ScanSegs f{s, x.decay, p.s0, 0};
+    LIN_TRY(lin::scan_segments(f, nullptr, p.B * p.H, sp.NS, p.Dk * p.Dv, st));
+    w.s_in = s;
+  }
+  w.a = q; w.b = k; w.c = v;
+  w.out = p.o;
+  w.pair_scale = w.far_scale = p.scale;
+  w.add_scale = 1.f;
+  w.s_end = p.s_out;
+  return lin::sweep(p.io_bf16, p.Dk, p.Dv, 0, LIN_PLAIN, w, st);
+}
+
+hipError_t launch_linattn_backward(const LinParams &p, hipStream_t st) {
+  const lin::Split sp = lin::split(p.B, p.T, p.H, p.io_bf16, true);
+  const lin::Layout l = lin::layout(p.B, p.T, p.Hk, p.H, p.Dk, p.Dv, sp, true);
+  const LinOperand q{p.q, 1}, k{p.k, 1}, v{p.v, 0}, dO{p.dO, 0};
+  const LinSeq seq = lin::seq_of(p, sp);
+  const float *s_in = p.s0, *ds_in = p.dsT;
+  if (sp.NS > 1) {
+    float *const s = (float *)(p.ws + l.s), *const ds = (float *)(p.ws + l.ds);
+    LinLocal x{seq, k, v, 1.f, 0, s, (float *)(p.ws + l.decay)};
+    LIN_TRY(lin::local(p.io_bf16, p.Dk, p.Dv, x, st));
+    LinLocal y{seq, q, dO, p.scale, 1, ds, (float *)(p.ws + l.ddecay)};
+    LIN_TRY(lin::local(p.io_bf16, p.Dk, p.Dv, y, st));
+    const lin::ScanSegs f{s, x.decay, p.s0, 0}, r{ds, y.decay, p.dsT, 1};
+    LIN_TRY(lin::scan_segments(f, &r, p.B * p.H, sp.NS, p.Dk * p.Dv, st));
+    s_in = s;
+    ds_in = ds;
+  }
+  const bool shared = p.H != p.Hk, gate = p.dg != nullptr;
+  LinSweep w{};
+  w.q = seq;
+  // dv
+  w.a = k; w.b = q; w.c = dO;
+  w.out = p.dv;
+  w.pair_scale = p.scale; w.far_scale = 1.f; w.add_scale = p.scale;
+  w.s_in = ds_in;
+  w.s_end = p.ds0;
+  LIN_TRY(lin::sweep(p.io_bf16, p.Dk, p.Dv, 1, LIN_PLAIN, w, st));
+  // dk
+  w.a = v; w.b = dO; w.c = q; w.d = k;
+  w.out = shared ? (void *)(p.ws + l.dk) : p.dk;
+  w.out_f32 = shared;
+  w.s_end = nullptr;
+  w.s_transposed = 1;
+  w.far_dot = (float *)(p.ws + l.early);
+  LIN_TRY(lin::sweep(p.io_bf16, p.Dv, p.Dk, 1, gate ? LIN_FAR : LIN_PLAIN, w,
+                     st));
+  // dq
+  w.a = dO; w.b = v; w.c = k; w.d = q;
+  w.out = shared ? (void *)(p.ws + l.dq) : p.dq;
+  w.far_scale = p.scale; w.add_scale = 1.f;
+  w.s_in = s_in;
+  w.e_with = ds_in;
+  w.far_dot = (float *)(p.ws + l.late);
+  w.pair_dot = (float *)(p.ws + l.pairs);
+  w.e_out = (float *)(p.ws + l.ends);
+  LIN_TRY(lin::sweep(p.io_bf16, p.Dv, p.Dk, 0,
+                     gate ? LIN_FAR_PAIRS : LIN_PLAIN, w, st));
+  if (shared) {
+    const size_t n4 = (size_t)p.B * p.T * p.Hk * p.Dk / 4;
+    const unsigned blocks = (unsigned)((n4 + 255) / 256);
+    for (int i = 0; i < 2; ++i) {
+      const float *x = (const float *)(p.ws + (i ? l.dk : l.dq));
+      void *y = i ? p.dk : p.dq;
+      if (p.io_bf16)
+        lin::kda_lin_heads<bf16><<<blocks, 256, 0, st>>>(x, (bf16 *)y, n4,
+                                                         p.Dk / 4, seq.G);
+      else
+        lin::kda_lin_heads<float><<<blocks, 256, 0, st>>>(x, (float *)y, n4,
+                                                          p.Dk / 4, seq.G);
+      LIN_TRY(hipGetLastError());
+    }
+  }
+  if (gate) {
+    double *const sums = (double *)(p.ws + l.sums);
+    lin::GateGrad x{seq, (const float *)(p.ws + l.late),
+                    (const float *)(p.ws + l.early),
+                    (const float *)(p.ws + l.pairs),
+                    (const float *)(p.ws + l.ends), p.dg,
+                    p.gate_fixed ? sums : nullptr};
+    const unsigned n = (unsigned)p.B * p.H * sp.NS;
+    lin::kda_lin_gate_grad<<<n, 64, 0, st>>>(x, lin_chunk(p.io_bf16));
+    LIN_TRY(hipGetLastError());
+    if (p.gate_fixed) {
+      lin::kda_lin_gate_sum<<<(p.H + 255) / 256, 256, 0, st>>>(
+          sums, p.dg, p.gate_bf16, p.B, p.H, sp.NS);
+      LIN_TRY(hipGetLastError());
+    }
+  }
+  return hipSuccess;
+}
+
+hipError_t launch_linattn_step(const LinStepParams &p, hipStream_t s) {
+  return p.io_bf16 ? lin::step_dk<bf16>(p, s) : lin::step_dk<float>(p, s);
+}
+
+}  // namespace kda

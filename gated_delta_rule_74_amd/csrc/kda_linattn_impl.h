@@ -1,0 +1,666 @@
+// kda_linattn_impl.h -- the sweep and the local pass of linear attention with
+// one decay per head (formulas in include/kda.h).
+//
+// Everything the operator computes over sequences is one map.  For tokens of
+// one head with rows a_i, b_i [D1], c_i [D2], log-decays g_i and a state
+// S [D1,D2] from before the first token, with G_i the sum of the log-decays
+// up to and including token i,
+//     out_i = sum_{j<=i} exp(G_i - G_j) (a_i . b_j) c_j + exp(G_i) S^T a_i
+//     S'    = exp(G_n) S + sum_j exp(G_n - G_j) b_j c_j^T
+// and the same from the other end (REV; sums over j >= i, exp(G_j - G_i), the
+// state from behind the last token, exp(G_n - G_i)).  Then
+//     o  is the map of (q, k, v),       dq that of (do, v, k),
+//     dv that of (k, q, do) reversed,   dk that of (v, do, q) reversed
+// with S transposed for dq and dk, and the scale put where it belongs.
+//
+// A workgroup takes one segment of one head, chunk by chunk, with the state in
+// registers: wave w owns 32 (or 16) columns of it, all D1 rows.  The pair
+// products of a chunk are made once, one 16-row tile a wave, and handed to all
+// waves through LDS as operand fragments; the state's accumulator tiles are
+// themselves the operand fragments of S^T a (kda_device.h), so it never
+// leaves its registers.
+//
+// Precision.  Decays between tokens are differences of sums held in 64 bits:
+// a sum over a chunk may reach 64e4 (g below -1e4 is taken as -1e4, whose exp
+// is 0) where fp32 differences would be off by 0.03.  With bf16 data the pair
+// products and the state are rounded to bf16 where they enter a product whose
+// result is rounded to bf16 itself (half a step each, as the result's own);
+// what ends up in fp32 (the state, and the dot products that the gate's
+// gradient is made of) takes the rounded-off rest as a second operand, which
+// leaves 2^-18.
+#pragma once
+#include "kda_device.h"
+#include "kda_linattn.h"
+
+namespace kda {
+namespace lin {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+// ---------------------------------------------------------------------------
+// fragments from LDS tiles [token][channel], 16 bytes of padding per row
+
+template <typename IO> constexpr int pad() { return 16 / (int)sizeof(IO); }
+
+// rows as operand rows (k = channels): row `row` + m, unit u
+template <typename IO, int D>
+__device__ __forceinline__ typename Mma<IO>::frag frag_row(const IO *t,
+                                                           int row, int u,
+                                                           int g, int m) {
+  constexpr int STR = D + pad<IO>();
+  constexpr int K = sizeof(IO) == 2 ? 32 : 16;
+  return Mma<IO>::load_k(t + (row + m) * STR + u * K, g, D > 16);
+}
+
+// channels as operand rows (k = tokens): channels col..col+15, tokens of unit
+// u.  bf16: a 4 x 16 block of tokens x channels is transposed on the way by
+// the LDS (each lane names 4 channels of one token and receives 4 tokens of
+// one channel).
+template <int STR>
+__device__ __forceinline__ bf16x8 frag_col(const bf16 *t, int col, int u,
+                                           int g, int m) {
+  const bf16 *p = t + (32 * u + 4 * g + (m >> 2)) * STR + col + (m & 3) * 4;
+  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
+  const s16x4 hi =
+      __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 16 * STR));
+  typedef short s16x8 __attribute__((ext_vector_type(8)));
+  return __builtin_bit_cast(
+      bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+template <int STR>
+__device__ __forceinline__ f32x4 frag_col(const float *t, int col, int u,
+                                          int g, int m) {
+  const float *p = t + (16 * u + 4 * g) * STR + col + m;
+  return f32x4{p[0], p[STR], p[2 * STR], p[3 * STR]};
+}
+
+// a fragment's weights: w[k] for its elements
+__device__ __forceinline__ void weights(const float *w, int u, int g,
+                                        float (&r)[8]) {
+  const f32x4 lo = *(const f32x4 *)(w + 32 * u + 4 * g);
+  const f32x4 hi = *(const f32x4 *)(w + 32 * u + 16 + 4 * g);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) r[e] = lo[e], r[4 + e] = hi[e];
+}
+__device__ __forceinline__ void weights(const float *w, int u, int g,
+                                        float (&r)[4]) {
+  const f32x4 lo = *(const f32x4 *)(w + 16 * u + 4 * g);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) r[e] = lo[e];
+}
+
+// ---------------------------------------------------------------------------
+// a chunk's rows on their way from memory to LDS
+
+template <typename IO, int D, int C, int NT> struct Rows {
+  static constexpr int UPR = D * (int)sizeof(IO) / 16;  // 16-byte units a row
+  static constexpr int N = (C * UPR + NT - 1) / NT;
+  uint4 r[N];
+  // rows from `live` on are zeros
+  __device__ __forceinline__ void fetch(const char *p, size_t stride,
+                                        int live) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int i = threadIdx.x + n * NT, row = i / UPR, col = i % UPR;
+      r[n] = uint4{0, 0, 0, 0};
+      if (row < live && row < C)
+        r[n] = *(const uint4 *)(p + row * stride + col * 16);
+    }
+  }
+  __device__ __forceinline__ void stash(IO *t) const {
+    constexpr int STR = D + pad<IO>();
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int i = threadIdx.x + n * NT, row = i / UPR, col = i % UPR;
+      if (i < C * UPR)
+        *(uint4 *)(t + row * STR + col * (16 / (int)sizeof(IO))) = r[n];
+    }
+  }
+};
+
+// where token 0 of sequence b, head h of an operand is, and the bytes from
+// token to token
+template <typename IO, int D>
+__device__ __forceinline__ const char *operand(const LinOperand &o,
+                                               const LinSeq &q, int b, int h,
+                                               size_t &stride) {
+  const int nh = o.shared ? q.H / q.G : q.H, hh = o.shared ? h / q.G : h;
+  stride = (size_t)nh * D * sizeof(IO);
+  return (const char *)o.p + ((size_t)b * q.T * nh + hh) * D * sizeof(IO);
+}
+
+// ---------------------------------------------------------------------------
+// a chunk's decays
+
+template <int C> struct Decays {
+  double G[C];                   // log2 of the decay up to and with a token
+  alignas(16) float first[C];    // exp(G_i), what the chunk's start reaches
+  alignas(16) float last[C];     // exp(G_C - G_i), what reaches its end
+  float total;                   // exp(G_C)
+};
+
+__device__ __forceinline__ float exp2_diff(double d) {
+  return __builtin_amdgcn_exp2f((float)d);
+}
+
+__device__ __forceinline__ float load_gate(const LinSeq &q, int b, int h,
+                                           int t) {
+  const size_t i = q.gate_fixed ? (size_t)h
+                                : ((size_t)b * q.T + t) * q.H + h;
+  return q.gate_bf16 ? (float)((const bf16 *)q.g)[i] : ((const float *)q.g)[i];
+}
+
+// by one wave: g the log-decay of token `lane` (0 past the end)
+template <int C>
+__device__ __forceinline__ double decays(Decays<C> &s, float g, float fs,
+                                         float ls, int lane) {
+  g = g < -1e4f ? -1e4f : g;
+  double x = lane < C ? (double)g * 1.4426950408889634074 : 0.0;
+#pragma unroll
+  for (int d = 1; d < C; d *= 2) {
+    const double y = __shfl_up(x, d, 64);
+    if (lane >= d) x += y;
+  }
+  const double end = __shfl(x, C - 1, 64);
+  if (lane < C) {
+    s.G[lane] = x;
+    s.first[lane] = fs * exp2_diff(x);
+    s.last[lane] = ls * exp2_diff(end - x);
+  }
+  if (lane == 0) s.total = exp2_diff(end);
+  return end;
+}
+
+// ---------------------------------------------------------------------------
+// S = total S + b^T diag(w) c over a chunk; the wave's columns start at `col`
+
+template <typename IO, int D1, int D2, int CT, int C>
+__device__ __forceinline__ void add_chunk(f32x4 (&S)[D1 / 16][CT],
+                                          const IO *tb, const IO *tc,
+                                          const float *w, float total,
+                                          int col, int g, int m) {
+  constexpr int KU = sizeof(IO) == 2 ? 32 : 16;
+  constexpr int NE = Mma<IO>::NE;
+  constexpr int S1 = D1 + pad<IO>(), S2 = D2 + pad<IO>();
+  typedef typename Mma<IO>::frag frag;
+#pragma unroll
+  for (int kt = 0; kt < D1 / 16; ++kt)
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) S[kt][ct] *= total;
+#pragma unroll
+  for (int u = 0; u < C / KU; ++u) {
+    float wt[NE];
+    weights(w, u, g, wt);
+    frag hi[CT], lo[CT];
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+      const frag c = frag_col<S2>(tc, col + ct * 16, u, g, m);
+#pragma unroll
+      for (int e = 0; e < NE; ++e) {
+        const float x = Mma<IO>::elem(c, e) * wt[e];
+        Mma<IO>::set(hi[ct], e, x);
+        if constexpr (sizeof(IO) == 2)
+          Mma<IO>::set(lo[ct], e, x - Mma<IO>::elem(hi[ct], e));
+      }
+    }
+#pragma unroll
+    for (int kt = 0; kt < D1 / 16; ++kt) {
+      const frag b = frag_col<S1>(tb, kt * 16, u, g, m);
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+        S[kt][ct] = Mma<IO>::mma(b, hi[ct], S[kt][ct]);
+        if constexpr (sizeof(IO) == 2)
+          S[kt][ct] = Mma<IO>::mma(b, lo[ct], S[kt][ct]);
+      }
+    }
+  }
+}
+
+// waves of a workgroup and columns a wave owns
+template <int D2> constexpr int nwaves() {
+  return D2 >= 64 ? 4 : D2 / 16;
+}
+
+// ---------------------------------------------------------------------------
+// the sweep
+
+template <typename IO, int D1, int D2, bool REV, int DOT>
+__global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
+    LinSweep p) {
+  constexpr int C = lin_chunk(sizeof(IO) == 2), NB = C / 16;
+  constexpr int NW = nwaves<D2>(), NT = 64 * NW;
+  constexpr int CT = D2 / 16 / NW, CW = CT * 16;
+  constexpr int TPU = Mma<IO>::TPU, KU = 16 * TPU, NE = Mma<IO>::NE;
+  constexpr int KT = D1 / 16, NKU = (KT + TPU - 1) / TPU;  // units over D1
+  constexpr int NDU = (D2 / 16 + TPU - 1) / TPU;           // units over D2
+  constexpr int NTU = C / KU;                              // units over tokens
+  constexpr int S1 = D1 + pad<IO>(), S2 = D2 + pad<IO>();
+  typedef typename Mma<IO>::frag frag;
+  __shared__ alignas(16) IO ta[C * S1], tb[C * S1], tc[C * S2];
+  __shared__ alignas(16) IO td[DOT ? C * S2 : 8];
+  __shared__ alignas(16) frag tp[NB * NTU * 64];
+  __shared__ Decays<C> dec;
+  __shared__ float far_part[DOT ? NW : 1][DOT ? C : 1];
+  __shared__ float pair_part[DOT == LIN_FAR_PAIRS ? NB : 1]
+                            [DOT == LIN_FAR_PAIRS ? C : 1];
+
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int g = lane >> 4, m = lane & 15;
+  const LinSeq &q = p.q;
+  const int h = blockIdx.x % q.H, bs = blockIdx.x / q.H;
+  const int s = bs % q.NS, b = bs / q.NS;
+  const size_t chain = (size_t)b * q.H + h;
+  int len = q.T;
+  if (q.lengths) len = min(max(q.lengths[b], 0), q.T);
+  const int t_begin = s * q.seg;
+  const int t_end = min(q.T, t_begin + q.seg);  // of the segment, dead or not
+  const int live_end = min(len, t_end);
+  const int nch = live_end > t_begin ? (live_end - t_begin + C - 1) / C : 0;
+
+  // out of dead tokens is zero
+  IO *const out = (IO *)p.out;
+  float *const out32 = (float *)p.out;
+  {
+    const int t0 = t_begin + nch * C;
+    const long long n = (long long)(t_end - t0) * (D2 / 8);
+    for (long long i = threadIdx.x; i < n; i += NT) {
+      const size_t at = (((size_t)b * q.T + t0 + i / (D2 / 8)) * q.H + h) * D2 +
+                        i % (D2 / 8) * 8;
+#pragma unroll
+      for (int e = 0; e < 8; e += 4) {
+        if (p.out_f32) *(f32x4 *)(out32 + at + e) = f32x4{0, 0, 0, 0};
+        else if constexpr (sizeof(IO) == 2)
+          *(uint2 *)(out + at + e) = uint2{0, 0};
+        else *(f32x4 *)(out + at + e) = f32x4{0, 0, 0, 0};
+      }
+    }
+  }
+
+  // the state's columns of this wave
+  f32x4 S[KT][CT];
+  const size_t s_at = (chain * q.NS + s) * D1 * D2;
+#pragma unroll
+  for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+      const int row = kt * 16 + 4 * g, col = w * CW + ct * 16 + m;
+      S[kt][ct] = f32x4{0, 0, 0, 0};
+      if (p.s_in) {
+        if (p.s_transposed)
+          S[kt][ct] = *(const f32x4 *)(p.s_in + s_at + (size_t)col * D1 + row);
+        else
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            S[kt][ct][e] = p.s_in[s_at + (size_t)(row + e) * D2 + col];
+      }
+    }
+
+  size_t sa, sb, sc, sd = 0;
+  const char *pa = operand<IO, D1>(p.a, q, b, h, sa);
+  const char *pb = operand<IO, D1>(p.b, q, b, h, sb);
+  const char *pc = operand<IO, D2>(p.c, q, b, h, sc);
+  const char *pd = nullptr;
+  if constexpr (DOT) pd = operand<IO, D2>(p.d, q, b, h, sd);
+  Rows<IO, D1, C, NT> ra, rb;
+  Rows<IO, D2, C, NT> rc, rd;
+  float gate = 0.f;
+  auto fetch = [&](int t0) {
+    const int live = live_end - t0;
+    ra.fetch(pa + (size_t)t0 * sa, sa, live);
+    rb.fetch(pb + (size_t)t0 * sb, sb, live);
+    rc.fetch(pc + (size_t)t0 * sc, sc, live);
+    if constexpr (DOT) rd.fetch(pd + (size_t)t0 * sd, sd, live);
+    if (w == 0)
+      gate = lane < C && lane < live ? load_gate(q, b, h, t0 + lane) : 0.f;
+  };
+  const bool last_seg = REV ? s == 0 : s == q.NS - 1;
+  const bool keep_end = (last_seg && p.s_end) || DOT == LIN_FAR_PAIRS;
+
+  if (nch > 0) fetch(t_begin + (REV ? nch - 1 : 0) * C);
+  for (int n = 0; n < nch; ++n) {
+    const int t0 = t_begin + (REV ? nch - 1 - n : n) * C;
+    ra.stash(ta);
+    rb.stash(tb);
+    rc.stash(tc);
+    if constexpr (DOT) rd.stash(td);
+    if (w == 0)
+      decays<C>(dec, gate, REV ? p.add_scale : p.far_scale,
+                REV ? p.far_scale : p.add_scale, lane);
+    __syncthreads();
+    if (n + 1 < nch) fetch(REV ? t0 - C : t0 + C);
+    const float *const far_w = REV ? dec.last : dec.first;
+    const float *const add_w = REV ? dec.first : dec.last;
+
+    // the pair products, transposed: rows j, columns i = rt * 16 + m
+    for (int rt = w; rt < NB; rt += NW) {
+      frag fa[NKU];
+#pragma unroll
+      for (int u = 0; u < NKU; ++u)
+        fa[u] = frag_row<IO, D1>(ta, rt * 16, u, g, m);
+      const int i = rt * 16 + m;
+      const double Gi = dec.G[i];
+      float run = 0.f;  // pairs of i with earlier tiles' j
+#pragma unroll
+      for (int u2 = 0; u2 < NTU; ++u2) {
+        if (REV ? u2 * TPU + TPU - 1 < rt : u2 * TPU > rt) continue;
+        f32x4 tile[2];
+        tile[0] = tile[1] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int x = 0; x < TPU; ++x) {
+          const int jt = u2 * TPU + x;
+          if (REV ? jt < rt : jt > rt) continue;
+          f32x4 acc{0, 0, 0, 0};
+#pragma unroll
+          for (int u = 0; u < NKU; ++u)
+            acc = Mma<IO>::mma(frag_row<IO, D1>(tb, jt * 16, u, g, m), fa[u],
+                               acc);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = jt * 16 + 4 * g + e;
+            const double d = REV ? dec.G[j] - Gi : Gi - dec.G[j];
+            const float f = acc[e] * (p.pair_scale * exp2_diff(d));
+            acc[e] = (REV ? j >= i : j <= i) ? f : 0.f;
+          }
+          tile[x] = acc;
+          if constexpr (DOT == LIN_FAR_PAIRS) {
+            // pairs (i, t') with t' < j, summed over i >= j
+            f32x4 qk{0, 0, 0, 0};
+#pragma unroll
+            for (int u = 0; u < NDU; ++u)
+              qk = Mma<IO>::mma(frag_row<IO, D2>(tc, jt * 16, u, g, m),
+                                frag_row<IO, D2>(td, rt * 16, u, g, m), qk);
+            qk *= acc;
+            const float tot = (qk[0] + qk[1]) + (qk[2] + qk[3]);
+            const float v1 = __shfl_up(tot, 16, 64);
+            const float v2 = __shfl_up(tot, 32, 64);
+            const float v3 = __shfl_up(tot, 48, 64);
+            float pre = run;
+            if (g >= 3) pre += v3;
+            if (g >= 2) pre += v2;
+            if (g >= 1) pre += v1;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int j = jt * 16 + 4 * g + e;
+              const float v = group_sum<16>(j <= i ? pre : 0.f);
+              if (m == 0) pair_part[rt][j] = v;
+              pre += qk[e];
+            }
+            run = __shfl(pre, 48 + m, 64);
+          }
+        }
+        tp[(rt * NTU + u2) * 64 + lane] = Mma<IO>::pack(tile[0], tile[1]);
+      }
+    }
+
+    // the state as operand fragments
+    frag fs[NKU][CT], fl[DOT && NE == 8 ? NKU : 1][CT];
+#pragma unroll
+    for (int u = 0; u < NKU; ++u)
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+        const f32x4 x = S[u * TPU][ct];
+        const f32x4 y = TPU == 2 && u * TPU + 1 < KT ? S[u * TPU + 1][ct]
+                                                     : f32x4{0, 0, 0, 0};
+        const frag f = Mma<IO>::pack(x, y);
+        fs[u][ct] = f;
+        if constexpr (DOT && NE == 8) {
+          f32x4 x2, y2;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x2[e] = x[e] - Mma<IO>::elem(f, e);
+            y2[e] = y[e] - Mma<IO>::elem(f, 4 + e);
+          }
+          fl[u][ct] = Mma<IO>::pack(x2, y2);
+        }
+      }
+    __syncthreads();
+
+    // out, transposed: rows are this wave's columns of c, columns tokens
+    frag fc[NTU][CT];
+#pragma unroll
+    for (int u = 0; u < NTU; ++u)
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct)
+        fc[u][ct] = frag_col<S2>(tc, w * CW + ct * 16, u, g, m);
+#pragma unroll
+    for (int rt = 0; rt < NB; ++rt) {
+      f32x4 acc[CT];
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) acc[ct] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int u = 0; u < NKU; ++u) {
+        const frag f = frag_row<IO, D1>(ta, rt * 16, u, g, m);
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+          acc[ct] = Mma<IO>::mma(fs[u][ct], f, acc[ct]);
+          if constexpr (DOT && NE == 8)
+            acc[ct] = Mma<IO>::mma(fl[u][ct], f, acc[ct]);
+        }
+      }
+      const float fw = far_w[rt * 16 + m];
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) acc[ct] *= fw;
+      if constexpr (DOT) {
+        float dot = 0.f;
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+          const IO *x = td + (rt * 16 + m) * S2 + w * CW + ct * 16 + 4 * g;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) dot += acc[ct][e] * to_f32(x[e]);
+        }
+        dot += __shfl_xor(dot, 16, 64);
+        dot += __shfl_xor(dot, 32, 64);
+        if (g == 0) far_part[w][rt * 16 + m] = dot;
+      }
+#pragma unroll
+      for (int u = 0; u < NTU; ++u) {
+        if (REV ? u * TPU + TPU - 1 < rt : u * TPU > rt) continue;
+        const frag f = tp[(rt * NTU + u) * 64 + lane];
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+          acc[ct] = Mma<IO>::mma(fc[u][ct], f, acc[ct]);
+      }
+      const int t = t0 + rt * 16 + m;
+      if (t < t_end) {
+        const size_t at = (((size_t)b * q.T + t) * q.H + h) * D2 + w * CW +
+                          4 * g;
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+          const f32x4 v = t < live_end ? acc[ct] : f32x4{0, 0, 0, 0};
+          if constexpr (sizeof(IO) == 2) {
+            if (p.out_f32) *(f32x4 *)(out32 + at + ct * 16) = v;
+            else
+              *(bf16x4 *)(out + at + ct * 16) =
+                  bf16x4{(bf16)v[0], (bf16)v[1], (bf16)v[2], (bf16)v[3]};
+          } else {
+            *(f32x4 *)(out + at + ct * 16) = v;
+          }
+        }
+      }
+    }
+    if (n + 1 < nch || keep_end)
+      add_chunk<IO, D1, D2, CT, C>(S, tb, tc, add_w, dec.total, w * CW, g, m);
+    __syncthreads();
+    if constexpr (DOT) {
+      const int t = t0 + threadIdx.x;
+      if (threadIdx.x < C && t < t_end) {
+        float x = 0.f;
+#pragma unroll
+        for (int i = 0; i < NW; ++i) x += far_part[i][threadIdx.x];
+        p.far_dot[chain * q.T + t] = x;
+        if constexpr (DOT == LIN_FAR_PAIRS) {
+          float y = 0.f;
+          for (int rt = threadIdx.x / 16; rt < NB; ++rt)
+            y += pair_part[rt][threadIdx.x];
+          p.pair_dot[chain * q.T + t] = y;
+        }
+      }
+    }
+  }
+
+  if (last_seg && p.s_end) {
+    float *const e = p.s_end + chain * D1 * D2;
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          e[(size_t)(kt * 16 + 4 * g + x) * D2 + w * CW + ct * 16 + m] =
+              S[kt][ct][x];
+  }
+  if constexpr (DOT == LIN_FAR_PAIRS) {
+    float x = 0.f;
+    if (p.e_with) {
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+          const int row = kt * 16 + 4 * g, col = w * CW + ct * 16 + m;
+          const f32x4 y =
+              *(const f32x4 *)(p.e_with + s_at + (size_t)col * D1 + row);
+          x += (S[kt][ct][0] * y[0] + S[kt][ct][1] * y[1]) +
+               (S[kt][ct][2] * y[2] + S[kt][ct][3] * y[3]);
+        }
+    }
+    x = group_sum<32>(x);
+    x += __shfl_xor(x, 32, 64);
+    __syncthreads();
+    if (lane == 0) far_part[w][0] = x;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      float y = 0.f;
+      for (int i = 0; i < NW; ++i) y += far_part[i][0];
+      p.e_out[chain * q.NS + s] = y;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// what a segment adds to a zero state, and its decay; the segment that no
+// other follows is left out
+
+template <typename IO, int D1, int D2>
+__global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_local(
+    LinLocal p) {
+  constexpr int C = lin_chunk(sizeof(IO) == 2);
+  constexpr int NW = nwaves<D2>(), NT = 64 * NW;
+  constexpr int CT = D2 / 16 / NW, CW = CT * 16, KT = D1 / 16;
+  constexpr int S1 = D1 + pad<IO>(), S2 = D2 + pad<IO>();
+  __shared__ alignas(16) IO tb[C * S1], tc[C * S2];
+  __shared__ Decays<C> dec;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int g = lane >> 4, m = lane & 15;
+  const LinSeq &q = p.q;
+  const int h = blockIdx.x % q.H, bs = blockIdx.x / q.H;
+  const int s = bs % (q.NS - 1) + p.rev, b = bs / (q.NS - 1);
+  const size_t chain = (size_t)b * q.H + h;
+  int len = q.T;
+  if (q.lengths) len = min(max(q.lengths[b], 0), q.T);
+  const int t_begin = s * q.seg;
+  const int live_end = min(len, min(q.T, t_begin + q.seg));
+  const int nch = live_end > t_begin ? (live_end - t_begin + C - 1) / C : 0;
+
+  f32x4 S[KT][CT];
+#pragma unroll
+  for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) S[kt][ct] = f32x4{0, 0, 0, 0};
+  size_t sb, sc;
+  const char *pb = operand<IO, D1>(p.b, q, b, h, sb);
+  const char *pc = operand<IO, D2>(p.c, q, b, h, sc);
+  Rows<IO, D1, C, NT> rb;
+  Rows<IO, D2, C, NT> rc;
+  float gate = 0.f;
+  double sum = 0.0;
+  auto fetch = [&](int t0) {
+    const int live = live_end - t0;
+    rb.fetch(pb + (size_t)t0 * sb, sb, live);
+    rc.fetch(pc + (size_t)t0 * sc, sc, live);
+    if (w == 0)
+      gate = lane < C && lane < live ? load_gate(q, b, h, t0 + lane) : 0.f;
+  };
+  if (nch > 0) fetch(t_begin + (p.rev ? nch - 1 : 0) * C);
+  for (int n = 0; n < nch; ++n) {
+    const int t0 = t_begin + (p.rev ? nch - 1 - n : n) * C;
+    rb.stash(tb);
+    rc.stash(tc);
+    if (w == 0) sum += decays<C>(dec, gate, p.add_scale, p.add_scale, lane);
+    __syncthreads();
+    if (n + 1 < nch) fetch(p.rev ? t0 - C : t0 + C);
+    add_chunk<IO, D1, D2, CT, C>(S, tb, tc, p.rev ? dec.first : dec.last,
+                                 dec.total, w * CW, g, m);
+    __syncthreads();
+  }
+  float *const o = p.s + (chain * q.NS + s) * D1 * D2;
+#pragma unroll
+  for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        o[(size_t)(kt * 16 + 4 * g + x) * D2 + w * CW + ct * 16 + m] =
+            S[kt][ct][x];
+  if (threadIdx.x == 0) p.decay[chain * q.NS + s] = exp2_diff(sum);
+}
+
+// ---------------------------------------------------------------------------
+// dispatch
+
+template <typename IO, int D1, int D2, bool REV, int DOT>
+hipError_t sweep_launch(const LinSweep &p, hipStream_t s) {
+  const unsigned n = (unsigned)p.q.B * p.q.H * p.q.NS;
+  kda_lin_sweep<IO, D1, D2, REV, DOT>
+      <<<n, 64 * nwaves<D2>(), 0, s>>>(p);
+  return hipGetLastError();
+}
+template <typename IO, int D1, int D2>
+hipError_t sweep_d2(int rev, int dot, const LinSweep &p, hipStream_t s) {
+  if (rev)
+    return dot == LIN_PLAIN ? sweep_launch<IO, D1, D2, true, LIN_PLAIN>(p, s)
+                            : sweep_launch<IO, D1, D2, true, LIN_FAR>(p, s);
+  return dot == LIN_PLAIN
+             ? sweep_launch<IO, D1, D2, false, LIN_PLAIN>(p, s)
+             : sweep_launch<IO, D1, D2, false, LIN_FAR_PAIRS>(p, s);
+}
+template <typename IO, int D1>
+hipError_t sweep(int D2, int rev, int dot, const LinSweep &p, hipStream_t s) {
+  switch (D2) {
+    case 16: return sweep_d2<IO, D1, 16>(rev, dot, p, s);
+    case 32: return sweep_d2<IO, D1, 32>(rev, dot, p, s);
+    case 64: return sweep_d2<IO, D1, 64>(rev, dot, p, s);
+    case 128: return sweep_d2<IO, D1, 128>(rev, dot, p, s);
+  }
+  return hipErrorInvalidValue;
+}
+template <typename IO, int D1, int D2>
+hipError_t local_d2(const LinLocal &p, hipStream_t s) {
+  const unsigned n = (unsigned)p.q.B * p.q.H * (p.q.NS - 1);
+  kda_lin_local<IO, D1, D2><<<n, 64 * nwaves<D2>(), 0, s>>>(p);
+  return hipGetLastError();
+}
+template <typename IO, int D1>
+hipError_t local(int D2, const LinLocal &p, hipStream_t s) {
+  switch (D2) {
+    case 16: return local_d2<IO, D1, 16>(p, s);
+    case 32: return local_d2<IO, D1, 32>(p, s);
+    case 64: return local_d2<IO, D1, 64>(p, s);
+    case 128: return local_d2<IO, D1, 128>(p, s);
+  }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace lin
+
+#define KDA_LIN_DEFINE(IO, TYPE, D1)                                       \
+  hipError_t lin_sweep_##IO##_##D1(int D2, int rev, int dot,               \
+                                   const LinSweep &p, hipStream_t s) {     \
+    return lin::sweep<TYPE, D1>(D2, rev, dot, p, s);                       \
+  }                                                                        \
+  hipError_t lin_local_##IO##_##D1(int D2, const LinLocal &p,              \
+                                   hipStream_t s) {                        \
+    return lin::local<TYPE, D1>(D2, p, s);                                 \
+  }
+
+}  // namespace kda

@@ -205,6 +205,16 @@ __global__ __launch_bounds__(SUM_COLS * SUM_LANES) void kda_sum_rows(
   }
 }
 
+hipError_t launch_sum_rows(const float *part, long long stride, int n, int lo,
+                           int hi, int C, float *out0, float *out1,
+                           hipStream_t s) {
+  hipLaunchKernelGGL(kda_sum_rows,
+                     dim3((hi - lo + SUM_COLS - 1) / SUM_COLS),
+                     dim3(SUM_COLS * SUM_LANES), 0, s, part, stride, n, lo, hi,
+                     C, out0, out1);
+  return hipGetLastError();
+}
+
 static int gn_groups(long long rows, int D) {
   const long long rpw = GN_THREADS / (D / 8);
   const long long n = (rows + rpw - 1) / rpw;

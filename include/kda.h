@@ -93,7 +93,10 @@ typedef enum kda_dtype {
    * what KDA refines into one coefficient per state row.  The result is
    * exactly that of the per-channel gate with g repeated over d_k; only g's
    * traffic shrinks (d_k-fold). */
-  KDA_GATE_HEAD = 16
+  KDA_GATE_HEAD = 16,
+  /* Flag for the gate_dtype of kda_linattn and its relatives only: g then
+   * holds one log-decay per head, [H], that every token shares. */
+  KDA_GATE_FIXED = 32
 } kda_dtype;
 
 /* beta ([LQNN-A] configuration checks): the model keeps beta in (0,1) so
@@ -474,6 +477,130 @@ kda_status kda_block_norm_backward(
     const void *dx, const void *dr_out, void *dy, void *dr, void *dz,
     float *dw_post, float *dw_pre, int rows, int C, void *workspace,
     size_t workspace_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Linear attention with one decay per head, the sibling of the mixer without
+ * the delta rule, and what makes its queries and keys.  The conventions of the
+ * operators above hold (dtype pairs, fp32 states and sums, results that are the
+ * same from call to call). */
+
+/* Bytes of device workspace kda_linattn and kda_linattn_backward need (0 if the
+ * sizes are invalid or unsupported, at least 256 otherwise); contents need no
+ * initialisation.  Calls that may overlap in time need workspaces of their
+ * own. */
+size_t kda_linattn_workspace_size(int B, int T, int Hk, int H, int Dk, int Dv,
+                                  kda_dtype qkv_dtype);
+size_t kda_linattn_backward_workspace_size(int B, int T, int Hk, int H, int Dk,
+                                           int Dv, kda_dtype qkv_dtype);
+
+/* Per sequence and head, with a state S [Dk,Dv], for each token t:
+ *     S_t = exp(g_t) S_{t-1} + k_t v_t^T,     o_t = scale S_t^T q_t
+ *   q, k     [B,T,Hk,Dk] in qkv_dtype.  H is a multiple of Hk: value head h has
+ *            the queries and keys of head h / (H / Hk)
+ *   v, o     [B,T,H,Dv] in qkv_dtype; Dk, Dv in {16,32,64,128}
+ *   g        log-decay of every token and head [B,T,H] in gate_dtype, or [H]
+ *            with KDA_GATE_FIXED; g <= 0, -inf forgets exactly (as does any g
+ *            below -1e4)
+ *   s0       initial state [B,H,Dk,Dv] fp32, or NULL for zeros
+ *   lengths  [B] int32 on the device, or NULL (every sequence has T tokens):
+ *            sequence b ends after lengths[b] tokens (clamped to 0..T).
+ *            Tokens from there on are not read, leave the state alone, and
+ *            their outputs are written as zeros.
+ *   o        must not alias an input
+ *   s_out    state after the last token [B,H,Dk,Dv] fp32, or NULL; may equal
+ *            s0
+ * With bf16 data o carries, beside its own rounding, one rounding of the pair
+ * products and one of the state to bf16 (half a step each); s_out is within
+ * about 2^-17 of its terms' magnitudes.  Values are not checked: an infinity or
+ * NaN in q, k or v may also reach the outputs of up to 63 tokens before it
+ * (those of its chunk: 0 * inf in the matrix products), never those of another
+ * sequence or head.
+ * Errors: KDA_EINVAL as elsewhere and for H not a multiple of Hk;
+ * KDA_EUNSUPPORTED for other Dk, Dv or dtype pairs, T > 2^30,
+ * H * max(Dk,Dv) > 2^22, B * H > 2^22, B * T * H * max(Dk,Dv) > 2^34. */
+kda_status kda_linattn(const void *q, const void *k, const void *v,
+                       kda_dtype qkv_dtype, const void *g,
+                       kda_dtype gate_dtype, const float *s0,
+                       const int *lengths, void *o, float *s_out, int B, int T,
+                       int Hk, int H, int Dk, int Dv, float scale,
+                       void *workspace, size_t workspace_bytes, void *stream);
+
+/* Gradient of kda_linattn for the loss sum(o * dO) + sum(s_out * dsT):
+ *   dS_t = scale q_t dO_t^T + exp(g_{t+1}) dS_{t+1}  (the last token's: + dsT)
+ *   dq_t = scale S_t dO_t;  dk_t = dS_t v_t;  dv_t = dS_t^T k_t  (dq and dk
+ *   summed over the value heads that share them);  dg_t = exp(g_t) times the
+ *   sum of dS_t * S_{t-1};  ds0 = exp(g_1) dS_1 (dsT for an empty sequence)
+ *   dO            [B,T,H,Dv] in qkv_dtype
+ *   dsT           [B,H,Dk,Dv] fp32 gradient of the final state, or NULL (zero)
+ *   dq, dk, dv    shaped like q, k, v, in qkv_dtype
+ *   dg            shaped like g, in gate_dtype (with KDA_GATE_FIXED the sum over
+ *                 all tokens), or NULL: not wanted
+ *   ds0           [B,H,Dk,Dv] fp32, or NULL
+ * Gradients of tokens past a sequence's length are written as zeros.  No
+ * output may alias an input or another output. */
+kda_status kda_linattn_backward(
+    const void *q, const void *k, const void *v, kda_dtype qkv_dtype,
+    const void *g, kda_dtype gate_dtype, const float *s0, const int *lengths,
+    const void *dO, const float *dsT, void *dq, void *dk, void *dv, void *dg,
+    float *ds0, int B, int T, int Hk, int H, int Dk, int Dv, float scale,
+    void *workspace, size_t workspace_bytes, void *stream);
+
+/* One token of it for N sequences: q, k [N,Hk,Dk], v [N,H,Dv], g [N,H] (or
+ * [H]), state [N,H,Dk,Dv] fp32 updated IN PLACE, o [N,H,Dv] in qkv_dtype (must
+ * not alias an input or the state).  KDA_EUNSUPPORTED from N * H = 2^24 on. */
+kda_status kda_linattn_step(const void *q, const void *k, const void *v,
+                            kda_dtype qkv_dtype, const void *g,
+                            kda_dtype gate_dtype, float *state, void *o, int N,
+                            int Hk, int H, int Dk, int Dv, float scale,
+                            void *stream);
+
+/* RMS norm of every query and key head and the rotation by position, in one
+ * pass over `rows` tokens.  For each head x [D] of a token at position p:
+ *     n = x / sqrt(mean(x^2) + eps) * w
+ *     the first rot channels of n are turned in pairs by p * inv_freq[i], the
+ *     others pass:  (a, b) -> (a cos - b sin, b cos + a sin)
+ * with pair i the channels i and i + rot/2, or with interleaved 2i and 2i + 1.
+ *   q, k       Hq and Hk heads of D values per token in io_dtype, D in
+ *              {16,32,64,128,256}; a token's heads are dense, tokens are
+ *              q_stride (k_stride) VALUES apart: at least heads * D, and a
+ *              multiple of 16 bytes, so that both may be parts of one fused
+ *              projection.  k may be NULL with Hk = 0
+ *   wq, wk     [D] fp32, or NULL: that side is not normed
+ *   positions  [rows] int32, any value; inv_freq [rot/2] fp32.  Angles are made
+ *              in 64 bits.  Both are NULL exactly when rot is 0
+ *   rot        0 <= rot <= D, a multiple of 16 (interleaved: of 8)
+ *   q_out, k_out  their own strides; each may equal its input with the same
+ *              stride (in place), and may lie in one buffer without overlap
+ * (An L2 norm, x / sqrt(sum x^2 + e), is w = 1/sqrt(D) with eps = e / D.)  A
+ * zero row with eps = 0 is NaN; squares that sum past 3.4e38 scale a row to
+ * zeros.
+ * Errors: KDA_EINVAL as elsewhere, for strides and combinations other than
+ * those above, and where neither side has a weight and rot is 0;
+ * KDA_EUNSUPPORTED: other D or rot, (Hq + Hk) * D > 2^22,
+ * rows * (Hq + Hk) * D > 2^34, rows >= 2^26. */
+kda_status kda_qk_norm_rope(const void *q, const void *k, kda_dtype io_dtype,
+                            long long q_stride, long long k_stride,
+                            const float *wq, const float *wk,
+                            const int *positions, const float *inv_freq,
+                            int rot, int interleaved, float eps, void *q_out,
+                            void *k_out, long long q_out_stride,
+                            long long k_out_stride, long long rows, int Hq,
+                            int Hk, int D, void *stream);
+
+/* Its gradient, from the same inputs and the gradients dq_out, dk_out of its
+ * outputs: dq, dk in io_dtype with strides of their own (each may equal its
+ * dq_out, dk_out with the same stride), dwq, dwk [D] fp32 (summed over tokens
+ * and heads in a fixed order; NULL exactly when the weights are). */
+size_t kda_qk_norm_rope_backward_workspace_size(long long rows, int Hq, int Hk,
+                                                int D);
+kda_status kda_qk_norm_rope_backward(
+    const void *q, const void *k, kda_dtype io_dtype, long long q_stride,
+    long long k_stride, const float *wq, const float *wk, const int *positions,
+    const float *inv_freq, int rot, int interleaved, float eps,
+    const void *dq_out, const void *dk_out, long long dq_out_stride,
+    long long dk_out_stride, void *dq, void *dk, long long dq_stride,
+    long long dk_stride, float *dwq, float *dwk, long long rows, int Hq,
+    int Hk, int D, void *workspace, size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }
