@@ -39,41 +39,90 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 // ---------------------------------------------------------------------------
-// fragments from LDS tiles [token][channel], 16 bytes of padding per row
+// LDS tiles [token][channel].
+//
+// bf16: read by rows as whole operand fragments of 16 bytes, and by columns in
+// 4 x 16 blocks that the LDS transposes.  A fragment's channels (32 u + 4 g..+3
+// and 32 u + 16 + 4 g..+3, see kda_device.h) lie side by side: 8-byte unit x of
+// a row, channels 4x..4x+3, is half (x >> 2 & 1) of 16-byte slot
+// 4 (x >> 3) + (x & 3).  Slots are permuted by an exclusive or with bits of the
+// row number, so that 16 rows' reads of one slot meet every bank once, and the
+// column reads, which take every other 8 bytes, meet it twice.  (Rows padded by
+// 16 bytes and fragments read as two halves: 38 % of the LDS's cycles were
+// conflicts, and assembling the halves took a register move for every one.)
+//
+// fp32: rows padded by 16 bytes serve both orders.
 
-template <typename IO> constexpr int pad() { return 16 / (int)sizeof(IO); }
+template <typename IO, int D> struct Tile;
 
-// rows as operand rows (k = channels): row `row` + m, unit u
-template <typename IO, int D>
-__device__ __forceinline__ typename Mma<IO>::frag frag_row(const IO *t,
-                                                           int row, int u,
-                                                           int g, int m) {
-  constexpr int STR = D + pad<IO>();
-  constexpr int K = sizeof(IO) == 2 ? 32 : 16;
-  return Mma<IO>::load_k(t + (row + m) * STR + u * K, g, D > 16);
-}
+template <int D> struct Tile<bf16, D> {
+  static constexpr int STR = D;
+  // rows over which all banks are met once, as a power of two
+  static constexpr int LB = D == 128 ? 0 : D == 64 ? 1 : 2;
+  __device__ static __forceinline__ int swz(int row) {
+    if constexpr (D == 16) return row >> 3 & 1;
+    return ((row >> LB & ((1 << (2 - LB)) - 1)) << 2) | (row >> 2 & 3);
+  }
+  // the element at (row, ch), ch a multiple of 4
+  __device__ static __forceinline__ int at(int row, int ch) {
+    const int x = ch >> 2;
+    // 32 bytes a row: the order stays, halves of the rows from 8 on change
+    if constexpr (D == 16) return row * D + ((x ^ swz(row) << 1) << 2);
+    const int slot = (x >> 3) * 4 + (x & 3);
+    return row * D + (slot ^ swz(row)) * 8 + (x >> 2 & 1) * 4;
+  }
+  // rows as operand rows (k = channels): row `row` + m, unit u
+  __device__ static __forceinline__ bf16x8 by_row(const bf16 *t, int row,
+                                                  int u, int g, int m) {
+    const bf16 *p = t + row * D + at(m, 32 * u + 4 * g);
+    if constexpr (D > 16) {
+      return *(const bf16x8 *)p;
+    } else {
+      const bf16x4 lo = *(const bf16x4 *)p;
+      const bf16x4 hi{(bf16)0.f, (bf16)0.f, (bf16)0.f, (bf16)0.f};
+      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+  }
+  // channels as operand rows (k = tokens): channels col..col+15, tokens of
+  // unit u: each lane names 4 channels of one token and receives 4 tokens of
+  // one channel
+  __device__ static __forceinline__ bf16x8 by_col(const bf16 *t, int col,
+                                                  int u, int g, int m) {
+    const bf16 *p = t + 32 * u * D + at(4 * g + (m >> 2), col + (m & 3) * 4);
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
+    const s16x4 hi =
+        __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 16 * D));
+    typedef short s16x8 __attribute__((ext_vector_type(8)));
+    return __builtin_bit_cast(
+        bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  }
+  // 16 bytes of a row, channels ch..ch+7
+  __device__ static __forceinline__ void put(bf16 *t, int row, int ch,
+                                             uint4 v) {
+    *(uint2 *)(t + at(row, ch)) = uint2{v.x, v.y};
+    *(uint2 *)(t + at(row, ch + 4)) = uint2{v.z, v.w};
+  }
+};
 
-// channels as operand rows (k = tokens): channels col..col+15, tokens of unit
-// u.  bf16: a 4 x 16 block of tokens x channels is transposed on the way by
-// the LDS (each lane names 4 channels of one token and receives 4 tokens of
-// one channel).
-template <int STR>
-__device__ __forceinline__ bf16x8 frag_col(const bf16 *t, int col, int u,
-                                           int g, int m) {
-  const bf16 *p = t + (32 * u + 4 * g + (m >> 2)) * STR + col + (m & 3) * 4;
-  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
-  const s16x4 hi =
-      __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 16 * STR));
-  typedef short s16x8 __attribute__((ext_vector_type(8)));
-  return __builtin_bit_cast(
-      bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-}
-template <int STR>
-__device__ __forceinline__ f32x4 frag_col(const float *t, int col, int u,
-                                          int g, int m) {
-  const float *p = t + (16 * u + 4 * g) * STR + col + m;
-  return f32x4{p[0], p[STR], p[2 * STR], p[3 * STR]};
-}
+template <int D> struct Tile<float, D> {
+  static constexpr int STR = D + 4;
+  __device__ static __forceinline__ int at(int row, int ch) {
+    return row * STR + ch;
+  }
+  __device__ static __forceinline__ f32x4 by_row(const float *t, int row,
+                                                 int u, int g, int m) {
+    return *(const f32x4 *)(t + (row + m) * STR + 16 * u + 4 * g);
+  }
+  __device__ static __forceinline__ f32x4 by_col(const float *t, int col,
+                                                 int u, int g, int m) {
+    const float *p = t + (16 * u + 4 * g) * STR + col + m;
+    return f32x4{p[0], p[STR], p[2 * STR], p[3 * STR]};
+  }
+  __device__ static __forceinline__ void put(float *t, int row, int ch,
+                                             uint4 v) {
+    *(uint4 *)(t + row * STR + ch) = v;
+  }
+};
 
 // a fragment's weights: w[k] for its elements
 __device__ __forceinline__ void weights(const float *w, int u, int g,
@@ -96,25 +145,39 @@ __device__ __forceinline__ void weights(const float *w, int u, int g,
 template <typename IO, int D, int C, int NT> struct Rows {
   static constexpr int UPR = D * (int)sizeof(IO) / 16;  // 16-byte units a row
   static constexpr int N = (C * UPR + NT - 1) / NT;
+  static constexpr int STEP = NT / UPR;  // rows from a thread's unit to its next
   uint4 r[N];
-  // rows from `live` on are zeros
-  __device__ __forceinline__ void fetch(const char *p, size_t stride,
+  // rows from `live` on are zeros.  A chunk is less than 2^30 bytes long (a
+  // token at most 2^24): one 32-bit offset a lane serves all its units, the
+  // rest of the address is the same for all lanes
+  __device__ __forceinline__ void fetch(const char *p, unsigned stride,
                                         int live) {
+    const int row0 = threadIdx.x / UPR;
+    const unsigned v = row0 * stride + threadIdx.x % UPR * 16;
+    if (live >= C && C % STEP == 0) {
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int i = threadIdx.x + n * NT, row = i / UPR, col = i % UPR;
-      r[n] = uint4{0, 0, 0, 0};
-      if (row < live && row < C)
-        r[n] = *(const uint4 *)(p + row * stride + col * 16);
+      for (int n = 0; n < N; ++n)
+        r[n] = *(const uint4 *)(p + (size_t)(n * STEP) * stride + v);
+    } else {
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        r[n] = uint4{0, 0, 0, 0};
+        if (row0 + n * STEP < live && row0 + n * STEP < C)
+          r[n] = *(const uint4 *)(p + (size_t)(n * STEP) * stride + v);
+      }
     }
   }
   __device__ __forceinline__ void stash(IO *t) const {
-    constexpr int STR = D + pad<IO>();
+    const int row0 = threadIdx.x / UPR;
+    const int ch = threadIdx.x % UPR * (16 / (int)sizeof(IO));
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      const int i = threadIdx.x + n * NT, row = i / UPR, col = i % UPR;
-      if (i < C * UPR)
-        *(uint4 *)(t + row * STR + col * (16 / (int)sizeof(IO))) = r[n];
+      if (C % STEP != 0 && row0 + n * STEP >= C) continue;
+      // 16 rows on, a row's units lie in the same order
+      if constexpr (STEP % 16 == 0)
+        Tile<IO, D>::put(t + n * STEP * Tile<IO, D>::STR, row0, ch, r[n]);
+      else
+        Tile<IO, D>::put(t, row0 + n * STEP, ch, r[n]);
     }
   }
 };
@@ -124,9 +187,9 @@ template <typename IO, int D, int C, int NT> struct Rows {
 template <typename IO, int D>
 __device__ __forceinline__ const char *operand(const LinOperand &o,
                                                const LinSeq &q, int b, int h,
-                                               size_t &stride) {
+                                               unsigned &stride) {
   const int nh = o.shared ? q.H / q.G : q.H, hh = o.shared ? h / q.G : h;
-  stride = (size_t)nh * D * sizeof(IO);
+  stride = (unsigned)nh * D * sizeof(IO);
   return (const char *)o.p + ((size_t)b * q.T * nh + hh) * D * sizeof(IO);
 }
 
@@ -173,40 +236,41 @@ __device__ __forceinline__ double decays(Decays<C> &s, float g, float fs,
 }
 
 // ---------------------------------------------------------------------------
-// S = total S + b^T diag(w) c over a chunk; the wave's columns start at `col`
+// S = total S + b^T diag(w) c over a chunk, c as operand fragments
 
-template <typename IO, int D1, int D2, int CT, int C>
-__device__ __forceinline__ void add_chunk(f32x4 (&S)[D1 / 16][CT],
-                                          const IO *tb, const IO *tc,
-                                          const float *w, float total,
-                                          int col, int g, int m) {
-  constexpr int KU = sizeof(IO) == 2 ? 32 : 16;
+template <typename IO, int D1, int CT, int C, int NTU>
+__device__ __forceinline__ void add_chunk(
+    f32x4 (&S)[D1 / 16][CT], const IO *tb,
+    const typename Mma<IO>::frag (&c)[NTU][CT], const float *w, float total,
+    int g, int m) {
   constexpr int NE = Mma<IO>::NE;
-  constexpr int S1 = D1 + pad<IO>(), S2 = D2 + pad<IO>();
   typedef typename Mma<IO>::frag frag;
 #pragma unroll
   for (int kt = 0; kt < D1 / 16; ++kt)
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) S[kt][ct] *= total;
 #pragma unroll
-  for (int u = 0; u < C / KU; ++u) {
+  for (int u = 0; u < NTU; ++u) {
     float wt[NE];
     weights(w, u, g, wt);
     frag hi[CT], lo[CT];
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
-      const frag c = frag_col<S2>(tc, col + ct * 16, u, g, m);
+      float x[8] = {};
 #pragma unroll
-      for (int e = 0; e < NE; ++e) {
-        const float x = Mma<IO>::elem(c, e) * wt[e];
-        Mma<IO>::set(hi[ct], e, x);
-        if constexpr (sizeof(IO) == 2)
-          Mma<IO>::set(lo[ct], e, x - Mma<IO>::elem(hi[ct], e));
+      for (int e = 0; e < NE; ++e) x[e] = Mma<IO>::elem(c[u][ct], e) * wt[e];
+      hi[ct] = Mma<IO>::pack(f32x4{x[0], x[1], x[2], x[3]},
+                             f32x4{x[4], x[5], x[6], x[7]});
+      if constexpr (sizeof(IO) == 2) {
+#pragma unroll
+        for (int e = 0; e < NE; ++e) x[e] -= Mma<IO>::elem(hi[ct], e);
+        lo[ct] = Mma<IO>::pack(f32x4{x[0], x[1], x[2], x[3]},
+                               f32x4{x[4], x[5], x[6], x[7]});
       }
     }
 #pragma unroll
     for (int kt = 0; kt < D1 / 16; ++kt) {
-      const frag b = frag_col<S1>(tb, kt * 16, u, g, m);
+      const frag b = Tile<IO, D1>::by_col(tb, kt * 16, u, g, m);
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) {
         S[kt][ct] = Mma<IO>::mma(b, hi[ct], S[kt][ct]);
@@ -215,6 +279,17 @@ __device__ __forceinline__ void add_chunk(f32x4 (&S)[D1 / 16][CT],
       }
     }
   }
+}
+
+// 4 values to out[at + lane]: at the same for all lanes
+template <typename IO>
+__device__ __forceinline__ void put4(void *out, int as_f32, size_t at,
+                                     unsigned lane, f32x4 v) {
+  if (sizeof(IO) == 4 || as_f32)
+    *(f32x4 *)((float *)out + at + lane) = v;
+  else
+    *(bf16x4 *)((bf16 *)out + at + lane) =
+        bf16x4{(bf16)v[0], (bf16)v[1], (bf16)v[2], (bf16)v[3]};
 }
 
 // waves of a workgroup and columns a wave owns
@@ -235,12 +310,13 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
   constexpr int KT = D1 / 16, NKU = (KT + TPU - 1) / TPU;  // units over D1
   constexpr int NDU = (D2 / 16 + TPU - 1) / TPU;           // units over D2
   constexpr int NTU = C / KU;                              // units over tokens
-  constexpr int S1 = D1 + pad<IO>(), S2 = D2 + pad<IO>();
   typedef typename Mma<IO>::frag frag;
-  __shared__ alignas(16) IO ta[C * S1], tb[C * S1], tc[C * S2];
-  __shared__ alignas(16) IO td[DOT ? C * S2 : 8];
+  typedef Tile<IO, D1> T1;
+  typedef Tile<IO, D2> T2;
+  __shared__ alignas(16) IO ta[C * T1::STR], tb[C * T1::STR], tc[C * T2::STR];
+  __shared__ alignas(16) IO td[DOT ? C * T2::STR : 8];
   __shared__ alignas(16) frag tp[NB * NTU * 64];
-  __shared__ Decays<C> dec;
+  __shared__ Decays<C> decs[2];
   __shared__ float far_part[DOT ? NW : 1][DOT ? C : 1];
   __shared__ float pair_part[DOT == LIN_FAR_PAIRS ? NB : 1]
                             [DOT == LIN_FAR_PAIRS ? C : 1];
@@ -259,21 +335,14 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
   const int nch = live_end > t_begin ? (live_end - t_begin + C - 1) / C : 0;
 
   // out of dead tokens is zero
-  IO *const out = (IO *)p.out;
-  float *const out32 = (float *)p.out;
   {
     const int t0 = t_begin + nch * C;
     const long long n = (long long)(t_end - t0) * (D2 / 8);
     for (long long i = threadIdx.x; i < n; i += NT) {
       const size_t at = (((size_t)b * q.T + t0 + i / (D2 / 8)) * q.H + h) * D2 +
                         i % (D2 / 8) * 8;
-#pragma unroll
-      for (int e = 0; e < 8; e += 4) {
-        if (p.out_f32) *(f32x4 *)(out32 + at + e) = f32x4{0, 0, 0, 0};
-        else if constexpr (sizeof(IO) == 2)
-          *(uint2 *)(out + at + e) = uint2{0, 0};
-        else *(f32x4 *)(out + at + e) = f32x4{0, 0, 0, 0};
-      }
+      put4<IO>(p.out, p.out_f32, at, 0, f32x4{0, 0, 0, 0});
+      put4<IO>(p.out, p.out_f32, at, 4, f32x4{0, 0, 0, 0});
     }
   }
 
@@ -296,7 +365,7 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
       }
     }
 
-  size_t sa, sb, sc, sd = 0;
+  unsigned sa, sb, sc, sd = 0;
   const char *pa = operand<IO, D1>(p.a, q, b, h, sa);
   const char *pb = operand<IO, D1>(p.b, q, b, h, sb);
   const char *pc = operand<IO, D2>(p.c, q, b, h, sc);
@@ -311,24 +380,39 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
     rb.fetch(pb + (size_t)t0 * sb, sb, live);
     rc.fetch(pc + (size_t)t0 * sc, sc, live);
     if constexpr (DOT) rd.fetch(pd + (size_t)t0 * sd, sd, live);
-    if (w == 0)
-      gate = lane < C && lane < live ? load_gate(q, b, h, t0 + lane) : 0.f;
+  };
+  // the decays of a chunk are made while the one before it is worked on, by
+  // the wave with the fewest pair products; their gates are loaded one more
+  // chunk ahead
+  const bool keeper = w == (REV ? NW - 1 : 0);
+  auto fetch_gate = [&](int n) {
+    if (!keeper || n >= nch) return;
+    const int t = t_begin + (REV ? nch - 1 - n : n) * C + lane;
+    gate = lane < C && t < live_end ? load_gate(q, b, h, t) : 0.f;
+  };
+  auto make_decays = [&](int n) {
+    if (keeper && n < nch)
+      decays<C>(decs[n & 1], gate, REV ? p.add_scale : p.far_scale,
+                REV ? p.far_scale : p.add_scale, lane);
   };
   const bool last_seg = REV ? s == 0 : s == q.NS - 1;
   const bool keep_end = (last_seg && p.s_end) || DOT == LIN_FAR_PAIRS;
 
   if (nch > 0) fetch(t_begin + (REV ? nch - 1 : 0) * C);
+  fetch_gate(0);
+  make_decays(0);
+  fetch_gate(1);
   for (int n = 0; n < nch; ++n) {
     const int t0 = t_begin + (REV ? nch - 1 - n : n) * C;
+    const Decays<C> &dec = decs[n & 1];
     ra.stash(ta);
     rb.stash(tb);
     rc.stash(tc);
     if constexpr (DOT) rd.stash(td);
-    if (w == 0)
-      decays<C>(dec, gate, REV ? p.add_scale : p.far_scale,
-                REV ? p.far_scale : p.add_scale, lane);
     __syncthreads();
     if (n + 1 < nch) fetch(REV ? t0 - C : t0 + C);
+    make_decays(n + 1);
+    fetch_gate(n + 2);
     const float *const far_w = REV ? dec.last : dec.first;
     const float *const add_w = REV ? dec.first : dec.last;
 
@@ -337,7 +421,7 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
       frag fa[NKU];
 #pragma unroll
       for (int u = 0; u < NKU; ++u)
-        fa[u] = frag_row<IO, D1>(ta, rt * 16, u, g, m);
+        fa[u] = T1::by_row(ta, rt * 16, u, g, m);
       const int i = rt * 16 + m;
       const double Gi = dec.G[i];
       float run = 0.f;  // pairs of i with earlier tiles' j
@@ -353,8 +437,7 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
           f32x4 acc{0, 0, 0, 0};
 #pragma unroll
           for (int u = 0; u < NKU; ++u)
-            acc = Mma<IO>::mma(frag_row<IO, D1>(tb, jt * 16, u, g, m), fa[u],
-                               acc);
+            acc = Mma<IO>::mma(T1::by_row(tb, jt * 16, u, g, m), fa[u], acc);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int j = jt * 16 + 4 * g + e;
@@ -368,8 +451,8 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
             f32x4 qk{0, 0, 0, 0};
 #pragma unroll
             for (int u = 0; u < NDU; ++u)
-              qk = Mma<IO>::mma(frag_row<IO, D2>(tc, jt * 16, u, g, m),
-                                frag_row<IO, D2>(td, rt * 16, u, g, m), qk);
+              qk = Mma<IO>::mma(T2::by_row(tc, jt * 16, u, g, m),
+                                T2::by_row(td, rt * 16, u, g, m), qk);
             qk *= acc;
             const float tot = (qk[0] + qk[1]) + (qk[2] + qk[3]);
             const float v1 = __shfl_up(tot, 16, 64);
@@ -393,94 +476,107 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
       }
     }
 
-    // the state as operand fragments
-    frag fs[NKU][CT], fl[DOT && NE == 8 ? NKU : 1][CT];
+    __builtin_amdgcn_sched_barrier(0);
+    // what the state gives to out, transposed: rows are this wave's columns
+    // of c, columns tokens
+    f32x4 acc[NB][CT];
 #pragma unroll
-    for (int u = 0; u < NKU; ++u)
+    for (int rt = 0; rt < NB; ++rt)
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) acc[rt][ct] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int u = 0; u < NKU; ++u) {
+      frag fs[CT], fl[CT];
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) {
         const f32x4 x = S[u * TPU][ct];
         const f32x4 y = TPU == 2 && u * TPU + 1 < KT ? S[u * TPU + 1][ct]
                                                      : f32x4{0, 0, 0, 0};
-        const frag f = Mma<IO>::pack(x, y);
-        fs[u][ct] = f;
+        fs[ct] = Mma<IO>::pack(x, y);
         if constexpr (DOT && NE == 8) {
           f32x4 x2, y2;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            x2[e] = x[e] - Mma<IO>::elem(f, e);
-            y2[e] = y[e] - Mma<IO>::elem(f, 4 + e);
+            x2[e] = x[e] - Mma<IO>::elem(fs[ct], e);
+            y2[e] = y[e] - Mma<IO>::elem(fs[ct], 4 + e);
           }
-          fl[u][ct] = Mma<IO>::pack(x2, y2);
+          fl[ct] = Mma<IO>::pack(x2, y2);
         }
       }
-    __syncthreads();
-
-    // out, transposed: rows are this wave's columns of c, columns tokens
-    frag fc[NTU][CT];
 #pragma unroll
-    for (int u = 0; u < NTU; ++u)
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct)
-        fc[u][ct] = frag_col<S2>(tc, w * CW + ct * 16, u, g, m);
-#pragma unroll
-    for (int rt = 0; rt < NB; ++rt) {
-      f32x4 acc[CT];
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct) acc[ct] = f32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int u = 0; u < NKU; ++u) {
-        const frag f = frag_row<IO, D1>(ta, rt * 16, u, g, m);
+      for (int rt = 0; rt < NB; ++rt) {
+        const frag f = T1::by_row(ta, rt * 16, u, g, m);
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
-          acc[ct] = Mma<IO>::mma(fs[u][ct], f, acc[ct]);
+          acc[rt][ct] = Mma<IO>::mma(fs[ct], f, acc[rt][ct]);
           if constexpr (DOT && NE == 8)
-            acc[ct] = Mma<IO>::mma(fl[u][ct], f, acc[ct]);
+            acc[rt][ct] = Mma<IO>::mma(fl[ct], f, acc[rt][ct]);
         }
       }
+    }
+#pragma unroll
+    for (int rt = 0; rt < NB; ++rt) {
       const float fw = far_w[rt * 16 + m];
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct) acc[ct] *= fw;
+      for (int ct = 0; ct < CT; ++ct) acc[rt][ct] *= fw;
       if constexpr (DOT) {
         float dot = 0.f;
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
-          const IO *x = td + (rt * 16 + m) * S2 + w * CW + ct * 16 + 4 * g;
+          const IO *x = td + T2::at(rt * 16 + m, w * CW + ct * 16 + 4 * g);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) dot += acc[ct][e] * to_f32(x[e]);
+          for (int e = 0; e < 4; ++e) dot += acc[rt][ct][e] * to_f32(x[e]);
         }
         dot += __shfl_xor(dot, 16, 64);
         dot += __shfl_xor(dot, 32, 64);
         if (g == 0) far_part[w][rt * 16 + m] = dot;
       }
+    }
+    __syncthreads();
+    frag fc[NTU][CT];
+#pragma unroll
+    for (int u = 0; u < NTU; ++u)
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct)
+        fc[u][ct] = T2::by_col(tc, w * CW + ct * 16, u, g, m);
+
+    // and the pairs
+    const size_t row = (size_t)q.H * D2;
+    const size_t o_chunk = (((size_t)b * q.T + t0) * q.H + h) * D2;
+    const unsigned o_lane = (unsigned)(m * row) + w * CW + 4 * g;
+#pragma unroll
+    for (int rt = 0; rt < NB; ++rt) {
 #pragma unroll
       for (int u = 0; u < NTU; ++u) {
         if (REV ? u * TPU + TPU - 1 < rt : u * TPU > rt) continue;
         const frag f = tp[(rt * NTU + u) * 64 + lane];
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
-          acc[ct] = Mma<IO>::mma(fc[u][ct], f, acc[ct]);
-      }
-      const int t = t0 + rt * 16 + m;
-      if (t < t_end) {
-        const size_t at = (((size_t)b * q.T + t) * q.H + h) * D2 + w * CW +
-                          4 * g;
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-          const f32x4 v = t < live_end ? acc[ct] : f32x4{0, 0, 0, 0};
-          if constexpr (sizeof(IO) == 2) {
-            if (p.out_f32) *(f32x4 *)(out32 + at + ct * 16) = v;
-            else
-              *(bf16x4 *)(out + at + ct * 16) =
-                  bf16x4{(bf16)v[0], (bf16)v[1], (bf16)v[2], (bf16)v[3]};
-          } else {
-            *(f32x4 *)(out + at + ct * 16) = v;
-          }
-        }
+          acc[rt][ct] = Mma<IO>::mma(fc[u][ct], f, acc[rt][ct]);
       }
     }
+    if (t0 + C <= live_end) {
+#pragma unroll
+      for (int rt = 0; rt < NB; ++rt)
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+          put4<IO>(p.out, p.out_f32,
+                   o_chunk + rt * 16 * row + ct * 16, o_lane, acc[rt][ct]);
+    } else {
+#pragma unroll
+      for (int rt = 0; rt < NB; ++rt) {
+        const int t = t0 + rt * 16 + m;
+        if (t >= t_end) continue;
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+          put4<IO>(p.out, p.out_f32,
+                   o_chunk + rt * 16 * row + ct * 16, o_lane,
+                   t < live_end ? acc[rt][ct] : f32x4{0, 0, 0, 0});
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
     if (n + 1 < nch || keep_end)
-      add_chunk<IO, D1, D2, CT, C>(S, tb, tc, add_w, dec.total, w * CW, g, m);
+      add_chunk<IO, D1, CT, C, NTU>(S, tb, fc, add_w, dec.total, g, m);
     __syncthreads();
     if constexpr (DOT) {
       const int t = t0 + threadIdx.x;
@@ -547,9 +643,11 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_local(
   constexpr int C = lin_chunk(sizeof(IO) == 2);
   constexpr int NW = nwaves<D2>(), NT = 64 * NW;
   constexpr int CT = D2 / 16 / NW, CW = CT * 16, KT = D1 / 16;
-  constexpr int S1 = D1 + pad<IO>(), S2 = D2 + pad<IO>();
-  __shared__ alignas(16) IO tb[C * S1], tc[C * S2];
-  __shared__ Decays<C> dec;
+  constexpr int NTU = C / (16 * Mma<IO>::TPU);
+  typedef typename Mma<IO>::frag frag;
+  __shared__ alignas(16) IO tb[C * Tile<IO, D1>::STR],
+      tc[C * Tile<IO, D2>::STR];
+  __shared__ Decays<C> decs[2];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int g = lane >> 4, m = lane & 15;
   const LinSeq &q = p.q;
@@ -567,7 +665,7 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_local(
   for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) S[kt][ct] = f32x4{0, 0, 0, 0};
-  size_t sb, sc;
+  unsigned sb, sc;
   const char *pb = operand<IO, D1>(p.b, q, b, h, sb);
   const char *pc = operand<IO, D2>(p.c, q, b, h, sc);
   Rows<IO, D1, C, NT> rb;
@@ -578,19 +676,38 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_local(
     const int live = live_end - t0;
     rb.fetch(pb + (size_t)t0 * sb, sb, live);
     rc.fetch(pc + (size_t)t0 * sc, sc, live);
-    if (w == 0)
-      gate = lane < C && lane < live ? load_gate(q, b, h, t0 + lane) : 0.f;
+  };
+  auto fetch_gate = [&](int n) {
+    if (w != 0 || n >= nch) return;
+    const int t = t_begin + (p.rev ? nch - 1 - n : n) * C + lane;
+    gate = lane < C && t < live_end ? load_gate(q, b, h, t) : 0.f;
+  };
+  auto make_decays = [&](int n) {
+    if (w == 0 && n < nch)
+      sum += decays<C>(decs[n & 1], gate, p.add_scale, p.add_scale, lane);
   };
   if (nch > 0) fetch(t_begin + (p.rev ? nch - 1 : 0) * C);
+  fetch_gate(0);
+  make_decays(0);
+  fetch_gate(1);
   for (int n = 0; n < nch; ++n) {
     const int t0 = t_begin + (p.rev ? nch - 1 - n : n) * C;
+    const Decays<C> &dec = decs[n & 1];
     rb.stash(tb);
     rc.stash(tc);
-    if (w == 0) sum += decays<C>(dec, gate, p.add_scale, p.add_scale, lane);
     __syncthreads();
     if (n + 1 < nch) fetch(p.rev ? t0 - C : t0 + C);
-    add_chunk<IO, D1, D2, CT, C>(S, tb, tc, p.rev ? dec.first : dec.last,
-                                 dec.total, w * CW, g, m);
+    make_decays(n + 1);
+    fetch_gate(n + 2);
+    frag fc[NTU][CT];
+#pragma unroll
+    for (int u = 0; u < NTU; ++u)
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct)
+        fc[u][ct] =
+            Tile<IO, D2>::by_col(tc, w * CW + ct * 16, u, g, m);
+    add_chunk<IO, D1, CT, C, NTU>(S, tb, fc, p.rev ? dec.first : dec.last,
+                                  dec.total, g, m);
     __syncthreads();
   }
   float *const o = p.s + (chain * q.NS + s) * D1 * D2;
