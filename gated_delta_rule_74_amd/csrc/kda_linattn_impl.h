@@ -31,11 +31,13 @@
 #pragma once
 #include "kda_device.h"
 #include "kda_linattn.h"
+#include "kda_vec.h"
 
 namespace kda {
 namespace lin {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 // ---------------------------------------------------------------------------
@@ -92,9 +94,8 @@ template <int D> struct Tile<bf16, D> {
     const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
     const s16x4 hi =
         __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 16 * D));
-    typedef short s16x8 __attribute__((ext_vector_type(8)));
-    return __builtin_bit_cast(
-        bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    const s16x8 r = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    return __builtin_bit_cast(bf16x8, r);
   }
   // 16 bytes of a row, channels ch..ch+7
   __device__ static __forceinline__ void put(bf16 *t, int row, int ch,
@@ -214,41 +215,68 @@ __device__ __forceinline__ float load_gate(const LinSeq &q, int b, int h,
   return q.gate_bf16 ? (float)((const bf16 *)q.g)[i] : ((const float *)q.g)[i];
 }
 
-// by one wave: g the log-decay of token `lane` (0 past the end)
-template <int C>
-__device__ __forceinline__ double decays(Decays<C> &s, float g, float fs,
-                                         float ls, int lane) {
-  g = g < -1e4f ? -1e4f : g;
-  double x = lane < C ? (double)g * 1.4426950408889634074 : 0.0;
-#pragma unroll
-  for (int d = 1; d < C; d *= 2) {
-    const double y = __shfl_up(x, d, 64);
-    if (lane >= d) x += y;
-  }
-  const double end = __shfl(x, C - 1, 64);
-  if (lane < C) {
-    s.G[lane] = x;
-    s.first[lane] = fs * exp2_diff(x);
-    s.last[lane] = ls * exp2_diff(end - x);
-  }
-  if (lane == 0) s.total = exp2_diff(end);
-  return end;
+// x plus that of the lane that DPP control CTRL names, 0 where there is none
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double add_dpp(double x) {
+  const long long v = __builtin_bit_cast(long long, x);
+  const int lo = __builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, false);
+  const int hi =
+      __builtin_amdgcn_update_dpp(0, (int)(v >> 32), CTRL, ROWS, 0xf, false);
+  return x + __builtin_bit_cast(
+                 double, (long long)hi << 32 | (unsigned)lo);
 }
 
+// The decays of up to 4 chunks are made at a time, a chunk by each wave: made
+// one by one ahead of their chunk, by one wave while the others work, they kept
+// the others waiting (4 of the local pass's 40 us at B1 T8192 H32 D128).
+constexpr int BATCH = 4;
+
+// by one wave: the sums G of a chunk's log-decays, g that of token `lane` (0
+// past the end); returns their end
+template <int C>
+__device__ __forceinline__ double decay_sums(float g, int lane, double &x) {
+  g = g < -1e4f ? -1e4f : g;
+  x = lane < C ? (double)g * 1.4426950408889634074 : 0.0;
+  x = add_dpp<0x111, 0xf>(x);  // row_shr:1, 2, 4, 8
+  x = add_dpp<0x112, 0xf>(x);
+  x = add_dpp<0x114, 0xf>(x);
+  x = add_dpp<0x118, 0xf>(x);
+  x = add_dpp<0x142, 0xa>(x);  // row_bcast:15 into rows 1 and 3
+  x = add_dpp<0x143, 0xc>(x);  // row_bcast:31 into rows 2 and 3
+  const long long v = __builtin_bit_cast(long long, x);
+  const int lo = __builtin_amdgcn_readlane((int)v, C - 1);
+  const int hi = __builtin_amdgcn_readlane((int)(v >> 32), C - 1);
+  return __builtin_bit_cast(double, (long long)hi << 32 | (unsigned)lo);
+}
+
+// the gates of a wave's chunks of a batch, and where a sequence's chunks are
+template <int C, int NW> struct Gates {
+  static constexpr int N = (BATCH + NW - 1) / NW;
+  float g[N];
+  // chunk n of nch, taken from the segment's end where `back` says so
+  __device__ __forceinline__ void fetch(const LinSeq &q, int b, int h, int n0,
+                                        int nch, bool back, int t_begin,
+                                        int live_end, int w, int lane) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int n = n0 + w + i * NW;
+      const int t = t_begin + (back ? nch - 1 - n : n) * C + lane;
+      g[i] = 0.f;
+      if (w + i * NW < BATCH && n < nch && lane < C && t < live_end)
+        g[i] = load_gate(q, b, h, t);
+    }
+  }
+};
+
 // ---------------------------------------------------------------------------
-// S = total S + b^T diag(w) c over a chunk, c as operand fragments
+// S += b^T diag(w) c over a chunk, c as operand fragments
 
 template <typename IO, int D1, int CT, int C, int NTU>
 __device__ __forceinline__ void add_chunk(
     f32x4 (&S)[D1 / 16][CT], const IO *tb,
-    const typename Mma<IO>::frag (&c)[NTU][CT], const float *w, float total,
-    int g, int m) {
+    const typename Mma<IO>::frag (&c)[NTU][CT], const float *w, int g, int m) {
   constexpr int NE = Mma<IO>::NE;
   typedef typename Mma<IO>::frag frag;
-#pragma unroll
-  for (int kt = 0; kt < D1 / 16; ++kt)
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct) S[kt][ct] *= total;
 #pragma unroll
   for (int u = 0; u < NTU; ++u) {
     float wt[NE];
@@ -281,15 +309,9 @@ __device__ __forceinline__ void add_chunk(
   }
 }
 
-// 4 values to out[at + lane]: at the same for all lanes
-template <typename IO>
-__device__ __forceinline__ void put4(void *out, int as_f32, size_t at,
-                                     unsigned lane, f32x4 v) {
-  if (sizeof(IO) == 4 || as_f32)
-    *(f32x4 *)((float *)out + at + lane) = v;
-  else
-    *(bf16x4 *)((bf16 *)out + at + lane) =
-        bf16x4{(bf16)v[0], (bf16)v[1], (bf16)v[2], (bf16)v[3]};
+__device__ __forceinline__ uint2 pack4(f32x4 v) {
+  return __builtin_bit_cast(
+      uint2, bf16x4{(bf16)v[0], (bf16)v[1], (bf16)v[2], (bf16)v[3]});
 }
 
 // waves of a workgroup and columns a wave owns
@@ -316,7 +338,7 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
   __shared__ alignas(16) IO ta[C * T1::STR], tb[C * T1::STR], tc[C * T2::STR];
   __shared__ alignas(16) IO td[DOT ? C * T2::STR : 8];
   __shared__ alignas(16) frag tp[NB * NTU * 64];
-  __shared__ Decays<C> decs[2];
+  __shared__ Decays<C> decs[BATCH];
   __shared__ float far_part[DOT ? NW : 1][DOT ? C : 1];
   __shared__ float pair_part[DOT == LIN_FAR_PAIRS ? NB : 1]
                             [DOT == LIN_FAR_PAIRS ? C : 1];
@@ -341,8 +363,8 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
     for (long long i = threadIdx.x; i < n; i += NT) {
       const size_t at = (((size_t)b * q.T + t0 + i / (D2 / 8)) * q.H + h) * D2 +
                         i % (D2 / 8) * 8;
-      put4<IO>(p.out, p.out_f32, at, 0, f32x4{0, 0, 0, 0});
-      put4<IO>(p.out, p.out_f32, at, 4, f32x4{0, 0, 0, 0});
+      if (sizeof(IO) == 4 || p.out_f32) store8_zero((float *)p.out + at);
+      else store8_zero((bf16 *)p.out + at);
     }
   }
 
@@ -373,7 +395,6 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
   if constexpr (DOT) pd = operand<IO, D2>(p.d, q, b, h, sd);
   Rows<IO, D1, C, NT> ra, rb;
   Rows<IO, D2, C, NT> rc, rd;
-  float gate = 0.f;
   auto fetch = [&](int t0) {
     const int live = live_end - t0;
     ra.fetch(pa + (size_t)t0 * sa, sa, live);
@@ -381,38 +402,46 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
     rc.fetch(pc + (size_t)t0 * sc, sc, live);
     if constexpr (DOT) rd.fetch(pd + (size_t)t0 * sd, sd, live);
   };
-  // the decays of a chunk are made while the one before it is worked on, by
-  // the wave with the fewest pair products; their gates are loaded one more
-  // chunk ahead
-  const bool keeper = w == (REV ? NW - 1 : 0);
-  auto fetch_gate = [&](int n) {
-    if (!keeper || n >= nch) return;
-    const int t = t_begin + (REV ? nch - 1 - n : n) * C + lane;
-    gate = lane < C && t < live_end ? load_gate(q, b, h, t) : 0.f;
+  Gates<C, NW> gates;
+  auto fetch_gates = [&](int n0) {
+    gates.fetch(q, b, h, n0, nch, REV, t_begin, live_end, w, lane);
   };
-  auto make_decays = [&](int n) {
-    if (keeper && n < nch)
-      decays<C>(decs[n & 1], gate, REV ? p.add_scale : p.far_scale,
-                REV ? p.far_scale : p.add_scale, lane);
+  auto make_decays = [&](int n0) {
+#pragma unroll
+    for (int i = 0; i < gates.N; ++i) {
+      const int x = w + i * NW;
+      if (x >= BATCH || n0 + x >= nch) break;
+      double G;
+      const double end = decay_sums<C>(gates.g[i], lane, G);
+      if (lane < C) {
+        decs[x].G[lane] = G;
+        decs[x].first[lane] = (REV ? p.add_scale : p.far_scale) * exp2_diff(G);
+        decs[x].last[lane] =
+            (REV ? p.far_scale : p.add_scale) * exp2_diff(end - G);
+      }
+      if (lane == 0) decs[x].total = exp2_diff(end);
+    }
   };
   const bool last_seg = REV ? s == 0 : s == q.NS - 1;
   const bool keep_end = (last_seg && p.s_end) || DOT == LIN_FAR_PAIRS;
 
+  fetch_gates(0);
   if (nch > 0) fetch(t_begin + (REV ? nch - 1 : 0) * C);
-  fetch_gate(0);
-  make_decays(0);
-  fetch_gate(1);
   for (int n = 0; n < nch; ++n) {
     const int t0 = t_begin + (REV ? nch - 1 - n : n) * C;
-    const Decays<C> &dec = decs[n & 1];
+    const Decays<C> &dec = decs[n % BATCH];
+    // loads come back in their order: gates are asked for before the rows of a
+    // chunk, and used four chunks later
+    if (n % BATCH == 0) {
+      make_decays(n);
+      fetch_gates(n + BATCH);
+    }
     ra.stash(ta);
     rb.stash(tb);
     rc.stash(tc);
     if constexpr (DOT) rd.stash(td);
     __syncthreads();
     if (n + 1 < nch) fetch(REV ? t0 - C : t0 + C);
-    make_decays(n + 1);
-    fetch_gate(n + 2);
     const float *const far_w = REV ? dec.last : dec.first;
     const float *const add_w = REV ? dec.first : dec.last;
 
@@ -541,7 +570,7 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
         fc[u][ct] = T2::by_col(tc, w * CW + ct * 16, u, g, m);
 
     // and the pairs
-    const size_t row = (size_t)q.H * D2;
+    const int row = q.H * D2;
     const size_t o_chunk = (((size_t)b * q.T + t0) * q.H + h) * D2;
     const unsigned o_lane = (unsigned)(m * row) + w * CW + 4 * g;
 #pragma unroll
@@ -555,28 +584,48 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
           acc[rt][ct] = Mma<IO>::mma(fc[u][ct], f, acc[rt][ct]);
       }
     }
-    if (t0 + C <= live_end) {
-#pragma unroll
-      for (int rt = 0; rt < NB; ++rt)
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-          put4<IO>(p.out, p.out_f32,
-                   o_chunk + rt * 16 * row + ct * 16, o_lane, acc[rt][ct]);
-    } else {
+    if (sizeof(IO) == 4 || p.out_f32) {
 #pragma unroll
       for (int rt = 0; rt < NB; ++rt) {
         const int t = t0 + rt * 16 + m;
         if (t >= t_end) continue;
+        float *const o =
+            (float *)p.out + o_chunk + (size_t)(rt * 16) * row + o_lane;
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
-          put4<IO>(p.out, p.out_f32,
-                   o_chunk + rt * 16 * row + ct * 16, o_lane,
-                   t < live_end ? acc[rt][ct] : f32x4{0, 0, 0, 0});
+          *(f32x4 *)(o + ct * 16) =
+              t < live_end ? acc[rt][ct] : f32x4{0, 0, 0, 0};
+      }
+    } else {
+      // two tiles side by side (CT = 2) or one below the other: after the swap
+      // a lane has 8 consecutive columns, of the first tile where g is even
+      bf16 *const o = (bf16 *)p.out + o_chunk;
+#pragma unroll
+      for (int x = 0; x < NB; x += 3 - CT) {
+        const uint2 a = pack4(acc[x][0]);
+        const uint2 c = CT == 2 ? pack4(acc[x][CT - 1])
+                                : pack4(acc[x + 2 - CT][0]);
+        const auto lo = __builtin_amdgcn_permlane16_swap(a.x, c.x, false, false);
+        const auto hi = __builtin_amdgcn_permlane16_swap(a.y, c.y, false, false);
+        uint4 v{lo[0], hi[0], lo[1], hi[1]};
+        const int rr = (CT == 2 ? x : x + (g & 1)) * 16 + m;
+        const int t = t0 + rr;
+        if (t >= live_end) v = uint4{0, 0, 0, 0};
+        if (t < t_end)
+          *(uint4 *)(o + (size_t)(x * 16) * row +
+                     (unsigned)((rr - x * 16) * row + w * CW +
+                                (CT == 2 ? (g & 1) * 16 : 0) +
+                                (g >> 1) * 8)) = v;
       }
     }
     __builtin_amdgcn_sched_barrier(0);
-    if (n + 1 < nch || keep_end)
-      add_chunk<IO, D1, CT, C, NTU>(S, tb, fc, add_w, dec.total, g, m);
+    if (n + 1 < nch || keep_end) {
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) S[kt][ct] *= dec.total;
+      add_chunk<IO, D1, CT, C, NTU>(S, tb, fc, add_w, g, m);
+    }
     __syncthreads();
     if constexpr (DOT) {
       const int t = t0 + threadIdx.x;
@@ -634,8 +683,12 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
 }
 
 // ---------------------------------------------------------------------------
-// what a segment adds to a zero state, and its decay; the segment that no
-// other follows is left out
+// What a segment adds to a zero state, and its decay; the segment that no other
+// follows is left out.  The chunks are taken from the end that the state leaves
+// by, so that a chunk's weights are final and nothing is rescaled, and what is
+// decayed to less than 2^-200 by then is left out with all that lies behind it:
+// it is 0 in fp32.
+constexpr double FORGOTTEN = -200.0;
 
 template <typename IO, int D1, int D2>
 __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_local(
@@ -647,7 +700,8 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_local(
   typedef typename Mma<IO>::frag frag;
   __shared__ alignas(16) IO tb[C * Tile<IO, D1>::STR],
       tc[C * Tile<IO, D2>::STR];
-  __shared__ Decays<C> decs[2];
+  __shared__ Decays<C> decs[BATCH];
+  __shared__ double ends[BATCH];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int g = lane >> 4, m = lane & 15;
   const LinSeq &q = p.q;
@@ -668,47 +722,76 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_local(
   unsigned sb, sc;
   const char *pb = operand<IO, D1>(p.b, q, b, h, sb);
   const char *pc = operand<IO, D2>(p.c, q, b, h, sc);
-  Rows<IO, D1, C, NT> rb;
-  Rows<IO, D2, C, NT> rc;
-  float gate = 0.f;
-  double sum = 0.0;
-  auto fetch = [&](int t0) {
-    const int live = live_end - t0;
-    rb.fetch(pb + (size_t)t0 * sb, sb, live);
-    rc.fetch(pc + (size_t)t0 * sc, sc, live);
+  // two chunks ahead: there is little to do between a chunk's loads and the
+  // next's
+  Rows<IO, D1, C, NT> rb[2];
+  Rows<IO, D2, C, NT> rc[2];
+  Gates<C, NW> gates;
+  const bool back = !p.rev;
+  double sum = 0.0;  // decay of the chunks taken
+  auto t_of = [&](int n) { return t_begin + (back ? nch - 1 - n : n) * C; };
+  auto fetch = [&](auto &b, auto &c, int n) {
+    if (n >= nch) return;
+    const int t0 = t_of(n), live = live_end - t0;
+    b.fetch(pb + (size_t)t0 * sb, sb, live);
+    c.fetch(pc + (size_t)t0 * sc, sc, live);
   };
-  auto fetch_gate = [&](int n) {
-    if (w != 0 || n >= nch) return;
-    const int t = t_begin + (p.rev ? nch - 1 - n : n) * C + lane;
-    gate = lane < C && t < live_end ? load_gate(q, b, h, t) : 0.f;
+  auto fetch_gates = [&](int n0) {
+    gates.fetch(q, b, h, n0, nch, back, t_begin, live_end, w, lane);
   };
-  auto make_decays = [&](int n) {
-    if (w == 0 && n < nch)
-      sum += decays<C>(decs[n & 1], gate, p.add_scale, p.add_scale, lane);
-  };
-  if (nch > 0) fetch(t_begin + (p.rev ? nch - 1 : 0) * C);
-  fetch_gate(0);
-  make_decays(0);
-  fetch_gate(1);
-  for (int n = 0; n < nch; ++n) {
-    const int t0 = t_begin + (p.rev ? nch - 1 - n : n) * C;
-    const Decays<C> &dec = decs[n & 1];
-    rb.stash(tb);
-    rc.stash(tc);
+  // the weights of up to 4 chunks from n0 on; false: they count as nothing
+  auto make_decays = [&](int n0) {
+    if (n0 > 0 && sum < FORGOTTEN) return false;
+    double G[gates.N];
+#pragma unroll
+    for (int i = 0; i < gates.N; ++i) {
+      const int x = w + i * NW;
+      if (x >= BATCH) break;
+      const double end = decay_sums<C>(gates.g[i], lane, G[i]);
+      if (lane == 0) ends[x] = end;
+    }
     __syncthreads();
-    if (n + 1 < nch) fetch(p.rev ? t0 - C : t0 + C);
-    make_decays(n + 1);
-    fetch_gate(n + 2);
+    double at[BATCH + 1];
+    at[0] = sum;
+#pragma unroll
+    for (int x = 0; x < BATCH; ++x) at[x + 1] = at[x] + ends[x];
+    sum = at[BATCH];
+#pragma unroll
+    for (int i = 0; i < gates.N; ++i) {
+#pragma unroll
+      for (int x = 0; x < BATCH; ++x)
+        if (x == w + i * NW && lane < C)
+          decs[x].first[lane] =
+              p.add_scale *
+              exp2_diff(back ? ends[x] - G[i] + at[x] : G[i] + at[x]);
+    }
+    return true;
+  };
+  auto step = [&](auto &b, auto &c, int n) {
+    if (n % BATCH == 0) {
+      if (!make_decays(n)) return false;
+      fetch_gates(n + BATCH);
+    }
+    b.stash(tb);
+    c.stash(tc);
+    __syncthreads();
+    fetch(b, c, n + 2);
     frag fc[NTU][CT];
 #pragma unroll
     for (int u = 0; u < NTU; ++u)
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct)
-        fc[u][ct] =
-            Tile<IO, D2>::by_col(tc, w * CW + ct * 16, u, g, m);
-    add_chunk<IO, D1, CT, C, NTU>(S, tb, fc, p.rev ? dec.first : dec.last,
-                                  dec.total, g, m);
+        fc[u][ct] = Tile<IO, D2>::by_col(tc, w * CW + ct * 16, u, g, m);
+    add_chunk<IO, D1, CT, C, NTU>(S, tb, fc, decs[n % BATCH].first, g, m);
     __syncthreads();
+    return true;
+  };
+  fetch_gates(0);
+  fetch(rb[0], rc[0], 0);
+  fetch(rb[1], rc[1], 1);
+  for (int n = 0; n < nch; n += 2) {
+    if (!step(rb[0], rc[0], n)) break;
+    if (n + 1 < nch && !step(rb[1], rc[1], n + 1)) break;
   }
   float *const o = p.s + (chain * q.NS + s) * D1 * D2;
 #pragma unroll
