@@ -62,8 +62,7 @@ struct LinOperand {
 struct LinSweep {
   LinSeq q;
   LinOperand a, b, c, d;      // [.., D1], [.., D1], [.., D2], [.., D2]
-  void *out;                  // [B,T,H,D2]
-  int out_f32;
+  void *out, *out_rest;       // [B,T,H,D2]; bf16: the rounded-off rest, or null
   float pair_scale, far_scale, add_scale;
   const float *s_in;          // [B,H,NS,D1,D2] (transposed: D2,D1) or null
   float *s_end;               // [B,H,D1,D2], of the last segment, or null

@@ -175,8 +175,7 @@ __global__ __launch_bounds__(256) void kda_lin_gate_sum(const double *sums,
 // gradients of shared query and key heads: the sum over the value heads that
 // share one, in their order
 
-template <typename IO>
-__global__ __launch_bounds__(256) void kda_lin_heads(const float *x, IO *y,
+__global__ __launch_bounds__(256) void kda_lin_heads(const float *x, float *y,
                                                      size_t n4, int D4,
                                                      int G) {
   const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
@@ -184,10 +183,25 @@ __global__ __launch_bounds__(256) void kda_lin_heads(const float *x, IO *y,
   const f32x4 *v = (const f32x4 *)x + i / D4 * G * D4 + i % D4;
   f32x4 s = v[0];
   for (int k = 1; k < G; ++k) s += v[(size_t)k * D4];
-  if constexpr (sizeof(IO) == 2)
-    ((bf16x4 *)y)[i] = bf16x4{(bf16)s[0], (bf16)s[1], (bf16)s[2], (bf16)s[3]};
-  else
-    ((f32x4 *)y)[i] = s;
+  ((f32x4 *)y)[i] = s;
+}
+// bf16: each value as a rounded one and the rest; 8 of them a thread
+__global__ __launch_bounds__(256) void kda_lin_heads2(const bf16 *x,
+                                                      const bf16 *rest,
+                                                      bf16 *y, size_t n8,
+                                                      int D8, int G) {
+  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n8) return;
+  const size_t at = i / D8 * G * D8 + i % D8;
+  float s[8] = {};
+  for (int k = 0; k < G; ++k) {
+    Raw8<bf16> a, b;
+    a.load(x + (at + (size_t)k * D8) * 8);
+    b.load(rest + (at + (size_t)k * D8) * 8);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e] += a.get(e) + b.get(e);
+  }
+  store8(y + i * 8, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -436,6 +450,9 @@ hipError_t launch_linattn_backward(const LinParams &p, hipStream_t st) {
     ds_in = ds;
   }
   const bool shared = p.H != p.Hk, gate = p.dg != nullptr;
+  // the sweeps that can write 32 bits of a bf16 result are those with the
+  // gate's sums
+  const bool dots = gate || (shared && p.io_bf16);
   LinSweep w{};
   w.q = seq;
   // dv
@@ -447,16 +464,20 @@ hipError_t launch_linattn_backward(const LinParams &p, hipStream_t st) {
   LIN_TRY(lin::sweep(p.io_bf16, p.Dk, p.Dv, 1, LIN_PLAIN, w, st));
   // dk
   w.a = v; w.b = dO; w.c = q; w.d = k;
+  // shared heads: 32 bits a value, in bf16 as two halves of the workspace
+  const size_t part = (size_t)p.B * p.T * p.H * p.Dk * 2;
+  const bool rest = shared && p.io_bf16;
   w.out = shared ? (void *)(p.ws + l.dk) : p.dk;
-  w.out_f32 = shared;
+  w.out_rest = rest ? p.ws + l.dk + part : nullptr;
   w.s_end = nullptr;
   w.s_transposed = 1;
   w.far_dot = (float *)(p.ws + l.early);
-  LIN_TRY(lin::sweep(p.io_bf16, p.Dv, p.Dk, 1, gate ? LIN_FAR : LIN_PLAIN, w,
+  LIN_TRY(lin::sweep(p.io_bf16, p.Dv, p.Dk, 1, dots ? LIN_FAR : LIN_PLAIN, w,
                      st));
   // dq
   w.a = dO; w.b = v; w.c = k; w.d = q;
   w.out = shared ? (void *)(p.ws + l.dq) : p.dq;
+  w.out_rest = rest ? p.ws + l.dq + part : nullptr;
   w.far_scale = p.scale; w.add_scale = 1.f;
   w.s_in = s_in;
   w.e_with = ds_in;
@@ -464,19 +485,21 @@ hipError_t launch_linattn_backward(const LinParams &p, hipStream_t st) {
   w.pair_dot = (float *)(p.ws + l.pairs);
   w.e_out = (float *)(p.ws + l.ends);
   LIN_TRY(lin::sweep(p.io_bf16, p.Dv, p.Dk, 0,
-                     gate ? LIN_FAR_PAIRS : LIN_PLAIN, w, st));
+                     dots ? LIN_FAR_PAIRS : LIN_PLAIN, w, st));
   if (shared) {
-    const size_t n4 = (size_t)p.B * p.T * p.Hk * p.Dk / 4;
-    const unsigned blocks = (unsigned)((n4 + 255) / 256);
+    const int V = p.io_bf16 ? 8 : 4;
+    const size_t n = (size_t)p.B * p.T * p.Hk * p.Dk / V;
+    const unsigned blocks = (unsigned)((n + 255) / 256);
     for (int i = 0; i < 2; ++i) {
-      const float *x = (const float *)(p.ws + (i ? l.dk : l.dq));
+      const char *x = p.ws + (i ? l.dk : l.dq);
       void *y = i ? p.dk : p.dq;
       if (p.io_bf16)
-        lin::kda_lin_heads<bf16><<<blocks, 256, 0, st>>>(x, (bf16 *)y, n4,
-                                                         p.Dk / 4, seq.G);
+        lin::kda_lin_heads2<<<blocks, 256, 0, st>>>(
+            (const bf16 *)x, (const bf16 *)(x + part), (bf16 *)y, n, p.Dk / V,
+            seq.G);
       else
-        lin::kda_lin_heads<float><<<blocks, 256, 0, st>>>(x, (float *)y, n4,
-                                                          p.Dk / 4, seq.G);
+        lin::kda_lin_heads<<<blocks, 256, 0, st>>>(
+            (const float *)x, (float *)y, n, p.Dk / V, seq.G);
       LIN_TRY(hipGetLastError());
     }
   }

@@ -141,6 +141,50 @@ __device__ __forceinline__ void weights(const float *w, int u, int g,
 }
 
 // ---------------------------------------------------------------------------
+// Memory is read and written through buffer resources, whose bounds take the
+// place of branches: what lies past `bytes` reads as 0 and is not written.  With
+// a branch around the loads or stores of a partial chunk the compiler waits
+// for everything in flight where the paths meet: the next chunk's rows came in
+// one operand after the other, and only once the last chunk's output was
+// written.
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void *p,
+                                                         long long bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<void *>(p), 0, bytes > 0 ? (int)bytes : 0, 0x00027000);
+}
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ uint4 load16(__amdgpu_buffer_rsrc_t r,
+                                        unsigned at) {
+  return __builtin_bit_cast(
+      uint4, (u32x4)__builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0));
+}
+__device__ __forceinline__ void store16(__amdgpu_buffer_rsrc_t r, unsigned at,
+                                        uint4 v) {
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), r, at,
+                                         0, 0);
+}
+
+// The wait before a loop over chunks: with rows in flight into the loop the
+// compiler would count, at every turn, as if no output had been written since
+// they were asked for, and wait for it.
+__device__ __forceinline__ void all_loaded() {
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+}
+
+// What is computed from x is computed here, and not kept in registers over a
+// whole loop: a chunk's offsets would take 24 of them.
+__device__ __forceinline__ void opaque(unsigned &x) {
+  asm volatile("" : "+v"(x));
+}
+
+// bytes of `rows` rows of `row` bytes, `stride` bytes apart
+__device__ __forceinline__ long long extent(int rows, unsigned stride,
+                                            int row) {
+  return rows > 0 ? (long long)(rows - 1) * stride + row : 0;
+}
+
+// ---------------------------------------------------------------------------
 // a chunk's rows on their way from memory to LDS
 
 template <typename IO, int D, int C, int NT> struct Rows {
@@ -148,25 +192,16 @@ template <typename IO, int D, int C, int NT> struct Rows {
   static constexpr int N = (C * UPR + NT - 1) / NT;
   static constexpr int STEP = NT / UPR;  // rows from a thread's unit to its next
   uint4 r[N];
-  // rows from `live` on are zeros.  A chunk is less than 2^30 bytes long (a
-  // token at most 2^24): one 32-bit offset a lane serves all its units, the
-  // rest of the address is the same for all lanes
+  // rows from `live` on (none where it is not above 0) are zeros.  A chunk is
+  // at most 2^30 bytes long (a token at most 2^24)
   __device__ __forceinline__ void fetch(const char *p, unsigned stride,
                                         int live) {
-    const int row0 = threadIdx.x / UPR;
-    const unsigned v = row0 * stride + threadIdx.x % UPR * 16;
-    if (live >= C && C % STEP == 0) {
+    const auto rs =
+        buffer(p, extent(live < C ? live : C, stride, D * (int)sizeof(IO)));
+    unsigned v = threadIdx.x / UPR * stride + threadIdx.x % UPR * 16;
+    opaque(v);
 #pragma unroll
-      for (int n = 0; n < N; ++n)
-        r[n] = *(const uint4 *)(p + (size_t)(n * STEP) * stride + v);
-    } else {
-#pragma unroll
-      for (int n = 0; n < N; ++n) {
-        r[n] = uint4{0, 0, 0, 0};
-        if (row0 + n * STEP < live && row0 + n * STEP < C)
-          r[n] = *(const uint4 *)(p + (size_t)(n * STEP) * stride + v);
-      }
-    }
+    for (int n = 0; n < N; ++n) r[n] = load16(rs, v + n * STEP * stride);
   }
   __device__ __forceinline__ void stash(IO *t) const {
     const int row0 = threadIdx.x / UPR;
@@ -201,6 +236,8 @@ template <int C> struct Decays {
   double G[C];                   // log2 of the decay up to and with a token
   alignas(16) float first[C];    // exp(G_i), what the chunk's start reaches
   alignas(16) float last[C];     // exp(G_C - G_i), what reaches its end
+  alignas(16) float tile[C];     // within 16 tokens: to their last, or (REV)
+                                 // from the one before their first
   float total;                   // exp(G_C)
 };
 
@@ -232,15 +269,17 @@ __device__ __forceinline__ double add_dpp(double x) {
 constexpr int BATCH = 4;
 
 // by one wave: the sums G of a chunk's log-decays, g that of token `lane` (0
-// past the end); returns their end
+// past the end), and the sums inside its 16 tokens; returns their end
 template <int C>
-__device__ __forceinline__ double decay_sums(float g, int lane, double &x) {
+__device__ __forceinline__ double decay_sums(float g, int lane, double &x,
+                                             double &tile) {
   g = g < -1e4f ? -1e4f : g;
   x = lane < C ? (double)g * 1.4426950408889634074 : 0.0;
   x = add_dpp<0x111, 0xf>(x);  // row_shr:1, 2, 4, 8
   x = add_dpp<0x112, 0xf>(x);
   x = add_dpp<0x114, 0xf>(x);
   x = add_dpp<0x118, 0xf>(x);
+  tile = x;
   x = add_dpp<0x142, 0xa>(x);  // row_bcast:15 into rows 1 and 3
   x = add_dpp<0x143, 0xc>(x);  // row_bcast:31 into rows 2 and 3
   const long long v = __builtin_bit_cast(long long, x);
@@ -314,9 +353,29 @@ __device__ __forceinline__ uint2 pack4(f32x4 v) {
       uint2, bf16x4{(bf16)v[0], (bf16)v[1], (bf16)v[2], (bf16)v[3]});
 }
 
+// what pack4's rounding leaves of v
+__device__ __forceinline__ f32x4 rest4(f32x4 v, uint2 r) {
+  return f32x4{v[0] - __uint_as_float(r.x << 16),
+               v[1] - __uint_as_float(r.x & 0xffff0000u),
+               v[2] - __uint_as_float(r.y << 16),
+               v[3] - __uint_as_float(r.y & 0xffff0000u)};
+}
+
 // waves of a workgroup and columns a wave owns
 template <int D2> constexpr int nwaves() {
   return D2 >= 64 ? 4 : D2 / 16;
+}
+
+// The wave that makes unit u2 (a 16 x 32 or 16 x 16 piece) of row rt of the pair
+// products.  A row's units by one wave would give the last wave four tiles of 16
+// x 16 and the first one; so it is three at most.  Sums along a row (by_row)
+// need it all in one place.
+template <int NW, int NB, bool REV, bool BY_ROW>
+__device__ constexpr int pair_owner(int rt, int u2) {
+  if (BY_ROW || NW != 4) return rt % NW;
+  const int r = REV ? NB - 1 - rt : rt, u = REV ? 1 - u2 : u2;
+  if (NB == 2) return r + u;  // units of one tile: (0,0), (1,0), (1,1)
+  return r == 3 ? u : r == 2 ? 2 : r == 1 ? 3 : 0;
 }
 
 // ---------------------------------------------------------------------------
@@ -363,29 +422,36 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
     for (long long i = threadIdx.x; i < n; i += NT) {
       const size_t at = (((size_t)b * q.T + t0 + i / (D2 / 8)) * q.H + h) * D2 +
                         i % (D2 / 8) * 8;
-      if (sizeof(IO) == 4 || p.out_f32) store8_zero((float *)p.out + at);
-      else store8_zero((bf16 *)p.out + at);
+      store8_zero((IO *)p.out + at);
+      if (DOT && p.out_rest) store8_zero((IO *)p.out_rest + at);
     }
   }
 
   // the state's columns of this wave
   f32x4 S[KT][CT];
-  const size_t s_at = (chain * q.NS + s) * D1 * D2;
+  const float *const s_at = p.s_in + (chain * q.NS + s) * D1 * D2;
+  const int s_col = w * CW + m;
+  if (!p.s_in) {
 #pragma unroll
-  for (int kt = 0; kt < KT; ++kt)
+    for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
-      const int row = kt * 16 + 4 * g, col = w * CW + ct * 16 + m;
-      S[kt][ct] = f32x4{0, 0, 0, 0};
-      if (p.s_in) {
-        if (p.s_transposed)
-          S[kt][ct] = *(const f32x4 *)(p.s_in + s_at + (size_t)col * D1 + row);
-        else
+      for (int ct = 0; ct < CT; ++ct) S[kt][ct] = f32x4{0, 0, 0, 0};
+  } else if (p.s_transposed) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            S[kt][ct][e] = p.s_in[s_at + (size_t)(row + e) * D2 + col];
-      }
-    }
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct)
+        S[kt][ct] = *(const f32x4 *)(s_at + (s_col + ct * 16) * D1 + kt * 16 +
+                                     4 * g);
+  } else {
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          S[kt][ct][e] = s_at[(kt * 16 + 4 * g + e) * D2 + s_col + ct * 16];
+  }
 
   unsigned sa, sb, sc, sd = 0;
   const char *pa = operand<IO, D1>(p.a, q, b, h, sa);
@@ -395,12 +461,13 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
   if constexpr (DOT) pd = operand<IO, D2>(p.d, q, b, h, sd);
   Rows<IO, D1, C, NT> ra, rb;
   Rows<IO, D2, C, NT> rc, rd;
-  auto fetch = [&](int t0) {
-    const int live = live_end - t0;
-    ra.fetch(pa + (size_t)t0 * sa, sa, live);
-    rb.fetch(pb + (size_t)t0 * sb, sb, live);
-    rc.fetch(pc + (size_t)t0 * sc, sc, live);
-    if constexpr (DOT) rd.fetch(pd + (size_t)t0 * sd, sd, live);
+  auto fetch = [&](int n) {
+    const int t0 = t_begin + (REV ? nch - 1 - n : n) * C;
+    const int live = n < nch ? live_end - t0 : 0;
+    ra.fetch(pa + (long long)t0 * sa, sa, live);
+    rb.fetch(pb + (long long)t0 * sb, sb, live);
+    rc.fetch(pc + (long long)t0 * sc, sc, live);
+    if constexpr (DOT) rd.fetch(pd + (long long)t0 * sd, sd, live);
   };
   Gates<C, NW> gates;
   auto fetch_gates = [&](int n0) {
@@ -411,10 +478,12 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
     for (int i = 0; i < gates.N; ++i) {
       const int x = w + i * NW;
       if (x >= BATCH || n0 + x >= nch) break;
-      double G;
-      const double end = decay_sums<C>(gates.g[i], lane, G);
+      double G, tile;
+      const double end = decay_sums<C>(gates.g[i], lane, G, tile);
+      if (!REV) tile = __shfl(tile, lane | 15, 64) - tile;
       if (lane < C) {
         decs[x].G[lane] = G;
+        decs[x].tile[lane] = exp2_diff(tile);
         decs[x].first[lane] = (REV ? p.add_scale : p.far_scale) * exp2_diff(G);
         decs[x].last[lane] =
             (REV ? p.far_scale : p.add_scale) * exp2_diff(end - G);
@@ -426,7 +495,8 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
   const bool keep_end = (last_seg && p.s_end) || DOT == LIN_FAR_PAIRS;
 
   fetch_gates(0);
-  if (nch > 0) fetch(t_begin + (REV ? nch - 1 : 0) * C);
+  fetch(0);
+  all_loaded();
   for (int n = 0; n < nch; ++n) {
     const int t0 = t_begin + (REV ? nch - 1 - n : n) * C;
     const Decays<C> &dec = decs[n % BATCH];
@@ -440,41 +510,56 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
     rb.stash(tb);
     rc.stash(tc);
     if constexpr (DOT) rd.stash(td);
-    __syncthreads();
-    if (n + 1 < nch) fetch(REV ? t0 - C : t0 + C);
+    barrier_keep_vmem();
+    fetch(n + 1);
     const float *const far_w = REV ? dec.last : dec.first;
     const float *const add_w = REV ? dec.first : dec.last;
 
-    // the pair products, transposed: rows j, columns i = rt * 16 + m
-    for (int rt = w; rt < NB; rt += NW) {
-      frag fa[NKU];
+    // the pair products, transposed: rows j, columns i = rt * 16 + m.  Where
+    // all of a tile's j lie before (REV: behind) its i, the decay between them
+    // is that from i to the border next to j's tile, one a lane, times that
+    // from there to j
 #pragma unroll
-      for (int u = 0; u < NKU; ++u)
-        fa[u] = T1::by_row(ta, rt * 16, u, g, m);
+    for (int rt = 0; rt < NB; ++rt) {
       const int i = rt * 16 + m;
-      const double Gi = dec.G[i];
       float run = 0.f;  // pairs of i with earlier tiles' j
 #pragma unroll
       for (int u2 = 0; u2 < NTU; ++u2) {
         if (REV ? u2 * TPU + TPU - 1 < rt : u2 * TPU > rt) continue;
+        if (pair_owner<NW, NB, REV, DOT == LIN_FAR_PAIRS>(rt, u2) != w)
+          continue;
         f32x4 tile[2];
         tile[0] = tile[1] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int u = 0; u < NKU; ++u) {
+          const frag fa = T1::by_row(ta, rt * 16, u, g, m);
+#pragma unroll
+          for (int x = 0; x < TPU; ++x) {
+            const int jt = u2 * TPU + x;
+            if (REV ? jt >= rt : jt <= rt)
+              tile[x] = Mma<IO>::mma(T1::by_row(tb, jt * 16, u, g, m), fa,
+                                     tile[x]);
+          }
+        }
 #pragma unroll
         for (int x = 0; x < TPU; ++x) {
           const int jt = u2 * TPU + x;
           if (REV ? jt < rt : jt > rt) continue;
-          f32x4 acc{0, 0, 0, 0};
+          f32x4 &acc = tile[x];
+          if (jt == rt) {
 #pragma unroll
-          for (int u = 0; u < NKU; ++u)
-            acc = Mma<IO>::mma(T1::by_row(tb, jt * 16, u, g, m), fa[u], acc);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int j = jt * 16 + 4 * g + e;
-            const double d = REV ? dec.G[j] - Gi : Gi - dec.G[j];
-            const float f = acc[e] * (p.pair_scale * exp2_diff(d));
-            acc[e] = (REV ? j >= i : j <= i) ? f : 0.f;
+            for (int e = 0; e < 4; ++e) {
+              const int j = jt * 16 + 4 * g + e;
+              const double d = REV ? dec.G[j] - dec.G[i] : dec.G[i] - dec.G[j];
+              const float f = acc[e] * (p.pair_scale * exp2_diff(d));
+              acc[e] = (REV ? j >= i : j <= i) ? f : 0.f;
+            }
+          } else {
+            const double d = REV ? dec.G[jt * 16 - 1] - dec.G[i]
+                                 : dec.G[i] - dec.G[jt * 16 + 15];
+            acc *= *(const f32x4 *)(dec.tile + jt * 16 + 4 * g) *
+                   (p.pair_scale * exp2_diff(d));
           }
-          tile[x] = acc;
           if constexpr (DOT == LIN_FAR_PAIRS) {
             // pairs (i, t') with t' < j, summed over i >= j
             f32x4 qk{0, 0, 0, 0};
@@ -561,7 +646,7 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
         if (g == 0) far_part[w][rt * 16 + m] = dot;
       }
     }
-    __syncthreads();
+    barrier_keep_vmem();
     frag fc[NTU][CT];
 #pragma unroll
     for (int u = 0; u < NTU; ++u)
@@ -570,9 +655,6 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
         fc[u][ct] = T2::by_col(tc, w * CW + ct * 16, u, g, m);
 
     // and the pairs
-    const int row = q.H * D2;
-    const size_t o_chunk = (((size_t)b * q.T + t0) * q.H + h) * D2;
-    const unsigned o_lane = (unsigned)(m * row) + w * CW + 4 * g;
 #pragma unroll
     for (int rt = 0; rt < NB; ++rt) {
 #pragma unroll
@@ -584,38 +666,56 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
           acc[rt][ct] = Mma<IO>::mma(fc[u][ct], f, acc[rt][ct]);
       }
     }
-    if (sizeof(IO) == 4 || p.out_f32) {
+    if (t0 + C > live_end) {
 #pragma unroll
-      for (int rt = 0; rt < NB; ++rt) {
-        const int t = t0 + rt * 16 + m;
-        if (t >= t_end) continue;
-        float *const o =
-            (float *)p.out + o_chunk + (size_t)(rt * 16) * row + o_lane;
+      for (int rt = 0; rt < NB; ++rt)
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
-          *(f32x4 *)(o + ct * 16) =
-              t < live_end ? acc[rt][ct] : f32x4{0, 0, 0, 0};
-      }
+          if (t0 + rt * 16 + m >= live_end) acc[rt][ct] = f32x4{0, 0, 0, 0};
+    }
+    const unsigned row = (unsigned)q.H * D2 * sizeof(IO);
+    const size_t o_at = (((size_t)b * q.T + t0) * q.H + h) * D2;
+    const long long o_bytes =
+        extent(min(C, t_end - t0), row, D2 * (int)sizeof(IO));
+    const auto o = buffer((IO *)p.out + o_at, o_bytes);
+    if constexpr (sizeof(IO) == 4) {
+      unsigned at = m * row + (w * CW + 4 * g) * 4;
+      opaque(at);
+#pragma unroll
+      for (int rt = 0; rt < NB; ++rt)
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+          store16(o, at + rt * 16 * row + ct * 64,
+                  __builtin_bit_cast(uint4, acc[rt][ct]));
     } else {
       // two tiles side by side (CT = 2) or one below the other: after the swap
-      // a lane has 8 consecutive columns, of the first tile where g is even
-      bf16 *const o = (bf16 *)p.out + o_chunk;
+      // a lane has 8 consecutive columns, of the first tile where g is even.
+      // (8 bytes a lane took 4 us more at B1 T8192 H32 D128.)  The rounded-off
+      // rest goes to a second tensor, where there is one
+      const auto o2 = buffer((IO *)p.out_rest + o_at,
+                             p.out_rest ? o_bytes : 0);
+      unsigned at = (CT == 2 ? m : m + (g & 1) * 16) * row +
+                    (w * CW + (CT == 2 ? (g & 1) * 16 : 0) + (g >> 1) * 8) * 2;
+      opaque(at);
 #pragma unroll
       for (int x = 0; x < NB; x += 3 - CT) {
-        const uint2 a = pack4(acc[x][0]);
-        const uint2 c = CT == 2 ? pack4(acc[x][CT - 1])
-                                : pack4(acc[x + 2 - CT][0]);
-        const auto lo = __builtin_amdgcn_permlane16_swap(a.x, c.x, false, false);
-        const auto hi = __builtin_amdgcn_permlane16_swap(a.y, c.y, false, false);
-        uint4 v{lo[0], hi[0], lo[1], hi[1]};
-        const int rr = (CT == 2 ? x : x + (g & 1)) * 16 + m;
-        const int t = t0 + rr;
-        if (t >= live_end) v = uint4{0, 0, 0, 0};
-        if (t < t_end)
-          *(uint4 *)(o + (size_t)(x * 16) * row +
-                     (unsigned)((rr - x * 16) * row + w * CW +
-                                (CT == 2 ? (g & 1) * 16 : 0) +
-                                (g >> 1) * 8)) = v;
+        constexpr int DY = 2 - CT;  // the second tile's row and column
+        const f32x4 a = acc[x][0], c = acc[x + DY][CT - 1];
+        uint2 ha = pack4(a), hc = pack4(c);
+        const auto l1 = __builtin_amdgcn_permlane16_swap(ha.x, hc.x, false, false);
+        const auto l2 = __builtin_amdgcn_permlane16_swap(ha.y, hc.y, false, false);
+        store16(o, at + x * 16 * row, uint4{l1[0], l2[0], l1[1], l2[1]});
+        if constexpr (DOT) {
+          // a store that meets no memory where there is no second tensor: a
+          // branch around it would make the next chunk wait for the first
+          if (p.out_rest) {
+            ha = pack4(rest4(a, ha));
+            hc = pack4(rest4(c, hc));
+          }
+          const auto r1 = __builtin_amdgcn_permlane16_swap(ha.x, hc.x, false, false);
+          const auto r2 = __builtin_amdgcn_permlane16_swap(ha.y, hc.y, false, false);
+          store16(o2, at + x * 16 * row, uint4{r1[0], r2[0], r1[1], r2[1]});
+        }
       }
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -626,7 +726,7 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
         for (int ct = 0; ct < CT; ++ct) S[kt][ct] *= dec.total;
       add_chunk<IO, D1, CT, C, NTU>(S, tb, fc, add_w, g, m);
     }
-    __syncthreads();
+    barrier_keep_vmem();
     if constexpr (DOT) {
       const int t = t0 + threadIdx.x;
       if (threadIdx.x < C && t < t_end) {
@@ -663,17 +763,17 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
           const int row = kt * 16 + 4 * g, col = w * CW + ct * 16 + m;
-          const f32x4 y =
-              *(const f32x4 *)(p.e_with + s_at + (size_t)col * D1 + row);
+          const f32x4 y = *(const f32x4 *)(
+              p.e_with + (chain * q.NS + s) * D1 * D2 + col * D1 + row);
           x += (S[kt][ct][0] * y[0] + S[kt][ct][1] * y[1]) +
                (S[kt][ct][2] * y[2] + S[kt][ct][3] * y[3]);
         }
     }
     x = group_sum<32>(x);
     x += __shfl_xor(x, 32, 64);
-    __syncthreads();
+    barrier_keep_vmem();
     if (lane == 0) far_part[w][0] = x;
-    __syncthreads();
+    barrier_keep_vmem();
     if (threadIdx.x == 0) {
       float y = 0.f;
       for (int i = 0; i < NW; ++i) y += far_part[i][0];
@@ -731,10 +831,9 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_local(
   double sum = 0.0;  // decay of the chunks taken
   auto t_of = [&](int n) { return t_begin + (back ? nch - 1 - n : n) * C; };
   auto fetch = [&](auto &b, auto &c, int n) {
-    if (n >= nch) return;
-    const int t0 = t_of(n), live = live_end - t0;
-    b.fetch(pb + (size_t)t0 * sb, sb, live);
-    c.fetch(pc + (size_t)t0 * sc, sc, live);
+    const int t0 = t_of(n), live = n < nch ? live_end - t0 : 0;
+    b.fetch(pb + (long long)t0 * sb, sb, live);
+    c.fetch(pc + (long long)t0 * sc, sc, live);
   };
   auto fetch_gates = [&](int n0) {
     gates.fetch(q, b, h, n0, nch, back, t_begin, live_end, w, lane);
@@ -747,10 +846,11 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_local(
     for (int i = 0; i < gates.N; ++i) {
       const int x = w + i * NW;
       if (x >= BATCH) break;
-      const double end = decay_sums<C>(gates.g[i], lane, G[i]);
+      double tile;
+      const double end = decay_sums<C>(gates.g[i], lane, G[i], tile);
       if (lane == 0) ends[x] = end;
     }
-    __syncthreads();
+    barrier_keep_vmem();
     double at[BATCH + 1];
     at[0] = sum;
 #pragma unroll
@@ -774,7 +874,7 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_local(
     }
     b.stash(tb);
     c.stash(tc);
-    __syncthreads();
+    barrier_keep_vmem();
     fetch(b, c, n + 2);
     frag fc[NTU][CT];
 #pragma unroll
@@ -783,12 +883,13 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_local(
       for (int ct = 0; ct < CT; ++ct)
         fc[u][ct] = Tile<IO, D2>::by_col(tc, w * CW + ct * 16, u, g, m);
     add_chunk<IO, D1, CT, C, NTU>(S, tb, fc, decs[n % BATCH].first, g, m);
-    __syncthreads();
+    barrier_keep_vmem();
     return true;
   };
   fetch_gates(0);
   fetch(rb[0], rc[0], 0);
   fetch(rb[1], rc[1], 1);
+  all_loaded();
   for (int n = 0; n < nch; n += 2) {
     if (!step(rb[0], rc[0], n)) break;
     if (n + 1 < nch && !step(rb[1], rc[1], n + 1)) break;
