@@ -92,7 +92,8 @@ enum LinDot { LIN_PLAIN = 0, LIN_FAR = 1, LIN_FAR_PAIRS = 2 };
 #define KDA_LIN_DECLARE(IO, D1)                                            \
   hipError_t lin_sweep_##IO##_##D1(int D2, int rev, int dot,               \
                                    const LinSweep &p, hipStream_t s);      \
-  hipError_t lin_local_##IO##_##D1(int D2, const LinLocal &p, hipStream_t s)
+  hipError_t lin_local_##IO##_##D1(int D2, const LinLocal &p,              \
+                                   const LinLocal *r, hipStream_t s)
 KDA_LIN_DECLARE(bf16, 16);
 KDA_LIN_DECLARE(bf16, 32);
 KDA_LIN_DECLARE(bf16, 64);

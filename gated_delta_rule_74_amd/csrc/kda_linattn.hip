@@ -18,6 +18,8 @@
 // j-terms, and E across its start is Z + sum of its i-terms; E at a segment's
 // end is the product of both states there.  Where a chunk forgets all but
 // 2^-40, Z is 0.
+#include <algorithm>
+
 #include "kda_linattn.h"
 #include "kda_vec.h"
 
@@ -32,13 +34,17 @@ struct Split {
 
 // Workgroups wanted, and the tokens that a segment has at least and (gradient)
 // at most: see the end of this file's launch logic.
-constexpr int WANTED = 512, MIN_CHUNKS = 4, MAX_CHUNKS = 64;
+#ifndef LIN_WAVES
+#define LIN_WAVES 2048
+#endif
+constexpr int WAVES = LIN_WAVES, MIN_CHUNKS = 4, MAX_CHUNKS = 64;
 
-Split split(int B, int T, int H, int io_bf16, bool grad) {
+Split split(int B, int T, int H, int D, int io_bf16, bool grad) {
   const int C = lin_chunk(io_bf16);
   const int nc = (T + C - 1) / C;
   const long long chains = (long long)B * H;
-  long long ns = (WANTED + chains - 1) / chains;
+  const int wanted = WAVES / (D == 128 ? 8 : 4);
+  long long ns = (wanted + chains - 1) / chains;
   if (ns > nc / MIN_CHUNKS) ns = nc / MIN_CHUNKS;
   if (ns < 1) ns = 1;
   int per = (int)((nc + ns - 1) / ns);
@@ -48,7 +54,7 @@ Split split(int B, int T, int H, int io_bf16, bool grad) {
 
 // ---------------------------------------------------------------------------
 // states before (after) every segment, from what each adds: the local sums are
-// replaced in place.  One thread has 4 elements of one head's states.
+// replaced in place.  One thread has one element of one head's states.
 
 struct ScanSegs {
   float *s;                  // [BH,NS,n]
@@ -58,32 +64,30 @@ struct ScanSegs {
 };
 __global__ __launch_bounds__(256) void kda_lin_scan(ScanSegs f, ScanSegs r,
                                                     int NS, int n) {
+  constexpr int AHEAD = 16;
   const ScanSegs p = blockIdx.z ? r : f;
-  const int i = (blockIdx.y * 256 + threadIdx.x) * 4;
+  const int i = blockIdx.y * 256 + threadIdx.x;
   if (i >= n) return;
   const size_t chain = blockIdx.x;
   float *const s = p.s + chain * NS * n + i;
   const float *const d = p.decay + chain * NS;
-  f32x4 S{0, 0, 0, 0};
-  if (p.first) S = *(const f32x4 *)(p.first + chain * n + i);
-  // the loads of 8 segments first: with one at a time, 16 segments of 32 heads
+  float S = p.first ? p.first[chain * n + i] : 0.f;
+  // the loads of 16 segments first: with one at a time, 16 segments of 32 heads
   // took 12 us
-  for (int k0 = 0; k0 < NS; k0 += 8) {
-    f32x4 x[8];
-    float a[8];
+  for (int k0 = 0; k0 < NS; k0 += AHEAD) {
+    float x[AHEAD], a[AHEAD];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < AHEAD; ++j) {
       const int k = min(k0 + j, NS - 1);
       const size_t at = p.rev ? NS - 1 - k : k;
-      x[j] = *(const f32x4 *)(s + at * n);
+      x[j] = s[at * n];
       a[j] = d[at];
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < AHEAD; ++j) {
       const int k = k0 + j;
-      if (k >= NS) break;
       const size_t at = p.rev ? NS - 1 - k : k;
-      *(f32x4 *)(s + at * n) = S;
+      if (k < NS) s[at * n] = S;
       S = S * a[j] + x[j];  // of the last, which is none, not used
     }
   }
@@ -316,17 +320,18 @@ hipError_t sweep(int io_bf16, int D1, int D2, int rev, int dot,
   }
   return hipErrorInvalidValue;
 }
+// of p, and of r beside it if given
 hipError_t local(int io_bf16, int D1, int D2, const LinLocal &p,
-                 hipStream_t s) {
+                 const LinLocal *r, hipStream_t s) {
   switch (D1) {
-    case 16: return io_bf16 ? lin_local_bf16_16(D2, p, s)
-                            : lin_local_f32_16(D2, p, s);
-    case 32: return io_bf16 ? lin_local_bf16_32(D2, p, s)
-                            : lin_local_f32_32(D2, p, s);
-    case 64: return io_bf16 ? lin_local_bf16_64(D2, p, s)
-                            : lin_local_f32_64(D2, p, s);
-    case 128: return io_bf16 ? lin_local_bf16_128(D2, p, s)
-                             : lin_local_f32_128(D2, p, s);
+    case 16: return io_bf16 ? lin_local_bf16_16(D2, p, r, s)
+                            : lin_local_f32_16(D2, p, r, s);
+    case 32: return io_bf16 ? lin_local_bf16_32(D2, p, r, s)
+                            : lin_local_f32_32(D2, p, r, s);
+    case 64: return io_bf16 ? lin_local_bf16_64(D2, p, r, s)
+                            : lin_local_f32_64(D2, p, r, s);
+    case 128: return io_bf16 ? lin_local_bf16_128(D2, p, r, s)
+                             : lin_local_f32_128(D2, p, r, s);
   }
   return hipErrorInvalidValue;
 }
@@ -376,7 +381,7 @@ Layout layout(int B, int T, int Hk, int H, int Dk, int Dv, Split sp,
 
 hipError_t scan_segments(const ScanSegs &f, const ScanSegs *r, int chains,
                          int NS, int n, hipStream_t s) {
-  const dim3 grid(chains, (n + 1023) / 1024, r ? 2 : 1);
+  const dim3 grid(chains, (n + 255) / 256, r ? 2 : 1);
   kda_lin_scan<<<grid, 256, 0, s>>>(f, r ? *r : f, NS, n);
   return hipGetLastError();
 }
@@ -386,19 +391,19 @@ hipError_t scan_segments(const ScanSegs &f, const ScanSegs *r, int chains,
 long long linattn_segments(int B, int T, int H) {
   long long most = 0;
   for (int i = 0; i < 4; ++i) {
-    const lin::Split sp = lin::split(B, T, H, i & 1, i & 2);
+    const lin::Split sp = lin::split(B, T, H, 16, i & 1, i & 2);
     const long long n = (long long)B * H * sp.NS;
     most = n > most ? n : most;
   }
   return most;
 }
 size_t linattn_ws_bytes(int B, int T, int H, int Dk, int Dv, int io_bf16) {
-  return lin::layout(B, T, H, H, Dk, Dv, lin::split(B, T, H, io_bf16, false),
+  return lin::layout(B, T, H, H, Dk, Dv, lin::split(B, T, H, std::max(Dk, Dv), io_bf16, false),
                      false).bytes;
 }
 size_t linattn_bwd_ws_bytes(int B, int T, int Hk, int H, int Dk, int Dv,
                             int io_bf16) {
-  return lin::layout(B, T, Hk, H, Dk, Dv, lin::split(B, T, H, io_bf16, true),
+  return lin::layout(B, T, Hk, H, Dk, Dv, lin::split(B, T, H, std::max(Dk, Dv), io_bf16, true),
                      true).bytes;
 }
 
@@ -409,7 +414,7 @@ size_t linattn_bwd_ws_bytes(int B, int T, int Hk, int H, int Dk, int Dv,
   } while (0)
 
 hipError_t launch_linattn(const LinParams &p, hipStream_t st) {
-  const lin::Split sp = lin::split(p.B, p.T, p.H, p.io_bf16, false);
+  const lin::Split sp = lin::split(p.B, p.T, p.H, std::max(p.Dk, p.Dv), p.io_bf16, false);
   const lin::Layout l =
       lin::layout(p.B, p.T, p.Hk, p.H, p.Dk, p.Dv, sp, false);
   const LinOperand q{p.q, 1}, k{p.k, 1}, v{p.v, 0};
@@ -419,7 +424,7 @@ hipError_t launch_linattn(const LinParams &p, hipStream_t st) {
   if (sp.NS > 1) {
     float *const s = (float *)(p.ws + l.s);
     LinLocal x{w.q, k, v, 1.f, 0, s, (float *)(p.ws + l.decay)};
-    LIN_TRY(lin::local(p.io_bf16, p.Dk, p.Dv, x, st));
+    LIN_TRY(lin::local(p.io_bf16, p.Dk, p.Dv, x, nullptr, st));
     const lin::ScanSegs f{s, x.decay, p.s0, 0};
     LIN_TRY(lin::scan_segments(f, nullptr, p.B * p.H, sp.NS, p.Dk * p.Dv, st));
     w.s_in = s;
@@ -433,7 +438,7 @@ hipError_t launch_linattn(const LinParams &p, hipStream_t st) {
 }
 
 hipError_t launch_linattn_backward(const LinParams &p, hipStream_t st) {
-  const lin::Split sp = lin::split(p.B, p.T, p.H, p.io_bf16, true);
+  const lin::Split sp = lin::split(p.B, p.T, p.H, std::max(p.Dk, p.Dv), p.io_bf16, true);
   const lin::Layout l = lin::layout(p.B, p.T, p.Hk, p.H, p.Dk, p.Dv, sp, true);
   const LinOperand q{p.q, 1}, k{p.k, 1}, v{p.v, 0}, dO{p.dO, 0};
   const LinSeq seq = lin::seq_of(p, sp);
@@ -441,9 +446,8 @@ hipError_t launch_linattn_backward(const LinParams &p, hipStream_t st) {
   if (sp.NS > 1) {
     float *const s = (float *)(p.ws + l.s), *const ds = (float *)(p.ws + l.ds);
     LinLocal x{seq, k, v, 1.f, 0, s, (float *)(p.ws + l.decay)};
-    LIN_TRY(lin::local(p.io_bf16, p.Dk, p.Dv, x, st));
     LinLocal y{seq, q, dO, p.scale, 1, ds, (float *)(p.ws + l.ddecay)};
-    LIN_TRY(lin::local(p.io_bf16, p.Dk, p.Dv, y, st));
+    LIN_TRY(lin::local(p.io_bf16, p.Dk, p.Dv, x, &y, st));
     const lin::ScanSegs f{s, x.decay, p.s0, 0}, r{ds, y.decay, p.dsT, 1};
     LIN_TRY(lin::scan_segments(f, &r, p.B * p.H, sp.NS, p.Dk * p.Dv, st));
     s_in = s;

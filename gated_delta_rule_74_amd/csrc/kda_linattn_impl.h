@@ -14,11 +14,13 @@
 // with S transposed for dq and dk, and the scale put where it belongs.
 //
 // A workgroup takes one segment of one head, chunk by chunk, with the state in
-// registers: wave w owns 32 (or 16) columns of it, all D1 rows.  The pair
-// products of a chunk are made once, one 16-row tile a wave, and handed to all
-// waves through LDS as operand fragments; the state's accumulator tiles are
-// themselves the operand fragments of S^T a (kda_device.h), so it never
-// leaves its registers.
+// registers: wave w owns 16 columns of it, all D1 rows (below 64 columns the
+// other waves of four only load and make pair products).  The pair products of
+// a chunk are made once and handed to all waves through LDS as operand
+// fragments; the state's accumulator tiles are themselves the operand fragments
+// of S^T a (kda_device.h), so it never leaves its registers.  A chunk's rows
+// come from memory two chunks ahead: one in registers, one in a second set of
+// LDS tiles.
 //
 // Precision.  Decays between tokens are differences of sums held in 64 bits:
 // a sum over a chunk may reach 64e4 (g below -1e4 is taken as -1e4, whose exp
@@ -308,42 +310,237 @@ template <int C, int NW> struct Gates {
 };
 
 // ---------------------------------------------------------------------------
-// S += b^T diag(w) c over a chunk, c as operand fragments
+// the parts of a chunk's work.  A wave has 16 columns: KT tiles of the state, NB
+// of the output.
 
-template <typename IO, int D1, int CT, int C, int NTU>
+template <typename IO> struct Shape {
+  static constexpr int TPU = Mma<IO>::TPU, KU = 16 * TPU;  // tiles a unit
+  static constexpr int C = lin_chunk(sizeof(IO) == 2), NB = C / 16;
+  static constexpr int NTU = C / KU;                       // units over tokens
+  // units over D channels
+  static constexpr int units(int D) { return (D / 16 + TPU - 1) / TPU; }
+  typedef typename Mma<IO>::frag frag;
+};
+
+// S += b^T diag(w) c over a chunk, c as operand fragments
+template <typename IO, int D1>
 __device__ __forceinline__ void add_chunk(
-    f32x4 (&S)[D1 / 16][CT], const IO *tb,
-    const typename Mma<IO>::frag (&c)[NTU][CT], const float *w, int g, int m) {
+    f32x4 (&S)[D1 / 16], const IO *tb,
+    const typename Mma<IO>::frag (&c)[Shape<IO>::NTU], const float *w, int g,
+    int m) {
   constexpr int NE = Mma<IO>::NE;
   typedef typename Mma<IO>::frag frag;
 #pragma unroll
-  for (int u = 0; u < NTU; ++u) {
+  for (int u = 0; u < Shape<IO>::NTU; ++u) {
     float wt[NE];
     weights(w, u, g, wt);
-    frag hi[CT], lo[CT];
+    float x[8] = {};
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
-      float x[8] = {};
+    for (int e = 0; e < NE; ++e) x[e] = Mma<IO>::elem(c[u], e) * wt[e];
+    const frag hi = Mma<IO>::pack(f32x4{x[0], x[1], x[2], x[3]},
+                                  f32x4{x[4], x[5], x[6], x[7]});
+    frag lo = hi;
+    if constexpr (sizeof(IO) == 2) {
 #pragma unroll
-      for (int e = 0; e < NE; ++e) x[e] = Mma<IO>::elem(c[u][ct], e) * wt[e];
-      hi[ct] = Mma<IO>::pack(f32x4{x[0], x[1], x[2], x[3]},
-                             f32x4{x[4], x[5], x[6], x[7]});
-      if constexpr (sizeof(IO) == 2) {
-#pragma unroll
-        for (int e = 0; e < NE; ++e) x[e] -= Mma<IO>::elem(hi[ct], e);
-        lo[ct] = Mma<IO>::pack(f32x4{x[0], x[1], x[2], x[3]},
-                               f32x4{x[4], x[5], x[6], x[7]});
-      }
+      for (int e = 0; e < NE; ++e) x[e] -= Mma<IO>::elem(hi, e);
+      lo = Mma<IO>::pack(f32x4{x[0], x[1], x[2], x[3]},
+                         f32x4{x[4], x[5], x[6], x[7]});
     }
 #pragma unroll
     for (int kt = 0; kt < D1 / 16; ++kt) {
       const frag b = Tile<IO, D1>::by_col(tb, kt * 16, u, g, m);
+      S[kt] = Mma<IO>::mma(b, hi, S[kt]);
+      if constexpr (sizeof(IO) == 2) S[kt] = Mma<IO>::mma(b, lo, S[kt]);
+    }
+  }
+}
+
+// acc = S^T a, transposed: rows are the wave's columns, columns tokens.  EXACT:
+// with what rounding the state to bf16 leaves
+template <typename IO, int D1, bool EXACT>
+__device__ __forceinline__ void far_part(f32x4 (&acc)[Shape<IO>::NB],
+                                         const f32x4 (&S)[D1 / 16],
+                                         const IO *ta, int g, int m) {
+  constexpr int TPU = Shape<IO>::TPU, KT = D1 / 16;
+  constexpr bool LO = EXACT && sizeof(IO) == 2;
+  typedef typename Mma<IO>::frag frag;
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct) {
-        S[kt][ct] = Mma<IO>::mma(b, hi[ct], S[kt][ct]);
-        if constexpr (sizeof(IO) == 2)
-          S[kt][ct] = Mma<IO>::mma(b, lo[ct], S[kt][ct]);
+  for (int rt = 0; rt < Shape<IO>::NB; ++rt) acc[rt] = f32x4{0, 0, 0, 0};
+#pragma unroll
+  for (int u = 0; u < Shape<IO>::units(D1); ++u) {
+    const f32x4 x = S[u * TPU];
+    f32x4 y{0, 0, 0, 0};
+    if constexpr (TPU == 2)
+      if (u * TPU + 1 < KT) y = S[u * TPU + 1];
+    const frag fs = Mma<IO>::pack(x, y);
+    frag fl = fs;
+    if constexpr (LO) {
+      f32x4 x2, y2;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x2[e] = x[e] - Mma<IO>::elem(fs, e);
+        y2[e] = y[e] - Mma<IO>::elem(fs, 4 + e);
       }
+      fl = Mma<IO>::pack(x2, y2);
+    }
+#pragma unroll
+    for (int rt = 0; rt < Shape<IO>::NB; ++rt) {
+      const frag f = Tile<IO, D1>::by_row(ta, rt * 16, u, g, m);
+      acc[rt] = Mma<IO>::mma(fs, f, acc[rt]);
+      if constexpr (LO) acc[rt] = Mma<IO>::mma(fl, f, acc[rt]);
+    }
+  }
+}
+
+// whether row rt has pairs in tile jt
+template <bool REV> constexpr bool has_pairs(int rt, int jt) {
+  return REV ? jt >= rt : jt <= rt;
+}
+// acc += c^T P^T: what the pairs give to out
+template <typename IO, bool REV>
+__device__ __forceinline__ void near_part(
+    f32x4 (&acc)[Shape<IO>::NB], const typename Mma<IO>::frag *tp,
+    const typename Mma<IO>::frag (&c)[Shape<IO>::NTU], int lane) {
+  constexpr int TPU = Shape<IO>::TPU, NTU = Shape<IO>::NTU;
+#pragma unroll
+  for (int rt = 0; rt < Shape<IO>::NB; ++rt)
+#pragma unroll
+    for (int u = 0; u < NTU; ++u)
+      if (has_pairs<REV>(rt, REV ? u * TPU + TPU - 1 : u * TPU))
+        acc[rt] = Mma<IO>::mma(c[u], tp[(rt * NTU + u) * 64 + lane], acc[rt]);
+}
+
+// The wave that makes unit u2 (a 16 x 32 piece, fp32 16 x 16) of row rt of the
+// pair products.  A row by one wave would give the last of four waves four
+// tiles of 16 x 16 and the first one; so it is three at most, over eight waves
+// two, and over eight with a second set of products (SET 1) three.
+template <int NW, int NB, bool REV, int SET>
+__device__ constexpr int pair_owner(int rt, int u2) {
+  const int r = REV ? NB - 1 - rt : rt, u = REV ? 1 - u2 : u2;
+  if (NB == 2) return r + u + (SET ? NW - 3 : 0);
+  if (NW == 8 && SET)
+    return r == 3 ? (u ? 3 : 1) : r == 2 ? (u ? 3 : 5) : r == 1 ? 0 : 1;
+  if (NW == 8) return 2 * r + u;
+  return (r == 3 ? u : r == 2 ? 2 : r == 1 ? 3 : 0) ^ SET;
+}
+
+// sums over the pairs of a tile, for the gate's gradient: for the tile's j, of
+// all pairs with an earlier j of the tile (of the diagonal tiles, whose i is no
+// earlier); for its i, of all pairs with this or a later i
+template <int NB> struct PairSums {
+  float by_j[NB][NB][16], by_i[NB][NB][16];
+  // the sum of all pairs (i, j) of a chunk with i >= t > j, in a fixed order
+  __device__ __forceinline__ float across(int t) const {
+    const int tt = t / 16, k = t % 16;
+    float v = by_j[tt][tt][k];
+    for (int rt = tt + 1; rt < NB; ++rt) v += by_j[rt][tt][k];
+    for (int jt = 0; jt < tt; ++jt) {
+      v += by_i[tt][jt][k];
+      for (int rt = tt + 1; rt < NB; ++rt) v += by_i[rt][jt][0];
+    }
+    return v;
+  }
+};
+
+template <int CTRL>
+__device__ __forceinline__ float add_row_shl(float x) {
+  return x + __int_as_float(__builtin_amdgcn_update_dpp(
+                 0, __float_as_int(x), CTRL, 0xf, 0xf, false));
+}
+
+template <int NB>
+__device__ __forceinline__ void pair_sums(PairSums<NB> &s, int rt, int jt,
+                                          f32x4 qk, int g, int m) {
+  float c[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) c[e] = rt == jt ? qk[e] : group_sum<16>(qk[e]);
+  const float tot = (c[0] + c[1]) + (c[2] + c[3]);
+  const float v1 = __shfl_up(tot, 16, 64), v2 = __shfl_up(tot, 32, 64),
+              v3 = __shfl_up(tot, 48, 64);
+  float pre = 0.f;
+  if (g >= 3) pre += v3;
+  if (g >= 2) pre += v2;
+  if (g >= 1) pre += v1;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float v =
+        rt == jt ? group_sum<16>(4 * g + e <= m ? pre : 0.f) : pre;
+    if (m == 0) s.by_j[rt][jt][4 * g + e] = v;
+    pre += c[e];
+  }
+  if (rt != jt) {
+    float r = (qk[0] + qk[1]) + (qk[2] + qk[3]);
+    r += __shfl_xor(r, 16, 64);
+    r += __shfl_xor(r, 32, 64);
+    r = add_row_shl<0x101>(r);
+    r = add_row_shl<0x102>(r);
+    r = add_row_shl<0x104>(r);
+    r = add_row_shl<0x108>(r);
+    if (g == 0) s.by_i[rt][jt][m] = r;
+  }
+}
+
+// The pair products of a chunk, transposed: rows j, columns i = rt * 16 + m.
+// Where all of a tile's j lie before (REV: behind) its i, the decay between them
+// is that from i to the border next to j's tile, one a lane, times that from
+// there to j.  D2 > 0: also the sums over the pairs' products with c_j . d_i
+template <typename IO, int D1, int D2, bool REV, int NW, int SET>
+__device__ __forceinline__ void pair_products(
+    typename Mma<IO>::frag *tp, const IO *ta, const IO *tb,
+    const Decays<Shape<IO>::C> &dec, float scale, int w, int lane,
+    const IO *tc, const IO *td, PairSums<Shape<IO>::NB> *sums) {
+  typedef Shape<IO> Sh;
+  typedef typename Mma<IO>::frag frag;
+  typedef Tile<IO, D1> T1;
+  constexpr int TPU = Sh::TPU, NB = Sh::NB, NTU = Sh::NTU;
+  const int g = lane >> 4, m = lane & 15;
+#pragma unroll
+  for (int rt = 0; rt < NB; ++rt) {
+    const int i = rt * 16 + m;
+#pragma unroll
+    for (int u2 = 0; u2 < NTU; ++u2) {
+      if (!has_pairs<REV>(rt, REV ? u2 * TPU + TPU - 1 : u2 * TPU)) continue;
+      if (pair_owner<NW, NB, REV, SET>(rt, u2) != w) continue;
+      f32x4 tile[2];
+      tile[0] = tile[1] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int u = 0; u < Sh::units(D1); ++u) {
+        const frag fa = T1::by_row(ta, rt * 16, u, g, m);
+#pragma unroll
+        for (int x = 0; x < TPU; ++x)
+          if (has_pairs<REV>(rt, u2 * TPU + x))
+            tile[x] = Mma<IO>::mma(
+                T1::by_row(tb, (u2 * TPU + x) * 16, u, g, m), fa, tile[x]);
+      }
+#pragma unroll
+      for (int x = 0; x < TPU; ++x) {
+        const int jt = u2 * TPU + x;
+        if (!has_pairs<REV>(rt, jt)) continue;
+        f32x4 &acc = tile[x];
+        if (jt == rt) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = jt * 16 + 4 * g + e;
+            const double d = REV ? dec.G[j] - dec.G[i] : dec.G[i] - dec.G[j];
+            const float f = acc[e] * (scale * exp2_diff(d));
+            acc[e] = (REV ? j >= i : j <= i) ? f : 0.f;
+          }
+        } else {
+          const double d = REV ? dec.G[jt * 16 - 1] - dec.G[i]
+                               : dec.G[i] - dec.G[jt * 16 + 15];
+          acc *= *(const f32x4 *)(dec.tile + jt * 16 + 4 * g) *
+                 (scale * exp2_diff(d));
+        }
+        if constexpr (D2 > 0) {
+          f32x4 qk{0, 0, 0, 0};
+#pragma unroll
+          for (int u = 0; u < Sh::units(D2); ++u)
+            qk = Mma<IO>::mma(Tile<IO, D2>::by_row(tc, jt * 16, u, g, m),
+                              Tile<IO, D2>::by_row(td, rt * 16, u, g, m), qk);
+          pair_sums<NB>(*sums, rt, jt, qk * acc, g, m);
+        }
+      }
+      tp[(rt * NTU + u2) * 64 + lane] = Mma<IO>::pack(tile[0], tile[1]);
     }
   }
 }
@@ -352,7 +549,6 @@ __device__ __forceinline__ uint2 pack4(f32x4 v) {
   return __builtin_bit_cast(
       uint2, bf16x4{(bf16)v[0], (bf16)v[1], (bf16)v[2], (bf16)v[3]});
 }
-
 // what pack4's rounding leaves of v
 __device__ __forceinline__ f32x4 rest4(f32x4 v, uint2 r) {
   return f32x4{v[0] - __uint_as_float(r.x << 16),
@@ -361,22 +557,158 @@ __device__ __forceinline__ f32x4 rest4(f32x4 v, uint2 r) {
                v[3] - __uint_as_float(r.y & 0xffff0000u)};
 }
 
-// waves of a workgroup and columns a wave owns
-template <int D2> constexpr int nwaves() {
-  return D2 >= 64 ? 4 : D2 / 16;
+// A chunk of the wave's 16 columns from `col` on to out[t0..] of one head of H,
+// D wide: `rows` rows, zeros from `live` on (none, where rows is 0).  bf16: after
+// a swap between lanes each has 8 consecutive columns of one row, of the lower
+// tile where g is odd (8 bytes a lane took 4 us more at B1 T8192 H32 D128);
+// REST: what rounding leaves goes to a second tensor, if there is one.  A store
+// that meets no memory takes the place of a branch, which would make the next
+// chunk wait for this one.
+template <typename IO, int D, bool REST>
+__device__ __forceinline__ void put_out(f32x4 (&acc)[Shape<IO>::NB], void *out,
+                                        void *rest, size_t at, int H, int rows,
+                                        int live, int col, int g, int m) {
+  constexpr int NB = Shape<IO>::NB;
+  if (live < Shape<IO>::C) {
+#pragma unroll
+    for (int rt = 0; rt < NB; ++rt)
+      if (rt * 16 + m >= live) acc[rt] = f32x4{0, 0, 0, 0};
+  }
+  const unsigned row = (unsigned)H * D * sizeof(IO);
+  const long long bytes = extent(rows, row, D * (int)sizeof(IO));
+  const auto o = buffer((IO *)out + at, bytes);
+  if constexpr (sizeof(IO) == 4) {
+    unsigned v = m * row + (col + 4 * g) * 4;
+    opaque(v);
+#pragma unroll
+    for (int rt = 0; rt < NB; ++rt)
+      store16(o, v + rt * 16 * row, __builtin_bit_cast(uint4, acc[rt]));
+  } else {
+    const auto o2 = buffer((IO *)rest + at, REST && rest ? bytes : 0);
+    unsigned v = (m + (g & 1) * 16) * row + (col + (g >> 1) * 8) * 2;
+    opaque(v);
+#pragma unroll
+    for (int rt = 0; rt < NB; rt += 2) {
+      uint2 a = pack4(acc[rt]), c = pack4(acc[rt + 1]);
+      auto x = __builtin_amdgcn_permlane16_swap(a.x, c.x, false, false);
+      auto y = __builtin_amdgcn_permlane16_swap(a.y, c.y, false, false);
+      store16(o, v + rt * 16 * row, uint4{x[0], y[0], x[1], y[1]});
+      if constexpr (REST) {
+        if (rest) {
+          a = pack4(rest4(acc[rt], a));
+          c = pack4(rest4(acc[rt + 1], c));
+        }
+        x = __builtin_amdgcn_permlane16_swap(a.x, c.x, false, false);
+        y = __builtin_amdgcn_permlane16_swap(a.y, c.y, false, false);
+        store16(o2, v + rt * 16 * row, uint4{x[0], y[0], x[1], y[1]});
+      }
+    }
+  }
 }
 
-// The wave that makes unit u2 (a 16 x 32 or 16 x 16 piece) of row rt of the pair
-// products.  A row's units by one wave would give the last wave four tiles of 16
-// x 16 and the first one; so it is three at most.  Sums along a row (by_row)
-// need it all in one place.
-template <int NW, int NB, bool REV, bool BY_ROW>
-__device__ constexpr int pair_owner(int rt, int u2) {
-  if (BY_ROW || NW != 4) return rt % NW;
-  const int r = REV ? NB - 1 - rt : rt, u = REV ? 1 - u2 : u2;
-  if (NB == 2) return r + u;  // units of one tile: (0,0), (1,0), (1,1)
-  return r == 3 ? u : r == 2 ? 2 : r == 1 ? 3 : 0;
+// the wave's columns of a state [D1,D2] (transposed: [D2,D1]); zeros for null
+template <int D1, int D2>
+__device__ __forceinline__ void load_state(f32x4 (&S)[D1 / 16], const float *p,
+                                           size_t at, int transposed, int col,
+                                           int g, int m) {
+  if (!p) {
+#pragma unroll
+    for (int kt = 0; kt < D1 / 16; ++kt) S[kt] = f32x4{0, 0, 0, 0};
+  } else if (transposed) {
+#pragma unroll
+    for (int kt = 0; kt < D1 / 16; ++kt)
+      S[kt] = *(const f32x4 *)(p + at + (col + m) * D1 + kt * 16 + 4 * g);
+  } else {
+#pragma unroll
+    for (int kt = 0; kt < D1 / 16; ++kt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        S[kt][e] = p[at + (kt * 16 + 4 * g + e) * D2 + col + m];
+  }
 }
+template <int D1, int D2>
+__device__ __forceinline__ void store_state(const f32x4 (&S)[D1 / 16], float *p,
+                                            int col, int g, int m) {
+#pragma unroll
+  for (int kt = 0; kt < D1 / 16; ++kt)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      p[(kt * 16 + 4 * g + e) * D2 + col + m] = S[kt][e];
+}
+
+// waves of a workgroup whose output is D2 wide
+template <int D2> constexpr int nwaves() { return D2 == 128 ? 8 : 4; }
+
+// where a workgroup's segment is
+struct Where {
+  int h, b, s;
+  size_t chain;
+  int t_begin, t_end, live_end, nch;
+  __device__ __forceinline__ Where(const LinSeq &q, int block, int NS, int s0,
+                                   int C) {
+    h = block % q.H;
+    const int bs = block / q.H;
+    s = bs % NS + s0;
+    b = bs / NS;
+    chain = (size_t)b * q.H + h;
+    int len = q.T;
+    if (q.lengths) len = min(max(q.lengths[b], 0), q.T);
+    t_begin = s * q.seg;
+    t_end = min(q.T, t_begin + q.seg);  // of the segment, dead or not
+    live_end = min(len, t_end);
+    nch = live_end > t_begin ? (live_end - t_begin + C - 1) / C : 0;
+  }
+  // first token of the n-th chunk taken
+  __device__ __forceinline__ int at(int n, bool back, int C) const {
+    return t_begin + (back ? nch - 1 - n : n) * C;
+  }
+};
+
+// zeros for the dead tokens of a segment behind its chunks
+template <typename IO, int D, int NT>
+__device__ __forceinline__ void zero_dead(void *out, const LinSeq &q,
+                                          const Where &at) {
+  if (!out) return;
+  const int t0 = at.t_begin + at.nch * Shape<IO>::C;
+  const long long n = (long long)(at.t_end - t0) * (D / 8);
+  for (long long i = threadIdx.x; i < n; i += NT)
+    store8_zero((IO *)out +
+                (((size_t)at.b * q.T + t0 + i / (D / 8)) * q.H + at.h) * D +
+                i % (D / 8) * 8);
+}
+
+// The decays of a sweep's chunks: those of BATCH chunks are made at a time,
+// into the half of `decs` that the chunks at work do not read.
+template <typename IO, int NW, bool REV> struct Keeper {
+  static constexpr int C = Shape<IO>::C;
+  Gates<C, NW> gates;
+  __device__ __forceinline__ void fetch(const LinSeq &q, const Where &at,
+                                        int n0, int w, int lane) {
+    gates.fetch(q, at.b, at.h, n0, at.nch, REV, at.t_begin, at.live_end, w,
+                lane);
+  }
+  // first, last: factors of the weights
+  __device__ __forceinline__ void make(Decays<C> *decs, const Where &at,
+                                       int n0, float first, float last, int w,
+                                       int lane) {
+#pragma unroll
+    for (int i = 0; i < gates.N; ++i) {
+      const int x = w + i * NW;
+      if (x >= BATCH || n0 + x >= at.nch) break;
+      Decays<C> &d = decs[(n0 + x) % (2 * BATCH)];
+      double G, tile;
+      const double end = decay_sums<C>(gates.g[i], lane, G, tile);
+      if (!REV) tile = __shfl(tile, lane | 15, 64) - tile;
+      if (lane < C) {
+        d.G[lane] = G;
+        d.tile[lane] = exp2_diff(tile);
+        d.first[lane] = first * exp2_diff(G);
+        d.last[lane] = last * exp2_diff(end - G);
+      }
+      if (lane == 0) d.total = exp2_diff(end);
+    }
+  }
+};
 
 // ---------------------------------------------------------------------------
 // the sweep
@@ -384,400 +716,168 @@ __device__ constexpr int pair_owner(int rt, int u2) {
 template <typename IO, int D1, int D2, bool REV, int DOT>
 __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
     LinSweep p) {
-  constexpr int C = lin_chunk(sizeof(IO) == 2), NB = C / 16;
-  constexpr int NW = nwaves<D2>(), NT = 64 * NW;
-  constexpr int CT = D2 / 16 / NW, CW = CT * 16;
-  constexpr int TPU = Mma<IO>::TPU, KU = 16 * TPU, NE = Mma<IO>::NE;
-  constexpr int KT = D1 / 16, NKU = (KT + TPU - 1) / TPU;  // units over D1
-  constexpr int NDU = (D2 / 16 + TPU - 1) / TPU;           // units over D2
-  constexpr int NTU = C / KU;                              // units over tokens
+  typedef Shape<IO> Sh;
   typedef typename Mma<IO>::frag frag;
   typedef Tile<IO, D1> T1;
   typedef Tile<IO, D2> T2;
-  __shared__ alignas(16) IO ta[C * T1::STR], tb[C * T1::STR], tc[C * T2::STR];
-  __shared__ alignas(16) IO td[DOT ? C * T2::STR : 8];
+  constexpr int C = Sh::C, NB = Sh::NB, NTU = Sh::NTU, KT = D1 / 16;
+  constexpr int NW = nwaves<D2>(), NT = 64 * NW, COLS = D2 / 16;
+  // a second set of tiles, unless it would keep a second workgroup of 4 waves
+  // off the CU
+  constexpr int SET = C * (2 * T1::STR + (DOT ? 2 : 1) * T2::STR);
+  constexpr bool TWO = NW == 8 || 2 * SET * sizeof(IO) <= 64 * 1024;
+  __shared__ alignas(16) IO ta[1 + TWO][C * T1::STR], tb[1 + TWO][C * T1::STR],
+      tc[1 + TWO][C * T2::STR];
+  __shared__ alignas(16) IO td[1 + TWO][DOT ? C * T2::STR : 8];
   __shared__ alignas(16) frag tp[NB * NTU * 64];
-  __shared__ Decays<C> decs[BATCH];
-  __shared__ float far_part[DOT ? NW : 1][DOT ? C : 1];
-  __shared__ float pair_part[DOT == LIN_FAR_PAIRS ? NB : 1]
-                            [DOT == LIN_FAR_PAIRS ? C : 1];
+  __shared__ Decays<C> decs[2 * BATCH];
+  __shared__ float far_dots[DOT ? COLS : 1][DOT ? C : 1];
+  __shared__ PairSums<DOT == LIN_FAR_PAIRS ? NB : 1> sums;
 
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int g = lane >> 4, m = lane & 15;
   const LinSeq &q = p.q;
-  const int h = blockIdx.x % q.H, bs = blockIdx.x / q.H;
-  const int s = bs % q.NS, b = bs / q.NS;
-  const size_t chain = (size_t)b * q.H + h;
-  int len = q.T;
-  if (q.lengths) len = min(max(q.lengths[b], 0), q.T);
-  const int t_begin = s * q.seg;
-  const int t_end = min(q.T, t_begin + q.seg);  // of the segment, dead or not
-  const int live_end = min(len, t_end);
-  const int nch = live_end > t_begin ? (live_end - t_begin + C - 1) / C : 0;
+  const Where at(q, blockIdx.x, q.NS, 0, C);
+  const int nch = at.nch;
+  const bool mine = COLS >= NW || w < COLS;  // has columns
+  const int col = mine ? w * 16 : 0;
+  zero_dead<IO, D2, NT>(p.out, q, at);
+  if (DOT) zero_dead<IO, D2, NT>(p.out_rest, q, at);
 
-  // out of dead tokens is zero
-  {
-    const int t0 = t_begin + nch * C;
-    const long long n = (long long)(t_end - t0) * (D2 / 8);
-    for (long long i = threadIdx.x; i < n; i += NT) {
-      const size_t at = (((size_t)b * q.T + t0 + i / (D2 / 8)) * q.H + h) * D2 +
-                        i % (D2 / 8) * 8;
-      store8_zero((IO *)p.out + at);
-      if (DOT && p.out_rest) store8_zero((IO *)p.out_rest + at);
-    }
-  }
-
-  // the state's columns of this wave
-  f32x4 S[KT][CT];
-  const float *const s_at = p.s_in + (chain * q.NS + s) * D1 * D2;
-  const int s_col = w * CW + m;
-  if (!p.s_in) {
-#pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct) S[kt][ct] = f32x4{0, 0, 0, 0};
-  } else if (p.s_transposed) {
-#pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct)
-        S[kt][ct] = *(const f32x4 *)(s_at + (s_col + ct * 16) * D1 + kt * 16 +
-                                     4 * g);
-  } else {
-#pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          S[kt][ct][e] = s_at[(kt * 16 + 4 * g + e) * D2 + s_col + ct * 16];
-  }
+  f32x4 S[KT];
+  const size_t s_at = (at.chain * q.NS + at.s) * D1 * D2;
+  load_state<D1, D2>(S, p.s_in, s_at, p.s_transposed, col, g, m);
 
   unsigned sa, sb, sc, sd = 0;
-  const char *pa = operand<IO, D1>(p.a, q, b, h, sa);
-  const char *pb = operand<IO, D1>(p.b, q, b, h, sb);
-  const char *pc = operand<IO, D2>(p.c, q, b, h, sc);
+  const char *pa = operand<IO, D1>(p.a, q, at.b, at.h, sa);
+  const char *pb = operand<IO, D1>(p.b, q, at.b, at.h, sb);
+  const char *pc = operand<IO, D2>(p.c, q, at.b, at.h, sc);
   const char *pd = nullptr;
-  if constexpr (DOT) pd = operand<IO, D2>(p.d, q, b, h, sd);
+  if constexpr (DOT) pd = operand<IO, D2>(p.d, q, at.b, at.h, sd);
   Rows<IO, D1, C, NT> ra, rb;
   Rows<IO, D2, C, NT> rc, rd;
   auto fetch = [&](int n) {
-    const int t0 = t_begin + (REV ? nch - 1 - n : n) * C;
-    const int live = n < nch ? live_end - t0 : 0;
+    const int t0 = at.at(n, REV, C), live = n < nch ? at.live_end - t0 : 0;
     ra.fetch(pa + (long long)t0 * sa, sa, live);
     rb.fetch(pb + (long long)t0 * sb, sb, live);
     rc.fetch(pc + (long long)t0 * sc, sc, live);
     if constexpr (DOT) rd.fetch(pd + (long long)t0 * sd, sd, live);
   };
-  Gates<C, NW> gates;
-  auto fetch_gates = [&](int n0) {
-    gates.fetch(q, b, h, n0, nch, REV, t_begin, live_end, w, lane);
+  auto stash = [&](int x) {
+    ra.stash(ta[x]);
+    rb.stash(tb[x]);
+    rc.stash(tc[x]);
+    if constexpr (DOT) rd.stash(td[x]);
   };
+  Keeper<IO, NW, REV> keeper;
   auto make_decays = [&](int n0) {
-#pragma unroll
-    for (int i = 0; i < gates.N; ++i) {
-      const int x = w + i * NW;
-      if (x >= BATCH || n0 + x >= nch) break;
-      double G, tile;
-      const double end = decay_sums<C>(gates.g[i], lane, G, tile);
-      if (!REV) tile = __shfl(tile, lane | 15, 64) - tile;
-      if (lane < C) {
-        decs[x].G[lane] = G;
-        decs[x].tile[lane] = exp2_diff(tile);
-        decs[x].first[lane] = (REV ? p.add_scale : p.far_scale) * exp2_diff(G);
-        decs[x].last[lane] =
-            (REV ? p.far_scale : p.add_scale) * exp2_diff(end - G);
-      }
-      if (lane == 0) decs[x].total = exp2_diff(end);
-    }
+    keeper.make(decs, at, n0, REV ? p.add_scale : p.far_scale,
+                REV ? p.far_scale : p.add_scale, w, lane);
+    keeper.fetch(q, at, n0 + BATCH, w, lane);
   };
-  const bool last_seg = REV ? s == 0 : s == q.NS - 1;
+  const bool last_seg = REV ? at.s == 0 : at.s == q.NS - 1;
   const bool keep_end = (last_seg && p.s_end) || DOT == LIN_FAR_PAIRS;
 
-  fetch_gates(0);
-  fetch(0);
-  all_loaded();
+  if (nch > 0) {
+    keeper.fetch(q, at, 0, w, lane);
+    fetch(0);
+    make_decays(0);
+    if constexpr (TWO) {
+      stash(0);
+      fetch(1);
+    }
+    all_loaded();
+    barrier_keep_vmem();
+  }
   for (int n = 0; n < nch; ++n) {
-    const int t0 = t_begin + (REV ? nch - 1 - n : n) * C;
-    const Decays<C> &dec = decs[n % BATCH];
+    const int t0 = at.at(n, REV, C), x = TWO ? n & 1 : 0;
+    const Decays<C> &dec = decs[n % (2 * BATCH)];
     // loads come back in their order: gates are asked for before the rows of a
     // chunk, and used four chunks later
-    if (n % BATCH == 0) {
-      make_decays(n);
-      fetch_gates(n + BATCH);
+    if (n % BATCH == BATCH - 1) make_decays(n + 1);
+    if constexpr (TWO) {
+      stash(x ^ 1);
+      fetch(n + 2);
+    } else {
+      stash(0);
+      barrier_keep_vmem();
+      fetch(n + 1);
     }
-    ra.stash(ta);
-    rb.stash(tb);
-    rc.stash(tc);
-    if constexpr (DOT) rd.stash(td);
-    barrier_keep_vmem();
-    fetch(n + 1);
-    const float *const far_w = REV ? dec.last : dec.first;
-    const float *const add_w = REV ? dec.first : dec.last;
-
-    // the pair products, transposed: rows j, columns i = rt * 16 + m.  Where
-    // all of a tile's j lie before (REV: behind) its i, the decay between them
-    // is that from i to the border next to j's tile, one a lane, times that
-    // from there to j
-#pragma unroll
-    for (int rt = 0; rt < NB; ++rt) {
-      const int i = rt * 16 + m;
-      float run = 0.f;  // pairs of i with earlier tiles' j
-#pragma unroll
-      for (int u2 = 0; u2 < NTU; ++u2) {
-        if (REV ? u2 * TPU + TPU - 1 < rt : u2 * TPU > rt) continue;
-        if (pair_owner<NW, NB, REV, DOT == LIN_FAR_PAIRS>(rt, u2) != w)
-          continue;
-        f32x4 tile[2];
-        tile[0] = tile[1] = f32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int u = 0; u < NKU; ++u) {
-          const frag fa = T1::by_row(ta, rt * 16, u, g, m);
-#pragma unroll
-          for (int x = 0; x < TPU; ++x) {
-            const int jt = u2 * TPU + x;
-            if (REV ? jt >= rt : jt <= rt)
-              tile[x] = Mma<IO>::mma(T1::by_row(tb, jt * 16, u, g, m), fa,
-                                     tile[x]);
-          }
-        }
-#pragma unroll
-        for (int x = 0; x < TPU; ++x) {
-          const int jt = u2 * TPU + x;
-          if (REV ? jt < rt : jt > rt) continue;
-          f32x4 &acc = tile[x];
-          if (jt == rt) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int j = jt * 16 + 4 * g + e;
-              const double d = REV ? dec.G[j] - dec.G[i] : dec.G[i] - dec.G[j];
-              const float f = acc[e] * (p.pair_scale * exp2_diff(d));
-              acc[e] = (REV ? j >= i : j <= i) ? f : 0.f;
-            }
-          } else {
-            const double d = REV ? dec.G[jt * 16 - 1] - dec.G[i]
-                                 : dec.G[i] - dec.G[jt * 16 + 15];
-            acc *= *(const f32x4 *)(dec.tile + jt * 16 + 4 * g) *
-                   (p.pair_scale * exp2_diff(d));
-          }
-          if constexpr (DOT == LIN_FAR_PAIRS) {
-            // pairs (i, t') with t' < j, summed over i >= j
-            f32x4 qk{0, 0, 0, 0};
-#pragma unroll
-            for (int u = 0; u < NDU; ++u)
-              qk = Mma<IO>::mma(T2::by_row(tc, jt * 16, u, g, m),
-                                T2::by_row(td, rt * 16, u, g, m), qk);
-            qk *= acc;
-            const float tot = (qk[0] + qk[1]) + (qk[2] + qk[3]);
-            const float v1 = __shfl_up(tot, 16, 64);
-            const float v2 = __shfl_up(tot, 32, 64);
-            const float v3 = __shfl_up(tot, 48, 64);
-            float pre = run;
-            if (g >= 3) pre += v3;
-            if (g >= 2) pre += v2;
-            if (g >= 1) pre += v1;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int j = jt * 16 + 4 * g + e;
-              const float v = group_sum<16>(j <= i ? pre : 0.f);
-              if (m == 0) pair_part[rt][j] = v;
-              pre += qk[e];
-            }
-            run = __shfl(pre, 48 + m, 64);
-          }
-        }
-        tp[(rt * NTU + u2) * 64 + lane] = Mma<IO>::pack(tile[0], tile[1]);
-      }
-    }
-
+    pair_products<IO, D1, DOT == LIN_FAR_PAIRS ? D2 : 0, REV, NW, 0>(
+        tp, ta[x], tb[x], dec, p.pair_scale, w, lane, tc[x], td[x],
+        (PairSums<NB> *)&sums);
     __builtin_amdgcn_sched_barrier(0);
-    // what the state gives to out, transposed: rows are this wave's columns
-    // of c, columns tokens
-    f32x4 acc[NB][CT];
-#pragma unroll
-    for (int rt = 0; rt < NB; ++rt)
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct) acc[rt][ct] = f32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int u = 0; u < NKU; ++u) {
-      frag fs[CT], fl[CT];
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct) {
-        const f32x4 x = S[u * TPU][ct];
-        const f32x4 y = TPU == 2 && u * TPU + 1 < KT ? S[u * TPU + 1][ct]
-                                                     : f32x4{0, 0, 0, 0};
-        fs[ct] = Mma<IO>::pack(x, y);
-        if constexpr (DOT && NE == 8) {
-          f32x4 x2, y2;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            x2[e] = x[e] - Mma<IO>::elem(fs[ct], e);
-            y2[e] = y[e] - Mma<IO>::elem(fs[ct], 4 + e);
-          }
-          fl[ct] = Mma<IO>::pack(x2, y2);
-        }
-      }
+    f32x4 acc[NB];
+    if (mine) {
+      far_part<IO, D1, DOT != LIN_PLAIN>(acc, S, ta[x], g, m);
+      const float *const far_w = REV ? dec.last : dec.first;
 #pragma unroll
       for (int rt = 0; rt < NB; ++rt) {
-        const frag f = T1::by_row(ta, rt * 16, u, g, m);
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-          acc[rt][ct] = Mma<IO>::mma(fs[ct], f, acc[rt][ct]);
-          if constexpr (DOT && NE == 8)
-            acc[rt][ct] = Mma<IO>::mma(fl[ct], f, acc[rt][ct]);
-        }
-      }
-    }
-#pragma unroll
-    for (int rt = 0; rt < NB; ++rt) {
-      const float fw = far_w[rt * 16 + m];
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct) acc[rt][ct] *= fw;
-      if constexpr (DOT) {
-        float dot = 0.f;
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-          const IO *x = td + T2::at(rt * 16 + m, w * CW + ct * 16 + 4 * g);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) dot += acc[rt][ct][e] * to_f32(x[e]);
-        }
-        dot += __shfl_xor(dot, 16, 64);
-        dot += __shfl_xor(dot, 32, 64);
-        if (g == 0) far_part[w][rt * 16 + m] = dot;
-      }
-    }
-    barrier_keep_vmem();
-    frag fc[NTU][CT];
-#pragma unroll
-    for (int u = 0; u < NTU; ++u)
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct)
-        fc[u][ct] = T2::by_col(tc, w * CW + ct * 16, u, g, m);
-
-    // and the pairs
-#pragma unroll
-    for (int rt = 0; rt < NB; ++rt) {
-#pragma unroll
-      for (int u = 0; u < NTU; ++u) {
-        if (REV ? u * TPU + TPU - 1 < rt : u * TPU > rt) continue;
-        const frag f = tp[(rt * NTU + u) * 64 + lane];
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-          acc[rt][ct] = Mma<IO>::mma(fc[u][ct], f, acc[rt][ct]);
-      }
-    }
-    if (t0 + C > live_end) {
-#pragma unroll
-      for (int rt = 0; rt < NB; ++rt)
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-          if (t0 + rt * 16 + m >= live_end) acc[rt][ct] = f32x4{0, 0, 0, 0};
-    }
-    const unsigned row = (unsigned)q.H * D2 * sizeof(IO);
-    const size_t o_at = (((size_t)b * q.T + t0) * q.H + h) * D2;
-    const long long o_bytes =
-        extent(min(C, t_end - t0), row, D2 * (int)sizeof(IO));
-    const auto o = buffer((IO *)p.out + o_at, o_bytes);
-    if constexpr (sizeof(IO) == 4) {
-      unsigned at = m * row + (w * CW + 4 * g) * 4;
-      opaque(at);
-#pragma unroll
-      for (int rt = 0; rt < NB; ++rt)
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-          store16(o, at + rt * 16 * row + ct * 64,
-                  __builtin_bit_cast(uint4, acc[rt][ct]));
-    } else {
-      // two tiles side by side (CT = 2) or one below the other: after the swap
-      // a lane has 8 consecutive columns, of the first tile where g is even.
-      // (8 bytes a lane took 4 us more at B1 T8192 H32 D128.)  The rounded-off
-      // rest goes to a second tensor, where there is one
-      const auto o2 = buffer((IO *)p.out_rest + o_at,
-                             p.out_rest ? o_bytes : 0);
-      unsigned at = (CT == 2 ? m : m + (g & 1) * 16) * row +
-                    (w * CW + (CT == 2 ? (g & 1) * 16 : 0) + (g >> 1) * 8) * 2;
-      opaque(at);
-#pragma unroll
-      for (int x = 0; x < NB; x += 3 - CT) {
-        constexpr int DY = 2 - CT;  // the second tile's row and column
-        const f32x4 a = acc[x][0], c = acc[x + DY][CT - 1];
-        uint2 ha = pack4(a), hc = pack4(c);
-        const auto l1 = __builtin_amdgcn_permlane16_swap(ha.x, hc.x, false, false);
-        const auto l2 = __builtin_amdgcn_permlane16_swap(ha.y, hc.y, false, false);
-        store16(o, at + x * 16 * row, uint4{l1[0], l2[0], l1[1], l2[1]});
+        acc[rt] *= far_w[rt * 16 + m];
         if constexpr (DOT) {
-          // a store that meets no memory where there is no second tensor: a
-          // branch around it would make the next chunk wait for the first
-          if (p.out_rest) {
-            ha = pack4(rest4(a, ha));
-            hc = pack4(rest4(c, hc));
-          }
-          const auto r1 = __builtin_amdgcn_permlane16_swap(ha.x, hc.x, false, false);
-          const auto r2 = __builtin_amdgcn_permlane16_swap(ha.y, hc.y, false, false);
-          store16(o2, at + x * 16 * row, uint4{r1[0], r2[0], r1[1], r2[1]});
+          const IO *y = td[x] + T2::at(rt * 16 + m, col + 4 * g);
+          float dot = 0.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) dot += acc[rt][e] * to_f32(y[e]);
+          dot += __shfl_xor(dot, 16, 64);
+          dot += __shfl_xor(dot, 32, 64);
+          if (g == 0) far_dots[w][rt * 16 + m] = dot;
         }
       }
     }
-    __builtin_amdgcn_sched_barrier(0);
-    if (n + 1 < nch || keep_end) {
-#pragma unroll
-      for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) S[kt][ct] *= dec.total;
-      add_chunk<IO, D1, CT, C, NTU>(S, tb, fc, add_w, g, m);
-    }
     barrier_keep_vmem();
+
+    frag fc[NTU];
+    if (mine) {
+#pragma unroll
+      for (int u = 0; u < NTU; ++u) fc[u] = T2::by_col(tc[x], col, u, g, m);
+      near_part<IO, REV>(acc, tp, fc, lane);
+    }
+    put_out<IO, D2, DOT != 0>(
+        acc, p.out, p.out_rest,
+        (((size_t)at.b * q.T + t0) * q.H + at.h) * D2, q.H,
+        mine ? min(C, at.t_end - t0) : 0, at.live_end - t0, col, g, m);
+    __builtin_amdgcn_sched_barrier(0);
+    if (mine && (n + 1 < nch || keep_end)) {
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) S[kt] *= dec.total;
+      add_chunk<IO, D1>(S, tb[x], fc, REV ? dec.first : dec.last, g, m);
+    }
     if constexpr (DOT) {
       const int t = t0 + threadIdx.x;
-      if (threadIdx.x < C && t < t_end) {
-        float x = 0.f;
+      if (threadIdx.x < C && t < at.t_end) {
+        float v = 0.f;
 #pragma unroll
-        for (int i = 0; i < NW; ++i) x += far_part[i][threadIdx.x];
-        p.far_dot[chain * q.T + t] = x;
-        if constexpr (DOT == LIN_FAR_PAIRS) {
-          float y = 0.f;
-          for (int rt = threadIdx.x / 16; rt < NB; ++rt)
-            y += pair_part[rt][threadIdx.x];
-          p.pair_dot[chain * q.T + t] = y;
-        }
+        for (int i = 0; i < COLS; ++i) v += far_dots[i][threadIdx.x];
+        p.far_dot[at.chain * q.T + t] = v;
+        if constexpr (DOT == LIN_FAR_PAIRS)
+          p.pair_dot[at.chain * q.T + t] = sums.across(threadIdx.x);
       }
     }
+    barrier_keep_vmem();
   }
 
-  if (last_seg && p.s_end) {
-    float *const e = p.s_end + chain * D1 * D2;
-#pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-          e[(size_t)(kt * 16 + 4 * g + x) * D2 + w * CW + ct * 16 + m] =
-              S[kt][ct][x];
-  }
+  if (mine && last_seg && p.s_end)
+    store_state<D1, D2>(S, p.s_end + at.chain * D1 * D2, col, g, m);
   if constexpr (DOT == LIN_FAR_PAIRS) {
-    float x = 0.f;
-    if (p.e_with) {
+    float v = 0.f;
+    if (mine && p.e_with) {
 #pragma unroll
-      for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-          const int row = kt * 16 + 4 * g, col = w * CW + ct * 16 + m;
-          const f32x4 y = *(const f32x4 *)(
-              p.e_with + (chain * q.NS + s) * D1 * D2 + col * D1 + row);
-          x += (S[kt][ct][0] * y[0] + S[kt][ct][1] * y[1]) +
-               (S[kt][ct][2] * y[2] + S[kt][ct][3] * y[3]);
-        }
+      for (int kt = 0; kt < KT; ++kt) {
+        const f32x4 y = *(const f32x4 *)(p.e_with + s_at + (col + m) * D1 +
+                                         kt * 16 + 4 * g);
+        v += (S[kt][0] * y[0] + S[kt][1] * y[1]) +
+             (S[kt][2] * y[2] + S[kt][3] * y[3]);
+      }
     }
-    x = group_sum<32>(x);
-    x += __shfl_xor(x, 32, 64);
-    barrier_keep_vmem();
-    if (lane == 0) far_part[w][0] = x;
+    v = group_sum<32>(v);
+    v += __shfl_xor(v, 32, 64);
+    if (mine && lane == 0) far_dots[w][0] = v;
     barrier_keep_vmem();
     if (threadIdx.x == 0) {
-      float y = 0.f;
-      for (int i = 0; i < NW; ++i) y += far_part[i][0];
-      p.e_out[chain * q.NS + s] = y;
+      v = 0.f;
+      for (int i = 0; i < COLS; ++i) v += far_dots[i][0];
+      p.e_out[at.chain * q.NS + at.s] = v;
     }
   }
 }
@@ -788,58 +888,53 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
 // by, so that a chunk's weights are final and nothing is rescaled, and what is
 // decayed to less than 2^-200 by then is left out with all that lies behind it:
 // it is 0 in fp32.
+
 constexpr double FORGOTTEN = -200.0;
 
 template <typename IO, int D1, int D2>
 __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_local(
-    LinLocal p) {
-  constexpr int C = lin_chunk(sizeof(IO) == 2);
-  constexpr int NW = nwaves<D2>(), NT = 64 * NW;
-  constexpr int CT = D2 / 16 / NW, CW = CT * 16, KT = D1 / 16;
-  constexpr int NTU = C / (16 * Mma<IO>::TPU);
+    LinLocal p0, LinLocal p1) {
+  typedef Shape<IO> Sh;
   typedef typename Mma<IO>::frag frag;
+  constexpr int C = Sh::C, NTU = Sh::NTU, KT = D1 / 16;
+  constexpr int NW = nwaves<D2>(), NT = 64 * NW, COLS = D2 / 16;
   __shared__ alignas(16) IO tb[C * Tile<IO, D1>::STR],
       tc[C * Tile<IO, D2>::STR];
-  __shared__ Decays<C> decs[BATCH];
+  __shared__ alignas(16) float wts[BATCH][C];
   __shared__ double ends[BATCH];
+  const LinLocal &p = blockIdx.y ? p1 : p0;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int g = lane >> 4, m = lane & 15;
   const LinSeq &q = p.q;
-  const int h = blockIdx.x % q.H, bs = blockIdx.x / q.H;
-  const int s = bs % (q.NS - 1) + p.rev, b = bs / (q.NS - 1);
-  const size_t chain = (size_t)b * q.H + h;
-  int len = q.T;
-  if (q.lengths) len = min(max(q.lengths[b], 0), q.T);
-  const int t_begin = s * q.seg;
-  const int live_end = min(len, min(q.T, t_begin + q.seg));
-  const int nch = live_end > t_begin ? (live_end - t_begin + C - 1) / C : 0;
+  const Where at(q, blockIdx.x, q.NS - 1, p.rev, C);
+  const int nch = at.nch;
+  const bool back = !p.rev;
+  const bool mine = COLS >= NW || w < COLS;
+  const int col = mine ? w * 16 : 0;
 
-  f32x4 S[KT][CT];
+  f32x4 S[KT];
 #pragma unroll
-  for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct) S[kt][ct] = f32x4{0, 0, 0, 0};
+  for (int kt = 0; kt < KT; ++kt) S[kt] = f32x4{0, 0, 0, 0};
   unsigned sb, sc;
-  const char *pb = operand<IO, D1>(p.b, q, b, h, sb);
-  const char *pc = operand<IO, D2>(p.c, q, b, h, sc);
+  const char *pb = operand<IO, D1>(p.b, q, at.b, at.h, sb);
+  const char *pc = operand<IO, D2>(p.c, q, at.b, at.h, sc);
   // two chunks ahead: there is little to do between a chunk's loads and the
   // next's
   Rows<IO, D1, C, NT> rb[2];
   Rows<IO, D2, C, NT> rc[2];
   Gates<C, NW> gates;
-  const bool back = !p.rev;
   double sum = 0.0;  // decay of the chunks taken
-  auto t_of = [&](int n) { return t_begin + (back ? nch - 1 - n : n) * C; };
   auto fetch = [&](auto &b, auto &c, int n) {
-    const int t0 = t_of(n), live = n < nch ? live_end - t0 : 0;
+    const int t0 = at.at(n, back, C), live = n < nch ? at.live_end - t0 : 0;
     b.fetch(pb + (long long)t0 * sb, sb, live);
     c.fetch(pc + (long long)t0 * sc, sc, live);
   };
   auto fetch_gates = [&](int n0) {
-    gates.fetch(q, b, h, n0, nch, back, t_begin, live_end, w, lane);
+    gates.fetch(q, at.b, at.h, n0, nch, back, at.t_begin, at.live_end, w,
+                lane);
   };
   // the weights of up to 4 chunks from n0 on; false: they count as nothing
-  auto make_decays = [&](int n0) {
+  auto make_weights = [&](int n0) {
     if (n0 > 0 && sum < FORGOTTEN) return false;
     double G[gates.N];
 #pragma unroll
@@ -851,38 +946,38 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_local(
       if (lane == 0) ends[x] = end;
     }
     barrier_keep_vmem();
-    double at[BATCH + 1];
-    at[0] = sum;
+    double before[BATCH + 1];
+    before[0] = sum;
 #pragma unroll
-    for (int x = 0; x < BATCH; ++x) at[x + 1] = at[x] + ends[x];
-    sum = at[BATCH];
+    for (int x = 0; x < BATCH; ++x) before[x + 1] = before[x] + ends[x];
+    sum = before[BATCH];
 #pragma unroll
     for (int i = 0; i < gates.N; ++i) {
 #pragma unroll
       for (int x = 0; x < BATCH; ++x)
         if (x == w + i * NW && lane < C)
-          decs[x].first[lane] =
+          wts[x][lane] =
               p.add_scale *
-              exp2_diff(back ? ends[x] - G[i] + at[x] : G[i] + at[x]);
+              exp2_diff(back ? ends[x] - G[i] + before[x] : G[i] + before[x]);
     }
     return true;
   };
   auto step = [&](auto &b, auto &c, int n) {
     if (n % BATCH == 0) {
-      if (!make_decays(n)) return false;
+      if (!make_weights(n)) return false;
       fetch_gates(n + BATCH);
     }
     b.stash(tb);
     c.stash(tc);
     barrier_keep_vmem();
     fetch(b, c, n + 2);
-    frag fc[NTU][CT];
+    if (mine) {
+      frag fc[NTU];
 #pragma unroll
-    for (int u = 0; u < NTU; ++u)
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct)
-        fc[u][ct] = Tile<IO, D2>::by_col(tc, w * CW + ct * 16, u, g, m);
-    add_chunk<IO, D1, CT, C, NTU>(S, tb, fc, decs[n % BATCH].first, g, m);
+      for (int u = 0; u < NTU; ++u)
+        fc[u] = Tile<IO, D2>::by_col(tc, col, u, g, m);
+      add_chunk<IO, D1>(S, tb, fc, wts[n % BATCH], g, m);
+    }
     barrier_keep_vmem();
     return true;
   };
@@ -894,16 +989,10 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_local(
     if (!step(rb[0], rc[0], n)) break;
     if (n + 1 < nch && !step(rb[1], rc[1], n + 1)) break;
   }
-  float *const o = p.s + (chain * q.NS + s) * D1 * D2;
-#pragma unroll
-  for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-        o[(size_t)(kt * 16 + 4 * g + x) * D2 + w * CW + ct * 16 + m] =
-            S[kt][ct][x];
-  if (threadIdx.x == 0) p.decay[chain * q.NS + s] = exp2_diff(sum);
+  if (mine)
+    store_state<D1, D2>(S, p.s + (at.chain * q.NS + at.s) * D1 * D2, col, g,
+                        m);
+  if (threadIdx.x == 0) p.decay[at.chain * q.NS + at.s] = exp2_diff(sum);
 }
 
 // ---------------------------------------------------------------------------
@@ -936,18 +1025,19 @@ hipError_t sweep(int D2, int rev, int dot, const LinSweep &p, hipStream_t s) {
   return hipErrorInvalidValue;
 }
 template <typename IO, int D1, int D2>
-hipError_t local_d2(const LinLocal &p, hipStream_t s) {
-  const unsigned n = (unsigned)p.q.B * p.q.H * (p.q.NS - 1);
-  kda_lin_local<IO, D1, D2><<<n, 64 * nwaves<D2>(), 0, s>>>(p);
+hipError_t local_d2(const LinLocal &p, const LinLocal *r, hipStream_t s) {
+  const dim3 n((unsigned)p.q.B * p.q.H * (p.q.NS - 1), r ? 2 : 1);
+  kda_lin_local<IO, D1, D2>
+      <<<n, 64 * nwaves<D2>(), 0, s>>>(p, r ? *r : p);
   return hipGetLastError();
 }
 template <typename IO, int D1>
-hipError_t local(int D2, const LinLocal &p, hipStream_t s) {
+hipError_t local(int D2, const LinLocal &p, const LinLocal *r, hipStream_t s) {
   switch (D2) {
-    case 16: return local_d2<IO, D1, 16>(p, s);
-    case 32: return local_d2<IO, D1, 32>(p, s);
-    case 64: return local_d2<IO, D1, 64>(p, s);
-    case 128: return local_d2<IO, D1, 128>(p, s);
+    case 16: return local_d2<IO, D1, 16>(p, r, s);
+    case 32: return local_d2<IO, D1, 32>(p, r, s);
+    case 64: return local_d2<IO, D1, 64>(p, r, s);
+    case 128: return local_d2<IO, D1, 128>(p, r, s);
   }
   return hipErrorInvalidValue;
 }
@@ -960,8 +1050,8 @@ hipError_t local(int D2, const LinLocal &p, hipStream_t s) {
     return lin::sweep<TYPE, D1>(D2, rev, dot, p, s);                       \
   }                                                                        \
   hipError_t lin_local_##IO##_##D1(int D2, const LinLocal &p,              \
-                                   hipStream_t s) {                        \
-    return lin::local<TYPE, D1>(D2, p, s);                                 \
+                                   const LinLocal *r, hipStream_t s) {     \
+    return lin::local<TYPE, D1>(D2, p, r, s);                              \
   }
 
 }  // namespace kda
