@@ -73,6 +73,18 @@ struct LinSweep {
   float *e_out;               // [B,H,NS]: <state behind the segment, e_with>
 };
 
+// The two reversed sweeps of the gradient in one, for Dk = Dv = D
+struct LinBoth {
+  LinSeq q;
+  LinOperand qs, ks, vs, dos;
+  void *dk, *dk_rest;         // as LinSweep's out
+  void *dv;
+  float scale;
+  const float *ds_in;         // [B,H,NS,D,D] or null
+  float *ds0;                 // [B,H,D,D] or null
+  float *early;               // [B,H,T]
+};
+
 // the state that each segment adds to a zero one
 struct LinLocal {
   LinSeq q;
@@ -93,7 +105,8 @@ enum LinDot { LIN_PLAIN = 0, LIN_FAR = 1, LIN_FAR_PAIRS = 2 };
   hipError_t lin_sweep_##IO##_##D1(int D2, int rev, int dot,               \
                                    const LinSweep &p, hipStream_t s);      \
   hipError_t lin_local_##IO##_##D1(int D2, const LinLocal &p,              \
-                                   const LinLocal *r, hipStream_t s)
+                                   const LinLocal *r, hipStream_t s);     \
+  hipError_t lin_both_##IO##_##D1(int dot, const LinBoth &p, hipStream_t s)
 KDA_LIN_DECLARE(bf16, 16);
 KDA_LIN_DECLARE(bf16, 32);
 KDA_LIN_DECLARE(bf16, 64);

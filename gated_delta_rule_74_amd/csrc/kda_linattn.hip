@@ -94,7 +94,10 @@ __global__ __launch_bounds__(256) void kda_lin_scan(ScanSegs f, ScanSegs r,
 }
 
 // ---------------------------------------------------------------------------
-// the gate's gradient from its parts; one wave has one segment of one head
+// The gate's gradient from its parts.  A workgroup has one segment of one head,
+// a wave a chunk at a time: first every chunk's sums, then E from chunk to
+// chunk, then the gradients, from the parts read again (one wave that walked
+// the segment's chunks took 12 us for 8 of them, 18 for 16).
 
 struct GateGrad {
   LinSeq q;
@@ -103,10 +106,15 @@ struct GateGrad {
   void *dg;                           // [B,T,H] in the gate's type
   double *sums;                       // [B,H,NS] instead, for a fixed decay
 };
+constexpr int GATE_WAVES = 16;
 
-__global__ __launch_bounds__(64) void kda_lin_gate_grad(GateGrad p, int C) {
+__global__ __launch_bounds__(64 * GATE_WAVES) void kda_lin_gate_grad(
+    GateGrad p, int C) {
+  __shared__ float sum_late[MAX_CHUNKS], sum_early[MAX_CHUNKS],
+      forgets[MAX_CHUNKS], both[MAX_CHUNKS];
+  __shared__ double totals[GATE_WAVES];
   const LinSeq &q = p.q;
-  const int lane = threadIdx.x;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int h = blockIdx.x % q.H, bs = blockIdx.x / q.H;
   const int s = bs % q.NS, b = bs / q.NS;
   const size_t chain = (size_t)b * q.H + h;
@@ -114,36 +122,62 @@ __global__ __launch_bounds__(64) void kda_lin_gate_grad(GateGrad p, int C) {
   if (q.lengths) len = min(max(q.lengths[b], 0), q.T);
   const int t_begin = s * q.seg, t_end = min(q.T, t_begin + q.seg);
   const int live_end = min(len, t_end);
-  float E = p.ends[chain * q.NS + s];
-  double total = 0.0;
-  for (int t0 = t_begin + (t_end - t_begin - 1) / C * C; t0 >= t_begin;
-       t0 -= C) {
-    const int t = t0 + lane;
-    const bool in = lane < C && t < t_end, live = lane < C && t < live_end;
-    float late = 0.f, early = 0.f, pairs = 0.f, g = 0.f;
-    if (live) {
+  const int nch = (t_end - t_begin + C - 1) / C;  // at most MAX_CHUNKS
+  float late, early, g;
+  auto load = [&](int c) {
+    const int t = t_begin + c * C + lane;
+    late = early = g = 0.f;
+    if (lane < C && t < live_end) {
       late = p.late[chain * q.T + t];
       early = p.early[chain * q.T + t];
-      pairs = p.pairs[chain * q.T + t];
       const size_t i = q.gate_fixed ? (size_t)h
                                     : ((size_t)b * q.T + t) * q.H + h;
       g = q.gate_bf16 ? (float)((const bf16 *)q.g)[i]
                       : ((const float *)q.g)[i];
     }
-    float x = late, y = early, G = g;  // from the token on; up to it; the chunk
+  };
+  for (int c = w; c < nch; c += GATE_WAVES) {
+    load(c);
+    float G = g;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
-      const float a = __shfl_down(x, d, 64), c = __shfl_up(y, d, 64);
-      if (lane + d < 64) x += a;
-      if (lane >= d) y += c;
+      late += __shfl_xor(late, d, 64);
+      early += __shfl_xor(early, d, 64);
       G += __shfl_xor(G, d, 64);
     }
-    const float sum_late = __shfl(x, 0, 64), sum_early = __shfl(y, 63, 64);
-    // exp(G) < 2^-40
-    const float Z = G < -27.7f ? 0.f : E - sum_early;
-    // a token that forgets everything has no gradient, whatever the sums say
+    if (lane == 0) {
+      sum_late[c] = late;
+      sum_early[c] = early;
+      forgets[c] = G;
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float E = p.ends[chain * q.NS + s];
+    for (int c = nch - 1; c >= 0; --c) {
+      // exp(G) < 2^-40
+      const float Z = forgets[c] < -27.7f ? 0.f : E - sum_early[c];
+      both[c] = Z;
+      E = Z + sum_late[c];
+    }
+  }
+  __syncthreads();
+  double total = 0.0;
+  for (int c = w; c < nch; c += GATE_WAVES) {
+    load(c);
+    const int t = t_begin + c * C + lane;
+    const bool in = lane < C && t < t_end, live = lane < C && t < live_end;
+    float x = late, y = early;  // from the token on; up to it
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const float a = __shfl_down(x, d, 64), e = __shfl_up(y, d, 64);
+      if (lane + d < 64) x += a;
+      if (lane >= d) y += e;
+    }
     const float up = __shfl_up(y, 1, 64);
-    float dg = pairs + x + (lane == 0 ? 0.f : up) + Z;
+    float dg = x + (lane == 0 ? 0.f : up) + both[c];
+    if (live) dg += p.pairs[chain * q.T + t];
+    // a token that forgets everything has no gradient, whatever the sums say
     if (!live || g < -1e4f) dg = 0.f;
     if (p.sums) {
       total += dg;
@@ -152,12 +186,16 @@ __global__ __launch_bounds__(64) void kda_lin_gate_grad(GateGrad p, int C) {
       if (q.gate_bf16) ((bf16 *)p.dg)[i] = (bf16)dg;
       else ((float *)p.dg)[i] = dg;
     }
-    E = Z + sum_late;
   }
   if (p.sums) {
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) total += __shfl_xor(total, d, 64);
-    if (lane == 0) p.sums[chain * q.NS + s] = total;
+    if (lane == 0) totals[w] = total;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int i = 1; i < GATE_WAVES; ++i) total += totals[i];
+      p.sums[chain * q.NS + s] = total;
+    }
   }
 }
 
@@ -320,6 +358,19 @@ hipError_t sweep(int io_bf16, int D1, int D2, int rev, int dot,
   }
   return hipErrorInvalidValue;
 }
+hipError_t both(int io_bf16, int D, int dot, const LinBoth &p, hipStream_t s) {
+  switch (D) {
+    case 16: return io_bf16 ? lin_both_bf16_16(dot, p, s)
+                            : lin_both_f32_16(dot, p, s);
+    case 32: return io_bf16 ? lin_both_bf16_32(dot, p, s)
+                            : lin_both_f32_32(dot, p, s);
+    case 64: return io_bf16 ? lin_both_bf16_64(dot, p, s)
+                            : lin_both_f32_64(dot, p, s);
+    case 128: return io_bf16 ? lin_both_bf16_128(dot, p, s)
+                             : lin_both_f32_128(dot, p, s);
+  }
+  return hipErrorInvalidValue;
+}
 // of p, and of r beside it if given
 hipError_t local(int io_bf16, int D1, int D2, const LinLocal &p,
                  const LinLocal *r, hipStream_t s) {
@@ -459,6 +510,23 @@ hipError_t launch_linattn_backward(const LinParams &p, hipStream_t st) {
   const bool dots = gate || (shared && p.io_bf16);
   LinSweep w{};
   w.q = seq;
+  // shared heads: 32 bits a value, in bf16 as two halves of the workspace
+  const size_t part = (size_t)p.B * p.T * p.H * p.Dk * 2;
+  const bool rest = shared && p.io_bf16;
+  float *const early = (float *)(p.ws + l.early);
+  void *const dk = shared ? (void *)(p.ws + l.dk) : p.dk;
+  void *const dk_rest = rest ? p.ws + l.dk + part : nullptr;
+  if (p.Dk == p.Dv) {
+    // dk and dv together: their sweeps read the same four tensors
+    LinBoth z{};
+    z.q = seq;
+    z.qs = q; z.ks = k; z.vs = v; z.dos = dO;
+    z.dk = dk; z.dk_rest = dk_rest; z.dv = p.dv;
+    z.scale = p.scale;
+    z.ds_in = ds_in; z.ds0 = p.ds0;
+    z.early = early;
+    LIN_TRY(lin::both(p.io_bf16, p.Dk, dots, z, st));
+  } else {
   // dv
   w.a = k; w.b = q; w.c = dO;
   w.out = p.dv;
@@ -468,17 +536,19 @@ hipError_t launch_linattn_backward(const LinParams &p, hipStream_t st) {
   LIN_TRY(lin::sweep(p.io_bf16, p.Dk, p.Dv, 1, LIN_PLAIN, w, st));
   // dk
   w.a = v; w.b = dO; w.c = q; w.d = k;
-  // shared heads: 32 bits a value, in bf16 as two halves of the workspace
-  const size_t part = (size_t)p.B * p.T * p.H * p.Dk * 2;
-  const bool rest = shared && p.io_bf16;
-  w.out = shared ? (void *)(p.ws + l.dk) : p.dk;
-  w.out_rest = rest ? p.ws + l.dk + part : nullptr;
+  w.out = dk;
+  w.out_rest = dk_rest;
   w.s_end = nullptr;
   w.s_transposed = 1;
-  w.far_dot = (float *)(p.ws + l.early);
+  w.far_dot = early;
   LIN_TRY(lin::sweep(p.io_bf16, p.Dv, p.Dk, 1, dots ? LIN_FAR : LIN_PLAIN, w,
                      st));
+  }
   // dq
+  w = LinSweep{};
+  w.q = seq;
+  w.pair_scale = p.scale;
+  w.s_transposed = 1;
   w.a = dO; w.b = v; w.c = k; w.d = q;
   w.out = shared ? (void *)(p.ws + l.dq) : p.dq;
   w.out_rest = rest ? p.ws + l.dq + part : nullptr;
@@ -515,7 +585,7 @@ hipError_t launch_linattn_backward(const LinParams &p, hipStream_t st) {
                     (const float *)(p.ws + l.ends), p.dg,
                     p.gate_fixed ? sums : nullptr};
     const unsigned n = (unsigned)p.B * p.H * sp.NS;
-    lin::kda_lin_gate_grad<<<n, 64, 0, st>>>(x, lin_chunk(p.io_bf16));
+    lin::kda_lin_gate_grad<<<n, 64 * lin::GATE_WAVES, 0, st>>>(x, lin_chunk(p.io_bf16));
     LIN_TRY(hipGetLastError());
     if (p.gate_fixed) {
       lin::kda_lin_gate_sum<<<(p.H + 255) / 256, 256, 0, st>>>(

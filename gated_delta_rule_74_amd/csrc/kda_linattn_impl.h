@@ -725,7 +725,7 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
   // a second set of tiles, unless it would keep a second workgroup of 4 waves
   // off the CU
   constexpr int SET = C * (2 * T1::STR + (DOT ? 2 : 1) * T2::STR);
-  constexpr bool TWO = NW == 8 || 2 * SET * sizeof(IO) <= 64 * 1024;
+  constexpr bool TWO = NW == 8 || 2 * SET * sizeof(IO) <= 48 * 1024;
   __shared__ alignas(16) IO ta[1 + TWO][C * T1::STR], tb[1 + TWO][C * T1::STR],
       tc[1 + TWO][C * T2::STR];
   __shared__ alignas(16) IO td[1 + TWO][DOT ? C * T2::STR : 8];
@@ -883,6 +883,160 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
 }
 
 // ---------------------------------------------------------------------------
+// dk and dv in one reversed sweep, for Dk = Dv: they read the same four tensors,
+// and the two states (one the other's transpose, each in the registers of the
+// waves that need it) come from the same rows.
+
+template <typename IO, int D, bool DOT>
+__global__ __launch_bounds__(64 * nwaves<D>(), 2) void kda_lin_both(
+    LinBoth p) {
+  typedef Shape<IO> Sh;
+  typedef typename Mma<IO>::frag frag;
+  typedef Tile<IO, D> TD;
+  constexpr bool REV = true;
+  constexpr int C = Sh::C, NB = Sh::NB, NTU = Sh::NTU, KT = D / 16;
+  constexpr int NW = nwaves<D>(), NT = 64 * NW, COLS = D / 16;
+  constexpr bool TWO = NW == 8 || 8 * C * TD::STR * sizeof(IO) <= 48 * 1024;
+  __shared__ alignas(16) IO tq[1 + TWO][C * TD::STR], tk[1 + TWO][C * TD::STR],
+      tv[1 + TWO][C * TD::STR], to[1 + TWO][C * TD::STR];
+  __shared__ alignas(16) frag tp[2][NB * NTU * 64];
+  __shared__ Decays<C> decs[2 * BATCH];
+  __shared__ float far_dots[DOT ? COLS : 1][DOT ? C : 1];
+
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int g = lane >> 4, m = lane & 15;
+  const LinSeq &q = p.q;
+  const Where at(q, blockIdx.x, q.NS, 0, C);
+  const int nch = at.nch;
+  const bool mine = COLS >= NW || w < COLS;
+  const int col = mine ? w * 16 : 0;
+  zero_dead<IO, D, NT>(p.dv, q, at);
+  zero_dead<IO, D, NT>(p.dk, q, at);
+  if (DOT) zero_dead<IO, D, NT>(p.dk_rest, q, at);
+
+  f32x4 S[KT], St[KT];  // dS, its transpose
+  const size_t s_at = (at.chain * q.NS + at.s) * D * D;
+  load_state<D, D>(S, p.ds_in, s_at, 0, col, g, m);
+  load_state<D, D>(St, p.ds_in, s_at, 1, col, g, m);
+
+  unsigned sq, sk, sv, so;
+  const char *pq = operand<IO, D>(p.qs, q, at.b, at.h, sq);
+  const char *pk = operand<IO, D>(p.ks, q, at.b, at.h, sk);
+  const char *pv = operand<IO, D>(p.vs, q, at.b, at.h, sv);
+  const char *po = operand<IO, D>(p.dos, q, at.b, at.h, so);
+  Rows<IO, D, C, NT> rq, rk, rv, ro;
+  auto fetch = [&](int n) {
+    const int t0 = at.at(n, REV, C), live = n < nch ? at.live_end - t0 : 0;
+    rq.fetch(pq + (long long)t0 * sq, sq, live);
+    rk.fetch(pk + (long long)t0 * sk, sk, live);
+    rv.fetch(pv + (long long)t0 * sv, sv, live);
+    ro.fetch(po + (long long)t0 * so, so, live);
+  };
+  auto stash = [&](int x) {
+    rq.stash(tq[x]);
+    rk.stash(tk[x]);
+    rv.stash(tv[x]);
+    ro.stash(to[x]);
+  };
+  Keeper<IO, NW, REV> keeper;
+  auto make_decays = [&](int n0) {
+    keeper.make(decs, at, n0, p.scale, 1.f, w, lane);
+    keeper.fetch(q, at, n0 + BATCH, w, lane);
+  };
+  const bool keep_end = at.s == 0 && p.ds0;
+
+  if (nch > 0) {
+    keeper.fetch(q, at, 0, w, lane);
+    fetch(0);
+    make_decays(0);
+    if constexpr (TWO) {
+      stash(0);
+      fetch(1);
+    }
+    all_loaded();
+    barrier_keep_vmem();
+  }
+  for (int n = 0; n < nch; ++n) {
+    const int t0 = at.at(n, REV, C), x = TWO ? n & 1 : 0;
+    const Decays<C> &dec = decs[n % (2 * BATCH)];
+    if (n % BATCH == BATCH - 1) make_decays(n + 1);
+    if constexpr (TWO) {
+      stash(x ^ 1);
+      fetch(n + 2);
+    } else {
+      stash(0);
+      barrier_keep_vmem();
+      fetch(n + 1);
+    }
+    pair_products<IO, D, 0, REV, NW, 0>(tp[0], tk[x], tq[x], dec, p.scale, w,
+                                        lane, nullptr, nullptr, nullptr);
+    pair_products<IO, D, 0, REV, NW, 1>(tp[1], tv[x], to[x], dec, p.scale, w,
+                                        lane, nullptr, nullptr, nullptr);
+    __builtin_amdgcn_sched_barrier(0);
+    f32x4 av[NB], ak[NB];
+    if (mine) {
+      far_part<IO, D, false>(av, S, tk[x], g, m);
+      far_part<IO, D, DOT>(ak, St, tv[x], g, m);
+#pragma unroll
+      for (int rt = 0; rt < NB; ++rt) {
+        const float fw = dec.last[rt * 16 + m];
+        av[rt] *= fw;
+        ak[rt] *= fw;
+        if constexpr (DOT) {
+          const IO *y = tk[x] + TD::at(rt * 16 + m, col + 4 * g);
+          float dot = 0.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) dot += ak[rt][e] * to_f32(y[e]);
+          dot += __shfl_xor(dot, 16, 64);
+          dot += __shfl_xor(dot, 32, 64);
+          if (g == 0) far_dots[w][rt * 16 + m] = dot;
+        }
+      }
+    }
+    barrier_keep_vmem();
+
+    frag fo[NTU], fq[NTU];
+    if (mine) {
+#pragma unroll
+      for (int u = 0; u < NTU; ++u) {
+        fo[u] = TD::by_col(to[x], col, u, g, m);
+        fq[u] = TD::by_col(tq[x], col, u, g, m);
+      }
+      near_part<IO, REV>(av, tp[0], fo, lane);
+      near_part<IO, REV>(ak, tp[1], fq, lane);
+    }
+    const size_t o_at = (((size_t)at.b * q.T + t0) * q.H + at.h) * D;
+    const int rows = mine ? min(C, at.t_end - t0) : 0;
+    put_out<IO, D, false>(av, p.dv, nullptr, o_at, q.H, rows,
+                          at.live_end - t0, col, g, m);
+    put_out<IO, D, DOT>(ak, p.dk, p.dk_rest, o_at, q.H, rows,
+                        at.live_end - t0, col, g, m);
+    __builtin_amdgcn_sched_barrier(0);
+    if (mine && (n + 1 < nch || keep_end)) {
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) {
+        S[kt] *= dec.total;
+        St[kt] *= dec.total;
+      }
+      add_chunk<IO, D>(S, tq[x], fo, dec.first, g, m);
+      add_chunk<IO, D>(St, to[x], fq, dec.first, g, m);
+    }
+    if constexpr (DOT) {
+      const int t = t0 + threadIdx.x;
+      if (threadIdx.x < C && t < at.t_end) {
+        float v = 0.f;
+#pragma unroll
+        for (int i = 0; i < COLS; ++i) v += far_dots[i][threadIdx.x];
+        p.early[at.chain * q.T + t] = v;
+      }
+    }
+    barrier_keep_vmem();
+  }
+  if (mine && keep_end)
+    store_state<D, D>(S, p.ds0 + at.chain * D * D, col, g, m);
+}
+
+// ---------------------------------------------------------------------------
 // What a segment adds to a zero state, and its decay; the segment that no other
 // follows is left out.  The chunks are taken from the end that the state leaves
 // by, so that a chunk's weights are final and nothing is rescaled, and what is
@@ -1024,6 +1178,13 @@ hipError_t sweep(int D2, int rev, int dot, const LinSweep &p, hipStream_t s) {
   }
   return hipErrorInvalidValue;
 }
+template <typename IO, int D>
+hipError_t both(int dot, const LinBoth &p, hipStream_t s) {
+  const unsigned n = (unsigned)p.q.B * p.q.H * p.q.NS, t = 64 * nwaves<D>();
+  if (dot) kda_lin_both<IO, D, true><<<n, t, 0, s>>>(p);
+  else kda_lin_both<IO, D, false><<<n, t, 0, s>>>(p);
+  return hipGetLastError();
+}
 template <typename IO, int D1, int D2>
 hipError_t local_d2(const LinLocal &p, const LinLocal *r, hipStream_t s) {
   const dim3 n((unsigned)p.q.B * p.q.H * (p.q.NS - 1), r ? 2 : 1);
@@ -1052,6 +1213,10 @@ hipError_t local(int D2, const LinLocal &p, const LinLocal *r, hipStream_t s) {
   hipError_t lin_local_##IO##_##D1(int D2, const LinLocal &p,              \
                                    const LinLocal *r, hipStream_t s) {     \
     return lin::local<TYPE, D1>(D2, p, r, s);                              \
+  }                                                                        \
+  hipError_t lin_both_##IO##_##D1(int dot, const LinBoth &p,               \
+                                  hipStream_t s) {                         \
+    return lin::both<TYPE, D1>(dot, p, s);                                 \
   }
 
 }  // namespace kda
