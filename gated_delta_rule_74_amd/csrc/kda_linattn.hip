@@ -34,10 +34,7 @@ struct Split {
 
 // Workgroups wanted, and the tokens that a segment has at least and (gradient)
 // at most: see the end of this file's launch logic.
-#ifndef LIN_WAVES
-#define LIN_WAVES 2048
-#endif
-constexpr int WAVES = LIN_WAVES, MIN_CHUNKS = 4, MAX_CHUNKS = 64;
+constexpr int WAVES = 2048, MIN_CHUNKS = 4, MAX_CHUNKS = 64;
 
 Split split(int B, int T, int H, int D, int io_bf16, bool grad) {
   const int C = lin_chunk(io_bf16);
@@ -247,45 +244,60 @@ __global__ __launch_bounds__(256) void kda_lin_heads2(const bf16 *x,
 }
 
 // ---------------------------------------------------------------------------
-// one token: S = exp(g) S + k v^T, o = scale S^T q.  The state is read and
-// written once and everything else is small.  A thread has 4 columns of every
-// R-th row of one head; the rows' sums meet in LDS.
+// one token: S = exp(g) S + k v^T, o = scale S^T q.  Bound by HBM: the state is
+// read and written once and everything else is small.  A slice of up to 32
+// columns of a head (128-byte pieces of its rows) goes to a workgroup or a part
+// of one; a thread has 4 columns of every R-th row, and the rows' sums meet in
+// LDS.  The slices of a head run one after another on one XCD.
+
+template <typename IO, int DK, int DV> struct Step {
+  static constexpr int CW = DV < 32 ? DV : 32, SLICES = DV / CW;
+  static constexpr int Q = CW / 4;                            // across a row
+  static constexpr int PER = DK * Q < 256 ? DK * Q : 256;     // threads a slice
+  static constexpr int SPB = 256 / PER, R = PER / Q, N = DK / R;
+};
 
 template <typename IO, int DK, int DV>
 __global__ __launch_bounds__(256) void kda_lin_step(LinStepParams p) {
-  constexpr int Q = DV / 4;                       // threads across a row
-  constexpr int PER = DK * DV / 4 < 256 ? DK * DV / 4 : 256;  // threads a head
-  constexpr int HPB = 256 / PER, R = PER / Q, N = DK / R;
-  __shared__ alignas(16) float sq[HPB][DK], sk[HPB][DK];
+  typedef Step<IO, DK, DV> P;
+  constexpr int N = P::N, R = P::R, Q = P::Q, PER = P::PER;
+  __shared__ alignas(16) float sq[P::SPB][DK], sk[P::SPB][DK];
   __shared__ f32x4 part[256];
   const int tid = threadIdx.x, sub = tid / PER, th = tid % PER;
-  const size_t heads = (size_t)p.N * p.H;
-  const size_t head = (size_t)blockIdx.x * HPB + sub;
+  // 8 x SLICES workgroups of one slice: 8 heads, a head's slices 8 apart
+  size_t block = blockIdx.x;
+  constexpr int GROUP = 8 * P::SLICES;
+  if (P::SPB == 1 && block / GROUP < gridDim.x / GROUP) {
+    const size_t x = block % GROUP;
+    block = block / GROUP * GROUP + x % 8 * P::SLICES + x / 8;
+  }
+  const size_t slice = block * P::SPB + sub;
+  const size_t heads = (size_t)p.N * p.H, head = slice / P::SLICES;
   const bool on = head < heads;
   const size_t n = head / p.H;
   const int h = (int)(head % p.H);
-  const int c = th % Q, r = th / Q;
+  const int c = (int)(slice % P::SLICES) * P::CW + th % Q * 4, r = th / Q;
   f32x4 S[N];
   f32x4 v{0, 0, 0, 0};
   float a = 0.f;
-  float *const st = p.state + head * DK * DV;
+  float *const st = p.state + head * DK * DV + c;
   if (on) {
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      S[i] = ld_stream<f32x4>(st + (size_t)(r + i * R) * DV + c * 4);
+      S[i] = ld_stream<f32x4>(st + (size_t)(r + i * R) * DV);
     const size_t hq = n * p.Hk + h / (p.H / p.Hk);
     for (int i = th; i < DK; i += PER) {
       sq[sub][i] = to_f32(((const IO *)p.q)[hq * DK + i]) * p.scale;
       sk[sub][i] = to_f32(((const IO *)p.k)[hq * DK + i]);
     }
-    const IO *pv = (const IO *)p.v + head * DV + c * 4;
+    const IO *pv = (const IO *)p.v + head * DV + c;
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = to_f32(pv[e]);
     const size_t gi = p.gate_fixed ? (size_t)h : head;
     a = expf(p.gate_bf16 ? (float)((const bf16 *)p.g)[gi]
                          : ((const float *)p.g)[gi]);
   }
-  __syncthreads();
+  barrier_keep_vmem();
   f32x4 o{0, 0, 0, 0};
   if (on) {
 #pragma unroll
@@ -294,15 +306,15 @@ __global__ __launch_bounds__(256) void kda_lin_step(LinStepParams p) {
       const float k = sk[sub][row], q = sq[sub][row];
       S[i] = S[i] * a + v * k;
       o += S[i] * q;
-      st_stream(st + (size_t)row * DV + c * 4, S[i]);
+      st_stream(st + (size_t)row * DV, S[i]);
     }
   }
   part[tid] = o;
-  __syncthreads();
+  barrier_keep_vmem();
   if (on && r == 0) {
 #pragma unroll
     for (int i = 1; i < R; ++i) o += part[tid + i * Q];
-    IO *po = (IO *)p.o + head * DV + c * 4;
+    IO *po = (IO *)p.o + head * DV + c;
     if constexpr (sizeof(IO) == 2)
       *(bf16x4 *)po =
           bf16x4{(bf16)o[0], (bf16)o[1], (bf16)o[2], (bf16)o[3]};
@@ -313,11 +325,10 @@ __global__ __launch_bounds__(256) void kda_lin_step(LinStepParams p) {
 
 template <typename IO, int DK, int DV>
 hipError_t step(const LinStepParams &p, hipStream_t s) {
-  constexpr int PER = DK * DV / 4 < 256 ? DK * DV / 4 : 256;
-  constexpr int HPB = 256 / PER;
-  const size_t heads = (size_t)p.N * p.H;
-  kda_lin_step<IO, DK, DV><<<(unsigned)((heads + HPB - 1) / HPB), 256, 0, s>>>(
-      p);
+  typedef Step<IO, DK, DV> P;
+  const size_t slices = (size_t)p.N * p.H * P::SLICES;
+  kda_lin_step<IO, DK, DV>
+      <<<(unsigned)((slices + P::SPB - 1) / P::SPB), 256, 0, s>>>(p);
   return hipGetLastError();
 }
 template <typename IO, int DK>

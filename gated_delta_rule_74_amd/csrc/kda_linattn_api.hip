@@ -170,7 +170,8 @@ kda_status kda_linattn_step(const void *q, const void *k, const void *v,
   if (!distinct({o, state}, {q, k, v, g})) return KDA_EINVAL;
   if (!dim_ok(Dk) || !dim_ok(Dv) || pair_of(io, gb) < 0)
     return KDA_EUNSUPPORTED;
-  if ((long long)N * H >= (1 << 24)) return KDA_EUNSUPPORTED;
+  // a workgroup of 256 for a quarter of a head
+  if ((long long)N * H >= (1 << 22)) return KDA_EUNSUPPORTED;
   kda::LinStepParams p{};
   p.q = q; p.k = k; p.v = v; p.g = g; p.state = state; p.o = o;
   p.io_bf16 = io == KDA_BF16; p.gate_bf16 = gb == KDA_BF16;

@@ -322,6 +322,29 @@ template <typename IO> struct Shape {
   typedef typename Mma<IO>::frag frag;
 };
 
+// Values are rounded in pairs; what is taken from f afterwards is taken from
+// the pairs.  (Left to itself the compiler rounds each value once more alone to
+// widen it again.)
+__device__ __forceinline__ void packed(bf16x8 &f) {
+  typedef unsigned u4 __attribute__((ext_vector_type(4)));
+  u4 v = __builtin_bit_cast(u4, f);
+  asm volatile("" : "+v"(v));
+  f = __builtin_bit_cast(bf16x8, v);
+}
+
+// An order for the compiler's scheduler: `ahead` LDS reads first, then reads and
+// matrix instructions in turn, until both are used up.  Left to itself it reads
+// an operand right before its use.
+template <int AHEAD, int READS, int MFMAS, int STEPS>
+__device__ __forceinline__ void reads_ahead() {
+  __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, MFMAS, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
+  }
+}
+
 // S += b^T diag(w) c over a chunk, c as operand fragments
 template <typename IO, int D1>
 __device__ __forceinline__ void add_chunk(
@@ -337,8 +360,9 @@ __device__ __forceinline__ void add_chunk(
     float x[8] = {};
 #pragma unroll
     for (int e = 0; e < NE; ++e) x[e] = Mma<IO>::elem(c[u], e) * wt[e];
-    const frag hi = Mma<IO>::pack(f32x4{x[0], x[1], x[2], x[3]},
-                                  f32x4{x[4], x[5], x[6], x[7]});
+    frag hi = Mma<IO>::pack(f32x4{x[0], x[1], x[2], x[3]},
+                            f32x4{x[4], x[5], x[6], x[7]});
+    if constexpr (sizeof(IO) == 2) packed(hi);
     frag lo = hi;
     if constexpr (sizeof(IO) == 2) {
 #pragma unroll
@@ -372,7 +396,8 @@ __device__ __forceinline__ void far_part(f32x4 (&acc)[Shape<IO>::NB],
     f32x4 y{0, 0, 0, 0};
     if constexpr (TPU == 2)
       if (u * TPU + 1 < KT) y = S[u * TPU + 1];
-    const frag fs = Mma<IO>::pack(x, y);
+    frag fs = Mma<IO>::pack(x, y);
+    if constexpr (LO) packed(fs);
     frag fl = fs;
     if constexpr (LO) {
       f32x4 x2, y2;
@@ -410,33 +435,44 @@ __device__ __forceinline__ void near_part(
         acc[rt] = Mma<IO>::mma(c[u], tp[(rt * NTU + u) * 64 + lane], acc[rt]);
 }
 
-// The wave that makes unit u2 (a 16 x 32 piece, fp32 16 x 16) of row rt of the
-// pair products.  A row by one wave would give the last of four waves four
-// tiles of 16 x 16 and the first one; so it is three at most, over eight waves
-// two, and over eight with a second set of products (SET 1) three.
-template <int NW, int NB, bool REV, int SET>
-__device__ constexpr int pair_owner(int rt, int u2) {
-  const int r = REV ? NB - 1 - rt : rt, u = REV ? 1 - u2 : u2;
-  if (NB == 2) return r + u + (SET ? NW - 3 : 0);
-  if (NW == 8 && SET)
-    return r == 3 ? (u ? 3 : 1) : r == 2 ? (u ? 3 : 5) : r == 1 ? 0 : 1;
-  if (NW == 8) return 2 * r + u;
-  return (r == 3 ? u : r == 2 ? 2 : r == 1 ? 3 : 0) ^ SET;
+// The units of the pair products: 16 x 32 pieces (fp32 16 x 16) of a row of
+// tiles, those with two tiles of pairs first.  Unit `idx`'s row and place in it,
+// for the map that looks back; the other's is its mirror image.
+template <int NB> constexpr int pair_units() { return NB == 2 ? 3 : 6; }
+template <int NB, bool REV>
+__device__ __forceinline__ void pair_unit(int idx, int &rt, int &u2) {
+  // rows and places as 4-bit fields: (3,0) (3,1) (2,0) (1,0) (2,1) (0,0); with
+  // two rows of tiles (1,0) (1,1) (0,0)
+  constexpr unsigned ROWS = NB == 2 ? 0x011 : 0x021233;
+  constexpr unsigned PLACES = NB == 2 ? 0x010 : 0x010010;
+  rt = ROWS >> 4 * idx & 15;
+  u2 = PLACES >> 4 * idx & 15;
+  if (REV) {
+    rt = NB - 1 - rt;
+    u2 = 1 - u2;
+  }
 }
 
 // sums over the pairs of a tile, for the gate's gradient: for the tile's j, of
 // all pairs with an earlier j of the tile (of the diagonal tiles, whose i is no
 // earlier); for its i, of all pairs with this or a later i
 template <int NB> struct PairSums {
-  float by_j[NB][NB][16], by_i[NB][NB][16];
-  // the sum of all pairs (i, j) of a chunk with i >= t > j, in a fixed order
+  alignas(16) float by_j[NB][NB][16], by_i[NB][NB][16];
+  // the sum of all pairs (i, j) of a chunk with i >= t > j, in a fixed order;
+  // every load is asked for at once, those that count for nothing among them
   __device__ __forceinline__ float across(int t) const {
     const int tt = t / 16, k = t % 16;
-    float v = by_j[tt][tt][k];
-    for (int rt = tt + 1; rt < NB; ++rt) v += by_j[rt][tt][k];
-    for (int jt = 0; jt < tt; ++jt) {
-      v += by_i[tt][jt][k];
-      for (int rt = tt + 1; rt < NB; ++rt) v += by_i[rt][jt][0];
+    float v = 0.f;
+#pragma unroll
+    for (int x = 0; x < NB; ++x) {
+      const float a = by_j[x][tt][k], b = by_i[tt][x][k];
+      v += x >= tt ? a : 0.f;
+      v += x < tt ? b : 0.f;
+#pragma unroll
+      for (int y = 0; y + 1 < x; ++y) {
+        const float c = by_i[x][y][0];
+        v += x > tt && y < tt ? c : 0.f;
+      }
     }
     return v;
   }
@@ -451,9 +487,10 @@ __device__ __forceinline__ float add_row_shl(float x) {
 template <int NB>
 __device__ __forceinline__ void pair_sums(PairSums<NB> &s, int rt, int jt,
                                           f32x4 qk, int g, int m) {
+  const bool diag = rt == jt;  // the same for the whole wave
   float c[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) c[e] = rt == jt ? qk[e] : group_sum<16>(qk[e]);
+  for (int e = 0; e < 4; ++e) c[e] = diag ? qk[e] : group_sum<16>(qk[e]);
   const float tot = (c[0] + c[1]) + (c[2] + c[3]);
   const float v1 = __shfl_up(tot, 16, 64), v2 = __shfl_up(tot, 32, 64),
               v3 = __shfl_up(tot, 48, 64);
@@ -461,14 +498,14 @@ __device__ __forceinline__ void pair_sums(PairSums<NB> &s, int rt, int jt,
   if (g >= 3) pre += v3;
   if (g >= 2) pre += v2;
   if (g >= 1) pre += v1;
+  f32x4 v;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const float v =
-        rt == jt ? group_sum<16>(4 * g + e <= m ? pre : 0.f) : pre;
-    if (m == 0) s.by_j[rt][jt][4 * g + e] = v;
+    v[e] = diag ? group_sum<16>(4 * g + e <= m ? pre : 0.f) : pre;
     pre += c[e];
   }
-  if (rt != jt) {
+  if (m == 0) *(f32x4 *)&s.by_j[rt][jt][4 * g] = v;
+  if (!diag) {
     float r = (qk[0] + qk[1]) + (qk[2] + qk[3]);
     r += __shfl_xor(r, 16, 64);
     r += __shfl_xor(r, 32, 64);
@@ -480,69 +517,109 @@ __device__ __forceinline__ void pair_sums(PairSums<NB> &s, int rt, int jt,
   }
 }
 
-// The pair products of a chunk, transposed: rows j, columns i = rt * 16 + m.
-// Where all of a tile's j lie before (REV: behind) its i, the decay between them
-// is that from i to the border next to j's tile, one a lane, times that from
-// there to j.  D2 > 0: also the sums over the pairs' products with c_j . d_i
-template <typename IO, int D1, int D2, bool REV, int NW, int SET>
-__device__ __forceinline__ void pair_products(
-    typename Mma<IO>::frag *tp, const IO *ta, const IO *tb,
-    const Decays<Shape<IO>::C> &dec, float scale, int w, int lane,
-    const IO *tc, const IO *td, PairSums<Shape<IO>::NB> *sums) {
+// The operands and the result of a chunk's pair products
+template <typename IO> struct PairSet {
+  const IO *a, *b;
+  typename Mma<IO>::frag *p;
+};
+
+// K units of the pair products of a chunk, from `first` on every NW-th of those
+// of all sets, transposed: rows j, columns i = rt * 16 + m.  Where all of a
+// tile's j lie before (REV: behind) its i, the decay between them is that from i
+// to the border next to j's tile, one a lane, times that from there to j.
+// D2 > 0: also the sums over the pairs' products with c_j . d_i.  The units go
+// side by side, in the same code for all waves (a branch for each unit let
+// nothing overlap: 24 of the 144 us of kda_lin_both at B1 T8192 H32 D128).
+template <typename IO, int D1, int D2, bool REV, int NW, int K, int SETS>
+__device__ __forceinline__ void pair_batch(
+    const PairSet<IO> (&sets)[SETS], const Decays<Shape<IO>::C> &dec,
+    float scale, int first, int lane, const IO *tc, const IO *td,
+    PairSums<Shape<IO>::NB> *sums) {
   typedef Shape<IO> Sh;
   typedef typename Mma<IO>::frag frag;
   typedef Tile<IO, D1> T1;
   constexpr int TPU = Sh::TPU, NB = Sh::NB, NTU = Sh::NTU;
+  constexpr int UNITS = pair_units<NB>();
   const int g = lane >> 4, m = lane & 15;
+  int rt[K], u2[K];
+  const IO *a[K], *b[K];
+  frag *p[K];
+  f32x4 tile[K][2];
 #pragma unroll
-  for (int rt = 0; rt < NB; ++rt) {
-    const int i = rt * 16 + m;
-#pragma unroll
-    for (int u2 = 0; u2 < NTU; ++u2) {
-      if (!has_pairs<REV>(rt, REV ? u2 * TPU + TPU - 1 : u2 * TPU)) continue;
-      if (pair_owner<NW, NB, REV, SET>(rt, u2) != w) continue;
-      f32x4 tile[2];
-      tile[0] = tile[1] = f32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int u = 0; u < Sh::units(D1); ++u) {
-        const frag fa = T1::by_row(ta, rt * 16, u, g, m);
-#pragma unroll
-        for (int x = 0; x < TPU; ++x)
-          if (has_pairs<REV>(rt, u2 * TPU + x))
-            tile[x] = Mma<IO>::mma(
-                T1::by_row(tb, (u2 * TPU + x) * 16, u, g, m), fa, tile[x]);
-      }
-#pragma unroll
-      for (int x = 0; x < TPU; ++x) {
-        const int jt = u2 * TPU + x;
-        if (!has_pairs<REV>(rt, jt)) continue;
-        f32x4 &acc = tile[x];
-        if (jt == rt) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int j = jt * 16 + 4 * g + e;
-            const double d = REV ? dec.G[j] - dec.G[i] : dec.G[i] - dec.G[j];
-            const float f = acc[e] * (scale * exp2_diff(d));
-            acc[e] = (REV ? j >= i : j <= i) ? f : 0.f;
-          }
-        } else {
-          const double d = REV ? dec.G[jt * 16 - 1] - dec.G[i]
-                               : dec.G[i] - dec.G[jt * 16 + 15];
-          acc *= *(const f32x4 *)(dec.tile + jt * 16 + 4 * g) *
-                 (scale * exp2_diff(d));
-        }
-        if constexpr (D2 > 0) {
-          f32x4 qk{0, 0, 0, 0};
-#pragma unroll
-          for (int u = 0; u < Sh::units(D2); ++u)
-            qk = Mma<IO>::mma(Tile<IO, D2>::by_row(tc, jt * 16, u, g, m),
-                              Tile<IO, D2>::by_row(td, rt * 16, u, g, m), qk);
-          pair_sums<NB>(*sums, rt, jt, qk * acc, g, m);
-        }
-      }
-      tp[(rt * NTU + u2) * 64 + lane] = Mma<IO>::pack(tile[0], tile[1]);
-    }
+  for (int k = 0; k < K; ++k) {
+    int idx = first + k * NW;
+    const bool second = SETS == 2 && idx >= UNITS;
+    if (second) idx -= UNITS;
+    pair_unit<NB, REV>(idx, rt[k], u2[k]);
+    const PairSet<IO> &s = sets[0], &s2 = sets[SETS - 1];
+    a[k] = (second ? s2.a : s.a) + rt[k] * 16 * T1::STR;
+    b[k] = (second ? s2.b : s.b) + u2[k] * 16 * TPU * T1::STR;
+    p[k] = (second ? s2.p : s.p) + (rt[k] * NTU + u2[k]) * 64;
+    tile[k][0] = tile[k][1] = f32x4{0, 0, 0, 0};
   }
+#pragma unroll
+  for (int u = 0; u < Sh::units(D1); ++u)
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const frag fa = T1::by_row(a[k], 0, u, g, m);
+#pragma unroll
+      for (int x = 0; x < TPU; ++x)
+        tile[k][x] =
+            Mma<IO>::mma(T1::by_row(b[k], x * 16, u, g, m), fa, tile[k][x]);
+    }
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int i = rt[k] * 16 + m;
+    const double Gi = dec.G[i];
+#pragma unroll
+    for (int x = 0; x < TPU; ++x) {
+      const int jt = u2[k] * TPU + x;
+      f32x4 &acc = tile[k][x];
+      if (jt == rt[k]) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = 4 * g + e;
+          const double d = REV ? dec.G[jt * 16 + j] - Gi
+                               : Gi - dec.G[jt * 16 + j];
+          const float f = acc[e] * (scale * exp2_diff(d));
+          acc[e] = (REV ? j >= m : j <= m) ? f : 0.f;
+        }
+      } else if (REV ? jt > rt[k] : jt < rt[k]) {
+        const double d = REV ? dec.G[jt * 16 - 1] - Gi
+                             : Gi - dec.G[jt * 16 + 15];
+        acc *= *(const f32x4 *)(dec.tile + jt * 16 + 4 * g) *
+               (scale * exp2_diff(d));
+      } else {
+        acc = f32x4{0, 0, 0, 0};
+        continue;
+      }
+      if constexpr (D2 > 0) {
+        f32x4 qk{0, 0, 0, 0};
+#pragma unroll
+        for (int u = 0; u < Sh::units(D2); ++u)
+          qk = Mma<IO>::mma(Tile<IO, D2>::by_row(tc, jt * 16, u, g, m),
+                            Tile<IO, D2>::by_row(td, rt[k] * 16, u, g, m), qk);
+        pair_sums<NB>(*sums, rt[k], jt, qk * acc, g, m);
+      }
+    }
+    p[k][lane] = Mma<IO>::pack(tile[k][0], tile[k][1]);
+  }
+}
+
+// all of a chunk's pair products, shared out over the waves
+template <typename IO, int D1, int D2, bool REV, int NW, int SETS>
+__device__ __forceinline__ void pair_products(
+    const PairSet<IO> (&sets)[SETS], const Decays<Shape<IO>::C> &dec,
+    float scale, int w, int lane, const IO *tc = nullptr,
+    const IO *td = nullptr, PairSums<Shape<IO>::NB> *sums = nullptr) {
+  constexpr int N = SETS * pair_units<Shape<IO>::NB>();
+  constexpr int FULL = N / NW, MORE = N % NW;
+  if (w < MORE)
+    pair_batch<IO, D1, D2, REV, NW, FULL + 1, SETS>(sets, dec, scale, w, lane,
+                                                    tc, td, sums);
+  else if constexpr (FULL > 0)
+    pair_batch<IO, D1, D2, REV, NW, FULL, SETS>(sets, dec, scale, w, lane, tc,
+                                                td, sums);
 }
 
 __device__ __forceinline__ uint2 pack4(f32x4 v) {
@@ -634,6 +711,15 @@ __device__ __forceinline__ void store_state(const f32x4 (&S)[D1 / 16], float *p,
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       p[(kt * 16 + 4 * g + e) * D2 + col + m] = S[kt][e];
+}
+
+// x[0][i] + x[1][i] + ..., in this order
+template <int N, int C>
+__device__ __forceinline__ float column_sum(const float (&x)[N][C], int i) {
+  float v = 0.f;
+#pragma unroll
+  for (int k = 0; k < N; ++k) v += x[k][i];
+  return v;
 }
 
 // waves of a workgroup whose output is D2 wide
@@ -731,8 +817,8 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
   __shared__ alignas(16) IO td[1 + TWO][DOT ? C * T2::STR : 8];
   __shared__ alignas(16) frag tp[NB * NTU * 64];
   __shared__ Decays<C> decs[2 * BATCH];
-  __shared__ float far_dots[DOT ? COLS : 1][DOT ? C : 1];
-  __shared__ PairSums<DOT == LIN_FAR_PAIRS ? NB : 1> sums;
+  __shared__ float far_dots[2][DOT ? COLS : 1][DOT ? C : 1];
+  __shared__ PairSums<DOT == LIN_FAR_PAIRS ? NB : 1> sums[2];
 
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int g = lane >> 4, m = lane & 15;
@@ -775,6 +861,15 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
                 REV ? p.far_scale : p.add_scale, w, lane);
     keeper.fetch(q, at, n0 + BATCH, w, lane);
   };
+  // a chunk's sums are put together while the next chunk's pair products are
+  // made, by the wave that has least to do with those
+  auto finish = [&](int n) {
+    const int t = at.at(n, REV, C) + lane;
+    if (w != NW - 1 || lane >= C || t >= at.t_end) return;
+    p.far_dot[at.chain * q.T + t] = column_sum(far_dots[n & 1], lane);
+    if constexpr (DOT == LIN_FAR_PAIRS)
+      p.pair_dot[at.chain * q.T + t] = sums[n & 1].across(lane);
+  };
   const bool last_seg = REV ? at.s == 0 : at.s == q.NS - 1;
   const bool keep_end = (last_seg && p.s_end) || DOT == LIN_FAR_PAIRS;
 
@@ -803,9 +898,12 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
       barrier_keep_vmem();
       fetch(n + 1);
     }
-    pair_products<IO, D1, DOT == LIN_FAR_PAIRS ? D2 : 0, REV, NW, 0>(
-        tp, ta[x], tb[x], dec, p.pair_scale, w, lane, tc[x], td[x],
-        (PairSums<NB> *)&sums);
+    const PairSet<IO> pairs[1] = {{ta[x], tb[x], tp}};
+    pair_products<IO, D1, DOT == LIN_FAR_PAIRS ? D2 : 0, REV, NW, 1>(
+        pairs, dec, p.pair_scale, w, lane, tc[x], td[x],
+        (PairSums<NB> *)&sums[n & 1]);
+    if constexpr (DOT)
+      if (n > 0) finish(n - 1);
     __builtin_amdgcn_sched_barrier(0);
     f32x4 acc[NB];
     if (mine) {
@@ -821,7 +919,7 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
           for (int e = 0; e < 4; ++e) dot += acc[rt][e] * to_f32(y[e]);
           dot += __shfl_xor(dot, 16, 64);
           dot += __shfl_xor(dot, 32, 64);
-          if (g == 0) far_dots[w][rt * 16 + m] = dot;
+          if (g == 0) far_dots[n & 1][w][rt * 16 + m] = dot;
         }
       }
     }
@@ -842,20 +940,12 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) S[kt] *= dec.total;
       add_chunk<IO, D1>(S, tb[x], fc, REV ? dec.first : dec.last, g, m);
-    }
-    if constexpr (DOT) {
-      const int t = t0 + threadIdx.x;
-      if (threadIdx.x < C && t < at.t_end) {
-        float v = 0.f;
-#pragma unroll
-        for (int i = 0; i < COLS; ++i) v += far_dots[i][threadIdx.x];
-        p.far_dot[at.chain * q.T + t] = v;
-        if constexpr (DOT == LIN_FAR_PAIRS)
-          p.pair_dot[at.chain * q.T + t] = sums.across(threadIdx.x);
-      }
+      if constexpr (sizeof(IO) == 2) reads_ahead<12, 2, 2, NTU * KT>();
     }
     barrier_keep_vmem();
   }
+  if constexpr (DOT)
+    if (nch > 0) finish(nch - 1);
 
   if (mine && last_seg && p.s_end)
     store_state<D1, D2>(S, p.s_end + at.chain * D1 * D2, col, g, m);
@@ -872,11 +962,12 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
     }
     v = group_sum<32>(v);
     v += __shfl_xor(v, 32, 64);
-    if (mine && lane == 0) far_dots[w][0] = v;
+    barrier_keep_vmem();  // the last chunk's sums have been read
+    if (mine && lane == 0) far_dots[0][w][0] = v;
     barrier_keep_vmem();
     if (threadIdx.x == 0) {
       v = 0.f;
-      for (int i = 0; i < COLS; ++i) v += far_dots[i][0];
+      for (int i = 0; i < COLS; ++i) v += far_dots[0][i][0];
       p.e_out[at.chain * q.NS + at.s] = v;
     }
   }
@@ -901,7 +992,7 @@ __global__ __launch_bounds__(64 * nwaves<D>(), 2) void kda_lin_both(
       tv[1 + TWO][C * TD::STR], to[1 + TWO][C * TD::STR];
   __shared__ alignas(16) frag tp[2][NB * NTU * 64];
   __shared__ Decays<C> decs[2 * BATCH];
-  __shared__ float far_dots[DOT ? COLS : 1][DOT ? C : 1];
+  __shared__ float far_dots[2][DOT ? COLS : 1][DOT ? C : 1];
 
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int g = lane >> 4, m = lane & 15;
@@ -943,6 +1034,11 @@ __global__ __launch_bounds__(64 * nwaves<D>(), 2) void kda_lin_both(
     keeper.make(decs, at, n0, p.scale, 1.f, w, lane);
     keeper.fetch(q, at, n0 + BATCH, w, lane);
   };
+  auto finish = [&](int n) {
+    const int t = at.at(n, REV, C) + lane;
+    if (w == NW - 1 && lane < C && t < at.t_end)
+      p.early[at.chain * q.T + t] = column_sum(far_dots[n & 1], lane);
+  };
   const bool keep_end = at.s == 0 && p.ds0;
 
   if (nch > 0) {
@@ -968,10 +1064,11 @@ __global__ __launch_bounds__(64 * nwaves<D>(), 2) void kda_lin_both(
       barrier_keep_vmem();
       fetch(n + 1);
     }
-    pair_products<IO, D, 0, REV, NW, 0>(tp[0], tk[x], tq[x], dec, p.scale, w,
-                                        lane, nullptr, nullptr, nullptr);
-    pair_products<IO, D, 0, REV, NW, 1>(tp[1], tv[x], to[x], dec, p.scale, w,
-                                        lane, nullptr, nullptr, nullptr);
+    const PairSet<IO> pairs[2] = {{tk[x], tq[x], tp[0]},
+                                  {tv[x], to[x], tp[1]}};
+    pair_products<IO, D, 0, REV, NW, 2>(pairs, dec, p.scale, w, lane);
+    if constexpr (DOT)
+      if (n > 0) finish(n - 1);
     __builtin_amdgcn_sched_barrier(0);
     f32x4 av[NB], ak[NB];
     if (mine) {
@@ -989,7 +1086,7 @@ __global__ __launch_bounds__(64 * nwaves<D>(), 2) void kda_lin_both(
           for (int e = 0; e < 4; ++e) dot += ak[rt][e] * to_f32(y[e]);
           dot += __shfl_xor(dot, 16, 64);
           dot += __shfl_xor(dot, 32, 64);
-          if (g == 0) far_dots[w][rt * 16 + m] = dot;
+          if (g == 0) far_dots[n & 1][w][rt * 16 + m] = dot;
         }
       }
     }
@@ -1020,18 +1117,12 @@ __global__ __launch_bounds__(64 * nwaves<D>(), 2) void kda_lin_both(
       }
       add_chunk<IO, D>(S, tq[x], fo, dec.first, g, m);
       add_chunk<IO, D>(St, to[x], fq, dec.first, g, m);
-    }
-    if constexpr (DOT) {
-      const int t = t0 + threadIdx.x;
-      if (threadIdx.x < C && t < at.t_end) {
-        float v = 0.f;
-#pragma unroll
-        for (int i = 0; i < COLS; ++i) v += far_dots[i][threadIdx.x];
-        p.early[at.chain * q.T + t] = v;
-      }
+      if constexpr (sizeof(IO) == 2) reads_ahead<16, 2, 2, 2 * NTU * KT>();
     }
     barrier_keep_vmem();
   }
+  if constexpr (DOT)
+    if (nch > 0) finish(nch - 1);
   if (mine && keep_end)
     store_state<D, D>(S, p.ds0 + at.chain * D * D, col, g, m);
 }

@@ -11,6 +11,8 @@
 // Angles.  position * inv_freq in fp32 would be off by 0.008 at position
 // 262143; in 64 bits, counted in turns, what is left after the whole turns is
 // exact to 1e-10, and a quarter turn is taken off before the rounding to fp32.
+#include <type_traits>
+
 #include "kda_layer.h"
 #include "kda_vec.h"
 
@@ -19,7 +21,11 @@ namespace qkn {
 
 constexpr int THREADS = 256, WAVES = THREADS / 64;
 // rows whose loads a wave issues before it uses the first
-constexpr int AHEAD = 4;
+#ifndef QK_AHEAD
+#define QK_AHEAD 4
+#define QK_WAVES 4096
+#endif
+constexpr int AHEAD = QK_AHEAD;
 
 // cosine and sine of 2 pi a: a's whole turns and quarters are taken off in 64
 // bits, what is left (|x| <= pi / 4) goes through the two Taylor series, whose
@@ -148,15 +154,17 @@ __global__ __launch_bounds__(THREADS) void kda_qk_norm_fwd(QkNormParams p,
   const IO *const k = (const IO *)p.k + at * p.k_stride + ch;
   IO *const qo = (IO *)p.q_out + at * p.qo_stride + ch;
   IO *const ko = (IO *)p.k_out + at * p.ko_stride + ch;
-  for (int h = h0; h < heads; h += step * AHEAD) {
-    Raw8<IO> raw[AHEAD];
+  // `n` rows of every lane, all their loads first
+  auto rows = [&](auto count, int h) {
+    constexpr int n = decltype(count)::value;
+    Raw8<IO> raw[n];
 #pragma unroll
-    for (int a = 0; a < AHEAD; ++a) {
+    for (int a = 0; a < n; ++a) {
       const int hh = min(h + a * step + mine, heads - 1);
       raw[a].load(hh < p.Hq ? q + hh * D : k + (hh - p.Hq) * D);
     }
 #pragma unroll
-    for (int a = 0; a < AHEAD; ++a) {
+    for (int a = 0; a < n; ++a) {
       const int hh = h + a * step + mine;
       const bool isq = hh < p.Hq;
       float x[8], ss = 0.f;
@@ -175,7 +183,11 @@ __global__ __launch_bounds__(THREADS) void kda_qk_norm_fwd(QkNormParams p,
       if (here && hh < heads)
         store8(isq ? qo + hh * D : ko + (hh - p.Hq) * D, x);
     }
-  }
+  };
+  int h = h0;
+  for (; h + (AHEAD - 1) * step < heads; h += AHEAD * step)
+    rows(std::integral_constant<int, AHEAD>{}, h);
+  for (; h < heads; h += step) rows(std::integral_constant<int, 1>{}, h);
 }
 
 template <typename IO, int D>
@@ -274,7 +286,7 @@ Grid grid_of(long long rows, int Hq, int Hk, int D, long long want) {
   g.units = groups * split;
   return g;
 }
-constexpr long long WANTED_WAVES = 4096;
+constexpr long long WANTED_WAVES = QK_WAVES;
 
 int bwd_groups(const Grid &g) {
   const long long n = (g.units + WAVES - 1) / WAVES;

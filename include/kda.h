@@ -547,7 +547,7 @@ kda_status kda_linattn_backward(
 
 /* One token of it for N sequences: q, k [N,Hk,Dk], v [N,H,Dv], g [N,H] (or
  * [H]), state [N,H,Dk,Dv] fp32 updated IN PLACE, o [N,H,Dv] in qkv_dtype (must
- * not alias an input or the state).  KDA_EUNSUPPORTED from N * H = 2^24 on. */
+ * not alias an input or the state).  KDA_EUNSUPPORTED from N * H = 2^22 on. */
 kda_status kda_linattn_step(const void *q, const void *k, const void *v,
                             kda_dtype qkv_dtype, const void *g,
                             kda_dtype gate_dtype, float *state, void *o, int N,

@@ -128,7 +128,7 @@ def _step(**kw):
     (dict(state=None), INV), (dict(o=None), INV), (dict(o=adr(4)), INV),
     (dict(state=adr(2)), INV), (dict(g=A + 2), INV), (dict(gt=7), INV),
     (dict(scale=float("nan")), INV), (dict(Dk=24), UNS), (dict(Dv=256), UNS),
-    (dict(io=F), UNS), (dict(N=1 << 23), UNS),
+    (dict(io=F), UNS), (dict(N=1 << 21), UNS),
 ])
 def test_linattn_step_rejects(kw, want):
     assert _step(**kw) == want
