@@ -11,8 +11,6 @@
 // Angles.  position * inv_freq in fp32 would be off by 0.008 at position
 // 262143; in 64 bits, counted in turns, what is left after the whole turns is
 // exact to 1e-10, and a quarter turn is taken off before the rounding to fp32.
-#include <type_traits>
-
 #include "kda_layer.h"
 #include "kda_vec.h"
 
@@ -20,12 +18,11 @@ namespace kda {
 namespace qkn {
 
 constexpr int THREADS = 256, WAVES = THREADS / 64;
-// rows whose loads a wave issues before it uses the first
-#ifndef QK_AHEAD
-#define QK_AHEAD 4
-#define QK_WAVES 4096
-#endif
-constexpr int AHEAD = QK_AHEAD;
+// Rows (of each lane's head) that are asked for at a time, while those before
+// them are worked on: 3 take 50.6 us at 8192 tokens of 32 + 32 heads of 128 and
+// 59.4 at 32768 of 16 + 2, 2 take 52.3 and 58.5, 1 54.9 and 62.0; 4 without the
+// overlap 54.1 and 68.4.
+constexpr int AHEAD = 3;
 
 // cosine and sine of 2 pi a: a's whole turns and quarters are taken off in 64
 // bits, what is left (|x| <= pi / 4) goes through the two Taylor series, whose
@@ -79,9 +76,11 @@ __device__ __forceinline__ void make_turns(const QkNormParams &p,
   // the previous token's values have been read
   __builtin_amdgcn_wave_barrier();
   for (int i = lane; i < tokens * half; i += 64) {
-    long long tok = first + i / half;
-    if (tok >= p.rows) tok = p.rows - 1;
-    const double a = (double)p.positions[tok] * (double)p.inv_freq[i % half];
+    // one token a wave is the usual case, and a division takes 40 instructions
+    const int n = tokens == 1 ? 0 : i / half;
+    const long long tok = first + n < p.rows ? first + n : p.rows - 1;
+    const double a =
+        (double)p.positions[tok] * (double)p.inv_freq[i - n * half];
     turn(a * 0.15915494309189535, tc[i], ts[i]);
   }
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -145,26 +144,24 @@ __global__ __launch_bounds__(THREADS) void kda_qk_norm_fwd(QkNormParams p,
   const int heads = p.Hq + p.Hk, step = gr.slots * gr.split;
   const int h0 = (int)(unit % gr.split) * gr.slots;
   const int mine = slot % gr.slots;
-  float wq[8], wk[8];
-  load8(p.wq ? p.wq + ch : nullptr, wq);
-  load8(p.wk ? p.wk + ch : nullptr, wk);
-  Turns t{};
-  if (p.rot) make_turns<D>(p, first, tokens, sub, ch, lane, tc[wave], ts[wave], t);
   const IO *const q = (const IO *)p.q + at * p.q_stride + ch;
   const IO *const k = (const IO *)p.k + at * p.k_stride + ch;
   IO *const qo = (IO *)p.q_out + at * p.qo_stride + ch;
   IO *const ko = (IO *)p.k_out + at * p.ko_stride + ch;
-  // `n` rows of every lane, all their loads first
-  auto rows = [&](auto count, int h) {
-    constexpr int n = decltype(count)::value;
-    Raw8<IO> raw[n];
+  // rows past the last head are read as the last
+  auto load = [&](Raw8<IO> (&raw)[AHEAD], int h) {
 #pragma unroll
-    for (int a = 0; a < n; ++a) {
+    for (int a = 0; a < AHEAD; ++a) {
       const int hh = min(h + a * step + mine, heads - 1);
       raw[a].load(hh < p.Hq ? q + hh * D : k + (hh - p.Hq) * D);
     }
+  };
+  Turns t{};
+  float wq[8], wk[8];
+  auto work = [&](const Raw8<IO> (&raw)[AHEAD], int h) {
 #pragma unroll
-    for (int a = 0; a < n; ++a) {
+    for (int a = 0; a < AHEAD; ++a) {
+      if (h + a * step >= heads) break;
       const int hh = h + a * step + mine;
       const bool isq = hh < p.Hq;
       float x[8], ss = 0.f;
@@ -175,7 +172,7 @@ __global__ __launch_bounds__(THREADS) void kda_qk_norm_fwd(QkNormParams p,
       }
       ss = group_sum<L>(ss);
       if (isq ? p.wq != nullptr : p.wk != nullptr) {
-        const float r = 1.f / sqrtf(ss / (float)D + p.eps);
+        const float r = l2_inv_norm(ss / (float)D + p.eps);
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = x[e] * r * (isq ? wq[e] : wk[e]);
       }
@@ -184,10 +181,20 @@ __global__ __launch_bounds__(THREADS) void kda_qk_norm_fwd(QkNormParams p,
         store8(isq ? qo + hh * D : ko + (hh - p.Hq) * D, x);
     }
   };
-  int h = h0;
-  for (; h + (AHEAD - 1) * step < heads; h += AHEAD * step)
-    rows(std::integral_constant<int, AHEAD>{}, h);
-  for (; h < heads; h += step) rows(std::integral_constant<int, 1>{}, h);
+  // the first rows are on their way while the angles are made, the next ones
+  // while these are worked on
+  Raw8<IO> ra[AHEAD], rb[AHEAD];
+  load(ra, h0);
+  load8(p.wq ? p.wq + ch : nullptr, wq);
+  load8(p.wk ? p.wk + ch : nullptr, wk);
+  if (p.rot)
+    make_turns<D>(p, first, tokens, sub, ch, lane, tc[wave], ts[wave], t);
+  for (int h = h0; h < heads; h += 2 * AHEAD * step) {
+    load(rb, h + AHEAD * step);
+    work(ra, h);
+    load(ra, h + 2 * AHEAD * step);
+    work(rb, h + AHEAD * step);
+  }
 }
 
 template <typename IO, int D>
@@ -233,7 +240,7 @@ __global__ __launch_bounds__(THREADS) void kda_qk_norm_bwd(QkNormParams p,
       ss = group_sum<L>(ss);
       if (p.rot) apply(t, p.interleaved, -1.f, d);
       const bool norm = isq ? p.wq != nullptr : p.wk != nullptr;
-      const float r = 1.f / sqrtf(ss / (float)D + p.eps);
+      const float r = l2_inv_norm(ss / (float)D + p.eps);
       float mean = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -268,7 +275,10 @@ __global__ __launch_bounds__(THREADS) void kda_qk_norm_bwd(QkNormParams p,
   }
 }
 
-// partial rows of the weight gradients
+// Partial rows of the weight gradients: four workgroups per CU (8191 tokens of
+// 32 + 8 heads: 512 take 64 us, 768 and 1024 56, 1280 58; two or three rows at
+// a time, or the next one's loads ahead, need more registers than four waves a
+// SIMD have and gain nothing).
 constexpr int MAX_WG = 1024;
 
 Grid grid_of(long long rows, int Hq, int Hk, int D, long long want) {
@@ -286,7 +296,8 @@ Grid grid_of(long long rows, int Hq, int Hk, int D, long long want) {
   g.units = groups * split;
   return g;
 }
-constexpr long long WANTED_WAVES = QK_WAVES;
+// (16384: the same, 65536: half again the time, as every wave makes its angles)
+constexpr long long WANTED_WAVES = 4096;
 
 int bwd_groups(const Grid &g) {
   const long long n = (g.units + WAVES - 1) / WAVES;

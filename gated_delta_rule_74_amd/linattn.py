@@ -163,12 +163,10 @@ def kda_linattn_step(q, k, v, g, state, *, scale=1.0, o=None, stream=None):
     return o
 
 
-def _token_stride(t, name):
-    """Values from token to token of t [..., H, D], whose last two dimensions
-    are dense and whose others are one range of evenly spaced tokens."""
-    if t.is_contiguous():
-        return t.shape[-2] * t.shape[-1]
-    shape, st = t.shape, t.stride()
+def _token_stride(shape, st, name):
+    """Values from token to token of a tensor [..., H, D] with these strides,
+    whose last two dimensions are dense and whose others are one range of
+    evenly spaced tokens."""
     if (st[-1] != 1 and shape[-1] != 1) or (st[-2] != shape[-1] and
                                             shape[-2] != 1):
         raise ValueError(f"{name}: the heads of a token must be dense")
@@ -184,56 +182,80 @@ def _token_stride(t, name):
     return shape[-2] * shape[-1] if step is None else step
 
 
-def _qk_codes(q, k, positions, inv_freq, wq, wk):
-    """Check the inputs; returns the dtype code, rows, Hq, Hk, D and rot."""
-    if q.dim() < 3:
-        raise ValueError(f"q has {q.dim()} dimensions, expected at least 3")
-    lead, Hq, D = q.shape[:-2], q.shape[-2], q.shape[-1]
-    io = _CODE.get(q.dtype)
+def _layout(t):
+    """shape, strides and dtype of a tensor or None"""
+    return None if t is None else (t.shape, t.stride(), t.dtype)
+
+
+@functools.lru_cache(maxsize=1024)
+def _qk_plan(q, k, positions, inv_freq, wq, wk, *more):
+    """The sizes of a call from its tensors' layouts (kept for the layouts that
+    came before: the checks take 6 us of a decode step's host time): dtype
+    code, rows, Hq, Hk, D, rot, then the token strides of q, k and of `more`,
+    (name, layout) of tensors shaped like q and k in turn."""
+    def need(what, shape, dtype, name):
+        if what is not None:
+            if tuple(what[0]) != tuple(shape):
+                raise ValueError(f"{name}: shape {tuple(what[0])}, expected "
+                                 f"{tuple(shape)}")
+            if what[2] != dtype:
+                raise ValueError(f"{name}: dtype {what[2]}, expected {dtype}")
+
+    qs, _, dtype = q
+    if len(qs) < 3:
+        raise ValueError(f"q has {len(qs)} dimensions, expected at least 3")
+    lead, Hq, D = qs[:-2], qs[-2], qs[-1]
+    io = _CODE.get(dtype)
     if io is None:
-        _io_dtype(q, "q")
+        raise ValueError(f"q: dtype {dtype}, expected float32 or bfloat16")
     Hk = 0
     if k is not None:
-        if k.shape[:-2] != lead or k.shape[-1] != D or \
-                k.dtype is not q.dtype or k.dim() != q.dim():
-            _need(k, (*lead, k.shape[-2] if k.dim() > 1 else 0, D), q.dtype,
-                  "k (must go with q)")
-        Hk = k.shape[-2]
+        Hk = k[0][-2] if len(k[0]) > 1 else 0
+        need(k, (*lead, Hk, D), dtype, "k (must go with q)")
     elif wk is not None:
         raise ValueError("wk without k")
-    _must(wq, (D,), _F32, "wq")
-    _must(wk, (D,), _F32, "wk")
+    need(wq, (D,), _F32, "wq")
+    need(wk, (D,), _F32, "wk")
     if (positions is None) != (inv_freq is None):
         raise ValueError("positions and inv_freq go together")
     rot = 0
     if inv_freq is not None:
-        if inv_freq.dim() != 1:
+        if len(inv_freq[0]) != 1:
             raise ValueError("inv_freq has one dimension")
-        rot = 2 * inv_freq.shape[0]
+        rot = 2 * inv_freq[0][0]
         if rot == 0:
             raise ValueError("inv_freq is empty")
-        _must(inv_freq, (rot // 2,), _F32, "inv_freq")
-        _must(positions, lead, torch.int32, "positions")
+        need(inv_freq, (rot // 2,), _F32, "inv_freq")
+        need(positions, lead, torch.int32, "positions")
     rows = 1
     for n in lead:
         rows *= n
     _int(max(Hq, Hk, D, rot), "size of q or k")
-    return io, rows, Hq, Hk, D, rot
-
-
-def _strided(dev, *ts):
-    """Data pointers and token strides of tensors (or None) on GPU `dev`."""
-    ptrs, steps = [], []
-    for t, name in ts:
+    strides = [_token_stride(qs, q[1], "q"),
+               0 if k is None else _token_stride(k[0], k[1], "k")]
+    for i, (name, t) in enumerate(more):
+        like = k if i % 2 else q
         if t is None:
-            ptrs.append(None)
-            steps.append(0)
-            continue
-        if t.get_device() != dev:
-            raise ValueError(f"{name} on {t.device}, expected cuda:{dev}")
-        steps.append(_token_stride(t, name))
-        ptrs.append(t.data_ptr())
-    return ptrs, steps
+            strides.append(like and like[0][-2] * D or 0)  # a new, dense one
+        elif like is None:
+            raise ValueError(f"{name} without k")
+        else:
+            need(t, like[0], dtype, name)
+            strides.append(_token_stride(t[0], t[1], name))
+    return (io, rows, Hq, Hk, D, rot), tuple(strides)
+
+
+def _pointer(t, dev, name):
+    """a strided tensor's data pointer (or None), on GPU number `dev`"""
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        raise ValueError(f"{name} on {t.device}, expected cuda:{dev}")
+    return t.data_ptr()
+
+
+def _dense(like):
+    return torch.empty_like(like, memory_format=torch.contiguous_format)
 
 
 def kda_qk_norm_rope(q, k, positions, inv_freq, *, wq=None, wk=None, eps=1e-6,
@@ -248,12 +270,10 @@ def kda_qk_norm_rope(q, k, positions, inv_freq, *, wq=None, wk=None, eps=1e-6,
     or with interleaved 2 i and 2 i + 1.  The heads of a token are dense;
     tokens may be apart, as parts of a fused projection are.  q_out, k_out may
     be q, k.  Returns (q_out, k_out or None)."""
-    io, rows, Hq, Hk, D, rot = _qk_codes(q, k, positions, inv_freq, wq, wk)
-    _must(q_out, q.shape, q.dtype, "q_out")
-    if k is not None:
-        _must(k_out, k.shape, k.dtype, "k_out")
-    elif k_out is not None:
-        raise ValueError("k_out without k")
+    (io, rows, Hq, Hk, D, rot), (sq, sk, so, sko) = _qk_plan(
+        _layout(q), _layout(k), _layout(positions), _layout(inv_freq),
+        _layout(wq), _layout(wk), ("q_out", _layout(q_out)),
+        ("k_out", _layout(k_out)))
     away = _elsewhere(q, stream)
     if away is not None:
         with away:
@@ -261,15 +281,15 @@ def kda_qk_norm_rope(q, k, positions, inv_freq, *, wq=None, wk=None, eps=1e-6,
                                     eps=eps, interleaved=interleaved,
                                     q_out=q_out, k_out=k_out)
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = _dense(q)
     if k_out is None and k is not None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        k_out = _dense(k)
     dev = q.get_device()
-    (pq, pk, po, ko), (sq, sk, so, sko) = _strided(
-        dev, (q, "q"), (k, "k"), (q_out, "q_out"), (k_out, "k_out"))
     p1, p2, pp, pf = _ptrs(dev, wq, wk, positions, inv_freq)
-    _check(_qk(pq, pk, io, sq, sk, p1, p2, pp, pf, rot, int(bool(interleaved)),
-               eps, po, ko, so, sko, rows, Hq, Hk, D, _raw_stream(dev)),
+    _check(_qk(q.data_ptr(), _pointer(k, dev, "k"), io, sq, sk, p1, p2, pp, pf,
+               rot, 1 if interleaved else 0, eps,
+               _pointer(q_out, dev, "q_out"), _pointer(k_out, dev, "k_out"),
+               so, sko, rows, Hq, Hk, D, _raw_stream(dev)),
            "kda_qk_norm_rope")
     return q_out, k_out
 
@@ -286,17 +306,15 @@ def kda_qk_norm_rope_backward(q, k, positions, inv_freq, dq_out, dk_out, *,
     write the gradients into (as parts of a fused projection's, or dq_out and
     dk_out themselves), or None for new ones.  Returns (dq, dk or None,
     dwq [D] fp32 or None, dwk or None)."""
-    io, rows, Hq, Hk, D, rot = _qk_codes(q, k, positions, inv_freq, wq, wk)
     if (k is None) != (dk_out is None):
         raise ValueError("k and dk_out go together")
-    if dk is not None and k is None:
-        raise ValueError("dk without k")
-    _need(dq_out, q.shape, q.dtype, "dq_out (must have q's shape and dtype)")
-    _must(dq, q.shape, q.dtype, "dq")
-    if k is not None:
-        _must(dk_out, k.shape, k.dtype, "dk_out (must have k's shape and "
-              "dtype)")
-        _must(dk, k.shape, k.dtype, "dk")
+    if dq_out is None:
+        raise ValueError("dq_out is missing")
+    (io, rows, Hq, Hk, D, rot), (sq, sk, so, sko, s1, s2) = _qk_plan(
+        _layout(q), _layout(k), _layout(positions), _layout(inv_freq),
+        _layout(wq), _layout(wk), ("dq_out", _layout(dq_out)),
+        ("dk_out", _layout(dk_out)), ("dq", _layout(dq)),
+        ("dk", _layout(dk)))
     away = _elsewhere(q, stream)
     if away is not None:
         with away:
@@ -308,18 +326,18 @@ def kda_qk_norm_rope_backward(q, k, positions, inv_freq, dq_out, dk_out, *,
              kda_qk_norm_rope_backward_workspace_size(rows, Hq, Hk, D), q,
              "kda_qk_norm_rope_backward")
     if dq is None:
-        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        dq = _dense(q)
     if dk is None and k is not None:
-        dk = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        dk = _dense(k)
     dwq, dwk = (None if w is None else torch.empty_like(w) for w in (wq, wk))
     dev = q.get_device()
-    (pq, pk, po, ko, d1, d2), (sq, sk, so, sko, s1, s2) = _strided(
-        dev, (q, "q"), (k, "k"), (dq_out, "dq_out"), (dk_out, "dk_out"),
-        (dq, "dq"), (dk, "dk"))
     p1, p2, pp, pf, g1, g2, pw = _ptrs(dev, wq, wk, positions, inv_freq, dwq,
                                        dwk, ws)
-    _check(_qk_bwd(pq, pk, io, sq, sk, p1, p2, pp, pf, rot,
-                   int(bool(interleaved)), eps, po, ko, so, sko, d1, d2, s1,
-                   s2, g1, g2, rows, Hq, Hk, D, pw, ws.numel(),
-                   _raw_stream(dev)), "kda_qk_norm_rope_backward")
+    _check(_qk_bwd(q.data_ptr(), _pointer(k, dev, "k"), io, sq, sk, p1, p2, pp,
+                   pf, rot, 1 if interleaved else 0, eps,
+                   _pointer(dq_out, dev, "dq_out"),
+                   _pointer(dk_out, dev, "dk_out"), so, sko,
+                   _pointer(dq, dev, "dq"), _pointer(dk, dev, "dk"), s1, s2,
+                   g1, g2, rows, Hq, Hk, D, pw, ws.numel(), _raw_stream(dev)),
+           "kda_qk_norm_rope_backward")
     return dq, dk, dwq, dwk

@@ -48,13 +48,15 @@ def test_workspace_sizes():
         for dt in (torch.bfloat16, torch.float32):
             assert f(1, 8192, 32, 32, 128, 128, dt) > 0
             assert f(1, 1, 1, 1, 16, 128, dt) >= 256
+            assert f((1 << 20) - 1, 4, 1, 4, 16, 16, dt) > 0
         for bad in [(0, 8, 1, 1, 16, 16), (1, 0, 1, 1, 16, 16),
                     (1, 8, 0, 1, 16, 16), (1, 8, 2, 3, 16, 16),
                     (1, 8, 2, 1, 16, 16), (1, 8, 1, 1, 48, 16),
                     (1, 8, 1, 1, 16, 256), (1, (1 << 30) + 1, 1, 1, 16, 16),
                     (1, 8, 1 << 20, 1 << 20, 16, 16),
                     (1 << 12, 1 << 20, 4, 4, 16, 16), (P + 1, 8, 1, 1, 16, 16),
-                    (1, P + 8, 1, 1, 16, 16), (1, 8, 1, 1, P + 16, 16)]:
+                    (1 << 20, 4, 4, 4, 16, 16), (1, 8, 1, 1, P + 16, 16),
+                    (1, P + 8, 1, 1, 16, 16)]:
             assert f(*bad, torch.bfloat16) == 0, bad
     f = kda.kda_qk_norm_rope_backward_workspace_size
     assert f(1, 1, 0, 16) > 0 and f(100000, 32, 8, 256) > 0
@@ -88,7 +90,7 @@ def _lin(**kw):
     (dict(Dk=48), UNS), (dict(Dv=256), UNS), (dict(io=F, gt=BF), UNS),
     (dict(io=F, gt=BF | FIXED), UNS), (dict(T=(1 << 30) + 1), UNS),
     (dict(B=1 << 20, T=1 << 20), UNS), (dict(H=1 << 20), UNS),
-    (dict(B=1 << 21), UNS),
+    (dict(B=1 << 21), UNS), (dict(B=1 << 20, T=4, Dv=64), UNS),
 ])
 def test_linattn_rejects(kw, want):
     assert _lin(**kw) == want
@@ -272,7 +274,10 @@ def test_binding_rejects_qk_norm_rope():
 
 def test_token_strides():
     x = t(3, 5, 96)  # [B, T, fused]
-    f = linattn._token_stride
+
+    def f(t, name):
+        return linattn._token_stride(t.shape, t.stride(), name)
+
     q = x[..., :64].unflatten(-1, (4, 16))
     assert f(q, "q") == 96
     assert f(q.contiguous(), "q") == 64
