@@ -23,8 +23,6 @@ struct LinParams {
   float scale;
   char *ws;
 };
-// segments of all heads, the larger of both passes' and dtypes'
-long long linattn_segments(int B, int T, int H);
 size_t linattn_ws_bytes(int B, int T, int H, int Dk, int Dv, int io_bf16);
 size_t linattn_bwd_ws_bytes(int B, int T, int Hk, int H, int Dk, int Dv,
                             int io_bf16);

@@ -32,19 +32,29 @@ struct Split {
   int NS, seg;
 };
 
-// Workgroups wanted, and the tokens that a segment has at least and (gradient)
-// at most: see the end of this file's launch logic.
-constexpr int WAVES = 2048, MIN_CHUNKS = 4, MAX_CHUNKS = 64;
+// Segments are as many as fill the GPU once, in whole rounds of workgroups: 256
+// of 8 waves at D = 128, one per CU (8192 tokens of 32 heads, forward: 102 us
+// with 256, 118 with 512, as every segment more is a state to write, scan and
+// read; 36 heads: 40 us with 216 workgroups, 48 with 288), 512 of at most 4
+// waves below (8192 tokens of 32 heads of 64: 46 us, 52 with 768).  Against
+// that:
+//  - The forward pass of up to 4 chunks stays in one launch (B1 T200 H32: 16 us,
+//    split 20); five gain (T320 H4: 15.5 us, 18), and so do two of the gradient.
+//  - A chunk more in a segment costs both passes 4.5 us, a segment more costs
+//    the scan 0.25: not more than 8 sqrt(chunks) segments (fp32 4096 tokens of 4
+//    heads: 21 us with 64, 26 with 128, 24 with 43).
+//  - The sums of kda_lin_gate_grad hold a segment of MAX_CHUNKS.
+constexpr int WORKGROUPS = 256, MAX_CHUNKS = 64;
 
 Split split(int B, int T, int H, int D, int io_bf16, bool grad) {
   const int C = lin_chunk(io_bf16);
   const int nc = (T + C - 1) / C;
   const long long chains = (long long)B * H;
-  const int wanted = WAVES / (D == 128 ? 8 : 4);
-  long long ns = (wanted + chains - 1) / chains;
-  if (ns > nc / MIN_CHUNKS) ns = nc / MIN_CHUNKS;
-  if (ns < 1) ns = 1;
+  const int wanted = D == 128 ? WORKGROUPS : 2 * WORKGROUPS;
+  const long long ns = chains < wanted ? wanted / chains : 1;
   int per = (int)((nc + ns - 1) / ns);
+  if (!grad && nc <= 4) per = nc;
+  while (64ll * per * per < nc) ++per;
   if (grad && per > MAX_CHUNKS) per = MAX_CHUNKS;
   return Split{(nc + per - 1) / per, per * C};
 }
@@ -196,16 +206,17 @@ __global__ __launch_bounds__(64 * GATE_WAVES) void kda_lin_gate_grad(
   }
 }
 
-// the gradient of a decay that all tokens of a head share
-__global__ __launch_bounds__(256) void kda_lin_gate_sum(const double *sums,
-                                                        void *dg,
-                                                        int gate_bf16, int B,
-                                                        int H, int NS) {
-  const int h = blockIdx.x * 256 + threadIdx.x;
-  if (h >= H) return;
+// the gradient of a decay that all tokens of a head share: a wave has a head
+__global__ __launch_bounds__(64) void kda_lin_gate_sum(const double *sums,
+                                                       void *dg, int gate_bf16,
+                                                       int B, int H, int NS) {
+  const int h = blockIdx.x;
   double x = 0.0;
-  for (int b = 0; b < B; ++b)
-    for (int s = 0; s < NS; ++s) x += sums[((size_t)b * H + h) * NS + s];
+  for (long long i = threadIdx.x; i < (long long)B * NS; i += 64)
+    x += sums[((size_t)(i / NS) * H + h) * NS + i % NS];
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) x += __shfl_xor(x, d, 64);
+  if (threadIdx.x) return;
   if (gate_bf16) ((bf16 *)dg)[h] = (bf16)(float)x;
   else ((float *)dg)[h] = (float)x;
 }
@@ -450,23 +461,14 @@ hipError_t scan_segments(const ScanSegs &f, const ScanSegs *r, int chains,
 
 }  // namespace lin
 
-long long linattn_segments(int B, int T, int H) {
-  long long most = 0;
-  for (int i = 0; i < 4; ++i) {
-    const lin::Split sp = lin::split(B, T, H, 16, i & 1, i & 2);
-    const long long n = (long long)B * H * sp.NS;
-    most = n > most ? n : most;
-  }
-  return most;
-}
 size_t linattn_ws_bytes(int B, int T, int H, int Dk, int Dv, int io_bf16) {
-  return lin::layout(B, T, H, H, Dk, Dv, lin::split(B, T, H, std::max(Dk, Dv), io_bf16, false),
-                     false).bytes;
+  const lin::Split sp = lin::split(B, T, H, std::max(Dk, Dv), io_bf16, false);
+  return lin::layout(B, T, H, H, Dk, Dv, sp, false).bytes;
 }
 size_t linattn_bwd_ws_bytes(int B, int T, int Hk, int H, int Dk, int Dv,
                             int io_bf16) {
-  return lin::layout(B, T, Hk, H, Dk, Dv, lin::split(B, T, H, std::max(Dk, Dv), io_bf16, true),
-                     true).bytes;
+  const lin::Split sp = lin::split(B, T, H, std::max(Dk, Dv), io_bf16, true);
+  return lin::layout(B, T, Hk, H, Dk, Dv, sp, true).bytes;
 }
 
 #define LIN_TRY(x)                      \
@@ -476,7 +478,8 @@ size_t linattn_bwd_ws_bytes(int B, int T, int Hk, int H, int Dk, int Dv,
   } while (0)
 
 hipError_t launch_linattn(const LinParams &p, hipStream_t st) {
-  const lin::Split sp = lin::split(p.B, p.T, p.H, std::max(p.Dk, p.Dv), p.io_bf16, false);
+  const lin::Split sp = lin::split(p.B, p.T, p.H, std::max(p.Dk, p.Dv),
+                                   p.io_bf16, false);
   const lin::Layout l =
       lin::layout(p.B, p.T, p.Hk, p.H, p.Dk, p.Dv, sp, false);
   const LinOperand q{p.q, 1}, k{p.k, 1}, v{p.v, 0};
@@ -500,7 +503,8 @@ hipError_t launch_linattn(const LinParams &p, hipStream_t st) {
 }
 
 hipError_t launch_linattn_backward(const LinParams &p, hipStream_t st) {
-  const lin::Split sp = lin::split(p.B, p.T, p.H, std::max(p.Dk, p.Dv), p.io_bf16, true);
+  const lin::Split sp = lin::split(p.B, p.T, p.H, std::max(p.Dk, p.Dv),
+                                   p.io_bf16, true);
   const lin::Layout l = lin::layout(p.B, p.T, p.Hk, p.H, p.Dk, p.Dv, sp, true);
   const LinOperand q{p.q, 1}, k{p.k, 1}, v{p.v, 0}, dO{p.dO, 0};
   const LinSeq seq = lin::seq_of(p, sp);
@@ -538,22 +542,22 @@ hipError_t launch_linattn_backward(const LinParams &p, hipStream_t st) {
     z.early = early;
     LIN_TRY(lin::both(p.io_bf16, p.Dk, dots, z, st));
   } else {
-  // dv
-  w.a = k; w.b = q; w.c = dO;
-  w.out = p.dv;
-  w.pair_scale = p.scale; w.far_scale = 1.f; w.add_scale = p.scale;
-  w.s_in = ds_in;
-  w.s_end = p.ds0;
-  LIN_TRY(lin::sweep(p.io_bf16, p.Dk, p.Dv, 1, LIN_PLAIN, w, st));
-  // dk
-  w.a = v; w.b = dO; w.c = q; w.d = k;
-  w.out = dk;
-  w.out_rest = dk_rest;
-  w.s_end = nullptr;
-  w.s_transposed = 1;
-  w.far_dot = early;
-  LIN_TRY(lin::sweep(p.io_bf16, p.Dv, p.Dk, 1, dots ? LIN_FAR : LIN_PLAIN, w,
-                     st));
+    // dv
+    w.a = k; w.b = q; w.c = dO;
+    w.out = p.dv;
+    w.pair_scale = p.scale; w.far_scale = 1.f; w.add_scale = p.scale;
+    w.s_in = ds_in;
+    w.s_end = p.ds0;
+    LIN_TRY(lin::sweep(p.io_bf16, p.Dk, p.Dv, 1, LIN_PLAIN, w, st));
+    // dk
+    w.a = v; w.b = dO; w.c = q; w.d = k;
+    w.out = dk;
+    w.out_rest = dk_rest;
+    w.s_end = nullptr;
+    w.s_transposed = 1;
+    w.far_dot = early;
+    LIN_TRY(lin::sweep(p.io_bf16, p.Dv, p.Dk, 1, dots ? LIN_FAR : LIN_PLAIN,
+                       w, st));
   }
   // dq
   w = LinSweep{};
@@ -596,11 +600,12 @@ hipError_t launch_linattn_backward(const LinParams &p, hipStream_t st) {
                     (const float *)(p.ws + l.ends), p.dg,
                     p.gate_fixed ? sums : nullptr};
     const unsigned n = (unsigned)p.B * p.H * sp.NS;
-    lin::kda_lin_gate_grad<<<n, 64 * lin::GATE_WAVES, 0, st>>>(x, lin_chunk(p.io_bf16));
+    lin::kda_lin_gate_grad<<<n, 64 * lin::GATE_WAVES, 0, st>>>(
+        x, lin_chunk(p.io_bf16));
     LIN_TRY(hipGetLastError());
     if (p.gate_fixed) {
-      lin::kda_lin_gate_sum<<<(p.H + 255) / 256, 256, 0, st>>>(
-          sums, p.dg, p.gate_bf16, p.B, p.H, sp.NS);
+      lin::kda_lin_gate_sum<<<p.H, 64, 0, st>>>(sums, p.dg, p.gate_bf16, p.B,
+                                                p.H, sp.NS);
       LIN_TRY(hipGetLastError());
     }
   }

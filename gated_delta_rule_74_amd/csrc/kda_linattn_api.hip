@@ -23,11 +23,12 @@ kda_status lin_sizes(int B, int T, int Hk, int H, int Dk, int Dv) {
   if (!dim_ok(Dk) || !dim_ok(Dv)) return KDA_EUNSUPPORTED;
   const long long D = Dk > Dv ? Dk : Dv;
   if (T > (1 << 30) || H > (1 << 22) / D) return KDA_EUNSUPPORTED;
-  // a grid has less than 2^32 threads: one workgroup of 256 for each segment
-  // of a head, and one thread for 4 values of the queries' gradient
-  if ((long long)B * H > (1 << 22)) return KDA_EUNSUPPORTED;
+  // a grid has less than 2^32 threads: one for 4 values of the queries'
+  // gradient, and a workgroup of up to 1024 for each segment of a head (below
+  // 2^22 in all: many heads have segments of 2048 tokens or more, and here at
+  // most 2^30 tokens)
   if ((long long)B * H * T > (1ll << 34) / D) return KDA_EUNSUPPORTED;
-  if (kda::linattn_segments(B, T, H) >= (1ll << 24)) return KDA_EUNSUPPORTED;
+  if ((long long)B * H >= (1 << 22)) return KDA_EUNSUPPORTED;
   return KDA_OK;
 }
 

@@ -19,8 +19,8 @@
 // a chunk are made once and handed to all waves through LDS as operand
 // fragments; the state's accumulator tiles are themselves the operand fragments
 // of S^T a (kda_device.h), so it never leaves its registers.  A chunk's rows
-// come from memory two chunks ahead: one in registers, one in a second set of
-// LDS tiles.
+// come from memory ahead of its turn: the next chunk's in registers, and at
+// D2 = 128 that after it, with a second set of LDS tiles.
 //
 // Precision.  Decays between tokens are differences of sums held in 64 bits:
 // a sum over a chunk may reach 64e4 (g below -1e4 is taken as -1e4, whose exp
@@ -144,11 +144,11 @@ __device__ __forceinline__ void weights(const float *w, int u, int g,
 
 // ---------------------------------------------------------------------------
 // Memory is read and written through buffer resources, whose bounds take the
-// place of branches: what lies past `bytes` reads as 0 and is not written.  With
-// a branch around the loads or stores of a partial chunk the compiler waits
-// for everything in flight where the paths meet: the next chunk's rows came in
-// one operand after the other, and only once the last chunk's output was
-// written.
+// place of branches: what lies past `bytes` reads as 0 and is not written.
+// With a branch around the loads or stores of a partial chunk the compiler
+// waits for everything in flight where the paths meet: the next chunk's rows
+// came in one operand after the other, and only once the last chunk's output
+// was written.
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void *p,
                                                          long long bytes) {
@@ -192,7 +192,7 @@ __device__ __forceinline__ long long extent(int rows, unsigned stride,
 template <typename IO, int D, int C, int NT> struct Rows {
   static constexpr int UPR = D * (int)sizeof(IO) / 16;  // 16-byte units a row
   static constexpr int N = (C * UPR + NT - 1) / NT;
-  static constexpr int STEP = NT / UPR;  // rows from a thread's unit to its next
+  static constexpr int STEP = NT / UPR;  // rows between a thread's units
   uint4 r[N];
   // rows from `live` on (none where it is not above 0) are zeros.  A chunk is
   // at most 2^30 bytes long (a token at most 2^24)
@@ -310,8 +310,8 @@ template <int C, int NW> struct Gates {
 };
 
 // ---------------------------------------------------------------------------
-// the parts of a chunk's work.  A wave has 16 columns: KT tiles of the state, NB
-// of the output.
+// the parts of a chunk's work.  A wave has 16 columns: KT tiles of the state,
+// NB of the output.
 
 template <typename IO> struct Shape {
   static constexpr int TPU = Mma<IO>::TPU, KU = 16 * TPU;  // tiles a unit
@@ -332,7 +332,7 @@ __device__ __forceinline__ void packed(bf16x8 &f) {
   f = __builtin_bit_cast(bf16x8, v);
 }
 
-// An order for the compiler's scheduler: `ahead` LDS reads first, then reads and
+// An order for the compiler's scheduler: AHEAD LDS reads first, then reads and
 // matrix instructions in turn, until both are used up.  Left to itself it reads
 // an operand right before its use.
 template <int AHEAD, int READS, int MFMAS, int STEPS>
@@ -436,8 +436,8 @@ __device__ __forceinline__ void near_part(
 }
 
 // The units of the pair products: 16 x 32 pieces (fp32 16 x 16) of a row of
-// tiles, those with two tiles of pairs first.  Unit `idx`'s row and place in it,
-// for the map that looks back; the other's is its mirror image.
+// tiles, those with two tiles of pairs first.  Unit `idx`'s row and place in
+// it, for the map that looks back; the other's is its mirror image.
 template <int NB> constexpr int pair_units() { return NB == 2 ? 3 : 6; }
 template <int NB, bool REV>
 __device__ __forceinline__ void pair_unit(int idx, int &rt, int &u2) {
@@ -525,8 +525,8 @@ template <typename IO> struct PairSet {
 
 // K units of the pair products of a chunk, from `first` on every NW-th of those
 // of all sets, transposed: rows j, columns i = rt * 16 + m.  Where all of a
-// tile's j lie before (REV: behind) its i, the decay between them is that from i
-// to the border next to j's tile, one a lane, times that from there to j.
+// tile's j lie before (REV: behind) its i, the decay between them is that from
+// i to the border next to j's tile, one a lane, times that from there to j.
 // D2 > 0: also the sums over the pairs' products with c_j . d_i.  The units go
 // side by side, in the same code for all waves (a branch for each unit let
 // nothing overlap: 24 of the 144 us of kda_lin_both at B1 T8192 H32 D128).
@@ -635,9 +635,9 @@ __device__ __forceinline__ f32x4 rest4(f32x4 v, uint2 r) {
 }
 
 // A chunk of the wave's 16 columns from `col` on to out[t0..] of one head of H,
-// D wide: `rows` rows, zeros from `live` on (none, where rows is 0).  bf16: after
-// a swap between lanes each has 8 consecutive columns of one row, of the lower
-// tile where g is odd (8 bytes a lane took 4 us more at B1 T8192 H32 D128);
+// D wide: `rows` rows, zeros from `live` on (none, where rows is 0).  bf16:
+// after a swap between lanes each has 8 consecutive columns of one row, of the
+// lower tile where g is odd (8 bytes a lane took 4 us more at B1 T8192 H32 D128);
 // REST: what rounding leaves goes to a second tensor, if there is one.  A store
 // that meets no memory takes the place of a branch, which would make the next
 // chunk wait for this one.
@@ -724,6 +724,12 @@ __device__ __forceinline__ float column_sum(const float (&x)[N][C], int i) {
 
 // waves of a workgroup whose output is D2 wide
 template <int D2> constexpr int nwaves() { return D2 == 128 ? 8 : 4; }
+// Whether a sweep has two sets of LDS tiles.  The one workgroup of 8 waves that a
+// CU has gains by it (B1 T8192 H32 D128: 114 us without, 107 with); with 4 waves
+// other workgroups on the CU fill the wait as well, and the second set keeps
+// them off it (gradient of B8 T4096 H32 D64: 497 us without, 768 with; D32 380
+// and 396).
+template <int NW> constexpr bool two_sets() { return NW == 8; }
 
 // where a workgroup's segment is
 struct Where {
@@ -808,10 +814,7 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
   typedef Tile<IO, D2> T2;
   constexpr int C = Sh::C, NB = Sh::NB, NTU = Sh::NTU, KT = D1 / 16;
   constexpr int NW = nwaves<D2>(), NT = 64 * NW, COLS = D2 / 16;
-  // a second set of tiles, unless it would keep a second workgroup of 4 waves
-  // off the CU
-  constexpr int SET = C * (2 * T1::STR + (DOT ? 2 : 1) * T2::STR);
-  constexpr bool TWO = NW == 8 || 2 * SET * sizeof(IO) <= 48 * 1024;
+  constexpr bool TWO = two_sets<NW>();
   __shared__ alignas(16) IO ta[1 + TWO][C * T1::STR], tb[1 + TWO][C * T1::STR],
       tc[1 + TWO][C * T2::STR];
   __shared__ alignas(16) IO td[1 + TWO][DOT ? C * T2::STR : 8];
@@ -974,9 +977,9 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
 }
 
 // ---------------------------------------------------------------------------
-// dk and dv in one reversed sweep, for Dk = Dv: they read the same four tensors,
-// and the two states (one the other's transpose, each in the registers of the
-// waves that need it) come from the same rows.
+// dk and dv in one reversed sweep, for Dk = Dv: they read the same four
+// tensors, and the two states (one the other's transpose, each in the registers
+// of the waves that need it) come from the same rows.
 
 template <typename IO, int D, bool DOT>
 __global__ __launch_bounds__(64 * nwaves<D>(), 2) void kda_lin_both(
@@ -987,7 +990,7 @@ __global__ __launch_bounds__(64 * nwaves<D>(), 2) void kda_lin_both(
   constexpr bool REV = true;
   constexpr int C = Sh::C, NB = Sh::NB, NTU = Sh::NTU, KT = D / 16;
   constexpr int NW = nwaves<D>(), NT = 64 * NW, COLS = D / 16;
-  constexpr bool TWO = NW == 8 || 8 * C * TD::STR * sizeof(IO) <= 48 * 1024;
+  constexpr bool TWO = two_sets<NW>();
   __shared__ alignas(16) IO tq[1 + TWO][C * TD::STR], tk[1 + TWO][C * TD::STR],
       tv[1 + TWO][C * TD::STR], to[1 + TWO][C * TD::STR];
   __shared__ alignas(16) frag tp[2][NB * NTU * 64];

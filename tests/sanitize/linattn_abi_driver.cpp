@@ -14,7 +14,6 @@
 static int launches = 0;
 static hipError_t refuse() { ++launches; return hipErrorInvalidValue; }
 namespace kda {
-long long linattn_segments(int B, int T, int H) { return (long long)B * H * (T / 4096 + 1); }
 size_t linattn_ws_bytes(int, int, int, int, int, int) { return 256; }
 size_t linattn_bwd_ws_bytes(int, int, int, int, int, int, int) { return 512; }
 hipError_t launch_linattn(const LinParams &, hipStream_t) { return refuse(); }
