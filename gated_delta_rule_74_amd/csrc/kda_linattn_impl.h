@@ -29,7 +29,8 @@
 // result is rounded to bf16 itself (half a step each, as the result's own);
 // what ends up in fp32 (the state, and the dot products that the gate's
 // gradient is made of) takes the rounded-off rest as a second operand, which
-// leaves 2^-18.
+// leaves 2^-17 of a term at most, 2.4e-6 in the mean (a third operand would
+// leave 1e-8, and takes 109 us for 102 at B1 T8192 H32 D128).
 #pragma once
 #include "kda_device.h"
 #include "kda_linattn.h"

@@ -511,7 +511,7 @@ size_t kda_linattn_backward_workspace_size(int B, int T, int Hk, int H, int Dk,
  *            s0
  * With bf16 data o carries, beside its own rounding, one rounding of the pair
  * products and one of the state to bf16 (half a step each); s_out is within
- * about 2^-17 of its terms' magnitudes, and terms that have decayed to less than
+ * 2^-17 of its terms' magnitudes, and terms that have decayed to less than
  * 2^-200 may count as none.  Values are not checked: an infinity or
  * NaN in q, k or v may also reach the outputs of up to 63 tokens before it
  * (those of its chunk: 0 * inf in the matrix products), never those of another

@@ -13,8 +13,8 @@ and sums over a chunk's 64 tokens cost a rounding per term.  So `kappa` times
 the magnitudes covers fp32 evaluation.  With bf16 data,
 - the pair products and the state are rounded to bf16 where they enter o, dq,
   dk and dv: 2^-8 of the magnitudes;
-- the state and the gate's gradient are made of two-part operands whose rest
-  is under 2^-18 each: 2^-17 and (two states) 2^-16.
+- the state and the gate's gradient are made of two-part operands, whose rest
+  is half a step of half a step: 2^-17 and (two states) 2^-16.
 The gate's gradient takes the sum over the pairs across a chunk's end from that
 across its start, so what those are off stays: 2 <N, M> at every boundary
 behind the token is added to its magnitude.

@@ -291,6 +291,77 @@ def test_long_segments_of_the_gradient(kda):
         within(n, a, want[n])
 
 
+def test_segments_that_forget(kda):
+    """enough heads that segments are several chunks long, and gates that
+    forget their first ones by their end"""
+    x, d = inputs(1, 1500, 1, 1, 128, 128, seed=23)
+    H = 64
+    y = {n: t.repeat_interleave(H, 1 if n == "s0" else 2).contiguous()
+         for n, t in x.items()}
+    do = d["do"].repeat_interleave(H, 2).contiguous()
+    dsT = d["dsT"].repeat_interleave(H, 1).contiguous()
+    want = ref.linattn(**x, **d)
+    four = [y[n] for n in "qkvg"]
+    o, s = kda.kda_linattn(*four, s0=y["s0"])
+    within("o", o[:, :, 5:6], want["o"])
+    within("s", s[:, 5:6], want["s"])
+    got = kda.kda_linattn_backward(*four, do, s0=y["s0"], dsT=dsT)
+    for n, t in zip(GRADS, got):
+        within(n, t[:, 5:6] if n == "ds0" else t[:, :, 5:6], want[n])
+
+
+@pytest.mark.parametrize("io", [BF, F])
+@pytest.mark.parametrize("Dk,Dv", [(64, 32), (16, 128), (128, 16), (32, 32)])
+@pytest.mark.parametrize("want_dg", [False, True])
+def test_shared_heads_of_any_width(kda, io, Dk, Dv, want_dg):
+    """with and without the gate's gradient, whose sums other kernels make"""
+    x, d = inputs(1, 330, 2, 6, Dk, Dv, io, seed=24)
+    want = ref.linattn(**x, **d)
+    got = kda.kda_linattn_backward(*[x[n] for n in "qkvg"], d["do"],
+                                   s0=x["s0"], dsT=d["dsT"], want_dg=want_dg)
+    for n, t in zip(GRADS, got):
+        if n != "dg" or want_dg:
+            within(n, t, want[n])
+
+
+def test_fixed_decays_of_many_sequences(kda):
+    x, d = inputs(130, 40, 1, 2, 16, 16, kind="fixed", seed=25)
+    check(kda, x, d)
+
+
+@pytest.mark.parametrize("io", [BF, F])
+def test_one_token_of_many_sequences(kda, io):
+    x, d = inputs(300, 1, 2, 4, 32, 16, io, seed=26)
+    check(kda, x, d)
+
+
+def test_offsets_past_32_bits(kda):
+    """More than 2^31 values in each tensor.  With exp(-1) a token, what is 150
+    tokens away is 1e-65 of itself: both ends are those of a short sequence."""
+    T, H, D, n, keep = (1 << 19) + 77, 32, 128, 300, 150
+    gen = torch.Generator(device="cuda").manual_seed(27)
+
+    def r():
+        return torch.randn(1, T, H, D, generator=gen, device="cuda", dtype=BF)
+
+    q, k, v, do = r() * 0.125, r() * 0.125, r(), r()
+    g = torch.full((1, T, H), -1.0, device="cuda")
+    o, s = kda.kda_linattn(q, k, v, g)
+    got = kda.kda_linattn_backward(q, k, v, g, do)
+    last = slice(T - n, T)
+    pick = [0, 31]
+    for part, inner in ((slice(0, n), slice(0, keep)),
+                        (last, slice(n - keep, n))):
+        def cut(t):
+            return t[:, part][:, :, pick].contiguous()
+        want = ref.linattn(cut(q), cut(k), cut(v), cut(g), do=cut(do))
+        for m, t in zip(("o", *GRADS), (o, *got[:4])):
+            within(m, cut(t)[:, inner],
+                   tuple(w[:, inner] for w in want[m]))
+        if part is last:
+            within("s", s[:, pick], want["s"])
+
+
 def test_own_stream_and_workspaces(kda):
     """two calls at once on two streams, each with its workspace"""
     x, d = inputs(1, 1500, 1, 2, 64, 64, seed=17)

@@ -163,6 +163,26 @@ def test_fused_projection_and_in_place(kda, dtype):
                                  q.shape, (T * Hq * D, Hq * D, D, 1)), **kw)
 
 
+def test_offsets_past_32_bits(kda):
+    """tokens 65536 values apart: more than 2^31 values from first to last"""
+    rows, D = 40001, 64
+    x = torch.empty(rows, 65536, dtype=BF, device="cuda")
+    x[:, :6 * D] = rn(rows, 6 * D, seed=40, dtype=BF)
+    q, k = (t.unflatten(-1, (2, D)) for t in (x[:, :2 * D], x[:, 2 * D:4 * D]))
+    dq = x[:, 4 * D:6 * D].unflatten(-1, (2, D))
+    w = rn(D, seed=41)
+    pos, inv = turns((rows,), 32)
+    kw = dict(wq=w, wk=w, eps=EPS)
+    dense = [t.contiguous() for t in (q, k, dq)]
+    want = kda.kda_qk_norm_rope_backward(dense[0], dense[1], pos, inv,
+                                         dense[2], dense[2], **kw)
+    got = kda.kda_qk_norm_rope_backward(q, k, pos, inv, dq, dq, **kw)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    want = kda.kda_qk_norm_rope(dense[0], dense[1], pos, inv, **kw)
+    got = kda.kda_qk_norm_rope(q, k, pos, inv, q_out=q, k_out=k, **kw)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_far_positions(kda):
     """up to the largest int: the angles are exact in 64 bits.  At 2^31 the
     reference's own product is off by 2^-22, so there the bound is wider by
