@@ -168,9 +168,9 @@ __device__ __forceinline__ void store16(__amdgpu_buffer_rsrc_t r, unsigned at,
                                          0, 0);
 }
 
-// The wait before a loop over chunks: with rows in flight into the loop the
-// compiler would count, at every turn, as if no output had been written since
-// they were asked for, and wait for it.
+// The wait before a loop over chunks, on every way into it: with rows or a state
+// in flight into the loop the compiler would count, at every turn, as if no
+// output had been written since they were asked for, and wait for it.
 __device__ __forceinline__ void all_loaded() {
   __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
 }
@@ -179,6 +179,11 @@ __device__ __forceinline__ void all_loaded() {
 // whole loop: a chunk's offsets would take 24 of them.
 __device__ __forceinline__ void opaque(unsigned &x) {
   asm volatile("" : "+v"(x));
+}
+
+// the wave's number, known to be the same for all its lanes
+__device__ __forceinline__ int wave_number() {
+  return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 }
 
 // bytes of `rows` rows of `row` bytes, `stride` bytes apart
@@ -248,11 +253,16 @@ __device__ __forceinline__ float exp2_diff(double d) {
   return __builtin_amdgcn_exp2f((float)d);
 }
 
-__device__ __forceinline__ float load_gate(const LinSeq &q, int b, int h,
-                                           int t) {
+// a gate's bits, which are not waited for, and its value
+__device__ __forceinline__ unsigned load_gate(const LinSeq &q, int b, int h,
+                                              int t) {
   const size_t i = q.gate_fixed ? (size_t)h
                                 : ((size_t)b * q.T + t) * q.H + h;
-  return q.gate_bf16 ? (float)((const bf16 *)q.g)[i] : ((const float *)q.g)[i];
+  return q.gate_bf16 ? ((const unsigned short *)q.g)[i]
+                     : ((const unsigned *)q.g)[i];
+}
+__device__ __forceinline__ float gate_value(const LinSeq &q, unsigned bits) {
+  return __uint_as_float(q.gate_bf16 ? bits << 16 : bits);
 }
 
 // x plus that of the lane that DPP control CTRL names, 0 where there is none
@@ -294,7 +304,7 @@ __device__ __forceinline__ double decay_sums(float g, int lane, double &x,
 // the gates of a wave's chunks of a batch, and where a sequence's chunks are
 template <int C, int NW> struct Gates {
   static constexpr int N = (BATCH + NW - 1) / NW;
-  float g[N];
+  unsigned g[N];
   // chunk n of nch, taken from the segment's end where `back` says so
   __device__ __forceinline__ void fetch(const LinSeq &q, int b, int h, int n0,
                                         int nch, bool back, int t_begin,
@@ -303,7 +313,7 @@ template <int C, int NW> struct Gates {
     for (int i = 0; i < N; ++i) {
       const int n = n0 + w + i * NW;
       const int t = t_begin + (back ? nch - 1 - n : n) * C + lane;
-      g[i] = 0.f;
+      g[i] = 0;
       if (w + i * NW < BATCH && n < nch && lane < C && t < live_end)
         g[i] = load_gate(q, b, h, t);
     }
@@ -781,8 +791,8 @@ template <typename IO, int NW, bool REV> struct Keeper {
                 lane);
   }
   // first, last: factors of the weights
-  __device__ __forceinline__ void make(Decays<C> *decs, const Where &at,
-                                       int n0, float first, float last, int w,
+  __device__ __forceinline__ void make(const LinSeq &q, Decays<C> *decs,
+                                       const Where &at, int n0, float first, float last, int w,
                                        int lane) {
 #pragma unroll
     for (int i = 0; i < gates.N; ++i) {
@@ -790,7 +800,7 @@ template <typename IO, int NW, bool REV> struct Keeper {
       if (x >= BATCH || n0 + x >= at.nch) break;
       Decays<C> &d = decs[(n0 + x) % (2 * BATCH)];
       double G, tile;
-      const double end = decay_sums<C>(gates.g[i], lane, G, tile);
+      const double end = decay_sums<C>(gate_value(q, gates.g[i]), lane, G, tile);
       if (!REV) tile = __shfl(tile, lane | 15, 64) - tile;
       if (lane < C) {
         d.G[lane] = G;
@@ -824,7 +834,7 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
   __shared__ float far_dots[2][DOT ? COLS : 1][DOT ? C : 1];
   __shared__ PairSums<DOT == LIN_FAR_PAIRS ? NB : 1> sums[2];
 
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, w = wave_number();
   const int g = lane >> 4, m = lane & 15;
   const LinSeq &q = p.q;
   const Where at(q, blockIdx.x, q.NS, 0, C);
@@ -861,7 +871,7 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
   };
   Keeper<IO, NW, REV> keeper;
   auto make_decays = [&](int n0) {
-    keeper.make(decs, at, n0, REV ? p.add_scale : p.far_scale,
+    keeper.make(q, decs, at, n0, REV ? p.add_scale : p.far_scale,
                 REV ? p.far_scale : p.add_scale, w, lane);
     keeper.fetch(q, at, n0 + BATCH, w, lane);
   };
@@ -885,9 +895,9 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
       stash(0);
       fetch(1);
     }
-    all_loaded();
     barrier_keep_vmem();
   }
+  all_loaded();
   for (int n = 0; n < nch; ++n) {
     const int t0 = at.at(n, REV, C), x = TWO ? n & 1 : 0;
     const Decays<C> &dec = decs[n % (2 * BATCH)];
@@ -979,40 +989,44 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
 
 // ---------------------------------------------------------------------------
 // dk and dv in one reversed sweep, for Dk = Dv: they read the same four
-// tensors, and the two states (one the other's transpose, each in the registers
-// of the waves that need it) come from the same rows.
+// tensors, and the two states (one the other's transpose) come from the same
+// rows.  Half of the waves have the state and dv, the others its transpose and
+// dk (with both in the registers of the same waves, eight of them, the gradient
+// of B1 T8192 H32 D128 took 298 us; with sixteen 270).
 
 template <typename IO, int D, bool DOT>
-__global__ __launch_bounds__(64 * nwaves<D>(), 2) void kda_lin_both(
+__global__ __launch_bounds__(128 * nwaves<D>(), 4) void kda_lin_both(
     LinBoth p) {
   typedef Shape<IO> Sh;
   typedef typename Mma<IO>::frag frag;
   typedef Tile<IO, D> TD;
   constexpr bool REV = true;
   constexpr int C = Sh::C, NB = Sh::NB, NTU = Sh::NTU, KT = D / 16;
-  constexpr int NW = nwaves<D>(), NT = 64 * NW, COLS = D / 16;
-  constexpr bool TWO = two_sets<NW>();
+  constexpr int HALF = nwaves<D>(), NW = 2 * HALF, NT = 64 * NW;
+  constexpr int COLS = D / 16;
+  constexpr bool TWO = two_sets<HALF>();
   __shared__ alignas(16) IO tq[1 + TWO][C * TD::STR], tk[1 + TWO][C * TD::STR],
       tv[1 + TWO][C * TD::STR], to[1 + TWO][C * TD::STR];
   __shared__ alignas(16) frag tp[2][NB * NTU * 64];
   __shared__ Decays<C> decs[2 * BATCH];
   __shared__ float far_dots[2][DOT ? COLS : 1][DOT ? C : 1];
 
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int g = lane >> 4, m = lane & 15;
+  const int lane = threadIdx.x & 63, w = wave_number();
+  int g = lane >> 4, m = lane & 15;
+  const bool dk = w >= HALF;  // dS's transpose and dk, or dS and dv
+  const int wc = w % HALF;
   const LinSeq &q = p.q;
   const Where at(q, blockIdx.x, q.NS, 0, C);
   const int nch = at.nch;
-  const bool mine = COLS >= NW || w < COLS;
-  const int col = mine ? w * 16 : 0;
+  const bool mine = COLS >= HALF || wc < COLS;
+  const int col = mine ? wc * 16 : 0;
   zero_dead<IO, D, NT>(p.dv, q, at);
   zero_dead<IO, D, NT>(p.dk, q, at);
   if (DOT) zero_dead<IO, D, NT>(p.dk_rest, q, at);
 
-  f32x4 S[KT], St[KT];  // dS, its transpose
-  const size_t s_at = (at.chain * q.NS + at.s) * D * D;
-  load_state<D, D>(S, p.ds_in, s_at, 0, col, g, m);
-  load_state<D, D>(St, p.ds_in, s_at, 1, col, g, m);
+  f32x4 S[KT];
+  load_state<D, D>(S, p.ds_in, (at.chain * q.NS + at.s) * D * D, dk, col, g,
+                   m);
 
   unsigned sq, sk, sv, so;
   const char *pq = operand<IO, D>(p.qs, q, at.b, at.h, sq);
@@ -1035,7 +1049,7 @@ __global__ __launch_bounds__(64 * nwaves<D>(), 2) void kda_lin_both(
   };
   Keeper<IO, NW, REV> keeper;
   auto make_decays = [&](int n0) {
-    keeper.make(decs, at, n0, p.scale, 1.f, w, lane);
+    keeper.make(q, decs, at, n0, p.scale, 1.f, w, lane);
     keeper.fetch(q, at, n0 + BATCH, w, lane);
   };
   auto finish = [&](int n) {
@@ -1044,6 +1058,14 @@ __global__ __launch_bounds__(64 * nwaves<D>(), 2) void kda_lin_both(
       p.early[at.chain * q.T + t] = column_sum(far_dots[n & 1], lane);
   };
   const bool keep_end = at.s == 0 && p.ds0;
+  // LDS addresses are made anew in each part of a chunk's work: kept over the
+  // loop they do not fit the registers, and a reload waits for the rows
+  auto fresh = [&] {
+    unsigned l = lane;
+    opaque(l);
+    g = l >> 4;
+    m = l & 15;
+  };
 
   if (nch > 0) {
     keeper.fetch(q, at, 0, w, lane);
@@ -1053,9 +1075,9 @@ __global__ __launch_bounds__(64 * nwaves<D>(), 2) void kda_lin_both(
       stash(0);
       fetch(1);
     }
-    all_loaded();
     barrier_keep_vmem();
   }
+  all_loaded();
   for (int n = 0; n < nch; ++n) {
     const int t0 = at.at(n, REV, C), x = TWO ? n & 1 : 0;
     const Decays<C> &dec = decs[n % (2 * BATCH)];
@@ -1070,64 +1092,57 @@ __global__ __launch_bounds__(64 * nwaves<D>(), 2) void kda_lin_both(
     }
     const PairSet<IO> pairs[2] = {{tk[x], tq[x], tp[0]},
                                   {tv[x], to[x], tp[1]}};
-    pair_products<IO, D, 0, REV, NW, 2>(pairs, dec, p.scale, w, lane);
+    fresh();
+    pair_products<IO, D, 0, REV, NW, 2>(pairs, dec, p.scale, w, g * 16 + m);
     if constexpr (DOT)
       if (n > 0) finish(n - 1);
-    __builtin_amdgcn_sched_barrier(0);
-    f32x4 av[NB], ak[NB];
+    f32x4 acc[NB];
+    fresh();
     if (mine) {
-      far_part<IO, D, false>(av, S, tk[x], g, m);
-      far_part<IO, D, DOT>(ak, St, tv[x], g, m);
+      if (DOT && dk) far_part<IO, D, true>(acc, S, tv[x], g, m);
+      else far_part<IO, D, false>(acc, S, dk ? tv[x] : tk[x], g, m);
 #pragma unroll
-      for (int rt = 0; rt < NB; ++rt) {
-        const float fw = dec.last[rt * 16 + m];
-        av[rt] *= fw;
-        ak[rt] *= fw;
-        if constexpr (DOT) {
+      for (int rt = 0; rt < NB; ++rt) acc[rt] *= dec.last[rt * 16 + m];
+      if (DOT && dk) {
+#pragma unroll
+        for (int rt = 0; rt < NB; ++rt) {
           const IO *y = tk[x] + TD::at(rt * 16 + m, col + 4 * g);
           float dot = 0.f;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) dot += ak[rt][e] * to_f32(y[e]);
+          for (int e = 0; e < 4; ++e) dot += acc[rt][e] * to_f32(y[e]);
           dot += __shfl_xor(dot, 16, 64);
           dot += __shfl_xor(dot, 32, 64);
-          if (g == 0) far_dots[n & 1][w][rt * 16 + m] = dot;
+          if (g == 0) far_dots[n & 1][wc][rt * 16 + m] = dot;
         }
       }
     }
     barrier_keep_vmem();
 
-    frag fo[NTU], fq[NTU];
+    frag fc[NTU];
+    fresh();
     if (mine) {
 #pragma unroll
-      for (int u = 0; u < NTU; ++u) {
-        fo[u] = TD::by_col(to[x], col, u, g, m);
-        fq[u] = TD::by_col(tq[x], col, u, g, m);
-      }
-      near_part<IO, REV>(av, tp[0], fo, lane);
-      near_part<IO, REV>(ak, tp[1], fq, lane);
+      for (int u = 0; u < NTU; ++u)
+        fc[u] = TD::by_col(dk ? tq[x] : to[x], col, u, g, m);
+      near_part<IO, REV>(acc, tp[dk], fc, g * 16 + m);
     }
-    const size_t o_at = (((size_t)at.b * q.T + t0) * q.H + at.h) * D;
-    const int rows = mine ? min(C, at.t_end - t0) : 0;
-    put_out<IO, D, false>(av, p.dv, nullptr, o_at, q.H, rows,
-                          at.live_end - t0, col, g, m);
-    put_out<IO, D, DOT>(ak, p.dk, p.dk_rest, o_at, q.H, rows,
-                        at.live_end - t0, col, g, m);
+    put_out<IO, D, DOT>(acc, dk ? p.dk : p.dv, dk ? p.dk_rest : nullptr,
+                        (((size_t)at.b * q.T + t0) * q.H + at.h) * D, q.H,
+                        mine ? min(C, at.t_end - t0) : 0, at.live_end - t0,
+                        col, g, m);
     __builtin_amdgcn_sched_barrier(0);
+    fresh();
     if (mine && (n + 1 < nch || keep_end)) {
 #pragma unroll
-      for (int kt = 0; kt < KT; ++kt) {
-        S[kt] *= dec.total;
-        St[kt] *= dec.total;
-      }
-      add_chunk<IO, D>(S, tq[x], fo, dec.first, g, m);
-      add_chunk<IO, D>(St, to[x], fq, dec.first, g, m);
-      if constexpr (sizeof(IO) == 2) reads_ahead<16, 2, 2, 2 * NTU * KT>();
+      for (int kt = 0; kt < KT; ++kt) S[kt] *= dec.total;
+      add_chunk<IO, D>(S, dk ? to[x] : tq[x], fc, dec.first, g, m);
+      if constexpr (sizeof(IO) == 2) reads_ahead<12, 2, 2, NTU * KT>();
     }
     barrier_keep_vmem();
   }
   if constexpr (DOT)
     if (nch > 0) finish(nch - 1);
-  if (mine && keep_end)
+  if (mine && keep_end && !dk)
     store_state<D, D>(S, p.ds0 + at.chain * D * D, col, g, m);
 }
 
@@ -1152,7 +1167,7 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_local(
   __shared__ alignas(16) float wts[BATCH][C];
   __shared__ double ends[BATCH];
   const LinLocal &p = blockIdx.y ? p1 : p0;
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, w = wave_number();
   const int g = lane >> 4, m = lane & 15;
   const LinSeq &q = p.q;
   const Where at(q, blockIdx.x, q.NS - 1, p.rev, C);
@@ -1191,7 +1206,7 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_local(
       const int x = w + i * NW;
       if (x >= BATCH) break;
       double tile;
-      const double end = decay_sums<C>(gates.g[i], lane, G[i], tile);
+      const double end = decay_sums<C>(gate_value(q, gates.g[i]), lane, G[i], tile);
       if (lane == 0) ends[x] = end;
     }
     barrier_keep_vmem();
@@ -1275,7 +1290,7 @@ hipError_t sweep(int D2, int rev, int dot, const LinSweep &p, hipStream_t s) {
 }
 template <typename IO, int D>
 hipError_t both(int dot, const LinBoth &p, hipStream_t s) {
-  const unsigned n = (unsigned)p.q.B * p.q.H * p.q.NS, t = 64 * nwaves<D>();
+  const unsigned n = (unsigned)p.q.B * p.q.H * p.q.NS, t = 128 * nwaves<D>();
   if (dot) kda_lin_both<IO, D, true><<<n, t, 0, s>>>(p);
   else kda_lin_both<IO, D, false><<<n, t, 0, s>>>(p);
   return hipGetLastError();
