@@ -103,8 +103,9 @@ __global__ __launch_bounds__(256) void kda_lin_scan(ScanSegs f, ScanSegs r,
 // ---------------------------------------------------------------------------
 // The gate's gradient from its parts.  A workgroup has one segment of one head,
 // a wave a chunk at a time: first every chunk's sums, then E from chunk to
-// chunk, then the gradients, from the parts read again (one wave that walked
-// the segment's chunks took 12 us for 8 of them, 18 for 16).
+// chunk (a lane has a chunk), then the gradients, from the parts still held or
+// read again (one wave that walked the segment's chunks took 12 us for 8 of
+// them, 18 for 16).
 
 struct GateGrad {
   LinSeq q;
@@ -130,13 +131,14 @@ __global__ __launch_bounds__(64 * GATE_WAVES) void kda_lin_gate_grad(
   const int t_begin = s * q.seg, t_end = min(q.T, t_begin + q.seg);
   const int live_end = min(len, t_end);
   const int nch = (t_end - t_begin + C - 1) / C;  // at most MAX_CHUNKS
-  float late, early, g;
+  float late, early, pairs, g;
   auto load = [&](int c) {
     const int t = t_begin + c * C + lane;
-    late = early = g = 0.f;
+    late = early = pairs = g = 0.f;
     if (lane < C && t < live_end) {
       late = p.late[chain * q.T + t];
       early = p.early[chain * q.T + t];
+      pairs = p.pairs[chain * q.T + t];
       const size_t i = q.gate_fixed ? (size_t)h
                                     : ((size_t)b * q.T + t) * q.H + h;
       g = q.gate_bf16 ? (float)((const bf16 *)q.g)[i]
@@ -145,33 +147,50 @@ __global__ __launch_bounds__(64 * GATE_WAVES) void kda_lin_gate_grad(
   };
   for (int c = w; c < nch; c += GATE_WAVES) {
     load(c);
-    float G = g;
+    float x = late, y = early, G = g;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
-      late += __shfl_xor(late, d, 64);
-      early += __shfl_xor(early, d, 64);
+      x += __shfl_xor(x, d, 64);
+      y += __shfl_xor(y, d, 64);
       G += __shfl_xor(G, d, 64);
     }
     if (lane == 0) {
-      sum_late[c] = late;
-      sum_early[c] = early;
+      sum_late[c] = x;
+      sum_early[c] = y;
       forgets[c] = G;
     }
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    float E = p.ends[chain * q.NS + s];
-    for (int c = nch - 1; c >= 0; --c) {
-      // exp(G) < 2^-40
-      const float Z = forgets[c] < -27.7f ? 0.f : E - sum_early[c];
-      both[c] = Z;
-      E = Z + sum_late[c];
+  if (w == 0) {
+    // a chunk's E from that behind it: (keeps it ? E : 0) + add
+    const int c = nch - 1 - lane;
+    bool keeps = true;
+    float add = 0.f, y = 0.f;
+    if (c >= 0) {
+      keeps = !(forgets[c] < -27.7f);  // exp(G) < 2^-40
+      y = sum_early[c];
+      add = sum_late[c] - (keeps ? y : 0.f);
     }
+    bool all = keeps;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const float a = __shfl_up(add, d, 64);
+      const bool k = __shfl_up((int)all, d, 64);
+      if (lane >= d) {
+        add += all ? a : 0.f;
+        all = all && k;
+      }
+    }
+    const float a = __shfl_up(add, 1, 64);
+    const bool k = __shfl_up((int)all, 1, 64);
+    float E = p.ends[chain * q.NS + s];
+    if (lane > 0) E = (k ? E : 0.f) + a;
+    if (c >= 0) both[c] = keeps ? E - y : 0.f;
   }
   __syncthreads();
   double total = 0.0;
   for (int c = w; c < nch; c += GATE_WAVES) {
-    load(c);
+    if (nch > GATE_WAVES) load(c);
     const int t = t_begin + c * C + lane;
     const bool in = lane < C && t < t_end, live = lane < C && t < live_end;
     float x = late, y = early;  // from the token on; up to it
@@ -182,8 +201,7 @@ __global__ __launch_bounds__(64 * GATE_WAVES) void kda_lin_gate_grad(
       if (lane >= d) y += e;
     }
     const float up = __shfl_up(y, 1, 64);
-    float dg = x + (lane == 0 ? 0.f : up) + both[c];
-    if (live) dg += p.pairs[chain * q.T + t];
+    float dg = x + (lane == 0 ? 0.f : up) + both[c] + pairs;
     // a token that forgets everything has no gradient, whatever the sums say
     if (!live || g < -1e4f) dg = 0.f;
     if (p.sums) {
@@ -222,26 +240,30 @@ __global__ __launch_bounds__(64) void kda_lin_gate_sum(const double *sums,
 }
 
 // ---------------------------------------------------------------------------
-// gradients of shared query and key heads: the sum over the value heads that
-// share one, in their order
+// gradients of shared query and key heads, both in one launch: the sum over the
+// value heads that share one, in their order
 
-__global__ __launch_bounds__(256) void kda_lin_heads(const float *x, float *y,
-                                                     size_t n4, int D4,
-                                                     int G) {
+struct Heads {
+  const char *x[2];  // fp32, or bf16 with the rounded-off rest `part` bytes on
+  void *y[2];
+  size_t part;
+};
+__global__ __launch_bounds__(256) void kda_lin_heads(Heads p, size_t n4,
+                                                     int D4, int G) {
   const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= n4) return;
-  const f32x4 *v = (const f32x4 *)x + i / D4 * G * D4 + i % D4;
+  const f32x4 *v = (const f32x4 *)p.x[blockIdx.y] + i / D4 * G * D4 + i % D4;
   f32x4 s = v[0];
   for (int k = 1; k < G; ++k) s += v[(size_t)k * D4];
-  ((f32x4 *)y)[i] = s;
+  ((f32x4 *)p.y[blockIdx.y])[i] = s;
 }
-// bf16: each value as a rounded one and the rest; 8 of them a thread
-__global__ __launch_bounds__(256) void kda_lin_heads2(const bf16 *x,
-                                                      const bf16 *rest,
-                                                      bf16 *y, size_t n8,
+// bf16: 8 values a thread
+__global__ __launch_bounds__(256) void kda_lin_heads2(Heads p, size_t n8,
                                                       int D8, int G) {
   const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= n8) return;
+  const bf16 *const x = (const bf16 *)p.x[blockIdx.y];
+  const bf16 *const rest = (const bf16 *)(p.x[blockIdx.y] + p.part);
   const size_t at = i / D8 * G * D8 + i % D8;
   float s[8] = {};
   for (int k = 0; k < G; ++k) {
@@ -251,7 +273,7 @@ __global__ __launch_bounds__(256) void kda_lin_heads2(const bf16 *x,
 #pragma unroll
     for (int e = 0; e < 8; ++e) s[e] += a.get(e) + b.get(e);
   }
-  store8(y + i * 8, s);
+  store8((bf16 *)p.y[blockIdx.y] + i * 8, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -578,19 +600,13 @@ hipError_t launch_linattn_backward(const LinParams &p, hipStream_t st) {
   if (shared) {
     const int V = p.io_bf16 ? 8 : 4;
     const size_t n = (size_t)p.B * p.T * p.Hk * p.Dk / V;
-    const unsigned blocks = (unsigned)((n + 255) / 256);
-    for (int i = 0; i < 2; ++i) {
-      const char *x = p.ws + (i ? l.dk : l.dq);
-      void *y = i ? p.dk : p.dq;
-      if (p.io_bf16)
-        lin::kda_lin_heads2<<<blocks, 256, 0, st>>>(
-            (const bf16 *)x, (const bf16 *)(x + part), (bf16 *)y, n, p.Dk / V,
-            seq.G);
-      else
-        lin::kda_lin_heads<<<blocks, 256, 0, st>>>(
-            (const float *)x, (float *)y, n, p.Dk / V, seq.G);
-      LIN_TRY(hipGetLastError());
-    }
+    const dim3 blocks((unsigned)((n + 255) / 256), 2);
+    const lin::Heads x{{p.ws + l.dq, p.ws + l.dk}, {p.dq, p.dk}, part};
+    if (p.io_bf16)
+      lin::kda_lin_heads2<<<blocks, 256, 0, st>>>(x, n, p.Dk / V, seq.G);
+    else
+      lin::kda_lin_heads<<<blocks, 256, 0, st>>>(x, n, p.Dk / V, seq.G);
+    LIN_TRY(hipGetLastError());
   }
   if (gate) {
     double *const sums = (double *)(p.ws + l.sums);
