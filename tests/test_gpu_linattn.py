@@ -324,8 +324,9 @@ def test_shared_heads_of_any_width(kda, io, Dk, Dv, want_dg):
             within(n, t, want[n])
 
 
-def test_fixed_decays_of_many_sequences(kda):
-    x, d = inputs(130, 40, 1, 2, 16, 16, kind="fixed", seed=25)
+@pytest.mark.parametrize("io,gate", [(BF, F), (BF, BF), (F, F)])
+def test_fixed_decays_of_many_sequences(kda, io, gate):
+    x, d = inputs(130, 40, 1, 2, 16, 16, io, gate, kind="fixed", seed=25)
     check(kda, x, d)
 
 

@@ -235,6 +235,20 @@ def test_special_rows(kda, dtype):
     assert not torch.isfinite(y[5, 0, 3])
 
 
+def test_squares_below_the_normal_range(kda):
+    """eps = 0 and squares of about 2^-130, multiples of 2^-149: the mean is off
+    by two half steps, 2^-149, of at least 2^-132, its root by 2^-18"""
+    q = torch.where(rn(5, 3, 64, seed=35) < 0, -2.0 ** -65, 2.0 ** -65.5)
+    w = rn(64, seed=36)
+    y, _ = kda.kda_qk_norm_rope(q, None, None, None, wq=w, eps=0.0)
+    x = q.double()
+    want = x / (x * x).mean(-1, keepdim=True).sqrt() * w.double()
+    assert ((y.double() - want).abs() <= 2.0 ** -17 * want.abs()).all()
+    z, _ = kda.kda_qk_norm_rope(torch.zeros_like(q), None, None, None, wq=w,
+                                eps=0.0)
+    assert torch.isnan(z).all()
+
+
 def test_streams_and_graphs(kda):
     q, k = rn(130, 4, 128, seed=35, dtype=BF), rn(130, 2, 128, seed=36,
                                                   dtype=BF)
