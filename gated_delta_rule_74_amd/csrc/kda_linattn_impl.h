@@ -464,6 +464,20 @@ __device__ __forceinline__ void pair_unit(int idx, int &rt, int &u2) {
   }
 }
 
+// x of rows 0 and 1 of 16 lanes, then of 2 and 3, side by side in one sum with y
+// in the odd rows: [x0 + x1, y0 + y1, x2 + x3, y2 + y3]
+__device__ __forceinline__ float add_rows(float x, float y) {
+  const auto r = __builtin_amdgcn_permlane16_swap(
+      __float_as_uint(x), __float_as_uint(y), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+// the same of halves of a wave: [x0 + x2, x1 + x3, y0 + y2, y1 + y3]
+__device__ __forceinline__ float add_halves(float x, float y) {
+  const auto r = __builtin_amdgcn_permlane32_swap(
+      __float_as_uint(x), __float_as_uint(y), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
 // sums over the pairs of a tile, for the gate's gradient: for the tile's j, of
 // all pairs with an earlier j of the tile (of the diagonal tiles, whose i is no
 // earlier); for its i, of all pairs with this or a later i
@@ -518,8 +532,8 @@ __device__ __forceinline__ void pair_sums(PairSums<NB> &s, int rt, int jt,
   if (m == 0) *(f32x4 *)&s.by_j[rt][jt][4 * g] = v;
   if (!diag) {
     float r = (qk[0] + qk[1]) + (qk[2] + qk[3]);
-    r += __shfl_xor(r, 16, 64);
-    r += __shfl_xor(r, 32, 64);
+    r = add_rows(r, r);
+    r = add_halves(r, r);
     r = add_row_shl<0x101>(r);
     r = add_row_shl<0x102>(r);
     r = add_row_shl<0x104>(r);
@@ -649,9 +663,9 @@ __device__ __forceinline__ f32x4 rest4(f32x4 v, uint2 r) {
 // D wide: `rows` rows, zeros from `live` on (none, where rows is 0).  bf16:
 // after a swap between lanes each has 8 consecutive columns of one row, of the
 // lower tile where g is odd (8 bytes a lane took 4 us more at B1 T8192 H32 D128);
-// REST: what rounding leaves goes to a second tensor, if there is one.  A store
-// that meets no memory takes the place of a branch, which would make the next
-// chunk wait for this one.
+// REST: what rounding leaves goes to a second tensor, if there is one.  (With
+// stores to nothing in the place of that branch, which is the same for a whole
+// wave, the gradient of B1 T8192 H32 D128 took 269 us, not 263.)
 template <typename IO, int D, bool REST>
 __device__ __forceinline__ void put_out(f32x4 (&acc)[Shape<IO>::NB], void *out,
                                         void *rest, size_t at, int H, int rows,
@@ -685,10 +699,10 @@ __device__ __forceinline__ void put_out(f32x4 (&acc)[Shape<IO>::NB], void *out,
         if (rest) {
           a = pack4(rest4(acc[rt], a));
           c = pack4(rest4(acc[rt + 1], c));
+          x = __builtin_amdgcn_permlane16_swap(a.x, c.x, false, false);
+          y = __builtin_amdgcn_permlane16_swap(a.y, c.y, false, false);
+          store16(o2, v + rt * 16 * row, uint4{x[0], y[0], x[1], y[1]});
         }
-        x = __builtin_amdgcn_permlane16_swap(a.x, c.x, false, false);
-        y = __builtin_amdgcn_permlane16_swap(a.y, c.y, false, false);
-        store16(o2, v + rt * 16 * row, uint4{x[0], y[0], x[1], y[1]});
       }
     }
   }
@@ -722,6 +736,29 @@ __device__ __forceinline__ void store_state(const f32x4 (&S)[D1 / 16], float *p,
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       p[(kt * 16 + 4 * g + e) * D2 + col + m] = S[kt][e];
+}
+
+// Dot products of a chunk's tokens, acc's columns against row `y` of a tile (the
+// wave's 16 channels from `col` on): summed over the four rows of lanes, token
+// `lane` in each lane
+template <typename IO, int D>
+__device__ __forceinline__ void put_dots(const f32x4 (&acc)[Shape<IO>::NB],
+                                         const IO *y, int col, int g, int m,
+                                         float *out) {
+  constexpr int NB = Shape<IO>::NB;
+  float dot[NB];
+#pragma unroll
+  for (int rt = 0; rt < NB; ++rt) {
+    const IO *p = y + Tile<IO, D>::at(rt * 16 + m, col + 4 * g);
+    dot[rt] = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) dot[rt] += acc[rt][e] * to_f32(p[e]);
+  }
+  const float a = add_rows(dot[0], dot[1]);
+  if constexpr (NB == 4)
+    out[g * 16 + m] = add_halves(a, add_rows(dot[2], dot[3]));
+  else if (const float b = add_halves(a, a); g < 2)
+    out[g * 16 + m] = b;
 }
 
 // x[0][i] + x[1][i] + ..., in this order
@@ -924,18 +961,9 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
       far_part<IO, D1, DOT != LIN_PLAIN>(acc, S, ta[x], g, m);
       const float *const far_w = REV ? dec.last : dec.first;
 #pragma unroll
-      for (int rt = 0; rt < NB; ++rt) {
-        acc[rt] *= far_w[rt * 16 + m];
-        if constexpr (DOT) {
-          const IO *y = td[x] + T2::at(rt * 16 + m, col + 4 * g);
-          float dot = 0.f;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) dot += acc[rt][e] * to_f32(y[e]);
-          dot += __shfl_xor(dot, 16, 64);
-          dot += __shfl_xor(dot, 32, 64);
-          if (g == 0) far_dots[n & 1][w][rt * 16 + m] = dot;
-        }
-      }
+      for (int rt = 0; rt < NB; ++rt) acc[rt] *= far_w[rt * 16 + m];
+      if constexpr (DOT)
+        put_dots<IO, D2>(acc, td[x], col, g, m, far_dots[n & 1][w]);
     }
     barrier_keep_vmem();
 
@@ -975,7 +1003,7 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
       }
     }
     v = group_sum<32>(v);
-    v += __shfl_xor(v, 32, 64);
+    v = add_halves(v, v);
     barrier_keep_vmem();  // the last chunk's sums have been read
     if (mine && lane == 0) far_dots[0][w][0] = v;
     barrier_keep_vmem();
@@ -1103,18 +1131,8 @@ __global__ __launch_bounds__(128 * nwaves<D>(), 4) void kda_lin_both(
       else far_part<IO, D, false>(acc, S, dk ? tv[x] : tk[x], g, m);
 #pragma unroll
       for (int rt = 0; rt < NB; ++rt) acc[rt] *= dec.last[rt * 16 + m];
-      if (DOT && dk) {
-#pragma unroll
-        for (int rt = 0; rt < NB; ++rt) {
-          const IO *y = tk[x] + TD::at(rt * 16 + m, col + 4 * g);
-          float dot = 0.f;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) dot += acc[rt][e] * to_f32(y[e]);
-          dot += __shfl_xor(dot, 16, 64);
-          dot += __shfl_xor(dot, 32, 64);
-          if (g == 0) far_dots[n & 1][wc][rt * 16 + m] = dot;
-        }
-      }
+      if (DOT && dk)
+        put_dots<IO, D>(acc, tk[x], col, g, m, far_dots[n & 1][wc]);
     }
     barrier_keep_vmem();
 
