@@ -478,6 +478,15 @@ __device__ __forceinline__ float add_halves(float x, float y) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
+// the sum of x over the rows of lanes before a lane's own: [0, x0, x0 + x1, ...]
+__device__ __forceinline__ float before_row(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(0u, __float_as_uint(x),
+                                                  false, false);
+  const auto h = __builtin_amdgcn_permlane32_swap(
+      0u, __float_as_uint(add_rows(x, x)), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(h[0]);
+}
+
 // sums over the pairs of a tile, for the gate's gradient: for the tile's j, of
 // all pairs with an earlier j of the tile (of the diagonal tiles, whose i is no
 // earlier); for its i, of all pairs with this or a later i
@@ -517,12 +526,7 @@ __device__ __forceinline__ void pair_sums(PairSums<NB> &s, int rt, int jt,
 #pragma unroll
   for (int e = 0; e < 4; ++e) c[e] = diag ? qk[e] : group_sum<16>(qk[e]);
   const float tot = (c[0] + c[1]) + (c[2] + c[3]);
-  const float v1 = __shfl_up(tot, 16, 64), v2 = __shfl_up(tot, 32, 64),
-              v3 = __shfl_up(tot, 48, 64);
-  float pre = 0.f;
-  if (g >= 3) pre += v3;
-  if (g >= 2) pre += v2;
-  if (g >= 1) pre += v1;
+  float pre = before_row(tot);
   f32x4 v;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
