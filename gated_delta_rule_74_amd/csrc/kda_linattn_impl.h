@@ -168,9 +168,9 @@ __device__ __forceinline__ void store16(__amdgpu_buffer_rsrc_t r, unsigned at,
                                          0, 0);
 }
 
-// The wait before a loop over chunks, on every way into it: with rows or a state
-// in flight into the loop the compiler would count, at every turn, as if no
-// output had been written since they were asked for, and wait for it.
+// The wait before a loop over chunks, on every way into it: with rows or a
+// state in flight into the loop the compiler would count, at every turn, as if
+// no output had been written since they were asked for, and wait for it.
 __device__ __forceinline__ void all_loaded() {
   __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
 }
@@ -464,8 +464,8 @@ __device__ __forceinline__ void pair_unit(int idx, int &rt, int &u2) {
   }
 }
 
-// x of rows 0 and 1 of 16 lanes, then of 2 and 3, side by side in one sum with y
-// in the odd rows: [x0 + x1, y0 + y1, x2 + x3, y2 + y3]
+// x of rows 0 and 1 of 16 lanes, then of 2 and 3, side by side in one sum with
+// y in the odd rows: [x0 + x1, y0 + y1, x2 + x3, y2 + y3]
 __device__ __forceinline__ float add_rows(float x, float y) {
   const auto r = __builtin_amdgcn_permlane16_swap(
       __float_as_uint(x), __float_as_uint(y), false, false);
@@ -478,7 +478,7 @@ __device__ __forceinline__ float add_halves(float x, float y) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-// the sum of x over the rows of lanes before a lane's own: [0, x0, x0 + x1, ...]
+// the sum of x over the rows of lanes before a lane's own: [0, x0, x0 + x1, ..]
 __device__ __forceinline__ float before_row(float x) {
   const auto r = __builtin_amdgcn_permlane16_swap(0u, __float_as_uint(x),
                                                   false, false);
@@ -666,7 +666,7 @@ __device__ __forceinline__ f32x4 rest4(f32x4 v, uint2 r) {
 // A chunk of the wave's 16 columns from `col` on to out[t0..] of one head of H,
 // D wide: `rows` rows, zeros from `live` on (none, where rows is 0).  bf16:
 // after a swap between lanes each has 8 consecutive columns of one row, of the
-// lower tile where g is odd (8 bytes a lane took 4 us more at B1 T8192 H32 D128);
+// lower tile where g is odd (8 bytes a lane: 4 us more at B1 T8192 H32 D128);
 // REST: what rounding leaves goes to a second tensor, if there is one.  (With
 // stores to nothing in the place of that branch, which is the same for a whole
 // wave, the gradient of B1 T8192 H32 D128 took 269 us, not 263.)
@@ -742,9 +742,9 @@ __device__ __forceinline__ void store_state(const f32x4 (&S)[D1 / 16], float *p,
       p[(kt * 16 + 4 * g + e) * D2 + col + m] = S[kt][e];
 }
 
-// Dot products of a chunk's tokens, acc's columns against row `y` of a tile (the
-// wave's 16 channels from `col` on): summed over the four rows of lanes, token
-// `lane` in each lane
+// Dot products of a chunk's tokens, acc's columns against the rows of tile `y`
+// (the wave's 16 channels from `col` on): summed over the four rows of lanes,
+// token `lane` in each lane
 template <typename IO, int D>
 __device__ __forceinline__ void put_dots(const f32x4 (&acc)[Shape<IO>::NB],
                                          const IO *y, int col, int g, int m,
@@ -776,11 +776,11 @@ __device__ __forceinline__ float column_sum(const float (&x)[N][C], int i) {
 
 // waves of a workgroup whose output is D2 wide
 template <int D2> constexpr int nwaves() { return D2 == 128 ? 8 : 4; }
-// Whether a sweep has two sets of LDS tiles.  The one workgroup of 8 waves that a
-// CU has gains by it (B1 T8192 H32 D128: 114 us without, 107 with); with 4 waves
-// other workgroups on the CU fill the wait as well, and the second set keeps
-// them off it (gradient of B8 T4096 H32 D64: 497 us without, 768 with; D32 380
-// and 396).
+// Whether a sweep has two sets of LDS tiles.  The one workgroup of D = 128 that
+// a CU has gains by it (B1 T8192 H32: 114 us without, 107 with); with fewer
+// waves other workgroups on the CU fill the wait as well, and the second set
+// keeps them off it (gradient of B8 T4096 H32 D64: 497 us without, 768 with;
+// D32 380 and 396).
 template <int NW> constexpr bool two_sets() { return NW == 8; }
 
 // where a workgroup's segment is
@@ -833,15 +833,16 @@ template <typename IO, int NW, bool REV> struct Keeper {
   }
   // first, last: factors of the weights
   __device__ __forceinline__ void make(const LinSeq &q, Decays<C> *decs,
-                                       const Where &at, int n0, float first, float last, int w,
-                                       int lane) {
+                                       const Where &at, int n0, float first,
+                                       float last, int w, int lane) {
 #pragma unroll
     for (int i = 0; i < gates.N; ++i) {
       const int x = w + i * NW;
       if (x >= BATCH || n0 + x >= at.nch) break;
       Decays<C> &d = decs[(n0 + x) % (2 * BATCH)];
       double G, tile;
-      const double end = decay_sums<C>(gate_value(q, gates.g[i]), lane, G, tile);
+      const double end = decay_sums<C>(gate_value(q, gates.g[i]), lane, G,
+                                      tile);
       if (!REV) tile = __shfl(tile, lane | 15, 64) - tile;
       if (lane < C) {
         d.G[lane] = G;
@@ -1228,7 +1229,8 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_local(
       const int x = w + i * NW;
       if (x >= BATCH) break;
       double tile;
-      const double end = decay_sums<C>(gate_value(q, gates.g[i]), lane, G[i], tile);
+      const double end = decay_sums<C>(gate_value(q, gates.g[i]), lane, G[i],
+                                       tile);
       if (lane == 0) ends[x] = end;
     }
     barrier_keep_vmem();

@@ -6,7 +6,8 @@
 // "slots"), which walks through the token's heads with the same channels in
 // the same lanes, so that the cosines and sines of a token are made once.  The
 // other value of a pair lies in the same lane (interleaved) or is fetched from
-// the lane rot / 16 away.
+// the lane rot / 16 away.  8192 tokens of 32 + 32 heads of 128: 47 us, 5.7
+// TB/s; the gradient of 8191 of 32 + 8: 43 us, 5.8 TB/s.
 //
 // Angles.  position * inv_freq in fp32 would be off by 0.008 at position
 // 262143; in 64 bits, counted in turns, what is left after the whole turns is
