@@ -25,12 +25,10 @@
 // Precision.  Decays between tokens are differences of sums held in 64 bits:
 // a sum over a chunk may reach 64e4 (g below -1e4 is taken as -1e4, whose exp
 // is 0) where fp32 differences would be off by 0.03.  With bf16 data the pair
-// products and the state are rounded to bf16 where they enter a product whose
-// result is rounded to bf16 itself (half a step each, as the result's own);
-// what ends up in fp32 (the state, and the dot products that the gate's
-// gradient is made of) takes the rounded-off rest as a second operand, which
-// leaves 2^-17 of a term at most, 2.4e-6 in the mean (a third operand would
-// leave 1e-8, and takes 109 us for 102 at B1 T8192 H32 D128).
+// products are rounded to bf16 where they enter a product whose result is
+// rounded to bf16 itself (half a step, as the result's own); the state enters
+// its products, and what is added to it, as a bf16 value and the rounded-off
+// rest, which leaves 2^-17 of a term at most, 2.4e-6 in the mean.
 #pragma once
 #include "kda_device.h"
 #include "kda_linattn.h"
@@ -390,14 +388,14 @@ __device__ __forceinline__ void add_chunk(
   }
 }
 
-// acc = S^T a, transposed: rows are the wave's columns, columns tokens.  EXACT:
-// with what rounding the state to bf16 leaves
-template <typename IO, int D1, bool EXACT>
+// acc = S^T a, transposed: rows are the wave's columns, columns tokens.  bf16:
+// the state in two parts, which leave 2^-17 of a term at most
+template <typename IO, int D1>
 __device__ __forceinline__ void far_part(f32x4 (&acc)[Shape<IO>::NB],
                                          const f32x4 (&S)[D1 / 16],
                                          const IO *ta, int g, int m) {
   constexpr int TPU = Shape<IO>::TPU, KT = D1 / 16;
-  constexpr bool LO = EXACT && sizeof(IO) == 2;
+  constexpr bool LO = sizeof(IO) == 2;
   typedef typename Mma<IO>::frag frag;
 #pragma unroll
   for (int rt = 0; rt < Shape<IO>::NB; ++rt) acc[rt] = f32x4{0, 0, 0, 0};
@@ -963,7 +961,7 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
     __builtin_amdgcn_sched_barrier(0);
     f32x4 acc[NB];
     if (mine) {
-      far_part<IO, D1, DOT != LIN_PLAIN>(acc, S, ta[x], g, m);
+      far_part<IO, D1>(acc, S, ta[x], g, m);
       const float *const far_w = REV ? dec.last : dec.first;
 #pragma unroll
       for (int rt = 0; rt < NB; ++rt) acc[rt] *= far_w[rt * 16 + m];
@@ -1132,8 +1130,7 @@ __global__ __launch_bounds__(128 * nwaves<D>(), 4) void kda_lin_both(
     f32x4 acc[NB];
     fresh();
     if (mine) {
-      if (DOT && dk) far_part<IO, D, true>(acc, S, tv[x], g, m);
-      else far_part<IO, D, false>(acc, S, dk ? tv[x] : tk[x], g, m);
+      far_part<IO, D>(acc, S, dk ? tv[x] : tk[x], g, m);
 #pragma unroll
       for (int rt = 0; rt < NB; ++rt) acc[rt] *= dec.last[rt * 16 + m];
       if (DOT && dk)

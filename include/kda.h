@@ -510,7 +510,7 @@ size_t kda_linattn_backward_workspace_size(int B, int T, int Hk, int H, int Dk,
  *   s_out    state after the last token [B,H,Dk,Dv] fp32, or NULL; may equal
  *            s0
  * With bf16 data o carries, beside its own rounding, one rounding of the pair
- * products and one of the state to bf16 (half a step each); s_out is within
+ * products to bf16 (half a step) and 2^-17 of the state's terms; s_out is within
  * 2^-17 of its terms' magnitudes, and terms that have decayed to less than
  * 2^-200 may count as none.  Values are not checked: an infinity or
  * NaN in q, k or v may also reach the outputs of up to 63 tokens before it
@@ -539,7 +539,8 @@ kda_status kda_linattn(const void *q, const void *k, const void *v,
  *                 all tokens), or NULL: not wanted
  *   ds0           [B,H,Dk,Dv] fp32, or NULL
  * Gradients of tokens past a sequence's length are written as zeros.  No
- * output may alias an input or another output. */
+ * output may alias an input or another output.  A gradient is the same whether
+ * dg and ds0 are wanted or not. */
 kda_status kda_linattn_backward(
     const void *q, const void *k, const void *v, kda_dtype qkv_dtype,
     const void *g, kda_dtype gate_dtype, const float *s0, const int *lengths,

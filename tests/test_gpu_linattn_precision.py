@@ -1,0 +1,110 @@
+"""How many bits of a product linear attention keeps: results that consist of
+one term each, so that every rounding on the way shows in full.
+
+A result in bf16 may be off by its own rounding, 2^-8 of the value, and by what
+an operand in two parts leaves, 2^-17 of the term; a factor exp(G) made of a
+difference of 64-bit sums is off by 4 u (its argument's rounding, under one for
+|G| <= 1, the hardware's exponential 2, a product 1) for each chunk that the
+term passes through, u = 2^-24."""
+import pytest
+import torch
+
+import linattn_ref as ref
+from layer_ref import U, within
+
+pytestmark = pytest.mark.gpu
+BF, F = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def kda():
+    import gated_delta_rule_74_amd as m
+    return m
+
+
+def one_hot(gen, *shape):
+    """exact in every type: a product with it picks one term"""
+    i = torch.randint(0, shape[-1], shape[:-1], generator=gen)
+    return torch.nn.functional.one_hot(i, shape[-1]).float()
+
+
+def terms(name, got, want, T, r=2.0 ** -17):
+    """got against values that are one term each"""
+    within(name, got, (want, (r + (8 + 4 * -(-T // 32)) * U) * want.abs()))
+
+
+def state_inputs(T, Dk, Dv, seed, H=3):
+    gen = torch.Generator().manual_seed(seed + T + 3 * Dk + Dv)
+    x = dict(q=one_hot(gen, 1, T, H, Dk), k=torch.zeros(1, T, H, Dk),
+             v=one_hot(gen, 1, T, H, Dv))
+    x = {n: t.to(BF) for n, t in x.items()}
+    # all of them forget exp(-1) at most
+    x["g"] = -torch.rand(1, T, H, generator=gen) / T
+    x["s0"] = torch.randn(1, H, Dk, Dv, generator=gen)
+    d = dict(do=one_hot(gen, 1, T, H, Dv).to(BF),
+             dsT=torch.randn(1, H, Dk, Dv, generator=gen))
+    return gen, x, d
+
+
+def cuda(x):
+    return {n: t.cuda() for n, t in x.items()}
+
+
+WIDTHS = [(16, 16), (32, 32), (64, 64), (128, 128), (128, 32), (16, 64)]
+
+
+@pytest.mark.parametrize("Dk,Dv", WIDTHS)
+@pytest.mark.parametrize("T", [1, 64, 130, 700])
+def test_a_state_in_the_output(kda, Dk, Dv, T):
+    """o = exp(G) s0^T q with nothing added: one element of s0 each"""
+    _, x, _ = state_inputs(T, Dk, Dv, 1)
+    want = ref.linattn(**x)["o"][0]
+    y = cuda(x)
+    o, _ = kda.kda_linattn(y["q"], y["k"], y["v"], y["g"], s0=y["s0"])
+    terms("o", o, want, T)
+
+
+@pytest.mark.parametrize("want_dg", [False, True])
+@pytest.mark.parametrize("Dk,Dv", WIDTHS)
+@pytest.mark.parametrize("T", [1, 64, 130, 700])
+def test_a_state_in_the_gradients(kda, Dk, Dv, T, want_dg):
+    """dq of a state that nothing is added to, dk and dv of a state's gradient
+    that nothing is added to"""
+    gen, x, d = state_inputs(T, Dk, Dv, 2)
+    want = ref.linattn(**x, **d)
+    y, e = cuda(x), cuda(d)
+    got = kda.kda_linattn_backward(y["q"], y["k"], y["v"], y["g"], e["do"],
+                                   s0=y["s0"], want_dg=want_dg)
+    terms("dq", got[0], want["dq"][0], T)
+    x["k"] = one_hot(gen, *x["k"].shape).to(BF)
+    d["do"].zero_()
+    want = ref.linattn(**x, **d)
+    y, e = cuda(x), cuda(d)
+    got = kda.kda_linattn_backward(y["q"], y["k"], y["v"], y["g"], e["do"],
+                                   dsT=e["dsT"], want_dg=want_dg)
+    terms("dk", got[1], want["dk"][0], T)
+    terms("dv", got[2], want["dv"][0], T)
+
+
+@pytest.mark.parametrize("io", [BF, F])
+@pytest.mark.parametrize("Dk,Dv", WIDTHS)
+@pytest.mark.parametrize("Hk", [1, 3])
+@pytest.mark.parametrize("T", [70, 1100])
+def test_gradients_do_not_depend_on_what_is_wanted(kda, io, Dk, Dv, Hk, T):
+    """the same bits with and without the gate's gradient, and with and without
+    the first state's"""
+    gen = torch.Generator().manual_seed(T + Dk + Dv)
+
+    def r(*s, dtype=io):
+        return torch.randn(*s, generator=gen).to(dtype).cuda()
+
+    four = (r(2, T, Hk, Dk), r(2, T, Hk, Dk), r(2, T, 3, Dv),
+            -r(2, T, 3, dtype=F).abs())
+    do, s0, dsT = r(2, T, 3, Dv), r(2, 3, Dk, Dv, dtype=F), r(2, 3, Dk, Dv,
+                                                              dtype=F)
+    full = kda.kda_linattn_backward(*four, do, s0=s0, dsT=dsT)
+    for dg, ds0 in ((False, True), (True, False), (False, False)):
+        part = kda.kda_linattn_backward(*four, do, s0=s0, dsT=dsT, want_dg=dg,
+                                        want_ds0=ds0)
+        for n, a, b in zip(("dq", "dk", "dv", "dg", "ds0"), full, part):
+            assert b is None or torch.equal(a, b), n
