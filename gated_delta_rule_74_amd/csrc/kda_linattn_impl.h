@@ -25,10 +25,9 @@
 // Precision.  Decays between tokens are differences of sums held in 64 bits:
 // a sum over a chunk may reach 64e4 (g below -1e4 is taken as -1e4, whose exp
 // is 0) where fp32 differences would be off by 0.03.  With bf16 data the pair
-// products are rounded to bf16 where they enter a product whose result is
-// rounded to bf16 itself (half a step, as the result's own); the state enters
-// its products, and what is added to it, as a bf16 value and the rounded-off
-// rest, which leaves 2^-17 of a term at most, 2.4e-6 in the mean.
+// products, the state, and what is added to it enter the matrix instructions as
+// a bf16 value and the rounded-off rest, which leaves 2^-17 of a term at most,
+// 2.4e-6 in the mean.
 #pragma once
 #include "kda_device.h"
 #include "kda_linattn.h"
@@ -276,7 +275,8 @@ __device__ __forceinline__ double add_dpp(double x) {
 
 // The decays of up to 4 chunks are made at a time, a chunk by each wave: made
 // one by one ahead of their chunk, by one wave while the others work, they kept
-// the others waiting (4 of the local pass's 40 us at B1 T8192 H32 D128).
+// the others waiting (4 of the local pass's 40 us at B1 T8192 H32 D128).  Of 2
+// in kda_lin_both, whose LDS holds no more.
 constexpr int BATCH = 4;
 
 // by one wave: the sums G of a chunk's log-decays, g that of token `lane` (0
@@ -300,7 +300,7 @@ __device__ __forceinline__ double decay_sums(float g, int lane, double &x,
 }
 
 // the gates of a wave's chunks of a batch, and where a sequence's chunks are
-template <int C, int NW> struct Gates {
+template <int C, int NW, int BATCH> struct Gates {
   static constexpr int N = (BATCH + NW - 1) / NW;
   unsigned g[N];
   // chunk n of nch, taken from the segment's end where `back` says so
@@ -430,26 +430,12 @@ __device__ __forceinline__ void far_part(f32x4 (&acc)[Shape<IO>::NB],
 template <bool REV> constexpr bool has_pairs(int rt, int jt) {
   return REV ? jt >= rt : jt <= rt;
 }
-// acc += c^T P^T: what the pairs give to out
-template <typename IO, bool REV>
-__device__ __forceinline__ void near_part(
-    f32x4 (&acc)[Shape<IO>::NB], const typename Mma<IO>::frag *tp,
-    const typename Mma<IO>::frag (&c)[Shape<IO>::NTU], int lane) {
-  constexpr int TPU = Shape<IO>::TPU, NTU = Shape<IO>::NTU;
-#pragma unroll
-  for (int rt = 0; rt < Shape<IO>::NB; ++rt)
-#pragma unroll
-    for (int u = 0; u < NTU; ++u)
-      if (has_pairs<REV>(rt, REV ? u * TPU + TPU - 1 : u * TPU))
-        acc[rt] = Mma<IO>::mma(c[u], tp[(rt * NTU + u) * 64 + lane], acc[rt]);
-}
-
 // The units of the pair products: 16 x 32 pieces (fp32 16 x 16) of a row of
 // tiles, those with two tiles of pairs first.  Unit `idx`'s row and place in
 // it, for the map that looks back; the other's is its mirror image.
 template <int NB> constexpr int pair_units() { return NB == 2 ? 3 : 6; }
 template <int NB, bool REV>
-__device__ __forceinline__ void pair_unit(int idx, int &rt, int &u2) {
+__host__ __device__ constexpr void pair_unit(int idx, int &rt, int &u2) {
   // rows and places as 4-bit fields: (3,0) (3,1) (2,0) (1,0) (2,1) (0,0); with
   // two rows of tiles (1,0) (1,1) (0,0)
   constexpr unsigned ROWS = NB == 2 ? 0x011 : 0x021233;
@@ -460,6 +446,41 @@ __device__ __forceinline__ void pair_unit(int idx, int &rt, int &u2) {
     rt = NB - 1 - rt;
     u2 = 1 - u2;
   }
+}
+// the unit at a row and place, as constants
+template <int NB, bool REV> constexpr int pair_slot(int rt, int u2) {
+  for (int idx = 0; idx < pair_units<NB>(); ++idx) {
+    int r = 0, p = 0;
+    pair_unit<NB, REV>(idx, r, p);
+    if (r == rt && p == u2) return idx;
+  }
+  return 0;
+}
+// A chunk's pair products in LDS: its units as operand fragments, bf16 with the
+// rounded-off rests behind them
+template <typename IO> constexpr int pair_frags() {
+  return pair_units<lin_chunk(sizeof(IO) == 2) / 16>() * 64 *
+         (sizeof(IO) == 2 ? 2 : 1);
+}
+
+// acc += c^T P^T: what the pairs give to out
+template <typename IO, bool REV>
+__device__ __forceinline__ void near_part(
+    f32x4 (&acc)[Shape<IO>::NB], const typename Mma<IO>::frag *tp,
+    const typename Mma<IO>::frag (&c)[Shape<IO>::NTU], int lane) {
+  constexpr int TPU = Shape<IO>::TPU, NTU = Shape<IO>::NTU;
+  constexpr int NB = Shape<IO>::NB;
+#pragma unroll
+  for (int rt = 0; rt < NB; ++rt)
+#pragma unroll
+    for (int u = 0; u < NTU; ++u)
+      if (has_pairs<REV>(rt, REV ? u * TPU + TPU - 1 : u * TPU)) {
+        const typename Mma<IO>::frag *const p =
+            tp + pair_slot<NB, REV>(rt, u) * 64 + lane;
+        acc[rt] = Mma<IO>::mma(c[u], p[0], acc[rt]);
+        if constexpr (sizeof(IO) == 2)
+          acc[rt] = Mma<IO>::mma(c[u], p[pair_units<NB>() * 64], acc[rt]);
+      }
 }
 
 // x of rows 0 and 1 of 16 lanes, then of 2 and 3, side by side in one sum with
@@ -565,7 +586,7 @@ __device__ __forceinline__ void pair_batch(
   typedef Shape<IO> Sh;
   typedef typename Mma<IO>::frag frag;
   typedef Tile<IO, D1> T1;
-  constexpr int TPU = Sh::TPU, NB = Sh::NB, NTU = Sh::NTU;
+  constexpr int TPU = Sh::TPU, NB = Sh::NB;
   constexpr int UNITS = pair_units<NB>();
   const int g = lane >> 4, m = lane & 15;
   int rt[K], u2[K];
@@ -581,7 +602,7 @@ __device__ __forceinline__ void pair_batch(
     const PairSet<IO> &s = sets[0], &s2 = sets[SETS - 1];
     a[k] = (second ? s2.a : s.a) + rt[k] * 16 * T1::STR;
     b[k] = (second ? s2.b : s.b) + u2[k] * 16 * TPU * T1::STR;
-    p[k] = (second ? s2.p : s.p) + (rt[k] * NTU + u2[k]) * 64;
+    p[k] = (second ? s2.p : s.p) + idx * 64;
     tile[k][0] = tile[k][1] = f32x4{0, 0, 0, 0};
   }
 #pragma unroll
@@ -629,7 +650,17 @@ __device__ __forceinline__ void pair_batch(
         pair_sums<NB>(*sums, rt[k], jt, qk * acc, g, m);
       }
     }
-    p[k][lane] = Mma<IO>::pack(tile[k][0], tile[k][1]);
+    frag hi = Mma<IO>::pack(tile[k][0], tile[k][1]);
+    if constexpr (sizeof(IO) == 2) {
+      packed(hi);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        tile[k][0][e] -= Mma<IO>::elem(hi, e);
+        tile[k][1][e] -= Mma<IO>::elem(hi, 4 + e);
+      }
+      p[k][UNITS * 64 + lane] = Mma<IO>::pack(tile[k][0], tile[k][1]);
+    }
+    p[k][lane] = hi;
   }
 }
 
@@ -821,9 +852,9 @@ __device__ __forceinline__ void zero_dead(void *out, const LinSeq &q,
 
 // The decays of a sweep's chunks: those of BATCH chunks are made at a time,
 // into the half of `decs` that the chunks at work do not read.
-template <typename IO, int NW, bool REV> struct Keeper {
+template <typename IO, int NW, bool REV, int BATCH> struct Keeper {
   static constexpr int C = Shape<IO>::C;
-  Gates<C, NW> gates;
+  Gates<C, NW, BATCH> gates;
   __device__ __forceinline__ void fetch(const LinSeq &q, const Where &at,
                                         int n0, int w, int lane) {
     gates.fetch(q, at.b, at.h, n0, at.nch, REV, at.t_begin, at.live_end, w,
@@ -869,7 +900,7 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
   __shared__ alignas(16) IO ta[1 + TWO][C * T1::STR], tb[1 + TWO][C * T1::STR],
       tc[1 + TWO][C * T2::STR];
   __shared__ alignas(16) IO td[1 + TWO][DOT ? C * T2::STR : 8];
-  __shared__ alignas(16) frag tp[NB * NTU * 64];
+  __shared__ alignas(16) frag tp[pair_frags<IO>()];
   __shared__ Decays<C> decs[2 * BATCH];
   __shared__ float far_dots[2][DOT ? COLS : 1][DOT ? C : 1];
   __shared__ PairSums<DOT == LIN_FAR_PAIRS ? NB : 1> sums[2];
@@ -909,7 +940,7 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
     rc.stash(tc[x]);
     if constexpr (DOT) rd.stash(td[x]);
   };
-  Keeper<IO, NW, REV> keeper;
+  Keeper<IO, NW, REV, BATCH> keeper;
   auto make_decays = [&](int n0) {
     keeper.make(q, decs, at, n0, REV ? p.add_scale : p.far_scale,
                 REV ? p.far_scale : p.add_scale, w, lane);
@@ -1034,13 +1065,13 @@ __global__ __launch_bounds__(128 * nwaves<D>(), 4) void kda_lin_both(
   constexpr bool REV = true;
   constexpr int C = Sh::C, NB = Sh::NB, NTU = Sh::NTU, KT = D / 16;
   constexpr int HALF = nwaves<D>(), NW = 2 * HALF, NT = 64 * NW;
-  constexpr int COLS = D / 16;
+  constexpr int COLS = D / 16, BATCH = 2;
   constexpr bool TWO = two_sets<HALF>();
   __shared__ alignas(16) IO tq[1 + TWO][C * TD::STR], tk[1 + TWO][C * TD::STR],
       tv[1 + TWO][C * TD::STR], to[1 + TWO][C * TD::STR];
-  __shared__ alignas(16) frag tp[2][NB * NTU * 64];
+  __shared__ alignas(16) frag tp[2][pair_frags<IO>()];
   __shared__ Decays<C> decs[2 * BATCH];
-  __shared__ float far_dots[2][DOT ? COLS : 1][DOT ? C : 1];
+  __shared__ float far_dots[DOT ? COLS : 1][DOT ? C : 1];
 
   const int lane = threadIdx.x & 63, w = wave_number();
   int g = lane >> 4, m = lane & 15;
@@ -1078,7 +1109,7 @@ __global__ __launch_bounds__(128 * nwaves<D>(), 4) void kda_lin_both(
     rv.stash(tv[x]);
     ro.stash(to[x]);
   };
-  Keeper<IO, NW, REV> keeper;
+  Keeper<IO, NW, REV, BATCH> keeper;
   auto make_decays = [&](int n0) {
     keeper.make(q, decs, at, n0, p.scale, 1.f, w, lane);
     keeper.fetch(q, at, n0 + BATCH, w, lane);
@@ -1086,7 +1117,7 @@ __global__ __launch_bounds__(128 * nwaves<D>(), 4) void kda_lin_both(
   auto finish = [&](int n) {
     const int t = at.at(n, REV, C) + lane;
     if (w == NW - 1 && lane < C && t < at.t_end)
-      p.early[at.chain * q.T + t] = column_sum(far_dots[n & 1], lane);
+      p.early[at.chain * q.T + t] = column_sum(far_dots, lane);
   };
   const bool keep_end = at.s == 0 && p.ds0;
   // LDS addresses are made anew in each part of a chunk's work: kept over the
@@ -1125,8 +1156,6 @@ __global__ __launch_bounds__(128 * nwaves<D>(), 4) void kda_lin_both(
                                   {tv[x], to[x], tp[1]}};
     fresh();
     pair_products<IO, D, 0, REV, NW, 2>(pairs, dec, p.scale, w, g * 16 + m);
-    if constexpr (DOT)
-      if (n > 0) finish(n - 1);
     f32x4 acc[NB];
     fresh();
     if (mine) {
@@ -1134,10 +1163,11 @@ __global__ __launch_bounds__(128 * nwaves<D>(), 4) void kda_lin_both(
 #pragma unroll
       for (int rt = 0; rt < NB; ++rt) acc[rt] *= dec.last[rt * 16 + m];
       if (DOT && dk)
-        put_dots<IO, D>(acc, tk[x], col, g, m, far_dots[n & 1][wc]);
+        put_dots<IO, D>(acc, tk[x], col, g, m, far_dots[wc]);
     }
     barrier_keep_vmem();
 
+    if constexpr (DOT) finish(n);
     frag fc[NTU];
     fresh();
     if (mine) {
@@ -1160,8 +1190,6 @@ __global__ __launch_bounds__(128 * nwaves<D>(), 4) void kda_lin_both(
     }
     barrier_keep_vmem();
   }
-  if constexpr (DOT)
-    if (nch > 0) finish(nch - 1);
   if (mine && keep_end && !dk)
     store_state<D, D>(S, p.ds0 + at.chain * D * D, col, g, m);
 }
@@ -1206,7 +1234,7 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_local(
   // next's
   Rows<IO, D1, C, NT> rb[2];
   Rows<IO, D2, C, NT> rc[2];
-  Gates<C, NW> gates;
+  Gates<C, NW, BATCH> gates;
   double sum = 0.0;  // decay of the chunks taken
   auto fetch = [&](auto &b, auto &c, int n) {
     const int t0 = at.at(n, back, C), live = n < nch ? at.live_end - t0 : 0;

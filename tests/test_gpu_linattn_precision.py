@@ -108,3 +108,98 @@ def test_gradients_do_not_depend_on_what_is_wanted(kda, io, Dk, Dv, Hk, T):
                                         want_ds0=ds0)
         for n, a, b in zip(("dq", "dk", "dv", "dg", "ds0"), full, part):
             assert b is None or torch.equal(a, b), n
+
+
+def pair_inputs(T, Dk, Dv, seed):
+    """every tensor dense, log-decays that add up to -1 at most"""
+    gen = torch.Generator().manual_seed(seed + T + 3 * Dk + Dv)
+    H = 3
+
+    def r(*s):
+        return torch.randn(*s, generator=gen).to(BF)
+
+    x = dict(q=r(1, T, H, Dk), k=r(1, T, H, Dk), v=r(1, T, H, Dv),
+             g=-torch.rand(1, T, H, generator=gen) / T)
+    return gen, x, dict(do=r(1, T, H, Dv))
+
+
+def only(x, t):
+    """x with zeros for all tokens but t"""
+    y = torch.zeros_like(x)
+    y[:, t] = x[:, t]
+    return y
+
+
+# the last chunk of 700 tokens begins at 640, for chunks of 32 and of 64
+@pytest.mark.parametrize("Dk,Dv", WIDTHS)
+@pytest.mark.parametrize("T,t0", [(2, 0), (40, 0), (64, 0), (700, 640)])
+def test_a_pair_product_in_the_output(kda, Dk, Dv, T, t0):
+    """o_i = exp(G_i - G_0) (q_i . k_0) v_0 of a one-hot q"""
+    gen, x, _ = pair_inputs(T, Dk, Dv, 3)
+    x["q"] = one_hot(gen, *x["q"].shape).to(BF)
+    x["v"] = only(x["v"], t0)
+    want = ref.linattn(**x)["o"][0]
+    y = cuda(x)
+    o, _ = kda.kda_linattn(*y.values())
+    terms("o", o, want, T)
+
+
+@pytest.mark.parametrize("want_dg", [False, True])
+@pytest.mark.parametrize("Dk,Dv", WIDTHS)
+@pytest.mark.parametrize("T,t0", [(2, 0), (40, 0), (64, 0), (700, 640)])
+def test_a_pair_product_in_the_gradients(kda, Dk, Dv, T, t0, want_dg):
+    """dq_i of one token's key; dk_j and dv_j of the last token's query and
+    gradient (what comes out of another chunk has been put into the state
+    before, in two parts once more)"""
+    gen, x, d = pair_inputs(T, Dk, Dv, 4)
+    one = {n: one_hot(gen, *t.shape).to(BF) for n, t in {**x, **d}.items()
+           if n != "g"}
+
+    def grads(**over):
+        y = {**x, **d, **over}
+        want = ref.linattn(**y)
+        y = cuda(y)
+        return kda.kda_linattn_backward(y["q"], y["k"], y["v"], y["g"],
+                                        y["do"], want_dg=want_dg), want
+
+    got, want = grads(do=one["do"], k=only(x["k"], t0))
+    terms("dq", got[0], want["dq"][0], T)
+    got, want = grads(v=one["v"], q=only(x["q"], T - 1))
+    terms("dk", got[1], want["dk"][0], T, 2.0 ** -16)
+    got, want = grads(k=one["k"], do=only(d["do"], T - 1))
+    terms("dv", got[2], want["dv"][0], T, 2.0 ** -16)
+
+
+@pytest.mark.parametrize("kind", ["softplus", "slow"])
+@pytest.mark.parametrize("Hk", [1, 2])
+@pytest.mark.parametrize("T,Dk,Dv", [(512, 128, 128), (900, 32, 64)])
+def test_errors_are_those_of_the_last_rounding(kda, kind, Hk, T, Dk, Dv):
+    """Over a whole tensor: a rounded value's distance from the true one is at
+    most its own rounding's (that of the true value, in the mean: to 1 % over
+    60,000 of them) and what was off before, 2^-17 of its terms' magnitudes."""
+    gen = torch.Generator().manual_seed(T + Hk)
+    B, H = 1, 2
+
+    def r(*s):
+        return torch.randn(*s, generator=gen)
+
+    x = dict(q=torch.nn.functional.normalize(r(B, T, Hk, Dk), dim=-1).to(BF),
+             k=torch.nn.functional.normalize(r(B, T, Hk, Dk), dim=-1).to(BF),
+             v=r(B, T, H, Dv).to(BF),
+             g=-torch.nn.functional.softplus(r(B, T, H)) if kind == "softplus"
+             else -0.002 * torch.rand(B, T, H, generator=gen),
+             s0=r(B, H, Dk, Dv))
+    d = dict(do=r(B, T, H, Dv).to(BF), dsT=r(B, H, Dk, Dv))
+    want = ref.linattn(**x, **d)
+    y, e = cuda(x), cuda(d)
+    four = [y[n] for n in "qkvg"]
+    got = [kda.kda_linattn(*four, s0=y["s0"])[0],
+           *kda.kda_linattn_backward(*four, e["do"], s0=y["s0"],
+                                     dsT=e["dsT"])[:3]]
+    # ref's slack is (2^-8 + kappa) times the magnitudes
+    kappa = (256 + 8 * -(-T // 32) + 2 * (Dk + Dv)) * U
+    for n, t in zip(("o", "dq", "dk", "dv"), got):
+        w, slack = want[n]
+        own = (w.to(BF).double() - w).norm()
+        before = slack.norm() / (2.0 ** -8 + kappa) * 2.0 ** -17
+        assert (t.cpu().double() - w).norm() <= 1.01 * own + before, n
