@@ -24,10 +24,11 @@
 //
 // Precision.  Decays between tokens are differences of sums held in 64 bits:
 // a sum over a chunk may reach 64e4 (g below -1e4 is taken as -1e4, whose exp
-// is 0) where fp32 differences would be off by 0.03.  With bf16 data the pair
-// products, the state, and what is added to it enter the matrix instructions as
-// a bf16 value and the rounded-off rest, which leaves 2^-17 of a term at most,
-// 2.4e-6 in the mean.
+// is 0) where fp32 differences would be off by 0.03.  With bf16 data what
+// is added to the state, and the state where the gate's gradient is made of its
+// product, are in three bf16 parts, which hold 24 bits; the pair products and the
+// state in what is rounded to bf16 afterwards in two, which leave 2^-17 of a
+// term at most.
 #pragma once
 #include "kda_device.h"
 #include "kda_linattn.h"
@@ -354,6 +355,33 @@ __device__ __forceinline__ void reads_ahead() {
   }
 }
 
+// what rounding left of x: x - hi, exact
+__device__ __forceinline__ f32x4 minus(f32x4 x, const bf16x8 &hi, int e0) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) x[e] -= Mma<bf16>::elem(hi, e0 + e);
+  return x;
+}
+// x, y as an operand and the parts that rounding leaves, one after the other
+template <int N>
+__device__ __forceinline__ void parts(f32x4 x, f32x4 y, bf16x8 (&f)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    f[i] = Mma<bf16>::pack(x, y);
+    if (i + 1 == N) break;
+    packed(f[i]);
+    x = minus(x, f[i], 0);
+    y = minus(y, f[i], 4);
+  }
+}
+template <int N>
+__device__ __forceinline__ void parts(f32x4 x, f32x4, f32x4 (&f)[N]) {
+  f[0] = x;
+}
+// how many of them a product takes: N, all bits of fp32 being one
+template <typename IO, int N> constexpr int parts_of() {
+  return sizeof(IO) == 2 ? N : 1;
+}
+
 // S += b^T diag(w) c over a chunk, c as operand fragments
 template <typename IO, int D1>
 __device__ __forceinline__ void add_chunk(
@@ -369,59 +397,44 @@ __device__ __forceinline__ void add_chunk(
     float x[8] = {};
 #pragma unroll
     for (int e = 0; e < NE; ++e) x[e] = Mma<IO>::elem(c[u], e) * wt[e];
-    frag hi = Mma<IO>::pack(f32x4{x[0], x[1], x[2], x[3]},
-                            f32x4{x[4], x[5], x[6], x[7]});
-    if constexpr (sizeof(IO) == 2) packed(hi);
-    frag lo = hi;
-    if constexpr (sizeof(IO) == 2) {
-#pragma unroll
-      for (int e = 0; e < NE; ++e) x[e] -= Mma<IO>::elem(hi, e);
-      lo = Mma<IO>::pack(f32x4{x[0], x[1], x[2], x[3]},
-                         f32x4{x[4], x[5], x[6], x[7]});
-    }
+    constexpr int N = parts_of<IO, 3>();
+    frag f[N];
+    parts(f32x4{x[0], x[1], x[2], x[3]}, f32x4{x[4], x[5], x[6], x[7]}, f);
 #pragma unroll
     for (int kt = 0; kt < D1 / 16; ++kt) {
       const frag b = Tile<IO, D1>::by_col(tb, kt * 16, u, g, m);
-      S[kt] = Mma<IO>::mma(b, hi, S[kt]);
-      if constexpr (sizeof(IO) == 2) S[kt] = Mma<IO>::mma(b, lo, S[kt]);
+#pragma unroll
+      for (int i = 0; i < N; ++i) S[kt] = Mma<IO>::mma(b, f[i], S[kt]);
     }
   }
 }
 
 // acc = S^T a, transposed: rows are the wave's columns, columns tokens.  bf16:
-// the state in two parts, which leave 2^-17 of a term at most
-template <typename IO, int D1>
+// of two parts of the state; THIRD: the third's in `more`
+template <typename IO, int D1, bool THIRD>
 __device__ __forceinline__ void far_part(f32x4 (&acc)[Shape<IO>::NB],
+                                         f32x4 (&more)[Shape<IO>::NB],
                                          const f32x4 (&S)[D1 / 16],
                                          const IO *ta, int g, int m) {
   constexpr int TPU = Shape<IO>::TPU, KT = D1 / 16;
-  constexpr bool LO = sizeof(IO) == 2;
+  constexpr int N = parts_of<IO, THIRD ? 3 : 2>();
   typedef typename Mma<IO>::frag frag;
 #pragma unroll
-  for (int rt = 0; rt < Shape<IO>::NB; ++rt) acc[rt] = f32x4{0, 0, 0, 0};
+  for (int rt = 0; rt < Shape<IO>::NB; ++rt)
+    acc[rt] = more[rt] = f32x4{0, 0, 0, 0};
 #pragma unroll
   for (int u = 0; u < Shape<IO>::units(D1); ++u) {
-    const f32x4 x = S[u * TPU];
     f32x4 y{0, 0, 0, 0};
     if constexpr (TPU == 2)
       if (u * TPU + 1 < KT) y = S[u * TPU + 1];
-    frag fs = Mma<IO>::pack(x, y);
-    if constexpr (LO) packed(fs);
-    frag fl = fs;
-    if constexpr (LO) {
-      f32x4 x2, y2;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x2[e] = x[e] - Mma<IO>::elem(fs, e);
-        y2[e] = y[e] - Mma<IO>::elem(fs, 4 + e);
-      }
-      fl = Mma<IO>::pack(x2, y2);
-    }
+    frag fs[N];
+    parts(S[u * TPU], y, fs);
 #pragma unroll
     for (int rt = 0; rt < Shape<IO>::NB; ++rt) {
       const frag f = Tile<IO, D1>::by_row(ta, rt * 16, u, g, m);
-      acc[rt] = Mma<IO>::mma(fs, f, acc[rt]);
-      if constexpr (LO) acc[rt] = Mma<IO>::mma(fl, f, acc[rt]);
+      acc[rt] = Mma<IO>::mma(fs[0], f, acc[rt]);
+      if constexpr (N > 1) acc[rt] = Mma<IO>::mma(fs[1], f, acc[rt]);
+      if constexpr (N > 2) more[rt] = Mma<IO>::mma(fs[2], f, more[rt]);
     }
   }
 }
@@ -456,11 +469,10 @@ template <int NB, bool REV> constexpr int pair_slot(int rt, int u2) {
   }
   return 0;
 }
-// A chunk's pair products in LDS: its units as operand fragments, bf16 with the
-// rounded-off rests behind them
+// A chunk's pair products in LDS: its units as operand fragments, part by part
 template <typename IO> constexpr int pair_frags() {
   return pair_units<lin_chunk(sizeof(IO) == 2) / 16>() * 64 *
-         (sizeof(IO) == 2 ? 2 : 1);
+         parts_of<IO, 2>();
 }
 
 // acc += c^T P^T: what the pairs give to out
@@ -477,9 +489,9 @@ __device__ __forceinline__ void near_part(
       if (has_pairs<REV>(rt, REV ? u * TPU + TPU - 1 : u * TPU)) {
         const typename Mma<IO>::frag *const p =
             tp + pair_slot<NB, REV>(rt, u) * 64 + lane;
-        acc[rt] = Mma<IO>::mma(c[u], p[0], acc[rt]);
-        if constexpr (sizeof(IO) == 2)
-          acc[rt] = Mma<IO>::mma(c[u], p[pair_units<NB>() * 64], acc[rt]);
+#pragma unroll
+        for (int i = 0; i < parts_of<IO, 2>(); ++i)
+          acc[rt] = Mma<IO>::mma(c[u], p[i * pair_units<NB>() * 64], acc[rt]);
       }
 }
 
@@ -650,17 +662,11 @@ __device__ __forceinline__ void pair_batch(
         pair_sums<NB>(*sums, rt[k], jt, qk * acc, g, m);
       }
     }
-    frag hi = Mma<IO>::pack(tile[k][0], tile[k][1]);
-    if constexpr (sizeof(IO) == 2) {
-      packed(hi);
+    constexpr int N = parts_of<IO, 2>();
+    frag f[N];
+    parts(tile[k][0], tile[k][1], f);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        tile[k][0][e] -= Mma<IO>::elem(hi, e);
-        tile[k][1][e] -= Mma<IO>::elem(hi, 4 + e);
-      }
-      p[k][UNITS * 64 + lane] = Mma<IO>::pack(tile[k][0], tile[k][1]);
-    }
-    p[k][lane] = hi;
+    for (int i = 0; i < N; ++i) p[k][i * UNITS * 64 + lane] = f[i];
   }
 }
 
@@ -992,12 +998,16 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
     __builtin_amdgcn_sched_barrier(0);
     f32x4 acc[NB];
     if (mine) {
-      far_part<IO, D1>(acc, S, ta[x], g, m);
+      f32x4 more[NB];
+      far_part<IO, D1, DOT != 0>(acc, more, S, ta[x], g, m);
       const float *const far_w = REV ? dec.last : dec.first;
 #pragma unroll
-      for (int rt = 0; rt < NB; ++rt) acc[rt] *= far_w[rt * 16 + m];
+      for (int rt = 0; rt < NB; ++rt) {
+        more[rt] = (acc[rt] + more[rt]) * far_w[rt * 16 + m];
+        acc[rt] *= far_w[rt * 16 + m];
+      }
       if constexpr (DOT)
-        put_dots<IO, D2>(acc, td[x], col, g, m, far_dots[n & 1][w]);
+        put_dots<IO, D2>(more, td[x], col, g, m, far_dots[n & 1][w]);
     }
     barrier_keep_vmem();
 
@@ -1016,7 +1026,7 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) S[kt] *= dec.total;
       add_chunk<IO, D1>(S, tb[x], fc, REV ? dec.first : dec.last, g, m);
-      if constexpr (sizeof(IO) == 2) reads_ahead<12, 2, 2, NTU * KT>();
+      if constexpr (sizeof(IO) == 2) reads_ahead<12, 2, 3, NTU * KT>();
     }
     barrier_keep_vmem();
   }
@@ -1159,11 +1169,16 @@ __global__ __launch_bounds__(128 * nwaves<D>(), 4) void kda_lin_both(
     f32x4 acc[NB];
     fresh();
     if (mine) {
-      far_part<IO, D>(acc, S, dk ? tv[x] : tk[x], g, m);
+      f32x4 more[NB];
+      if (DOT && dk) far_part<IO, D, true>(acc, more, S, tv[x], g, m);
+      else far_part<IO, D, false>(acc, more, S, dk ? tv[x] : tk[x], g, m);
 #pragma unroll
-      for (int rt = 0; rt < NB; ++rt) acc[rt] *= dec.last[rt * 16 + m];
+      for (int rt = 0; rt < NB; ++rt) {
+        more[rt] = (acc[rt] + more[rt]) * dec.last[rt * 16 + m];
+        acc[rt] *= dec.last[rt * 16 + m];
+      }
       if (DOT && dk)
-        put_dots<IO, D>(acc, tk[x], col, g, m, far_dots[wc]);
+        put_dots<IO, D>(more, tk[x], col, g, m, far_dots[wc]);
     }
     barrier_keep_vmem();
 
@@ -1186,7 +1201,7 @@ __global__ __launch_bounds__(128 * nwaves<D>(), 4) void kda_lin_both(
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) S[kt] *= dec.total;
       add_chunk<IO, D>(S, dk ? to[x] : tq[x], fc, dec.first, g, m);
-      if constexpr (sizeof(IO) == 2) reads_ahead<12, 2, 2, NTU * KT>();
+      if constexpr (sizeof(IO) == 2) reads_ahead<12, 2, 3, NTU * KT>();
     }
     barrier_keep_vmem();
   }

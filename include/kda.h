@@ -509,9 +509,9 @@ size_t kda_linattn_backward_workspace_size(int B, int T, int Hk, int H, int Dk,
  *   o        must not alias an input
  *   s_out    state after the last token [B,H,Dk,Dv] fp32, or NULL; may equal
  *            s0
- * With bf16 data o is, before its own rounding, within 2^-16 of its terms'
- * magnitudes, s_out within 2^-17; terms that have decayed below 2^-200 may
- * count as none.  Values are not checked: an infinity or
+ * With bf16 data o is, before its own rounding, within 2^-17 of its terms'
+ * magnitudes; what is written in fp32 is as with fp32 data.  Terms that have
+ * decayed below 2^-200 may count as none.  Values are not checked: an infinity or
  * NaN in q, k or v may also reach the outputs of up to 63 tokens before it
  * (those of its chunk: 0 * inf in the matrix products), never those of another
  * sequence or head.

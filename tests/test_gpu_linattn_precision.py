@@ -203,3 +203,49 @@ def test_errors_are_those_of_the_last_rounding(kda, kind, Hk, T, Dk, Dv):
         own = (w.to(BF).double() - w).norm()
         before = slack.norm() / (2.0 ** -8 + kappa) * 2.0 ** -17
         assert (t.cpu().double() - w).norm() <= 1.01 * own + before, n
+
+
+@pytest.mark.parametrize("Dk,Dv", WIDTHS)
+@pytest.mark.parametrize("T", [1, 40, 130, 500])
+def test_a_term_of_the_states_has_all_bits(kda, Dk, Dv, T):
+    """the state of one token's key and value, the first state's gradient of
+    one token's query and output: fp32 products of bf16 values"""
+    gen, x, d = pair_inputs(T, Dk, Dv, 5)
+    x["k"], x["v"] = only(x["k"], 0), only(x["v"], 0)
+    x["q"], d["do"] = only(x["q"], T - 1), only(d["do"], T - 1)
+    want = ref.linattn(**x, **d, dsT=torch.zeros(1, 3, Dk, Dv))
+    y, e = cuda(x), cuda(d)
+    _, s = kda.kda_linattn(*[y[n] for n in "qkvg"])
+    terms("s", s, want["s"][0], T, 0)
+    got = kda.kda_linattn_backward(*[y[n] for n in "qkvg"], e["do"])
+    terms("ds0", got[4], want["ds0"][0], T, 0)
+
+
+@pytest.mark.parametrize("Dk,Dv", WIDTHS)
+@pytest.mark.parametrize("T", [1, 40, 130, 500])
+def test_a_term_of_the_gate_gradient_has_all_bits(kda, Dk, Dv, T):
+    """dg of the last token's query and the first state, which is one element
+    of it for every token; of the first token's key and the last state's
+    gradient, one element for every later one"""
+    gen, x, d = state_inputs(T, Dk, Dv, 6)
+    x["v"].zero_()
+    x["q"], d["do"] = only(x["q"], T - 1), only(d["do"], T - 1)
+    d["dsT"].zero_()
+    want = ref.linattn(**x, **d)["dg"][0]
+    y, e = cuda(x), cuda(d)
+    got = kda.kda_linattn_backward(*[y[n] for n in "qkvg"], e["do"],
+                                   s0=y["s0"])
+    assert (want.abs().amax((0, 1)) > 0).all()
+    terms("dg", got[3], want, T, 0)
+    _, x, d = state_inputs(T, Dk, Dv, 7)
+    x["k"] = only(one_hot(gen, *x["k"].shape).to(BF), 0)
+    d["do"].zero_()
+    x["s0"].zero_()
+    want = ref.linattn(**x, **d)["dg"][0]
+    y, e = cuda(x), cuda(d)
+    got = kda.kda_linattn_backward(*[y[n] for n in "qkvg"], e["do"],
+                                   dsT=e["dsT"])
+    # the first token's is a difference of two of the others
+    n = 8 + 4 * -(-T // 32)
+    within("dg", got[3], (want, n * U * want.abs().amax(1, keepdim=True)
+                          .expand_as(want)))
