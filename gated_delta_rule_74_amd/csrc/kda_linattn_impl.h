@@ -382,30 +382,49 @@ template <typename IO, int N> constexpr int parts_of() {
   return sizeof(IO) == 2 ? N : 1;
 }
 
-// S += b^T diag(w) c over a chunk, c as operand fragments
+// S = decay S + b^T diag(w) c over a chunk, c as operand fragments.  The chunk's
+// own part is summed up by itself and costs the state one rounding
 template <typename IO, int D1>
 __device__ __forceinline__ void add_chunk(
-    f32x4 (&S)[D1 / 16], const IO *tb,
+    f32x4 (&S)[D1 / 16], float decay, const IO *tb,
     const typename Mma<IO>::frag (&c)[Shape<IO>::NTU], const float *w, int g,
     int m) {
-  constexpr int NE = Mma<IO>::NE;
+  constexpr int NE = Mma<IO>::NE, N = parts_of<IO, 3>(), NTU = Shape<IO>::NTU;
+  // tiles side by side, so that a product need not wait for the one before it
+  constexpr int K = D1 == 16 ? 1 : 2;
   typedef typename Mma<IO>::frag frag;
+  frag f[NTU][N];
 #pragma unroll
-  for (int u = 0; u < Shape<IO>::NTU; ++u) {
+  for (int u = 0; u < NTU; ++u) {
     float wt[NE];
     weights(w, u, g, wt);
     float x[8] = {};
 #pragma unroll
     for (int e = 0; e < NE; ++e) x[e] = Mma<IO>::elem(c[u], e) * wt[e];
-    constexpr int N = parts_of<IO, 3>();
-    frag f[N];
-    parts(f32x4{x[0], x[1], x[2], x[3]}, f32x4{x[4], x[5], x[6], x[7]}, f);
+    parts(f32x4{x[0], x[1], x[2], x[3]}, f32x4{x[4], x[5], x[6], x[7]}, f[u]);
+  }
 #pragma unroll
-    for (int kt = 0; kt < D1 / 16; ++kt) {
-      const frag b = Tile<IO, D1>::by_col(tb, kt * 16, u, g, m);
+  for (int kt = 0; kt < D1 / 16; kt += K) {
+    f32x4 own[K];
 #pragma unroll
-      for (int i = 0; i < N; ++i) S[kt] = Mma<IO>::mma(b, f[i], S[kt]);
+    for (int k = 0; k < K; ++k) own[k] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int u = 0; u < NTU; ++u) {
+      frag b[K];
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        b[k] = Tile<IO, D1>::by_col(tb, (kt + k) * 16, u, g, m);
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+          own[k] = Mma<IO>::mma(b[k], f[u][i], own[k]);
     }
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        S[kt + k][e] = __builtin_fmaf(S[kt + k][e], decay, own[k][e]);
   }
 }
 
@@ -1023,10 +1042,9 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
         mine ? min(C, at.t_end - t0) : 0, at.live_end - t0, col, g, m);
     __builtin_amdgcn_sched_barrier(0);
     if (mine && (n + 1 < nch || keep_end)) {
-#pragma unroll
-      for (int kt = 0; kt < KT; ++kt) S[kt] *= dec.total;
-      add_chunk<IO, D1>(S, tb[x], fc, REV ? dec.first : dec.last, g, m);
-      if constexpr (sizeof(IO) == 2) reads_ahead<12, 2, 3, NTU * KT>();
+      add_chunk<IO, D1>(S, dec.total, tb[x], fc, REV ? dec.first : dec.last, g,
+                        m);
+      if constexpr (sizeof(IO) == 2) reads_ahead<12, 4, 6, NTU * KT / 2>();
     }
     barrier_keep_vmem();
   }
@@ -1198,10 +1216,8 @@ __global__ __launch_bounds__(128 * nwaves<D>(), 4) void kda_lin_both(
     __builtin_amdgcn_sched_barrier(0);
     fresh();
     if (mine && (n + 1 < nch || keep_end)) {
-#pragma unroll
-      for (int kt = 0; kt < KT; ++kt) S[kt] *= dec.total;
-      add_chunk<IO, D>(S, dk ? to[x] : tq[x], fc, dec.first, g, m);
-      if constexpr (sizeof(IO) == 2) reads_ahead<12, 2, 3, NTU * KT>();
+      add_chunk<IO, D>(S, dec.total, dk ? to[x] : tq[x], fc, dec.first, g, m);
+      if constexpr (sizeof(IO) == 2) reads_ahead<12, 4, 6, NTU * KT / 2>();
     }
     barrier_keep_vmem();
   }
@@ -1304,7 +1320,7 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_local(
 #pragma unroll
       for (int u = 0; u < NTU; ++u)
         fc[u] = Tile<IO, D2>::by_col(tc, col, u, g, m);
-      add_chunk<IO, D1>(S, tb, fc, wts[n % BATCH], g, m);
+      add_chunk<IO, D1>(S, 1.f, tb, fc, wts[n % BATCH], g, m);
     }
     barrier_keep_vmem();
     return true;

@@ -249,3 +249,34 @@ def test_a_term_of_the_gate_gradient_has_all_bits(kda, Dk, Dv, T):
     n = 8 + 4 * -(-T // 32)
     within("dg", got[3], (want, n * U * want.abs().amax(1, keepdim=True)
                           .expand_as(want)))
+
+
+@pytest.mark.parametrize("io", [BF, F])
+@pytest.mark.parametrize("Dk,Dv", [(32, 32), (64, 128)])
+def test_a_state_is_rounded_once_a_chunk(kda, io, Dk, Dv):
+    """With decays of 0.001 a token in the mean a state remembers 1000 of them,
+    31 chunks of 32.  Every chunk rounds it once (in the mean of squares u /
+    sqrt 3 of its elements) and multiplies it by a rounded decay (within u,
+    likewise), a token's own weight is within 3 u: sqrt(31 / 3 + 31 / 3 + 3) u,
+    4.9 u of the state's norm."""
+    gen = torch.Generator().manual_seed(Dk)
+    T = 4096
+
+    def r(*s):
+        return torch.randn(*s, generator=gen).to(io)
+
+    unit = torch.nn.functional.normalize
+    x = dict(q=unit(r(1, T, 1, Dk), dim=-1), k=unit(r(1, T, 1, Dk), dim=-1),
+             v=r(1, T, 1, Dv),
+             g=-0.002 * torch.rand(1, T, 1, generator=gen))
+    do = r(1, T, 1, Dv)
+    # many of the same head: one segment a sequence; the sums of 64 chunks
+    y = {n: t.repeat_interleave(600, 2).contiguous() for n, t in x.items()}
+    y = cuda(y)
+    want = ref.linattn(**x, do=do)
+    _, s = kda.kda_linattn(*y.values())
+    ds0 = kda.kda_linattn_backward(
+        *y.values(), do.repeat_interleave(600, 2).contiguous().cuda())[4]
+    for n, t in (("s", s), ("ds0", ds0)):
+        w = want[n][0]
+        assert (t[:, :1].cpu().double() - w).norm() <= 4.9 * U * w.norm(), n
