@@ -67,6 +67,9 @@ struct LinSweep {
   int s_transposed;           // s_in and e_with are [.., D2, D1]
   float *far_dot;             // [B,H,T]: d . (out's part from the state)
   float *pair_dot;            // [B,H,T]: the pairs across each token
+  float *size;                // [B,H,chunks]: of the state before (reversed:
+                              // behind) the chunk, the sum of its magnitudes
+                              // (reversed: the largest)
   const float *e_with;        // laid out as s_in, or null (zeros)
   float *e_out;               // [B,H,NS]: <state behind the segment, e_with>
 };
@@ -81,6 +84,7 @@ struct LinBoth {
   const float *ds_in;         // [B,H,NS,D,D] or null
   float *ds0;                 // [B,H,D,D] or null
   float *early;               // [B,H,T]
+  float *size;                // [B,H,chunks]: the largest of |dS| behind it
 };
 
 // the state that each segment adds to a zero one

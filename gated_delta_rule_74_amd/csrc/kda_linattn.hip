@@ -16,8 +16,13 @@
 // from t on), j alone (far_dot of dk's, summed up to t), neither (Z).  With E
 // the sum over the pairs across a chunk's end, Z = E - sum of the chunk's
 // j-terms, and E across its start is Z + sum of its i-terms; E at a segment's
-// end is the product of both states there.  Where a chunk forgets all but
-// 2^-40, Z is 0.
+// end is the product of both states there.  That is a difference of rounded
+// sums: where a chunk forgets much, or the tokens behind have the larger
+// gradients, what E is off (some 2^-24 of what it was) can be more than Z is.
+// But with S before and dS behind the chunk |Z| is at most exp(G) times the sum
+// of the |S| and the largest |dS| (sums of squares would be tighter, and leave
+// the range of fp32): what is over that is taken off, and where that is less
+// than E may be off, Z counts as 0, so that nothing of it is carried on.
 //
 // Measured at B1 T8192 H32 D128, bf16: forward 102 us, of which the local pass
 // 28, the scan 8 and the sweep 64 (450 MB in all at 4.4 TB/s: HBM, and the
@@ -35,7 +40,7 @@ namespace lin {
 constexpr size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 struct Split {
-  int NS, seg;
+  int NS, seg, chunks;  // segments, tokens of each, chunks of the sequence
 };
 
 // Segments are as many as fill the GPU once, in whole rounds of workgroups: 256
@@ -63,7 +68,7 @@ Split split(int B, int T, int H, int D, int io_bf16, bool grad) {
   if (!grad && nc <= 4) per = nc;
   while (64ll * per * per < nc) ++per;
   if (grad && per > MAX_CHUNKS) per = MAX_CHUNKS;
-  return Split{(nc + per - 1) / per, per * C};
+  return Split{(nc + per - 1) / per, per * C, nc};
 }
 
 // ---------------------------------------------------------------------------
@@ -110,23 +115,27 @@ __global__ __launch_bounds__(256) void kda_lin_scan(ScanSegs f, ScanSegs r,
 // ---------------------------------------------------------------------------
 // The gate's gradient from its parts.  A workgroup has one segment of one head,
 // a wave a chunk at a time: first every chunk's sums, then E from chunk to
-// chunk (a lane has a chunk), then the gradients, from the parts still held or
-// read again (one wave that walked the segment's chunks took 12 us for 8 of
-// them, 18 for 16).
+// chunk, then the gradients, from the parts still held or read again (one wave
+// that walked the segment's chunks took 12 us for 8 of them, 18 for 16).
 
 struct GateGrad {
   LinSeq q;
   const float *late, *early, *pairs;  // [B,H,T]
   const float *ends;                  // [B,H,NS]
+  const float *before, *behind;       // [B,H,chunks]: sum |S|, max |dS|
   void *dg;                           // [B,T,H] in the gate's type
   double *sums;                       // [B,H,NS] instead, for a fixed decay
 };
 constexpr int GATE_WAVES = 16;
+// what a sum that E is made of may be off, of its own size: 8 half steps; one
+// sum's and another's are independent, so that their squares add up
+constexpr float OFF = 0x1p-21f;
+__device__ __forceinline__ float off2(float x) { return (OFF * x) * (OFF * x); }
 
 __global__ __launch_bounds__(64 * GATE_WAVES) void kda_lin_gate_grad(
     GateGrad p, int C) {
-  __shared__ float sum_late[MAX_CHUNKS], sum_early[MAX_CHUNKS],
-      forgets[MAX_CHUNKS], both[MAX_CHUNKS];
+  __shared__ double sum_late[MAX_CHUNKS], sum_early[MAX_CHUNKS];
+  __shared__ float most[MAX_CHUNKS], both[MAX_CHUNKS];
   __shared__ double totals[GATE_WAVES];
   const LinSeq &q = p.q;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
@@ -138,6 +147,7 @@ __global__ __launch_bounds__(64 * GATE_WAVES) void kda_lin_gate_grad(
   const int t_begin = s * q.seg, t_end = min(q.T, t_begin + q.seg);
   const int live_end = min(len, t_end);
   const int nch = (t_end - t_begin + C - 1) / C;  // at most MAX_CHUNKS
+  const size_t chunk0 = chain * ((q.T + C - 1) / C) + t_begin / C;
   float late, early, pairs, g;
   auto load = [&](int c) {
     const int t = t_begin + c * C + lane;
@@ -154,7 +164,12 @@ __global__ __launch_bounds__(64 * GATE_WAVES) void kda_lin_gate_grad(
   };
   for (int c = w; c < nch; c += GATE_WAVES) {
     load(c);
-    float x = late, y = early, G = g;
+    // nothing is forgotten behind a sequence's end
+    const bool alive = t_begin + c * C < live_end;
+    const float S = alive ? p.before[chunk0 + c] : 0.f;
+    const float dS = alive ? p.behind[chunk0 + c] : 0.f;
+    double x = late, y = early;
+    float G = g;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
       x += __shfl_xor(x, d, 64);
@@ -164,35 +179,33 @@ __global__ __launch_bounds__(64 * GATE_WAVES) void kda_lin_gate_grad(
     if (lane == 0) {
       sum_late[c] = x;
       sum_early[c] = y;
-      forgets[c] = G;
+      // the most that Z can be: exp and the sums are off by less than 2^-8
+      most[c] = !alive ? INFINITY
+                : G < -87.f ? 0.f : expf(G) * 0x1.01p0f * S * dS;
     }
   }
   __syncthreads();
   if (w == 0) {
-    // a chunk's E from that behind it: (keeps it ? E : 0) + add
-    const int c = nch - 1 - lane;
-    bool keeps = true;
-    float add = 0.f, y = 0.f;
-    if (c >= 0) {
-      keeps = !(forgets[c] < -27.7f);  // exp(G) < 2^-40
-      y = sum_early[c];
-      add = sum_late[c] - (keeps ? y : 0.f);
-    }
-    bool all = keeps;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const float a = __shfl_up(add, d, 64);
-      const bool k = __shfl_up((int)all, d, 64);
-      if (lane >= d) {
-        add += all ? a : 0.f;
-        all = all && k;
+    // every lane does all, in 64 bits: what E's own sums are rounded by would
+    // add up over the chunks
+    double E = p.ends[chain * q.NS + s];
+    float off = off2((float)E), keep = 0.f;
+#pragma unroll 4
+    for (int c = nch - 1; c >= 0; --c) {
+      const double x = sum_late[c], y = sum_early[c];
+      const float cap = most[c];
+      double Z = E - y;
+      off += off2((float)y);
+      Z = Z > cap ? cap : Z < -cap ? -cap : Z;
+      if ((cap == 0.f || cap * cap < off) && Z == Z) {  // a NaN stays
+        Z = 0.0;
+        off = cap * cap;
       }
+      keep = lane == c ? (float)Z : keep;
+      E = Z + x;
+      off += off2((float)x);
     }
-    const float a = __shfl_up(add, 1, 64);
-    const bool k = __shfl_up((int)all, 1, 64);
-    float E = p.ends[chain * q.NS + s];
-    if (lane > 0) E = (k ? E : 0.f) + a;
-    if (c >= 0) both[c] = keeps ? E - y : 0.f;
+    if (lane < nch) both[lane] = keep;
   }
   __syncthreads();
   double total = 0.0;
@@ -450,7 +463,8 @@ LinSeq seq_of(const LinParams &p, Split sp) {
 
 // the workspace, part by part
 struct Layout {
-  size_t s, ds, decay, ddecay, late, early, pairs, ends, sums, dq, dk, bytes;
+  size_t s, ds, decay, ddecay, late, early, pairs, ends, before, behind, sums,
+      dq, dk, bytes;
 };
 Layout layout(int B, int T, int Hk, int H, int Dk, int Dv, Split sp,
               bool grad) {
@@ -473,6 +487,8 @@ Layout layout(int B, int T, int Hk, int H, int Dk, int Dv, Split sp,
     l.early = take(rows);
     l.pairs = take(rows);
     l.ends = take(segs * 4);
+    l.before = take(chains * sp.chunks * 4);
+    l.behind = take(chains * sp.chunks * 4);
     l.sums = take(segs * 8);
     const size_t part = H != Hk ? rows * Dk : 0;
     l.dq = take(part);
@@ -570,6 +586,7 @@ hipError_t launch_linattn_backward(const LinParams &p, hipStream_t st) {
     z.scale = p.scale;
     z.ds_in = ds_in; z.ds0 = p.ds0;
     z.early = early;
+    z.size = (float *)(p.ws + l.behind);
     LIN_TRY(lin::both(p.io_bf16, p.Dk, dots, z, st));
   } else {
     // dv
@@ -586,6 +603,7 @@ hipError_t launch_linattn_backward(const LinParams &p, hipStream_t st) {
     w.s_end = nullptr;
     w.s_transposed = 1;
     w.far_dot = early;
+    w.size = (float *)(p.ws + l.behind);
     LIN_TRY(lin::sweep(p.io_bf16, p.Dv, p.Dk, 1, dots ? LIN_FAR : LIN_PLAIN,
                        w, st));
   }
@@ -602,6 +620,7 @@ hipError_t launch_linattn_backward(const LinParams &p, hipStream_t st) {
   w.e_with = ds_in;
   w.far_dot = (float *)(p.ws + l.late);
   w.pair_dot = (float *)(p.ws + l.pairs);
+  w.size = (float *)(p.ws + l.before);
   w.e_out = (float *)(p.ws + l.ends);
   LIN_TRY(lin::sweep(p.io_bf16, p.Dv, p.Dk, 0,
                      dots ? LIN_FAR_PAIRS : LIN_PLAIN, w, st));
@@ -621,7 +640,9 @@ hipError_t launch_linattn_backward(const LinParams &p, hipStream_t st) {
     lin::GateGrad x{seq, (const float *)(p.ws + l.late),
                     (const float *)(p.ws + l.early),
                     (const float *)(p.ws + l.pairs),
-                    (const float *)(p.ws + l.ends), p.dg,
+                    (const float *)(p.ws + l.ends),
+                    (const float *)(p.ws + l.before),
+                    (const float *)(p.ws + l.behind), p.dg,
                     p.gate_fixed ? sums : nullptr};
     const unsigned n = (unsigned)p.B * p.H * sp.NS;
     lin::kda_lin_gate_grad<<<n, 64 * lin::GATE_WAVES, 0, st>>>(

@@ -819,6 +819,38 @@ __device__ __forceinline__ void put_dots(const f32x4 (&acc)[Shape<IO>::NB],
     out[g * 16 + m] = b;
 }
 
+// magnitudes added up, or the largest
+template <bool SUM> __device__ __forceinline__ float join(float x, float y) {
+  return SUM ? x + y : fmaxf(x, y);
+}
+// of the wave's columns of a state, in every lane
+template <bool SUM, int KT>
+__device__ __forceinline__ float size_of(const f32x4 (&S)[KT]) {
+  f32x4 a{0, 0, 0, 0};
+#pragma unroll
+  for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) a[e] = join<SUM>(a[e], fabsf(S[kt][e]));
+  float v = join<SUM>(join<SUM>(a[0], a[1]), join<SUM>(a[2], a[3]));
+  v = join<SUM>(v, dpp_mov<0xB1>(v));   // as group_sum<16>
+  v = join<SUM>(v, dpp_mov<0x4E>(v));
+  v = join<SUM>(v, dpp_mov<0x124>(v));
+  v = join<SUM>(v, dpp_mov<0x128>(v));
+  const unsigned b = __float_as_uint(v);
+  const auto r = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+  v = join<SUM>(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  const unsigned d = __float_as_uint(v);
+  const auto h = __builtin_amdgcn_permlane32_swap(d, d, false, false);
+  return join<SUM>(__uint_as_float(h[0]), __uint_as_float(h[1]));
+}
+template <bool SUM, int N>
+__device__ __forceinline__ float joined(const float (&x)[N]) {
+  float v = 0.f;
+#pragma unroll
+  for (int k = 0; k < N; ++k) v = join<SUM>(v, x[k]);
+  return v;
+}
+
 // x[0][i] + x[1][i] + ..., in this order
 template <int N, int C>
 __device__ __forceinline__ float column_sum(const float (&x)[N][C], int i) {
@@ -855,6 +887,11 @@ struct Where {
     t_end = min(q.T, t_begin + q.seg);  // of the segment, dead or not
     live_end = min(len, t_end);
     nch = live_end > t_begin ? (live_end - t_begin + C - 1) / C : 0;
+  }
+  // a chunk's place in [B,H,chunks], from its first token
+  __device__ __forceinline__ size_t chunk(const LinSeq &q, int t0,
+                                          int C) const {
+    return chain * ((q.T + C - 1) / C) + t0 / C;
   }
   // first token of the n-th chunk taken
   __device__ __forceinline__ int at(int n, bool back, int C) const {
@@ -928,6 +965,7 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
   __shared__ alignas(16) frag tp[pair_frags<IO>()];
   __shared__ Decays<C> decs[2 * BATCH];
   __shared__ float far_dots[2][DOT ? COLS : 1][DOT ? C : 1];
+  __shared__ float sizes[2][DOT ? COLS : 1];
   __shared__ PairSums<DOT == LIN_FAR_PAIRS ? NB : 1> sums[2];
 
   const int lane = threadIdx.x & 63, w = wave_number();
@@ -974,9 +1012,11 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
   // a chunk's sums are put together while the next chunk's pair products are
   // made, by the wave that has least to do with those
   auto finish = [&](int n) {
-    const int t = at.at(n, REV, C) + lane;
+    const int t0 = at.at(n, REV, C), t = t0 + lane;
     if (w != NW - 1 || lane >= C || t >= at.t_end) return;
     p.far_dot[at.chain * q.T + t] = column_sum(far_dots[n & 1], lane);
+    if (lane == 0)
+      p.size[at.chunk(q, t0, C)] = joined<!REV>(sizes[n & 1]);
     if constexpr (DOT == LIN_FAR_PAIRS)
       p.pair_dot[at.chain * q.T + t] = sums[n & 1].across(lane);
   };
@@ -1025,8 +1065,10 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
         more[rt] = (acc[rt] + more[rt]) * far_w[rt * 16 + m];
         acc[rt] *= far_w[rt * 16 + m];
       }
-      if constexpr (DOT)
+      if constexpr (DOT) {
         put_dots<IO, D2>(more, td[x], col, g, m, far_dots[n & 1][w]);
+        sizes[n & 1][w] = size_of<!REV>(S);
+      }
     }
     barrier_keep_vmem();
 
@@ -1100,6 +1142,7 @@ __global__ __launch_bounds__(128 * nwaves<D>(), 4) void kda_lin_both(
   __shared__ alignas(16) frag tp[2][pair_frags<IO>()];
   __shared__ Decays<C> decs[2 * BATCH];
   __shared__ float far_dots[DOT ? COLS : 1][DOT ? C : 1];
+  __shared__ float sizes[DOT ? COLS : 1];
 
   const int lane = threadIdx.x & 63, w = wave_number();
   int g = lane >> 4, m = lane & 15;
@@ -1143,9 +1186,10 @@ __global__ __launch_bounds__(128 * nwaves<D>(), 4) void kda_lin_both(
     keeper.fetch(q, at, n0 + BATCH, w, lane);
   };
   auto finish = [&](int n) {
-    const int t = at.at(n, REV, C) + lane;
-    if (w == NW - 1 && lane < C && t < at.t_end)
-      p.early[at.chain * q.T + t] = column_sum(far_dots, lane);
+    const int t0 = at.at(n, REV, C), t = t0 + lane;
+    if (w != NW - 1 || lane >= C || t >= at.t_end) return;
+    p.early[at.chain * q.T + t] = column_sum(far_dots, lane);
+    if (lane == 0) p.size[at.chunk(q, t0, C)] = joined<false>(sizes);
   };
   const bool keep_end = at.s == 0 && p.ds0;
   // LDS addresses are made anew in each part of a chunk's work: kept over the
@@ -1195,8 +1239,10 @@ __global__ __launch_bounds__(128 * nwaves<D>(), 4) void kda_lin_both(
         more[rt] = (acc[rt] + more[rt]) * dec.last[rt * 16 + m];
         acc[rt] *= dec.last[rt * 16 + m];
       }
-      if (DOT && dk)
+      if (DOT && dk) {
         put_dots<IO, D>(more, tk[x], col, g, m, far_dots[wc]);
+        sizes[wc] = size_of<false>(S);
+      }
     }
     barrier_keep_vmem();
 

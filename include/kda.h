@@ -537,6 +537,13 @@ kda_status kda_linattn(const void *q, const void *k, const void *v,
  *   dg            shaped like g, in gate_dtype (with KDA_GATE_FIXED the sum over
  *                 all tokens), or NULL: not wanted
  *   ds0           [B,H,Dk,Dv] fp32, or NULL
+ * dg is put together from sums over chunks of 64 tokens (fp32 data: 32).  It is
+ * off by some 2^-18 of the terms of <dS, S> (the root of the sum of their
+ * squares) at the token and at the ends of the up to 64 chunks from its own on;
+ * of the latter never by more than its chunk lets through, twice exp(the
+ * chunk's sum of g) times the sum of |S| before it and the largest |dS| behind
+ * it.  So the dg of a token that forgets nearly all is accurate to the size of
+ * the others', not to its own.
  * Gradients of tokens past a sequence's length are written as zeros.  No
  * output may alias an input or another output.  A gradient is the same whether
  * dg and ds0 are wanted or not. */

@@ -1,0 +1,184 @@
+"""The gate's gradient of linear attention on the GPU where it is put together
+over many chunks: against the 64-bit formula within the bounds of
+linattn_gate_ref, which the mistakes that such sums can hold do not meet."""
+import pytest
+import torch
+
+from layer_ref import within
+from linattn_gate_ref import Parts
+
+pytestmark = pytest.mark.gpu
+BF, F = torch.bfloat16, torch.float32
+CHUNK = {BF: 64, F: 32}
+
+
+@pytest.fixture(scope="module")
+def kda():
+    import gated_delta_rule_74_amd as m
+    return m
+
+
+def inputs(B, T, Hk, H, Dk, Dv, io, kind, seed=0):
+    gen = torch.Generator().manual_seed(seed + T + 31 * Dk + Dv)
+
+    def r(*s):
+        return torch.randn(*s, generator=gen)
+
+    unit = torch.nn.functional.normalize
+    x = dict(q=unit(r(B, T, Hk, Dk), dim=-1).to(io),
+             k=unit(r(B, T, Hk, Dk), dim=-1).to(io), v=r(B, T, H, Dv).to(io),
+             s0=r(B, H, Dk, Dv))
+    x["g"] = {
+        "slow": lambda: -0.002 * torch.rand(B, T, H, generator=gen),
+        # chunks leave e^-5 to e^-10 of what is before them
+        "weak": lambda: -0.3 * torch.rand(B, T, H, generator=gen),
+        "fixed": lambda: -torch.exp2(-2.0 - 3 * torch.arange(H)),
+        "softplus": lambda: -torch.nn.functional.softplus(r(B, T, H)),
+    }[kind]()
+    return x, dict(do=r(B, T, H, Dv).to(io), dsT=r(B, H, Dk, Dv))
+
+
+def gradient(kda, x, d, times=1, lengths=None, scale=1.0):
+    """dg of heads repeated `times` over, of the first of each; the others'
+    must be the same"""
+    def many(n, t):
+        if t is None:
+            return None
+        dim = 0 if t.dim() == 1 else 1 if n in ("s0", "dsT") else 2
+        return torch.cat([t.cuda()] * times, dim).contiguous()
+
+    y = {n: many(n, t) for n, t in {**x, **d}.items()}
+    n = None if lengths is None else torch.tensor(lengths, dtype=torch.int32,
+                                                  device="cuda")
+    dg = kda.kda_linattn_backward(
+        y["q"], y["k"], y["v"], y["g"], y["do"], s0=y.get("s0"),
+        dsT=y.get("dsT"), lengths=n, scale=scale)[3]
+    H = x["v"].shape[2]
+    assert torch.equal(dg, torch.cat([dg[..., :H]] * times, -1))
+    return dg[..., :H].cpu()
+
+
+def check(kda, x, d, times=1, seg=1 << 20, lengths=None, scale=1.0,
+          norm=False):
+    """norm: also over the whole tensor, 16 half steps of the values.  A fixed
+    decay's is the sum of its tokens' values, which cancel while their errors
+    need not: a chunk's two sums are off by 2 half steps of W each, W is about
+    three times the values, and those of 65 chunks in a segment stay, sqrt(130)
+    * 2 * 3 = 68 half steps of the values' magnitudes; 2^-17 are 128."""
+    p = Parts(x, d, CHUNK[x["q"].dtype], seg,
+              None if lengths is None else torch.tensor(lengths), scale)
+    want = p.gradient()
+    got = gradient(kda, x, d, times, lengths, scale)
+    within("dg", got, want)
+    if norm and p.fixed:
+        terms = torch.stack(p.E[:p.T], 1).abs().sum((0, 1))
+        assert ((got - want[0]).abs() <= 2.0 ** -17 * terms).all()
+    elif norm:
+        assert (got - want[0]).norm() <= 2.0 ** -20 * want[0].norm()
+    return got, want
+
+
+# 600 heads of 16 or 32 fill the GPU: a sequence is one segment, of 64 chunks at
+# most
+LENGTHS = [(1, 0), (2, -1), (16, 0), (17, 5), (64, -3), (65, 0)]
+
+
+@pytest.mark.parametrize("io", [BF, F])
+@pytest.mark.parametrize("kind,chunks,over", [
+    (kind, *n) for kind in ("slow", "fixed") for n in LENGTHS] + [
+    (kind, *n) for kind in ("weak", "softplus") for n in LENGTHS[:4]])
+def test_segments_of_chunks(kda, io, kind, chunks, over):
+    C = CHUNK[io]
+    T = chunks * C + over
+    x, d = inputs(1, T, 2, 2, 16, 16 if chunks % 2 else 32, io, kind)
+    check(kda, x, d, 300, 64 * C, norm=True)
+
+
+@pytest.mark.parametrize("io", [BF, F])
+@pytest.mark.parametrize("kind", ["slow", "fixed"])
+@pytest.mark.parametrize("Dk,Dv", [(64, 64), (128, 128), (32, 128)])
+def test_segments_of_any_width(kda, io, kind, Dk, Dv):
+    x, d = inputs(1, 9 * CHUNK[io] + 7, 1, 2, Dk, Dv, io, kind)
+    check(kda, x, d, 300, norm=True)
+
+
+@pytest.mark.parametrize("io", [BF, F])
+@pytest.mark.parametrize("kind", ["slow", "fixed"])
+@pytest.mark.parametrize("T", [577, 900, 1500])
+def test_short_segments(kda, io, kind, T):
+    """few heads: a segment is a chunk or two"""
+    x, d = inputs(1, T, 1, 2, 32, 32, io, kind)
+    check(kda, x, d, norm=True)
+
+
+@pytest.mark.parametrize("io", [BF, F])
+@pytest.mark.parametrize("kind", ["slow", "weak", "fixed"])
+def test_ragged_segments(kda, io, kind):
+    """lengths at and beside chunks' ends, of sequences of one segment each"""
+    C = CHUNK[io]
+    T = 20 * C
+    n = [T, T - 1, 16 * C, 16 * C + 1, 5 * C - 1, 1, 0, T + 9]
+    x, d = inputs(len(n), T, 1, 1, 16, 16, io, kind)
+    got, _ = check(kda, x, d, 80, lengths=n)
+    if kind != "fixed":
+        for b, m in enumerate(n):
+            assert (got[b, m:] == 0).all()
+
+
+@pytest.mark.parametrize("io", [BF, F])
+@pytest.mark.parametrize("times", [1, 300])
+@pytest.mark.parametrize("g0", [-5.0, -10.0, -16.0, -20.0, -27.0, -60.0])
+@pytest.mark.parametrize("later", [1.0, 1000.0])
+def test_one_token_that_forgets(kda, io, times, g0, later):
+    """a token that forgets nearly all among some that forget little, as a new
+    document in a packed row; with gradients that are larger behind it"""
+    x, d = inputs(1, 512, 1, 2, 16, 16, io, "slow", seed=1)
+    x["g"][:, 300] = g0
+    d["do"][:, 300:] = (later * d["do"][:, 300:].float()).to(io)
+    d["dsT"] *= later
+    check(kda, x, d, times)
+
+
+@pytest.mark.parametrize("io", [BF, F])
+@pytest.mark.parametrize("times", [1, 300])
+@pytest.mark.parametrize("g", [-0.2, -0.02])
+def test_a_loss_on_the_last_tokens(kda, io, times, g):
+    """a prompt without a loss: gradients decay from its end on, in long
+    segments far below what they begin with; the sum over all tokens, of a
+    fixed decay, has no more of them than there is"""
+    C = CHUNK[io]
+    T = 40 * C + 3
+    x, d = inputs(1, T, 1, 2, 16, 16, io, "slow", seed=2)
+    x["g"] = torch.full_like(x["g"], g)
+    d["do"][:, :-8] = 0
+    d["dsT"] = None
+    got, (want, _) = check(kda, x, d, times)
+    if g == -0.2:
+        assert (got[0, :20 * C].abs() < 1e-30).all()
+    total = want.sum((0, 1))
+    x["g"] = torch.full((2,), g)
+    fixed, (want, _) = check(kda, x, d, times)
+    torch.testing.assert_close(want, total, rtol=1e-9, atol=0)
+    # as in check: of the sum of the values' magnitudes
+    assert ((fixed - want).abs() <= 2.0 ** -17 * got.abs().sum((0, 1))).all()
+
+
+@pytest.mark.parametrize("io", [BF, F])
+def test_a_state_that_is_nothing(kda, io):
+    """no first state and a first token that forgets: nothing crosses it"""
+    x, d = inputs(1, 200, 1, 2, 32, 32, io, "slow", seed=3)
+    x["s0"] = None
+    x["g"][:, 0] = -float("inf")
+    got, _ = check(kda, x, d)
+    assert (got[:, 0] == 0).all()
+
+
+@pytest.mark.parametrize("io", [BF, F])
+@pytest.mark.parametrize("big", [1e-12, 1e12])
+def test_states_of_any_size(kda, io, big):
+    """squares of states far from 1, and of gradients as far the other way"""
+    x, d = inputs(1, 700, 1, 2, 32, 32, io, "slow", seed=4)
+    x["v"], x["s0"] = (x["v"].float() * big).to(io), x["s0"] * big
+    d["do"] = (d["do"].float() / big).to(io)
+    d["dsT"] = d["dsT"] / big
+    check(kda, x, d, 300)
