@@ -511,10 +511,14 @@ size_t kda_linattn_backward_workspace_size(int B, int T, int Hk, int H, int Dk,
  *            s0
  * With bf16 data o is, before its own rounding, within 2^-17 of its terms'
  * magnitudes; what is written in fp32 is as with fp32 data.  Terms that have
- * decayed below 2^-200 may count as none.  Values are not checked: an infinity or
- * NaN in q, k or v may also reach the outputs of up to 63 tokens before it
- * (those of its chunk: 0 * inf in the matrix products), never those of another
- * sequence or head.
+ * decayed below 2^-200 may count as none.  Values are not checked.  An infinity
+ * or NaN in q, k, v or s0 reaches
+ *   - through the state every later token of its sequence and head; a g of -inf
+ *     does not clear it (0 * inf is NaN)
+ *   - the outputs of up to 63 tokens before it (those of its chunk: 0 * inf in
+ *     the matrix products)
+ *   - where it is in q or k, all the value heads that share them
+ * and no other sequence or head.
  * Errors: KDA_EINVAL as elsewhere and for H not a multiple of Hk;
  * KDA_EUNSUPPORTED for other Dk, Dv or dtype pairs, T > 2^30,
  * H * max(Dk,Dv) > 2^22, B * T * H * max(Dk,Dv) > 2^34, or
@@ -544,6 +548,10 @@ kda_status kda_linattn(const void *q, const void *k, const void *v,
  * chunk's sum of g) times the sum of |S| before it and the largest |dS| behind
  * it.  So the dg of a token that forgets nearly all is accurate to the size of
  * the others', not to its own.
+ * An infinity or NaN in an input may reach every gradient of its sequence and
+ * of the value heads that have it, and the dq and dk that these share with
+ * others, but no other sequence's or head's (a fixed decay's dg has all
+ * sequences).
  * Gradients of tokens past a sequence's length are written as zeros.  No
  * output may alias an input or another output.  A gradient is the same whether
  * dg and ds0 are wanted or not. */
