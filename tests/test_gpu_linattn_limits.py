@@ -1,9 +1,12 @@
 """What include/kda.h says of linear attention at the ends of its range: where
-an infinity or NaN goes."""
+an infinity or NaN goes, and from where on a decayed term may be nothing."""
 import math
 
 import pytest
 import torch
+
+import linattn_ref as ref
+from layer_ref import U, within
 
 pytestmark = pytest.mark.gpu
 BF, F = torch.bfloat16, torch.float32
@@ -106,3 +109,29 @@ def test_where_a_bad_value_goes_in_the_gradients(kda, io, Hk, name):
     # what a gradient of the last state reaches is every token's
     if name == "dsT":
         assert bad[3][1, :, 3].isnan().all()
+
+
+@pytest.mark.parametrize("io", [BF, F])
+@pytest.mark.parametrize("T", [2, 40, 64, 130, 700])
+@pytest.mark.parametrize("where", ["one", "all"])
+def test_decayed_terms_stay_down_to_the_limit(kda, io, T, where):
+    """a term of 2^100 decayed by 2^-125, by one gate or all of them, keeps its
+    bits (4 u a chunk, and the argument of the exponential is rounded by 63 u
+    of its 125 ln 2 once)"""
+    x = {n: torch.zeros(1, T, 1, 16, dtype=io) for n in "qkv"}
+    x["k"][0, 0, 0, 3], x["v"][0, 0, 0, 5] = 2.0 ** 50, 2.0 ** 50
+    x["q"][0, T - 1, 0, 3] = 1.0
+    x["g"] = torch.zeros(1, T, 1)
+    ln = -125 * math.log(2.0)
+    if where == "one":
+        x["g"][0, T // 2] = ln
+    else:
+        x["g"][0, 1:] = ln / (T - 1)
+    want = ref.linattn(**x)
+    o, s = kda.kda_linattn(*[t.cuda() for t in x.values()])
+    slack = (64 + 4 * -(-T // 32)) * U
+    for n, t in (("o", o), ("s", s)):
+        w = want[n][0]
+        assert (w != 0).any()
+        r = 2.0 ** -17 if n == "o" and io == BF else 0
+        within(n, t, (w, (slack + r) * w.abs()))
