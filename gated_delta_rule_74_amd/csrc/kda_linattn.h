@@ -70,6 +70,11 @@ struct LinSweep {
   float *size;                // [B,H,chunks]: of the state before (reversed:
                               // behind) the chunk, the sum of its magnitudes
                               // (reversed: the largest)
+  float *marks;               // [B,H,NS,marks,D1*D2]: the state's gradient at
+                              // a segment's marks (reversed: written)
+  float *mark_e;              // [B,H,NS,marks]: <state, gradient> there, NaN
+                              // where it has not been read (reversed: whether
+                              // it has been written)
   const float *e_with;        // laid out as s_in, or null (zeros)
   float *e_out;               // [B,H,NS]: <state behind the segment, e_with>
 };
@@ -85,6 +90,7 @@ struct LinBoth {
   float *ds0;                 // [B,H,D,D] or null
   float *early;               // [B,H,T]
   float *size;                // [B,H,chunks]: the largest of |dS| behind it
+  float *marks, *mark_e;      // as LinSweep's
 };
 
 // the state that each segment adds to a zero one
@@ -99,6 +105,12 @@ struct LinLocal {
 
 // chunk of a sweep
 constexpr int lin_chunk(int io_bf16) { return io_bf16 ? 64 : 32; }
+// Marks lie before every LIN_MARK-th chunk of a segment but its first: there the
+// product of the state and its gradient is made anew for the gate's gradient, if
+// the chunk before leaves more than LIN_MARK_MIN of what comes to it.
+constexpr int LIN_MARK = 8;
+constexpr float LIN_MARK_MIN = 0x1p-24f;
+constexpr int lin_marks(int chunks) { return (chunks - 1) / LIN_MARK; }
 
 // variants of a sweep
 enum LinDot { LIN_PLAIN = 0, LIN_FAR = 1, LIN_FAR_PAIRS = 2 };

@@ -16,7 +16,9 @@
 // from t on), j alone (far_dot of dk's, summed up to t), neither (Z).  With E
 // the sum over the pairs across a chunk's end, Z = E - sum of the chunk's
 // j-terms, and E across its start is Z + sum of its i-terms; E at a segment's
-// end is the product of both states there.  That is a difference of rounded
+// end, and at its marks (kda_linattn.h), is the product of both states there (the
+// gradient's is written by the sweep of dk and read by dq's), as what E is off
+// would add up over 64 chunks.  From there on it is a difference of rounded
 // sums: where a chunk forgets much, or the tokens behind have the larger
 // gradients, what E is off (some 2^-24 of what it was) can be more than Z is.
 // But with S before and dS behind the chunk |Z| is at most exp(G) times the sum
@@ -40,7 +42,8 @@ namespace lin {
 constexpr size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 struct Split {
-  int NS, seg, chunks;  // segments, tokens of each, chunks of the sequence
+  int NS, seg;      // segments, tokens of each
+  int per, chunks;  // chunks of a segment, of the sequence
 };
 
 // Segments are as many as fill the GPU once, in whole rounds of workgroups: 256
@@ -68,7 +71,7 @@ Split split(int B, int T, int H, int D, int io_bf16, bool grad) {
   if (!grad && nc <= 4) per = nc;
   while (64ll * per * per < nc) ++per;
   if (grad && per > MAX_CHUNKS) per = MAX_CHUNKS;
-  return Split{(nc + per - 1) / per, per * C, nc};
+  return Split{(nc + per - 1) / per, per * C, per, nc};
 }
 
 // ---------------------------------------------------------------------------
@@ -123,6 +126,7 @@ struct GateGrad {
   const float *late, *early, *pairs;  // [B,H,T]
   const float *ends;                  // [B,H,NS]
   const float *before, *behind;       // [B,H,chunks]: sum |S|, max |dS|
+  const float *marks, *wrote;         // [B,H,NS,marks]: E anew, or NaN; if
   void *dg;                           // [B,T,H] in the gate's type
   double *sums;                       // [B,H,NS] instead, for a fixed decay
 };
@@ -135,7 +139,7 @@ __device__ __forceinline__ float off2(float x) { return (OFF * x) * (OFF * x); }
 __global__ __launch_bounds__(64 * GATE_WAVES) void kda_lin_gate_grad(
     GateGrad p, int C) {
   __shared__ double sum_late[MAX_CHUNKS], sum_early[MAX_CHUNKS];
-  __shared__ float most[MAX_CHUNKS], both[MAX_CHUNKS];
+  __shared__ float most[MAX_CHUNKS], both[MAX_CHUNKS], anew[MAX_CHUNKS];
   __shared__ double totals[GATE_WAVES];
   const LinSeq &q = p.q;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
@@ -179,6 +183,13 @@ __global__ __launch_bounds__(64 * GATE_WAVES) void kda_lin_gate_grad(
     if (lane == 0) {
       sum_late[c] = x;
       sum_early[c] = y;
+      // a mark at the end of the chunk that has been written and read
+      anew[c] = NAN;
+      if ((c + 1) % LIN_MARK == 0 && t_begin + (c + 1) * C < live_end) {
+        const size_t i = (chain * q.NS + s) * lin_marks(q.seg / C) +
+                         (c + 1) / LIN_MARK - 1;
+        if (p.wrote[i] != 0.f) anew[c] = p.marks[i];
+      }
       // the most that Z can be: exp and the sums are off by less than 2^-8
       most[c] = !alive ? INFINITY
                 : G < -87.f ? 0.f : expf(G) * 0x1.01p0f * S * dS;
@@ -194,6 +205,10 @@ __global__ __launch_bounds__(64 * GATE_WAVES) void kda_lin_gate_grad(
     for (int c = nch - 1; c >= 0; --c) {
       const double x = sum_late[c], y = sum_early[c];
       const float cap = most[c];
+      if (anew[c] == anew[c]) {
+        E = anew[c];
+        off = off2(anew[c]);
+      }
       double Z = E - y;
       off += off2((float)y);
       Z = Z > cap ? cap : Z < -cap ? -cap : Z;
@@ -463,8 +478,8 @@ LinSeq seq_of(const LinParams &p, Split sp) {
 
 // the workspace, part by part
 struct Layout {
-  size_t s, ds, decay, ddecay, late, early, pairs, ends, before, behind, sums,
-      dq, dk, bytes;
+  size_t s, ds, decay, ddecay, late, early, pairs, ends, before, behind, marks,
+      mark_e, wrote, sums, dq, dk, bytes;
 };
 Layout layout(int B, int T, int Hk, int H, int Dk, int Dv, Split sp,
               bool grad) {
@@ -489,6 +504,10 @@ Layout layout(int B, int T, int Hk, int H, int Dk, int Dv, Split sp,
     l.ends = take(segs * 4);
     l.before = take(chains * sp.chunks * 4);
     l.behind = take(chains * sp.chunks * 4);
+    const size_t marks = segs * lin_marks(sp.per);
+    l.marks = take(marks * Dk * Dv * 4);
+    l.mark_e = take(marks * 4);
+    l.wrote = take(marks * 4);
     l.sums = take(segs * 8);
     const size_t part = H != Hk ? rows * Dk : 0;
     l.dq = take(part);
@@ -587,6 +606,8 @@ hipError_t launch_linattn_backward(const LinParams &p, hipStream_t st) {
     z.ds_in = ds_in; z.ds0 = p.ds0;
     z.early = early;
     z.size = (float *)(p.ws + l.behind);
+    z.marks = (float *)(p.ws + l.marks);
+    z.mark_e = (float *)(p.ws + l.wrote);
     LIN_TRY(lin::both(p.io_bf16, p.Dk, dots, z, st));
   } else {
     // dv
@@ -604,6 +625,8 @@ hipError_t launch_linattn_backward(const LinParams &p, hipStream_t st) {
     w.s_transposed = 1;
     w.far_dot = early;
     w.size = (float *)(p.ws + l.behind);
+    w.marks = (float *)(p.ws + l.marks);
+    w.mark_e = (float *)(p.ws + l.wrote);
     LIN_TRY(lin::sweep(p.io_bf16, p.Dv, p.Dk, 1, dots ? LIN_FAR : LIN_PLAIN,
                        w, st));
   }
@@ -621,6 +644,8 @@ hipError_t launch_linattn_backward(const LinParams &p, hipStream_t st) {
   w.far_dot = (float *)(p.ws + l.late);
   w.pair_dot = (float *)(p.ws + l.pairs);
   w.size = (float *)(p.ws + l.before);
+  w.marks = (float *)(p.ws + l.marks);
+  w.mark_e = (float *)(p.ws + l.mark_e);
   w.e_out = (float *)(p.ws + l.ends);
   LIN_TRY(lin::sweep(p.io_bf16, p.Dv, p.Dk, 0,
                      dots ? LIN_FAR_PAIRS : LIN_PLAIN, w, st));
@@ -642,7 +667,9 @@ hipError_t launch_linattn_backward(const LinParams &p, hipStream_t st) {
                     (const float *)(p.ws + l.pairs),
                     (const float *)(p.ws + l.ends),
                     (const float *)(p.ws + l.before),
-                    (const float *)(p.ws + l.behind), p.dg,
+                    (const float *)(p.ws + l.behind),
+                    (const float *)(p.ws + l.mark_e),
+                    (const float *)(p.ws + l.wrote), p.dg,
                     p.gate_fixed ? sums : nullptr};
     const unsigned n = (unsigned)p.B * p.H * sp.NS;
     lin::kda_lin_gate_grad<<<n, 64 * lin::GATE_WAVES, 0, st>>>(

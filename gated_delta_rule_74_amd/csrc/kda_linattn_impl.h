@@ -851,6 +851,16 @@ __device__ __forceinline__ float joined(const float (&x)[N]) {
   return v;
 }
 
+// The wave's columns of a state at a mark, as they lie in the registers: 16
+// bytes a lane and tile
+template <int KT>
+__device__ __forceinline__ void put_mark(const f32x4 (&S)[KT], float *p, int w,
+                                         int lane) {
+#pragma unroll
+  for (int kt = 0; kt < KT; ++kt)
+    st_stream(p + ((w * KT + kt) * 64 + lane) * 4, S[kt]);
+}
+
 // x[0][i] + x[1][i] + ..., in this order
 template <int N, int C>
 __device__ __forceinline__ float column_sum(const float (&x)[N][C], int i) {
@@ -887,6 +897,13 @@ struct Where {
     t_end = min(q.T, t_begin + q.seg);  // of the segment, dead or not
     live_end = min(len, t_end);
     nch = live_end > t_begin ? (live_end - t_begin + C - 1) / C : 0;
+  }
+  // the mark before the segment's n-th chunk, in [B,H,NS,marks]
+  __device__ __forceinline__ static bool marked(int n) {
+    return n > 0 && n % LIN_MARK == 0;
+  }
+  __device__ __forceinline__ size_t mark(const LinSeq &q, int n, int C) const {
+    return (chain * q.NS + s) * lin_marks(q.seg / C) + n / LIN_MARK - 1;
   }
   // a chunk's place in [B,H,chunks], from its first token
   __device__ __forceinline__ size_t chunk(const LinSeq &q, int t0,
@@ -965,7 +982,7 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
   __shared__ alignas(16) frag tp[pair_frags<IO>()];
   __shared__ Decays<C> decs[2 * BATCH];
   __shared__ float far_dots[2][DOT ? COLS : 1][DOT ? C : 1];
-  __shared__ float sizes[2][DOT ? COLS : 1];
+  __shared__ float sizes[2][DOT ? COLS : 1], across[2][DOT ? COLS : 1];
   __shared__ PairSums<DOT == LIN_FAR_PAIRS ? NB : 1> sums[2];
 
   const int lane = threadIdx.x & 63, w = wave_number();
@@ -1009,14 +1026,24 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
                 REV ? p.far_scale : p.add_scale, w, lane);
     keeper.fetch(q, at, n0 + BATCH, w, lane);
   };
+  // whether the mark behind a chunk is
+  auto wanted = [&](int n) {
+    return decs[n % (2 * BATCH)].total > LIN_MARK_MIN;
+  };
   // a chunk's sums are put together while the next chunk's pair products are
   // made, by the wave that has least to do with those
   auto finish = [&](int n) {
     const int t0 = at.at(n, REV, C), t = t0 + lane;
     if (w != NW - 1 || lane >= C || t >= at.t_end) return;
     p.far_dot[at.chain * q.T + t] = column_sum(far_dots[n & 1], lane);
-    if (lane == 0)
+    if (lane == 0) {
       p.size[at.chunk(q, t0, C)] = joined<!REV>(sizes[n & 1]);
+      if (REV && at.marked(nch - n) && n > 0)
+        p.mark_e[at.mark(q, nch - n, C)] = wanted(n) ? 1.f : 0.f;
+      if (!REV && at.marked(n))
+        p.mark_e[at.mark(q, n, C)] =
+            wanted(n - 1) ? joined<true>(across[n & 1]) : NAN;
+    }
     if constexpr (DOT == LIN_FAR_PAIRS)
       p.pair_dot[at.chain * q.T + t] = sums[n & 1].across(lane);
   };
@@ -1037,8 +1064,20 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
   for (int n = 0; n < nch; ++n) {
     const int t0 = at.at(n, REV, C), x = TWO ? n & 1 : 0;
     const Decays<C> &dec = decs[n % (2 * BATCH)];
-    // loads come back in their order: gates are asked for before the rows of a
-    // chunk, and used four chunks later
+    uint4 marked[KT];  // where there is no mark, nothing is read
+    if constexpr (DOT == LIN_FAR_PAIRS) {
+      int bytes = 0;
+      if (at.marked(n))
+        bytes = __builtin_amdgcn_readfirstlane(
+            mine && wanted(n - 1) ? D1 * D2 * 4 : 0);
+      const auto r =
+          buffer(p.marks + (bytes ? at.mark(q, n, C) : 0) * (D1 * D2), bytes);
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt)
+        marked[kt] = load16(r, ((w * KT + kt) * 64 + lane) * 16);
+    }
+    // loads come back in their order: these and gates are asked for before the
+    // rows of a chunk, and gates used four chunks later
     if (n % BATCH == BATCH - 1) make_decays(n + 1);
     if constexpr (TWO) {
       stash(x ^ 1);
@@ -1068,6 +1107,24 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
       if constexpr (DOT) {
         put_dots<IO, D2>(more, td[x], col, g, m, far_dots[n & 1][w]);
         sizes[n & 1][w] = size_of<!REV>(S);
+      }
+      if constexpr (DOT == LIN_FAR) {
+        if (at.marked(nch - n) && n > 0 && wanted(n))
+          put_mark(S, p.marks + at.mark(q, nch - n, C) * (D1 * D2), w, lane);
+      }
+      if constexpr (DOT == LIN_FAR_PAIRS) {
+        if (at.marked(n)) {
+          float v = 0.f;
+#pragma unroll
+          for (int kt = 0; kt < KT; ++kt) {
+            const f32x4 y = __builtin_bit_cast(f32x4, marked[kt]);
+            v += (S[kt][0] * y[0] + S[kt][1] * y[1]) +
+                 (S[kt][2] * y[2] + S[kt][3] * y[3]);
+          }
+          v = group_sum<16>(v);
+          v = add_rows(v, v);
+          across[n & 1][w] = add_halves(v, v);
+        }
       }
     }
     barrier_keep_vmem();
@@ -1185,11 +1242,18 @@ __global__ __launch_bounds__(128 * nwaves<D>(), 4) void kda_lin_both(
     keeper.make(q, decs, at, n0, p.scale, 1.f, w, lane);
     keeper.fetch(q, at, n0 + BATCH, w, lane);
   };
+  auto wanted = [&](int n) {
+    return decs[n % (2 * BATCH)].total > LIN_MARK_MIN;
+  };
   auto finish = [&](int n) {
     const int t0 = at.at(n, REV, C), t = t0 + lane;
     if (w != NW - 1 || lane >= C || t >= at.t_end) return;
     p.early[at.chain * q.T + t] = column_sum(far_dots, lane);
-    if (lane == 0) p.size[at.chunk(q, t0, C)] = joined<false>(sizes);
+    if (lane == 0) {
+      p.size[at.chunk(q, t0, C)] = joined<false>(sizes);
+      if (at.marked(nch - n) && n > 0)
+        p.mark_e[at.mark(q, nch - n, C)] = wanted(n) ? 1.f : 0.f;
+    }
   };
   const bool keep_end = at.s == 0 && p.ds0;
   // LDS addresses are made anew in each part of a chunk's work: kept over the
@@ -1242,6 +1306,9 @@ __global__ __launch_bounds__(128 * nwaves<D>(), 4) void kda_lin_both(
       if (DOT && dk) {
         put_dots<IO, D>(more, tk[x], col, g, m, far_dots[wc]);
         sizes[wc] = size_of<false>(S);
+        if (at.marked(nch - n) && n > 0 && wanted(n))
+          put_mark(S, p.marks + at.mark(q, nch - n, C) * (D * D), wc,
+                   g * 16 + m);
       }
     }
     barrier_keep_vmem();

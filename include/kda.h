@@ -542,12 +542,13 @@ kda_status kda_linattn(const void *q, const void *k, const void *v,
  *                 all tokens), or NULL: not wanted
  *   ds0           [B,H,Dk,Dv] fp32, or NULL
  * dg is put together from sums over chunks of 64 tokens (fp32 data: 32).  It is
- * off by some 2^-18 of the terms of <dS, S> (the root of the sum of their
- * squares) at the token and at the ends of the up to 64 chunks from its own on;
- * of the latter never by more than its chunk lets through, twice exp(the
- * chunk's sum of g) times the sum of |S| before it and the largest |dS| behind
- * it.  So the dg of a token that forgets nearly all is accurate to the size of
- * the others', not to its own.
+ * off by at most some 2^-18 of the terms of <dS, S> (the root of the sum of
+ * their squares) at the token and at the ends of the chunks from its own on, up
+ * to 8 of them or as far as they let through more than 2^-24; of the latter
+ * never by more than its own chunk lets through, twice exp(the chunk's sum of g)
+ * times the sum of |S| before it and the largest |dS| behind it.  So the dg of a
+ * token that forgets nearly all is accurate to the size of the others', not to
+ * its own.
  * An infinity or NaN in an input may reach every gradient of its sequence and
  * of the value heads that have it, and the dq and dk that these share with
  * others, but no other sequence's or head's (a fixed decay's dg has all

@@ -12,7 +12,8 @@ that they add up by their squares: to K W, with
 (o element by element, N and M the recurrences of dS and S over squares: the
 roots of the sums of squares of the elements' and of the pairs' products) and K
 = 2^-18, 64 half steps: a state is rounded 4 times a chunk, over 64 chunks 16
-half steps in the mean of squares; four times that.
+half steps in the mean of squares; four times that.  (The sums begin anew every
+8 chunks, which these bounds need not know.)
 
 Z, the pairs around a whole chunk, is what is across its end less what reaches
 into it, and the next chunk's E is what Z and the chunk's own make: each is off

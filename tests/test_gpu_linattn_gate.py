@@ -4,7 +4,7 @@ linattn_gate_ref, which the mistakes that such sums can hold do not meet."""
 import pytest
 import torch
 
-from layer_ref import within
+from layer_ref import U, within
 from linattn_gate_ref import Parts
 
 pytestmark = pytest.mark.gpu
@@ -62,17 +62,19 @@ def check(kda, x, d, times=1, seg=1 << 20, lengths=None, scale=1.0,
           norm=False):
     """norm: also over the whole tensor, 16 half steps of the values.  A fixed
     decay's is the sum of its tokens' values, which cancel while their errors
-    need not: a chunk's two sums are off by 2 half steps of W each, W is about
-    three times the values, and those of 65 chunks in a segment stay, sqrt(130)
-    * 2 * 3 = 68 half steps of the values' magnitudes; 2^-17 are 128."""
+    need not: a chunk's two sums are off by 2 half steps of W at its ends each,
+    and those of 8 chunks stay until the product of the states is made anew,
+    sqrt(16) * 2 = 8 half steps of the largest W that far for every token."""
     p = Parts(x, d, CHUNK[x["q"].dtype], seg,
               None if lengths is None else torch.tensor(lengths), scale)
     want = p.gradient()
     got = gradient(kda, x, d, times, lengths, scale)
     within("dg", got, want)
     if norm and p.fixed:
-        terms = torch.stack(p.E[:p.T], 1).abs().sum((0, 1))
-        assert ((got - want[0]).abs() <= 2.0 ** -17 * terms).all()
+        ends = [*range(0, p.T, p.C), p.T]
+        W = sum((b - a) * torch.stack([p.W[e] for e in ends[i:i + 9]]).amax(0)
+                for i, (a, b) in enumerate(zip(ends, ends[1:])))
+        assert ((got - want[0]).abs() <= 8 * U * W.sum(0)).all()
     elif norm:
         assert (got - want[0]).norm() <= 2.0 ** -20 * want[0].norm()
     return got, want
@@ -157,10 +159,8 @@ def test_a_loss_on_the_last_tokens(kda, io, times, g):
         assert (got[0, :20 * C].abs() < 1e-30).all()
     total = want.sum((0, 1))
     x["g"] = torch.full((2,), g)
-    fixed, (want, _) = check(kda, x, d, times)
+    _, (want, _) = check(kda, x, d, times, norm=True)
     torch.testing.assert_close(want, total, rtol=1e-9, atol=0)
-    # as in check: of the sum of the values' magnitudes
-    assert ((fixed - want).abs() <= 2.0 ** -17 * got.abs().sum((0, 1))).all()
 
 
 @pytest.mark.parametrize("io", [BF, F])
