@@ -26,11 +26,13 @@
 // the range of fp32): what is over that is taken off, and where that is less
 // than E may be off, Z counts as 0, so that nothing of it is carried on.
 //
-// Measured at B1 T8192 H32 D128, bf16: forward 102 us, of which the local pass
-// 28, the scan 8 and the sweep 64 (450 MB in all at 4.4 TB/s: HBM, and the
-// latency between the two halves of a chunk's work); gradient 260 us, of which
-// local passes 23, scan 16, dk and dv 116, dq 111, the gate 9 (LDS reads, as
-// every wave reads whole tiles, and the same latency).
+// Measured at B1 T8192 H32 D128, bf16: forward 117 us, under the profiler local
+// pass 35, scan 9 and sweep 81 (450 MB in all at 3.8 TB/s: the latency between
+// the two halves of a chunk's work, and the parts of bf16 operands); gradient
+// 314 us, local passes 30, scan 16, dk and dv 163, dq 137, the gate 12 (the
+// same, and LDS reads, as every wave reads whole tiles).  With
+// operands in two parts or one (102 and 260 us) results were off by half as much
+// again as their own rounding, and states by 2.4e-6.
 #include <algorithm>
 
 #include "kda_linattn.h"
@@ -47,17 +49,19 @@ struct Split {
 };
 
 // Segments are as many as fill the GPU once, in whole rounds of workgroups: 256
-// of 8 waves at D = 128, one per CU (8192 tokens of 32 heads, forward: 102 us
-// with 256, 118 with 512, as every segment more is a state to write, scan and
-// read; 36 heads: 40 us with 216 workgroups, 48 with 288), 512 of at most 4
-// waves below (8192 tokens of 32 heads of 64: 46 us, 52 with 768).  Against
-// that:
-//  - The forward pass of up to 4 chunks stays in one launch (B1 T200 H32: 16
-//    us, split 20); five gain (T320 H4: 15.5 us, 18), and so do two of the
-//    gradient.
-//  - A chunk more in a segment costs both passes 4.5 us, a segment more costs
+// of 8 waves at D = 128, one per CU (8192 tokens of 32 heads, forward: 114 us
+// with 256, 129 with 512, as every segment more is a state to write, scan and
+// read, 186 with 128; 36 heads of 1531: 44 us with 216 workgroups, 54 with 288),
+// 512 of at most 4 waves below (8192 tokens of 32 heads of 64: 51 us, 53 with
+// 704, 64 with 256).  Against that:
+//  - The forward pass of up to 4 chunks stays in one launch (T200: 32 heads 19.5
+//    us, split 22; 4 heads 18.4 and 19.4); five or six gain (T320 H4: 19 us
+//    split, 22 in one; T384 H32 23.5 and 26).  The gradient's of two gain with
+//    few heads (4: 39 us split, 41 in one; 32 have 47 and 42), three with 32
+//    (48 and 55).
+//  - A chunk more in a segment costs both passes some 5 us, a segment more costs
 //    the scan 0.25: not more than 8 sqrt(chunks) segments (fp32 4096 tokens of
-//    4 heads: 21 us with 64, 26 with 128, 24 with 43).
+//    4 heads of 128: 39 us with 64, 49 with 128, 39 with 43, 47 with 32).
 //  - The sums of kda_lin_gate_grad hold a segment of MAX_CHUNKS.
 constexpr int WORKGROUPS = 256, MAX_CHUNKS = 64;
 
@@ -152,6 +156,7 @@ __global__ __launch_bounds__(64 * GATE_WAVES) void kda_lin_gate_grad(
   const int live_end = min(len, t_end);
   const int nch = (t_end - t_begin + C - 1) / C;  // at most MAX_CHUNKS
   const size_t chunk0 = chain * ((q.T + C - 1) / C) + t_begin / C;
+  const size_t mark0 = (chain * q.NS + s) * lin_marks(q.seg / C);
   float late, early, pairs, g;
   auto load = [&](int c) {
     const int t = t_begin + c * C + lane;
@@ -172,6 +177,11 @@ __global__ __launch_bounds__(64 * GATE_WAVES) void kda_lin_gate_grad(
     const bool alive = t_begin + c * C < live_end;
     const float S = alive ? p.before[chunk0 + c] : 0.f;
     const float dS = alive ? p.behind[chunk0 + c] : 0.f;
+    // a mark at the end of the chunk, if it has been written and read
+    const bool mark = (c + 1) % LIN_MARK == 0 &&
+                      t_begin + (c + 1) * C < live_end;
+    const size_t m = mark0 + c / LIN_MARK;
+    const float wrote = mark ? p.wrote[m] : 0.f, E = mark ? p.marks[m] : NAN;
     double x = late, y = early;
     float G = g;
 #pragma unroll
@@ -183,13 +193,7 @@ __global__ __launch_bounds__(64 * GATE_WAVES) void kda_lin_gate_grad(
     if (lane == 0) {
       sum_late[c] = x;
       sum_early[c] = y;
-      // a mark at the end of the chunk that has been written and read
-      anew[c] = NAN;
-      if ((c + 1) % LIN_MARK == 0 && t_begin + (c + 1) * C < live_end) {
-        const size_t i = (chain * q.NS + s) * lin_marks(q.seg / C) +
-                         (c + 1) / LIN_MARK - 1;
-        if (p.wrote[i] != 0.f) anew[c] = p.marks[i];
-      }
+      anew[c] = wrote != 0.f ? E : NAN;
       // the most that Z can be: exp and the sums are off by less than 2^-8
       most[c] = !alive ? INFINITY
                 : G < -87.f ? 0.f : expf(G) * 0x1.01p0f * S * dS;

@@ -276,7 +276,7 @@ __device__ __forceinline__ double add_dpp(double x) {
 
 // The decays of up to 4 chunks are made at a time, a chunk by each wave: made
 // one by one ahead of their chunk, by one wave while the others work, they kept
-// the others waiting (4 of the local pass's 40 us at B1 T8192 H32 D128).  Of 2
+// the others waiting (4 us of the local pass at B1 T8192 H32 D128).  Of 2
 // in kda_lin_both, whose LDS holds no more.
 constexpr int BATCH = 4;
 
@@ -608,7 +608,7 @@ template <typename IO> struct PairSet {
 // i to the border next to j's tile, one a lane, times that from there to j.
 // D2 > 0: also the sums over the pairs' products with c_j . d_i.  The units go
 // side by side, in the same code for all waves (a branch for each unit let
-// nothing overlap: 24 of the 144 us of kda_lin_both at B1 T8192 H32 D128).
+// nothing overlap: 24 us of kda_lin_both at B1 T8192 H32 D128).
 template <typename IO, int D1, int D2, bool REV, int NW, int K, int SETS>
 __device__ __forceinline__ void pair_batch(
     const PairSet<IO> (&sets)[SETS], const Decays<Shape<IO>::C> &dec,
@@ -723,7 +723,7 @@ __device__ __forceinline__ f32x4 rest4(f32x4 v, uint2 r) {
 // lower tile where g is odd (8 bytes a lane: 4 us more at B1 T8192 H32 D128);
 // REST: what rounding leaves goes to a second tensor, if there is one.  (With
 // stores to nothing in the place of that branch, which is the same for a whole
-// wave, the gradient of B1 T8192 H32 D128 took 269 us, not 263.)
+// wave, the gradient of B1 T8192 H32 D128 took 6 us more.)
 template <typename IO, int D, bool REST>
 __device__ __forceinline__ void put_out(f32x4 (&acc)[Shape<IO>::NB], void *out,
                                         void *rest, size_t at, int H, int rows,
@@ -873,10 +873,10 @@ __device__ __forceinline__ float column_sum(const float (&x)[N][C], int i) {
 // waves of a workgroup whose output is D2 wide
 template <int D2> constexpr int nwaves() { return D2 == 128 ? 8 : 4; }
 // Whether a sweep has two sets of LDS tiles.  The one workgroup of D = 128 that
-// a CU has gains by it (B1 T8192 H32: 114 us without, 107 with); with fewer
-// waves other workgroups on the CU fill the wait as well, and the second set
-// keeps them off it (gradient of B8 T4096 H32 D64: 497 us without, 768 with;
-// D32 380 and 396).
+// a CU has gains by it (B1 T8192 H32: 124 us without, 119 with; gradient 329 and
+// 320); with fewer waves other workgroups on the CU fill the wait as well, and
+// the second set keeps them off it (gradient of B8 T4096 H32 D64: 509 us without,
+// 698 with; D32 382 and 388).
 template <int NW> constexpr bool two_sets() { return NW == 8; }
 
 // where a workgroup's segment is
@@ -1181,7 +1181,8 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
 // tensors, and the two states (one the other's transpose) come from the same
 // rows.  Half of the waves have the state and dv, the others its transpose and
 // dk (with both in the registers of the same waves, eight of them, the gradient
-// of B1 T8192 H32 D128 took 298 us; with sixteen 270).
+// of B1 T8192 H32 D128 took 298 us and with sixteen 270, when bf16 operands had
+// fewer parts).  Nearly half of its 314 now; the registers hold no more.
 
 template <typename IO, int D, bool DOT>
 __global__ __launch_bounds__(128 * nwaves<D>(), 4) void kda_lin_both(

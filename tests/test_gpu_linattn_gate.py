@@ -182,3 +182,42 @@ def test_states_of_any_size(kda, io, big):
     d["do"] = (d["do"].float() / big).to(io)
     d["dsT"] = d["dsT"] / big
     check(kda, x, d, 300)
+
+
+@pytest.mark.parametrize("io", [BF, F])
+@pytest.mark.parametrize("kind", ["slow", "softplus", "fixed"])
+def test_what_a_workspace_holds_does_not_matter(kda, io, kind):
+    """sequences of several marks, of lengths before, at and behind them; the
+    marks that nothing is asked of are not read; captured and replayed too"""
+    C = CHUNK[io]
+    T = 27 * C
+    n = torch.tensor([T, 8 * C, 8 * C + 1, 16 * C - 1, 3, 0, 24 * C, 25 * C],
+                     dtype=torch.int32, device="cuda")
+    x, d = inputs(8, T, 1, 1, 32, 64, io, kind, seed=6)
+    y = {k: t.cuda().repeat_interleave(70, 0 if t.dim() == 1 else 1 if k in
+                                       ("s0", "dsT") else 2).contiguous()
+         for k, t in {**x, **d}.items()}
+    size = kda.kda_linattn_backward_workspace_size(8, T, 70, 70, 32, 64, io)
+
+    def run(ws):
+        return kda.kda_linattn_backward(
+            *[y[k] for k in "qkvg"], y["do"], s0=y["s0"], dsT=y["dsT"],
+            lengths=n, workspace=ws)
+
+    base = run(torch.zeros(size, dtype=torch.uint8, device="cuda"))
+    # NaNs, and values like any
+    ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+    assert all(torch.equal(a, b) for a, b in zip(base, run(ws)))
+    ws.fill_(63)
+    assert all(torch.equal(a, b) for a, b in zip(base, run(ws)))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = run(ws)
+    for fill in (255, 63, 0):
+        ws.fill_(fill)
+        for t in got:
+            t.fill_(7)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(base, got))
+        run(None)
