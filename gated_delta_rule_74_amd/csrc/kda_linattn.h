@@ -107,7 +107,12 @@ struct LinLocal {
 constexpr int lin_chunk(int io_bf16) { return io_bf16 ? 64 : 32; }
 // Marks lie before every LIN_MARK-th chunk of a segment but its first: there the
 // product of the state and its gradient is made anew for the gate's gradient, if
-// the chunk before leaves more than LIN_MARK_MIN of what comes to it.
+// the chunk before leaves more than LIN_MARK_MIN of what comes to it.  dg of slow
+// gates is 4e-7 off without marks, 2.5e-7 with every 8th, 2.3e-7 with every 4th,
+// of fixed decays 1e-6 to 2e-6, 3e-7 to 1e-6 and 2e-7 to 1e-6; the gradient of B8
+// T4096 H32 D64 takes 521, 530 and 544 us.  Where a chunk forgets all but 2^-24,
+// what crosses it is cut to that in any case (B1 T8192 H32 D128 with such gates:
+// 310 us without marks, 315 so, 320 with all).
 constexpr int LIN_MARK = 8;
 constexpr float LIN_MARK_MIN = 0x1p-24f;
 constexpr int lin_marks(int chunks) { return (chunks - 1) / LIN_MARK; }

@@ -1026,7 +1026,7 @@ __global__ __launch_bounds__(64 * nwaves<D2>(), 2) void kda_lin_sweep(
                 REV ? p.far_scale : p.add_scale, w, lane);
     keeper.fetch(q, at, n0 + BATCH, w, lane);
   };
-  // whether the mark behind a chunk is
+  // whether a mark behind chunk n is written and read
   auto wanted = [&](int n) {
     return decs[n % (2 * BATCH)].total > LIN_MARK_MIN;
   };

@@ -512,8 +512,8 @@ size_t kda_linattn_backward_workspace_size(int B, int T, int Hk, int H, int Dk,
  * With bf16 data o is, before its own rounding, within 2^-17 of its terms'
  * magnitudes; what is written in fp32 is as with fp32 data (of terms that are
  * below 2^-100 the last bits may be lost).  Terms that have decayed below 2^-126
- * may count as none.  Values are not checked.  An infinity
- * or NaN in q, k, v or s0 reaches
+ * may count as none.  Values are not checked.  An infinity or NaN in q, k, v or
+ * s0 reaches
  *   - through the state every later token of its sequence and head; a g of -inf
  *     does not clear it (0 * inf is NaN)
  *   - the outputs of up to 63 tokens before it (those of its chunk: 0 * inf in

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from layer_ref import U, within
-from linattn_gate_ref import Parts
+from linattn_gate_ref import K, Parts
 
 pytestmark = pytest.mark.gpu
 BF, F = torch.bfloat16, torch.float32
@@ -221,3 +221,22 @@ def test_what_a_workspace_holds_does_not_matter(kda, io, kind):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(base, got))
         run(None)
+
+
+@pytest.mark.parametrize("io", [BF, F])
+@pytest.mark.parametrize("D", [16, 64, 128])
+@pytest.mark.parametrize("g0", [-18.0, -20.0, -24.0])
+@pytest.mark.parametrize("seed", [0, 1, 2])
+def test_no_gradient_is_rounding_alone(kda, io, D, g0, seed):
+    """A token that forgets so much that what crosses its chunk, exp(g0) of what
+    is across its end (2^-26 at most, 8 half steps of fp32 are 2^-21), cannot be
+    told from rounding: it counts as nothing, and the rest is the token's own to
+    its accuracy."""
+    C = CHUNK[io]
+    x, d = inputs(1, 512, 1, 2, D, D, io, "slow", seed=seed)
+    x["g"][:, 300] = g0
+    p = Parts(x, d, C, 1 << 20)
+    want = p.gradient()[0][0, 300]
+    got = gradient(kda, x, d, 1 if D == 128 else 300)[0, 300]
+    off = p.Z[300 // C][0].abs() + K * p.W[300][0]
+    assert ((got - want).abs() <= off).all()
